@@ -244,7 +244,7 @@ def _plain_glr(s):
         if c["way"] == "fwd":
             return out
     dy = s["dy"].float()
-    w = _gate_out(s, dy)
+    w = dy.clone() if s["z"] is None else _gate_out(s, dy)   # not the input itself, to which the next line would add
     w[..., -1] += s["dh_final"]
     # g_t = w_t + a_(t+1) g_(t+1): the same scan from the other end
     g = _scan(torch.nn.functional.pad(a[..., 1:], (0, 1)).flip(-1), w.flip(-1)).flip(-1)
