@@ -314,6 +314,130 @@ ss_status ss_scan_bwd_seg(int64_t batch, int64_t dim, int dstate, int64_t seqlen
                           float* dA, float* dDskip, float* ddt_bias, float* dh0,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gated linear recurrence: one state per channel, a gate of its own on what it
+ * keeps, and optional gates on its input and output.  Theorem 1 in the reader's
+ * notes on the Mamba paper (kurisu.si, "Main results (verified)") shows that the
+ * selective state-space model with one state is a gated recurrence, h = (1 - s) h
+ * + s x; this is that recurrence by itself, for recurrent layers that stand next
+ * to the scan.  With s = sigmoid(r[b,d,t] + r_bias[d]) and iota = sigmoid(i[b,d,t]
+ * + i_bias[d]) (1 without i):
+ *
+ *   SS_GLR_CONVEX      a = f + (1 - f) s, f = decay[d] in [0, 1], a floor under
+ *                      the decay (NULL: 0);  u = (1 - a) iota x
+ *   SS_GLR_NORMALISED  a = exp(-decay_scale softplus(decay[d]) s), decay required;
+ *                      u = sqrt(1 - a^2) iota x, which keeps the variance of a
+ *                      state whose inputs have variance one
+ *   h_t = a_t h_(t-1) + u_t,   y_t = h_t silu(z_t)  (h_t without z)
+ *
+ * Layouts are the scan's: x, r, i, z, y (batch, dim, seqlen) in the I/O dtype (the
+ * step: (batch, dim)); decay, r_bias, i_bias (dim) and h0, h_final, state
+ * (batch, dim) fp32.  i, z, r_bias, i_bias, h0 and h_final are nullable; i_bias
+ * needs i.  decay_scale must be positive and finite with SS_GLR_NORMALISED and is
+ * not read otherwise.  The state and all arithmetic are fp32; y and the gradients
+ * of I/O tensors are rounded once.  Tensors need only their elements' alignment
+ * (4 bytes for fp32 vectors and states), and any seqlen >= 0 runs at full
+ * vector width.  A token that must not change the state (padding) has r = +inf
+ * (convex) or r = -inf (normalised) and a finite x: its decay is exactly 1 and
+ * its input exactly 0, and its gradients of x, r and i are zero.
+ *
+ * Ownership, streams, errors and overlaps are as for ss_scan_fwd.  Results are
+ * deterministic: every sum runs in a fixed order.
+ *
+ *  ss_glr_fwd: h_final is the state after the last token (h0 when seqlen is 0).
+ *    ckpt (nullable, ss_glr_ckpt_bytes) receives the state entering every 2048
+ *    tokens, for ss_glr_bwd.  The workspace (ss_glr_fwd_workspace_bytes; 0 bytes,
+ *    and then not looked at, unless few rows are long) is 256-byte aligned.
+ *  ss_glr_bwd: given dy (batch, dim, seqlen) and dh_final (batch, dim; NULL =
+ *    zero), writes dx, dr (required when seqlen > 0), di and dz (given exactly
+ *    when i and z are), and, where not NULL, the fp32 gradients ddecay, dr_bias,
+ *    di_bias (dim; summed over batch and tokens; di_bias needs i) and dh0
+ *    (batch, dim).  ddecay is of decay itself (through its softplus in the
+ *    normalised kind), also when decay is NULL (read as zero).  ckpt (nullable)
+ *    is what ss_glr_fwd stored for the same inputs; without it the states are
+ *    recomputed.  The workspace (ss_glr_bwd_workspace_bytes) is as above; its size
+ *    does not depend on ckpt.
+ *  ss_glr_step: one token.  state_out may be state_in itself (updated in place).
+ *
+ * Each size query returns 0 for invalid sizes. */
+typedef enum { SS_GLR_CONVEX = 0, SS_GLR_NORMALISED = 1 } ss_glr_kind;
+
+size_t ss_glr_ckpt_bytes(int64_t batch, int64_t dim, int64_t seqlen);
+size_t ss_glr_fwd_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen);
+ss_status ss_glr_fwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss_glr_kind kind, float decay_scale,
+                     const void* x, const void* r, const void* i, const void* z,
+                     const float* decay, const float* r_bias, const float* i_bias, const float* h0,
+                     void* y, float* h_final, float* ckpt,
+                     void* workspace, size_t workspace_bytes, void* stream);
+size_t ss_glr_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen);
+ss_status ss_glr_bwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss_glr_kind kind, float decay_scale,
+                     const void* x, const void* r, const void* i, const void* z,
+                     const float* decay, const float* r_bias, const float* i_bias, const float* h0,
+                     const void* dy, const float* dh_final, const float* ckpt,
+                     void* dx, void* dr, void* di, void* dz,
+                     float* ddecay, float* dr_bias, float* di_bias, float* dh0,
+                     void* workspace, size_t workspace_bytes, void* stream);
+ss_status ss_glr_step(int64_t batch, int64_t dim, ss_dtype io, ss_glr_kind kind, float decay_scale,
+                      const float* state_in, float* state_out,
+                      const void* x, const void* r, const void* i, const void* z,
+                      const float* decay, const float* r_bias, const float* i_bias,
+                      void* y, void* stream);
+
+/* Norm and position rotation of queries and keys, in one pass.  In the attention
+ * view of a selective scan (first abstract of the "Mamba models" page) its C_t
+ * are the queries and its B_t the keys; this call makes them from the rows that
+ * a projection wrote: for every token and head, with v the head's N = head_dim
+ * values and w the weight (N, fp32; NULL = ones) of the queries or of the keys,
+ *
+ *     n = w v / sqrt(mean(v^2) + eps)
+ *     (n1, n2) -> (n1 cos - n2 sin, n2 cos + n1 sin)   for every rotated pair j,
+ *                 of angle  position[b,t] * inv_freq[j]
+ *
+ * The first rot_dim values are rotated: value j with value j + rot_dim/2, or 2j
+ * with 2j + 1 under SS_QK_INTERLEAVED.  rot_dim is even, 0 <= rot_dim <= head_dim;
+ * inv_freq (rot_dim/2, fp64, radians per token) may be NULL when it is 0.
+ * positions (batch, seqlen) int64, NULL for pos0 + t; negative ones rotate
+ * backwards.  Angles are formed in fp64 and reduced to a turn before anything is
+ * rounded, so a position of 2^40 is as exact as a small one; all else is fp32,
+ * each output rounded once.  eps must be positive and finite.
+ *
+ * Inputs: value n of head h of token (b, t) of the queries is at
+ * q[b q_stride[0] + t q_stride[1] + h q_stride[2] + n], strides in elements and
+ * nonnegative, so q and k may be columns of one projection's rows; the same for k
+ * with k_stride.  q (or k) is NULL exactly when its head count is 0.
+ * Outputs are contiguous: (batch, seqlen, heads, head_dim), or with
+ * SS_QK_FEATURE_MAJOR (batch, heads, head_dim, seqlen), which for one head is the
+ * layout in which the scan takes C and B (and at seqlen 1 that of the decode
+ * step); head_dim is then one of the scan's dstates, 1, 2, 4, 8 or 16.
+ * head_dim is otherwise 1 to 256.  No output may overlap an input's span of
+ * addresses.  q_out, k_out, dq_out and dk_out are 16-byte aligned; q, k, dq and
+ * dk need only their elements' alignment.
+ *
+ * The backward takes the forward's inputs and the gradients dq_out, dk_out of
+ * its outputs in their layout, and writes dq, dk (batch, seqlen, heads, head_dim)
+ * under strides of their own, which may be interleaved columns of one buffer's
+ * rows (no two values may share an address), and, where not NULL, dwq and dwk
+ * (head_dim, fp32), the gradients of the weights (also of weights that are NULL),
+ * summed in a fixed order.  Its workspace (ss_qk_norm_rot_bwd_workspace_bytes,
+ * 256-byte aligned) holds their partial sums. */
+typedef enum { SS_QK_INTERLEAVED = 1u, SS_QK_FEATURE_MAJOR = 2u } ss_qk_flags;
+
+ss_status ss_qk_norm_rot(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim,
+                         ss_dtype io, uint32_t flags, float eps,
+                         const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                         const float* wq, const float* wk, const double* inv_freq,
+                         const int64_t* positions, int64_t pos0,
+                         void* q_out, void* k_out, void* stream);
+size_t ss_qk_norm_rot_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim);
+ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim,
+                             ss_dtype io, uint32_t flags, float eps,
+                             const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                             const float* wq, const float* wk, const double* inv_freq,
+                             const int64_t* positions, int64_t pos0,
+                             const void* dq_out, const void* dk_out,
+                             void* dq, const int64_t* dq_stride, void* dk, const int64_t* dk_stride,
+                             float* dwq, float* dwk,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the static device scratch array behind ss_scan_fwd_noalloc (32 MiB per GPU). */
 #define SS_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
 

@@ -96,6 +96,24 @@ def _load():
     lib.ss_scan_fwd_noalloc.restype = _int
     lib.ss_scan_fwd_noalloc.argtypes = ([_i64, _i64, _int, _i64, _int, ctypes.c_uint32] + [_vp] * 12
                                         + [ctypes.POINTER(ss_scan_plan), _vp])
+    _f32 = ctypes.c_float
+    _st = ctypes.POINTER(_i64)
+    for name in ("ss_glr_ckpt_bytes", "ss_glr_fwd_workspace_bytes", "ss_glr_bwd_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
+        getattr(lib, name).argtypes = [_i64, _i64, _i64]
+    lib.ss_glr_fwd.restype = _int
+    lib.ss_glr_fwd.argtypes = [_i64, _i64, _i64, _int, _int, _f32] + [_vp] * 12 + [ctypes.c_size_t, _vp]
+    lib.ss_glr_bwd.restype = _int
+    lib.ss_glr_bwd.argtypes = [_i64, _i64, _i64, _int, _int, _f32] + [_vp] * 20 + [ctypes.c_size_t, _vp]
+    lib.ss_glr_step.restype = _int
+    lib.ss_glr_step.argtypes = [_i64, _i64, _int, _int, _f32] + [_vp] * 11
+    _qk = [_i64, _i64, _int, _int, _int, _int, _int, ctypes.c_uint32, _f32, _vp, _st, _vp, _st, _vp, _vp, _vp, _vp, _i64]
+    lib.ss_qk_norm_rot.restype = _int
+    lib.ss_qk_norm_rot.argtypes = _qk + [_vp] * 3
+    lib.ss_qk_norm_rot_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.ss_qk_norm_rot_bwd_workspace_bytes.argtypes = [_i64, _i64, _int, _int, _int]
+    lib.ss_qk_norm_rot_bwd.restype = _int
+    lib.ss_qk_norm_rot_bwd.argtypes = _qk + [_vp, _vp, _vp, _st, _vp, _st, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.ss_timing_enable.restype = _int
     lib.ss_timing_enable.argtypes = [_int]
     lib.ss_timing_reset.restype = _int
@@ -251,6 +269,67 @@ def ss_scan_shard_state_zoh(batch, dim, dstate, seqlen, io, x, dt, B, A, dt_bias
 
 def ss_scan_shard_combine(batch, dim, dstate, nshards, A, dsum, h_end, h0, h_in, h_final, stream=None):
     _check(lib.ss_scan_shard_combine(batch, dim, dstate, nshards, A, dsum, h_end, h0, h_in, h_final, stream))
+
+
+SS_GLR_CONVEX, SS_GLR_NORMALISED = 0, 1
+
+
+def ss_glr_ckpt_bytes(batch, dim, seqlen) -> int:
+    return int(lib.ss_glr_ckpt_bytes(batch, dim, seqlen))
+
+
+def ss_glr_fwd_workspace_bytes(batch, dim, seqlen) -> int:
+    return int(lib.ss_glr_fwd_workspace_bytes(batch, dim, seqlen))
+
+
+def ss_glr_fwd(batch, dim, seqlen, io, kind, decay_scale, x, r, i, z, decay, r_bias, i_bias, h0, y, h_final, ckpt,
+               workspace, workspace_bytes, stream=None):
+    _check(lib.ss_glr_fwd(batch, dim, seqlen, io, kind, decay_scale, x, r, i, z, decay, r_bias, i_bias, h0, y, h_final,
+                          ckpt, workspace, workspace_bytes, stream))
+
+
+def ss_glr_bwd_workspace_bytes(batch, dim, seqlen) -> int:
+    return int(lib.ss_glr_bwd_workspace_bytes(batch, dim, seqlen))
+
+
+def ss_glr_bwd(batch, dim, seqlen, io, kind, decay_scale, x, r, i, z, decay, r_bias, i_bias, h0, dy, dh_final, ckpt,
+               dx, dr, di, dz, ddecay, dr_bias, di_bias, dh0, workspace, workspace_bytes, stream=None):
+    _check(lib.ss_glr_bwd(batch, dim, seqlen, io, kind, decay_scale, x, r, i, z, decay, r_bias, i_bias, h0, dy, dh_final,
+                          ckpt, dx, dr, di, dz, ddecay, dr_bias, di_bias, dh0, workspace, workspace_bytes, stream))
+
+
+def ss_glr_step(batch, dim, io, kind, decay_scale, state_in, state_out, x, r, i, z, decay, r_bias, i_bias, y,
+                stream=None):
+    _check(lib.ss_glr_step(batch, dim, io, kind, decay_scale, state_in, state_out, x, r, i, z, decay, r_bias, i_bias, y,
+                           stream))
+
+
+SS_QK_INTERLEAVED = 1
+SS_QK_FEATURE_MAJOR = 2
+
+
+def _strides(s):
+    """(batch, token, head) strides in elements as the C entry points take them; None without that side."""
+    return None if s is None else (_i64 * 3)(*s)
+
+
+def ss_qk_norm_rot(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, q_stride, k, k_stride, wq, wk,
+                   inv_freq, positions, pos0, q_out, k_out, stream=None):
+    _check(lib.ss_qk_norm_rot(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, _strides(q_stride),
+                              k, _strides(k_stride), wq, wk, inv_freq, positions, pos0, q_out, k_out, stream))
+
+
+def ss_qk_norm_rot_bwd_workspace_bytes(batch, seqlen, heads_q, heads_k, head_dim) -> int:
+    return int(lib.ss_qk_norm_rot_bwd_workspace_bytes(batch, seqlen, heads_q, heads_k, head_dim))
+
+
+def ss_qk_norm_rot_bwd(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, q_stride, k, k_stride,
+                       wq, wk, inv_freq, positions, pos0, dq_out, dk_out, dq, dq_stride, dk, dk_stride, dwq, dwk,
+                       workspace, workspace_bytes, stream=None):
+    _check(lib.ss_qk_norm_rot_bwd(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q,
+                                  _strides(q_stride), k, _strides(k_stride), wq, wk, inv_freq, positions, pos0, dq_out,
+                                  dk_out, dq, _strides(dq_stride), dk, _strides(dk_stride), dwq, dwk, workspace,
+                                  workspace_bytes, stream))
 
 
 def ss_timing_enable(enable: bool):

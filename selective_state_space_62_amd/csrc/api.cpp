@@ -11,9 +11,18 @@
 #include <string>
 #include <vector>
 
+#include "api_checks.h"
 #include "internal.h"
 
 namespace {
+
+using ssscan::aligned;
+using ssscan::elem_bytes;
+using ssscan::kMaxDim;
+using ssscan::overlap;
+using ssscan::Range;
+using ssscan::rng;
+using ssscan::round256;
 
 thread_local std::string g_last_error;
 
@@ -53,25 +62,6 @@ namespace {
 
 bool valid_dstate(int n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
 
-int elem_bytes(ss_dtype io) { return io == SS_BF16 ? 2 : 4; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-  const char* name;
-  uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range rng(const char* name, const void* p, int64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{name, lo, p ? lo + (uintptr_t)bytes : lo};
-}
-
-bool overlap(const Range& a, const Range& b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
 // Device properties are queried once per device.
 int device_cus() {
   static std::mutex mu;
@@ -87,8 +77,6 @@ int device_cus() {
   }
   return cache[dev];
 }
-
-constexpr int64_t kMaxDim = int64_t(1) << 40;
 
 ss_status check_sizes(int64_t batch, int64_t dim, int dstate, int64_t seqlen, ss_dtype io) {
   if (io != SS_F32 && io != SS_BF16) return fail(SS_ERR_UNSUPPORTED, "io dtype %d is not SS_F32 or SS_BF16", (int)io);
@@ -194,8 +182,6 @@ ss_status make_plan(int64_t batch, int64_t dim, int dstate, int64_t seqlen, ss_d
 struct WsLayout {
   size_t agg_h, agg_s, h_in, total;
 };
-
-size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // The forward's scratch: on chunked plans only, each chunk's end state from a
 // zero start and sum of Delta, and each chunk's entering state.

@@ -1,0 +1,206 @@
+// Device code shared by the gated linear recurrence's kernels (gfx950).
+#pragma once
+
+#include "device_common.h"
+#include "glr.h"
+#include "internal.h"
+
+namespace ssscan {
+namespace glr {
+
+using namespace dev;
+
+constexpr int kConvex = 0, kNormalised = 1;
+constexpr int kV = 8;             // tokens per lane and tile
+constexpr float kTiny = 1.17549435e-38f;
+
+// kV consecutive elements of a row as they are in memory.
+template <typename IO>
+struct Raw {
+  static constexpr int kWords = kV * (int)sizeof(typename IO::T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float operator[](int j) const { return span_elem<IO>(w, j); }
+};
+
+template <typename IO>
+__device__ __forceinline__ Raw<IO> load_raw(const typename IO::T* __restrict__ p, int valid) {
+  Raw<IO> o;
+#pragma unroll
+  for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = 0u;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    if (j < valid) {
+      if constexpr (IO::kPerSpan == 4) o.w[j] = __float_as_uint(p[j]);
+      else o.w[j >> 1] |= (uint32_t)p[j] << ((j & 1) * 16);
+    }
+  }
+  return o;
+}
+
+template <typename IO>
+__device__ __forceinline__ void store_raw(typename IO::T* __restrict__ p, int valid, const float (&v)[kV]) {
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
+    if (j < valid) store_one<IO>(p, j, v[j]);
+}
+
+// What a row's tokens share: the biases times -log2(e), and of the decay
+//   convex:     c0 = f, c1 = 1 - f
+//   normalised: c0 = -l log2(e), c1 = 2 l, with l = decay_scale softplus(decay)
+struct RowConst {
+  float rb, ib, c0, c1;
+};
+
+template <int KIND>
+__device__ __forceinline__ RowConst row_const(const GlrArgs& p, int64_t d) {
+  RowConst c;
+  c.rb = p.r_bias ? -kLog2e * p.r_bias[d] : 0.0f;
+  c.ib = p.i_bias ? -kLog2e * p.i_bias[d] : 0.0f;
+  const float v = p.decay ? p.decay[d] : 0.0f;
+  if constexpr (KIND == kConvex) {
+    c.c0 = v;
+    c.c1 = 1.0f - v;
+  } else {
+    const float l = p.decay_scale * softplus_dt(v, 0.0f);
+    c.c0 = -kLog2e * l;
+    c.c1 = 2.0f * l;
+  }
+  return c;
+}
+
+// sigmoid(v + bias), given nb = -log2(e) bias; e receives exp(-(v + bias)).
+__device__ __forceinline__ float sigmoid_e(float v, float nb, float& e) {
+  e = __builtin_amdgcn_exp2f(fmaf(v, -kLog2e, nb));
+  return __builtin_amdgcn_rcpf(1.0f + e);   // 0 where e overflowed
+}
+
+// 1 - s of the sigmoid above without cancellation: e s where s is the larger
+// half.  e s is never formed from an overflowed e (the comparison selects 1 - s).
+__device__ __forceinline__ float one_minus(float s, float e) { return e > 1.0f ? 1.0f - s : e * s; }
+
+// 1 - a^2 of the normalised kind, with w = 2 l s and a = e^(-w/2).  1 - a a loses
+// digits as a nears 1 (the usual case: decays of 0.9 to 0.999), so below w = 1/8 it
+// is the Taylor polynomial of 1 - e^-w, whose first dropped term is w^5/720, 4.3e-8
+// relative there; above, a's rounding costs at most 6e-8/0.117 in 1 - a^2.
+__device__ __forceinline__ float one_minus_sq(float w, float a) {
+  float t = fmaf(w, 1.0f / 120.0f, -1.0f / 24.0f);
+  t = fmaf(t, w, 1.0f / 6.0f);
+  t = fmaf(t, w, -0.5f);
+  t = fmaf(t, w, 1.0f) * w;
+  return w < 0.125f ? t : fmaf(-a, a, 1.0f);
+}
+
+// One token's decay a and input weight m.
+template <int KIND>
+__device__ __forceinline__ void gate(float r, const RowConst& c, float& a, float& m) {
+  float e;
+  const float s = sigmoid_e(r, c.rb, e);
+  if constexpr (KIND == kConvex) {
+    a = fmaf(c.c1, s, c.c0);
+    m = c.c1 * one_minus(s, e);
+  } else {
+    a = __builtin_amdgcn_exp2f(c.c0 * s);
+    const float q = one_minus_sq(c.c1 * s, a);
+    m = q * __builtin_amdgcn_rsqf(fmaxf(q, kTiny));   // sqrt(q); 0 at 0
+  }
+}
+
+// --- scans over the wave's 64 lanes of maps h -> A h + B -----------------------
+// In each step a lane joins its piece with the one `k` lanes away, or with the
+// identity where there is none (update_dpp keeps `old` for a missing source).
+
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xf, false);
+}
+
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ void join(float& A, float& B) {
+  const float a = dpp<CTRL, ROWS>(1.0f, A), b = dpp<CTRL, ROWS>(0.0f, B);
+  B = fmaf(A, b, B);
+  A *= a;
+}
+
+// Lane l gets the composition of lanes 0 .. l, lane 0's applied first.
+__device__ __forceinline__ void scan_up(float& A, float& B) {
+  join<0x111>(A, B);        // row_shr:1, 2, 4, 8 within rows of 16 lanes
+  join<0x112>(A, B);
+  join<0x114>(A, B);
+  join<0x118>(A, B);
+  join<0x142, 0xa>(A, B);   // row_bcast:15 into rows 1 and 3
+  join<0x143, 0xc>(A, B);   // row_bcast:31 into rows 2 and 3
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// Lane l gets the composition of lanes l .. 63, lane 63's applied first.  There is
+// no broadcast towards lower rows, so the rows' totals go through scalars.
+__device__ __forceinline__ void scan_down(float& A, float& B, int lane) {
+  join<0x101>(A, B);        // row_shl:1, 2, 4, 8
+  join<0x102>(A, B);
+  join<0x104>(A, B);
+  join<0x108>(A, B);
+  const float a3 = lane_value(A, 48), b3 = lane_value(B, 48);
+  const float a2 = lane_value(A, 32), b2 = lane_value(B, 32);
+  const float a1 = lane_value(A, 16), b1 = lane_value(B, 16);
+  const float a23 = a2 * a3, b23 = fmaf(a2, b3, b2);
+  const float a123 = a1 * a23, b123 = fmaf(a1, b23, b1);
+  const int row = lane >> 4;
+  const float a = row == 0 ? a123 : row == 1 ? a23 : row == 2 ? a3 : 1.0f;
+  const float b = row == 0 ? b123 : row == 1 ? b23 : row == 2 ? b3 : 0.0f;
+  B = fmaf(A, b, B);
+  A *= a;
+}
+
+// The compositions of the lanes before (after) a lane's own, from those above.
+__device__ __forceinline__ float shift_up(float old, float v) { return dpp<0x138>(old, v); }     // wave_shr:1
+__device__ __forceinline__ float shift_down(float old, float v) { return dpp<0x130>(old, v); }   // wave_shl:1
+
+// Sum over the wave's lanes in a fixed order, in lane 63.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111>(0.0f, v);
+  v += dpp<0x112>(0.0f, v);
+  v += dpp<0x114>(0.0f, v);
+  v += dpp<0x118>(0.0f, v);
+  v += dpp<0x142, 0xa>(0.0f, v);
+  v += dpp<0x143, 0xc>(0.0f, v);
+  return v;
+}
+
+// --- launch shape ---------------------------------------------------------------
+// Workgroups of 256 threads hold 4 / W rows of W waves; a grid dimension's
+// threads are 32-bit, so large launches use two dimensions.
+inline bool grid_of(int64_t blocks, dim3* g) {
+  constexpr int64_t kX = int64_t(1) << 22;
+  if (blocks <= kX) {
+    *g = dim3((unsigned)blocks);
+    return true;
+  }
+  const int64_t y = (blocks + kX - 1) / kX;
+  if (y > 65535) return false;
+  *g = dim3((unsigned)kX, (unsigned)y);
+  return true;
+}
+
+__device__ __forceinline__ int64_t block_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+inline int waves_for(int64_t seqlen) { return seqlen <= 64 * kV ? 1 : seqlen <= 128 * kV ? 2 : 4; }
+
+// OP<io, kind, has i, has z>::go(a, s) for the call's form.
+template <template <typename, int, bool, bool> class OP, typename IO, int KIND>
+hipError_t by_gates(const GlrArgs& a, hipStream_t s) {
+  if (a.i) return a.z ? OP<IO, KIND, true, true>::go(a, s) : OP<IO, KIND, true, false>::go(a, s);
+  return a.z ? OP<IO, KIND, false, true>::go(a, s) : OP<IO, KIND, false, false>::go(a, s);
+}
+
+template <template <typename, int, bool, bool> class OP>
+hipError_t by_form(const GlrArgs& a, hipStream_t s) {
+  if (a.io == kIoBf16)
+    return a.kind == kConvex ? by_gates<OP, BF16, kConvex>(a, s) : by_gates<OP, BF16, kNormalised>(a, s);
+  return a.kind == kConvex ? by_gates<OP, F32, kConvex>(a, s) : by_gates<OP, F32, kNormalised>(a, s);
+}
+
+}  // namespace glr
+}  // namespace ssscan

@@ -1,0 +1,252 @@
+// Norm and position rotation of queries and keys, forward and backward (gfx950).
+//
+// A wave takes one vector (the values of one head at one token) at a time; a lane
+// holds pairs of values that a rotation mixes, so that after the sum of squares
+// no value crosses lanes.
+#include "device_common.h"
+#include "internal.h"
+#include "qk_norm_rot.h"
+
+namespace ssscan {
+namespace {
+
+using namespace dev;
+
+constexpr int kSlots = 2;   // pairs per lane: head_dim <= 256
+
+// cos and sin of pos * freq (radians).  The angle in turns is formed and reduced
+// to an eighth of a turn in fp64 (an fp32 product is off by radians at positions
+// of millions); the rest is a Taylor polynomial on |x| <= pi/4, whose first dropped
+// terms are below 2e-9 (sin) and 3e-8 (cos).
+__device__ __forceinline__ void angle(double pos, double freq, float& c, float& s) {
+  const double turns = pos * (freq * 0.15915494309189533577);
+  const double f = turns - __builtin_rint(turns);
+  const double q = __builtin_rint(4.0 * f);
+  const float x = (float)(f - 0.25 * q) * 6.28318530717958647693f;
+  const float x2 = x * x;
+  float ps = fmaf(x2, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  ps = fmaf(ps, x2, 1.0f / 120.0f);
+  ps = fmaf(ps, x2, -1.0f / 6.0f);
+  ps = fmaf(ps * x2, x, x);
+  float pc = fmaf(x2, 1.0f / 40320.0f, -1.0f / 720.0f);
+  pc = fmaf(pc, x2, 1.0f / 24.0f);
+  pc = fmaf(pc, x2, -0.5f);
+  pc = fmaf(pc, x2, 1.0f);
+  const int k = (int)q & 3;
+  const float cs = k & 1 ? ps : pc, sn = k & 1 ? pc : ps;
+  c = k == 1 || k == 2 ? -cs : cs;
+  s = k >= 2 ? -sn : sn;
+}
+
+__device__ __forceinline__ float wave_total(float v) {
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k);
+  return v;
+}
+
+// The places of pair p's two values; the second is -1 for a last single value.
+__device__ __forceinline__ void places(const QkArgs& a, int p, int& j1, int& j2) {
+  if (p < a.half) {
+    j1 = a.interleaved ? 2 * p : p;
+    j2 = a.interleaved ? 2 * p + 1 : p + a.half;
+  } else {
+    j1 = 2 * p;
+    j2 = j1 + 1 < a.n ? j1 + 1 : -1;
+  }
+}
+
+struct Vec {
+  int64_t b, t, tok;
+  int h;
+};
+
+__device__ __forceinline__ Vec vec_of(const QkArgs& a, int64_t v, int heads) {
+  Vec o;
+  o.tok = v / heads;
+  o.h = (int)(v - o.tok * heads);
+  o.b = o.tok / a.seqlen;
+  o.t = o.tok - o.b * a.seqlen;
+  return o;
+}
+
+// Where value j of the vector stands in the contiguous output layout.
+__device__ __forceinline__ int64_t out_index(const QkArgs& a, const Vec& v, int heads, int j) {
+  if (a.feature_major) return ((v.b * heads + v.h) * a.n + j) * a.seqlen + v.t;
+  return (v.tok * heads + v.h) * a.n + j;
+}
+
+__device__ __forceinline__ double position(const QkArgs& a, const Vec& v) {
+  return (double)(a.positions ? a.positions[v.tok] : a.pos0 + v.t);
+}
+
+template <typename IO>
+__global__ __launch_bounds__(256) void qk_fwd_kernel(QkArgs a) {
+  using T = typename IO::T;
+  const QkSide& sd = a.side[blockIdx.z];
+  const int lane = threadIdx.x & 63;
+  const int64_t vectors = a.batch * a.seqlen * sd.heads;
+  const int64_t waves = (int64_t)gridDim.x * 4;
+  const int pairs = a.half + (a.n - 2 * a.half + 1) / 2;
+  for (int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); v < vectors; v += waves) {
+    const Vec o = vec_of(a, v, sd.heads);
+    const T* in = (const T*)sd.in + o.b * sd.stride[0] + o.t * sd.stride[1] + o.h * sd.stride[2];
+    T* out = (T*)sd.out;
+    float x[kSlots][2];
+    float sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int p = lane + 64 * k;
+      int j1, j2;
+      places(a, p, j1, j2);
+      x[k][0] = p < pairs ? load_one<IO>(in, j1) : 0.0f;
+      x[k][1] = p < pairs && j2 >= 0 ? load_one<IO>(in, j2) : 0.0f;
+      sq = fmaf(x[k][0], x[k][0], sq);
+      sq = fmaf(x[k][1], x[k][1], sq);
+    }
+    const float rho = 1.0f / __builtin_sqrtf(wave_total(sq) / (float)a.n + a.eps);
+    const double pos = position(a, o);
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int p = lane + 64 * k;
+      if (p >= pairs) continue;
+      int j1, j2;
+      places(a, p, j1, j2);
+      float n1 = x[k][0] * rho * (sd.w ? sd.w[j1] : 1.0f);
+      float n2 = j2 >= 0 ? x[k][1] * rho * (sd.w ? sd.w[j2] : 1.0f) : 0.0f;
+      if (p < a.half) {
+        float c, s;
+        angle(pos, a.inv_freq[p], c, s);
+        const float r1 = n1 * c - n2 * s;
+        n2 = fmaf(n2, c, n1 * s);
+        n1 = r1;
+      }
+      store_one<IO>(out, out_index(a, o, sd.heads, j1), n1);
+      if (j2 >= 0) store_one<IO>(out, out_index(a, o, sd.heads, j2), n2);
+    }
+  }
+}
+
+// With n = rho w v and o the rotated n: dn is the gradient of o rotated back, and
+// with p = w dn, dv = rho p - rho^3 v mean(p v), dw = sum of dn rho v.
+template <typename IO>
+__global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
+  using T = typename IO::T;
+  __shared__ float s_dw[4][256];
+  const QkSide& sd = a.side[blockIdx.z];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t vectors = a.batch * a.seqlen * sd.heads;
+  const int64_t waves = (int64_t)gridDim.x * 4;
+  const int pairs = a.half + (a.n - 2 * a.half + 1) / 2;
+  float dw[kSlots][2] = {};
+  for (int64_t v = (int64_t)blockIdx.x * 4 + wave; v < vectors; v += waves) {
+    const Vec o = vec_of(a, v, sd.heads);
+    const T* in = (const T*)sd.in + o.b * sd.stride[0] + o.t * sd.stride[1] + o.h * sd.stride[2];
+    T* din = (T*)sd.din + o.b * sd.dstride[0] + o.t * sd.dstride[1] + o.h * sd.dstride[2];
+    const T* dout = (const T*)sd.dout;
+    const double pos = position(a, o);
+    float x[kSlots][2], d[kSlots][2], pw[kSlots][2];
+    float sq = 0.0f, pv = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int p = lane + 64 * k;
+      int j1, j2;
+      places(a, p, j1, j2);
+      const bool one = p < pairs, two = one && j2 >= 0;
+      x[k][0] = one ? load_one<IO>(in, j1) : 0.0f;
+      x[k][1] = two ? load_one<IO>(in, j2) : 0.0f;
+      float d1 = one ? load_one<IO>(dout, out_index(a, o, sd.heads, j1)) : 0.0f;
+      float d2 = two ? load_one<IO>(dout, out_index(a, o, sd.heads, j2)) : 0.0f;
+      if (p < a.half) {
+        float c, s;
+        angle(pos, a.inv_freq[p], c, s);
+        const float r1 = fmaf(d1, c, d2 * s);
+        d2 = d2 * c - d1 * s;
+        d1 = r1;
+      }
+      d[k][0] = d1;
+      d[k][1] = d2;
+      pw[k][0] = one && sd.w ? d1 * sd.w[j1] : d1;
+      pw[k][1] = two && sd.w ? d2 * sd.w[j2] : d2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sq = fmaf(x[k][h], x[k][h], sq);
+        pv = fmaf(pw[k][h], x[k][h], pv);
+      }
+    }
+    const float rho = 1.0f / __builtin_sqrtf(wave_total(sq) / (float)a.n + a.eps);
+    const float back = rho * rho * (wave_total(pv) / (float)a.n);
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int p = lane + 64 * k;
+      int j1, j2;
+      places(a, p, j1, j2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) dw[k][h] = fmaf(d[k][h], rho * x[k][h], dw[k][h]);
+      if (p < pairs) store_one<IO>(din, j1, rho * (pw[k][0] - x[k][0] * back));
+      if (p < pairs && j2 >= 0) store_one<IO>(din, j2, rho * (pw[k][1] - x[k][1] * back));
+    }
+  }
+  if (!sd.dw) return;
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k) {
+    const int p = lane + 64 * k;
+    int j1, j2;
+    places(a, p, j1, j2);
+    if (p < pairs) s_dw[wave][j1] = dw[k][0];
+    if (p < pairs && j2 >= 0) s_dw[wave][j2] = dw[k][1];
+  }
+  __syncthreads();
+  const int j = threadIdx.x;
+  if (j < a.n)
+    a.part[((int64_t)blockIdx.x * 2 + blockIdx.z) * a.n + j] = (s_dw[0][j] + s_dw[1][j]) + (s_dw[2][j] + s_dw[3][j]);
+}
+
+// dw[j] of a side: the workgroups' partial sums in a fixed order, 16 runs of them
+// summed by 16 lanes and then joined.
+__global__ __launch_bounds__(256) void qk_reduce_kernel(QkArgs a, int64_t blocks) {
+  __shared__ float s_sum[16][16];
+  const QkSide& sd = a.side[blockIdx.z];
+  if (!sd.dw) return;
+  const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int j = (int)blockIdx.x * 16 + col;
+  float v = 0.0f;
+  if (j < a.n)
+    for (int64_t b = run; b < blocks; b += 16) v += a.part[(b * 2 + blockIdx.z) * a.n + j];
+  s_sum[run][col] = v;
+  __syncthreads();
+  if (run == 0 && j < a.n) {
+    for (int k = 1; k < 16; ++k) v += s_sum[k][col];
+    sd.dw[j] = v;
+  }
+}
+
+}  // namespace
+
+int64_t qk_bwd_blocks(int64_t batch, int64_t seqlen, int heads_q, int heads_k) {
+  const int64_t vectors = batch * seqlen * (heads_q > heads_k ? heads_q : heads_k);
+  const int64_t blocks = (vectors + 3) / 4;
+  return blocks < 1024 ? blocks : 1024;
+}
+
+hipError_t launch_qk_norm_rot(const QkArgs& a, hipStream_t s) {
+  const int hmax = a.side[0].heads > a.side[1].heads ? a.side[0].heads : a.side[1].heads;
+  int64_t blocks = (a.batch * a.seqlen * hmax + 3) / 4;
+  if (blocks > 8192) blocks = 8192;
+  const dim3 g((unsigned)blocks, 1, 2);
+  if (a.io == kIoBf16) hipLaunchKernelGGL((qk_fwd_kernel<BF16>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((qk_fwd_kernel<F32>), g, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_qk_norm_rot_bwd(const QkArgs& a, hipStream_t s) {
+  const int64_t blocks = qk_bwd_blocks(a.batch, a.seqlen, a.side[0].heads, a.side[1].heads);
+  const dim3 g((unsigned)blocks, 1, 2);
+  if (a.io == kIoBf16) hipLaunchKernelGGL((qk_bwd_kernel<BF16>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((qk_bwd_kernel<F32>), g, dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!a.side[0].dw && !a.side[1].dw)) return e;
+  hipLaunchKernelGGL(qk_reduce_kernel, dim3((unsigned)((a.n + 15) / 16), 1, 2), dim3(256), 0, s, a, blocks);
+  return hipGetLastError();
+}
+
+}  // namespace ssscan

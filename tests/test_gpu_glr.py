@@ -1,0 +1,441 @@
+"""The gated linear recurrence on the GPU against the formulas in 64 bits."""
+import numpy as np
+import pytest
+
+import bounds
+from bounds import U, V, check, recur, sigmoid
+from gpu_util import log, to_f64
+
+pytestmark = pytest.mark.gpu
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+SCALE = 8.0
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def ss():
+    import selective_state_space_62_amd as m
+    return m
+
+
+def problem(dev, seed, batch, dim, L, io="bf16", kind="normalised", i=True, z=True, h0=True, decay=True, bias=True,
+            step=False):
+    """Seeded inputs on the GPU, every value exact in its type."""
+    import torch
+    gen = torch.Generator().manual_seed(seed)
+    dt = torch.float32 if io == "f32" else torch.bfloat16
+    full = (batch, dim) if step else (batch, dim, L)
+
+    def n(*shape, dtype=torch.float32):
+        return torch.randn(shape, generator=gen).to(dtype).to(dev)
+
+    p = dict(x=n(*full, dtype=dt), r=n(*full, dtype=dt), i=n(*full, dtype=dt) if i else None,
+             z=n(*full, dtype=dt) if z else None, kind=kind)
+    if kind == "convex":
+        p["decay"] = torch.rand(dim, generator=gen).to(dev) if decay else None
+    else:   # from fast decays to ones within 1e-3 of 1, where 1 - a^2 cancels
+        p["decay"] = (torch.rand(dim, generator=gen) * 10 - 9).to(dev)
+    p["r_bias"] = n(dim) if bias else None
+    p["i_bias"] = n(dim) if bias and i else None
+    p["h0"] = n(batch, dim) if h0 else None
+    return p
+
+
+def f64(t):
+    return None if t is None else to_f64(t)
+
+
+def forward(p, adds):
+    """Gates, states and outputs with their bounds (batch, D, L)."""
+    col = lambda t: V(0.0) if t is None else V(f64(t)[:, None])  # noqa: E731
+    x, r = V(f64(p["x"])), V(f64(p["r"])) + col(p["r_bias"])
+    s, oms = sigmoid(r), sigmoid(-r)
+    g = {"s": s, "oms": oms, "x": x}
+    if p["kind"] == "convex":
+        f = col(p["decay"])
+        one = V(1.0) - f
+        g["a"], g["m"], g["one"] = f + one * s, one * oms, one
+    else:
+        d = f64(p["decay"])[:, None]
+        soft = np.logaddexp(0.0, d)
+        # softplus from log2(1 + e^-|d|): the exponent's rounding, exp2, the sum, log2 and the last sum
+        l = V(SCALE * soft, SCALE * soft * U * (2 * np.abs(d) + 10))
+        ls = l * s
+        a = np.exp(-ls.v)
+        g["a"] = V(a, a * (ls.e + 2 * U * np.abs(ls.v) + 2 * U))
+        q = -np.expm1(-2 * ls.v)
+        # by the polynomial below w = 1/8 (terms: 6 roundings and 4.3e-8 dropped), else 1 - a^2
+        rel = np.where(2 * ls.v < 0.125, (ls.e / np.maximum(ls.v, 1e-300)) + 8 * U, (2 * a * g["a"].e + 2 * U) / np.maximum(q, 0.1))
+        g["rel_q"], g["ls"] = rel, ls
+        g["m"] = V(np.sqrt(q), np.sqrt(q) * (0.5 * rel + 4 * U))
+        k = ls.v / np.maximum(np.sqrt(q), 1e-300)
+        g["k"] = V(k, k * (ls.e / np.maximum(ls.v, 1e-300) + 0.5 * rel + 4 * U))
+    g["ix"] = x
+    if p["i"] is not None:
+        i = V(f64(p["i"])) + col(p["i_bias"])
+        g["iota"], g["omi"] = sigmoid(i), sigmoid(-i)
+        g["ix"] = x * g["iota"]
+    h0 = np.zeros(x.v.shape[:2]) if p["h0"] is None else f64(p["h0"])
+    g["u"] = g["m"] * g["ix"]
+    g["h"], g["before"] = recur(g["a"], g["u"], V(h0), adds)
+    z = None if p["z"] is None else V(f64(p["z"]))
+    g["y"] = g["h"] if z is None else g["h"] * bounds.silu(z)
+    return g
+
+
+def backward(p, g, dy, dh, adds):
+    dy = V(dy)
+    w = dy if p["z"] is None else dy * bounds.silu(V(f64(p["z"])))
+    # G_t = a_t (w_t + G_(t+1)): the recurrence from the end over a and a w
+    G, after = recur(g["a"][..., ::-1], (g["a"] * w)[..., ::-1], V(dh), adds)
+    gg = w + after[..., ::-1]
+    out = {"dh0": G[..., -1]}
+    if p["kind"] == "convex":
+        da = gg * (g["before"] - g["ix"])
+        out["dr"] = da * g["m"] * g["s"]
+        dd, factor = da * g["oms"], 1.0
+    else:
+        dd = gg * g["a"] * (g["a"] * g["k"] * g["ix"] - g["ls"] * g["before"])
+        out["dr"] = dd * g["oms"]
+        d = f64(p["decay"])
+        factor = 1.0 / (1.0 + np.exp(-d)) / np.logaddexp(0.0, d)
+    gm = gg * g["m"]
+    out["dx"] = gm
+    if p["i"] is not None:
+        out["dx"] = gm * g["iota"]
+        out["di"] = gm * g["ix"] * g["omi"]
+    if p["z"] is not None:
+        z = V(f64(p["z"]))
+        out["dz"] = dy * g["h"] * (sigmoid(z) * (V(1.0) + z * sigmoid(-z)))
+    batch, _, L = dy.v.shape
+    steps = L / 64 + batch + 24
+    for name, per in (("ddecay", dd), ("dr_bias", out["dr"]), ("di_bias", out.get("di"))):
+        if per is not None:
+            s = per.sum((0, 2), steps)
+            f = factor if name == "ddecay" else 1.0
+            out[name] = V(s.v * f, np.abs(s.e * f) + 30 * U * np.abs(s.v * f))
+    return out
+
+
+def adds(L):
+    """Roundings between a token's term and the row's end besides the ones counted per token: 8 within a
+    lane, 7 over the wave, 4 over its waves, twice for the replay, one for each tile."""
+    return 40 + L / 512
+
+
+def run_fwd(ss, p, **kw):
+    import torch
+    y, h = ss.glr_fwd(**p, **kw)
+    torch.cuda.synchronize()
+    return y, h
+
+
+FORMS = [("convex", "f32", True, True, True), ("convex", "bf16", False, False, False), ("normalised", "f32", True, False, True),
+         ("normalised", "bf16", True, True, True), ("normalised", "f32", False, True, False), ("convex", "bf16", True, False, True)]
+# one token, odd ones, the borders of a lane (8), of 16 lanes (128), a wave (512), two and four waves (1024, 2048), and past them
+LENGTHS = [1, 2, 7, 8, 9, 63, 127, 128, 129, 511, 512, 513, 1023, 1025, 2047, 2048, 2049, 4100, 6145]
+
+
+@pytest.mark.parametrize("kind,io,i,z,h0", FORMS)
+@pytest.mark.parametrize("L", LENGTHS)
+def test_forward(ss, dev, L, kind, io, i, z, h0):
+    p = problem(dev, 100 + L, 2, 5, L, io, kind, i, z, h0)
+    y, h = run_fwd(ss, p)
+    g = forward(p, adds(L))
+    check("y", f64(y), g["y"], HALF[io])
+    check("h_final", f64(h), g["h"][..., -1], 0.0)
+
+
+@pytest.mark.parametrize("kind,io,i,z,h0", FORMS)
+@pytest.mark.parametrize("L", LENGTHS)
+def test_backward(ss, dev, L, kind, io, i, z, h0):
+    import torch
+    p = problem(dev, 200 + L, 2, 5, L, io, kind, i, z, h0)
+    gen = torch.Generator().manual_seed(L)
+    dy = torch.randn(p["x"].shape, generator=gen).to(p["x"].dtype).to(dev)
+    dh = torch.randn((2, 5), generator=gen).to(dev)
+    want = backward(p, forward(p, adds(L)), f64(dy), f64(dh), adds(L))
+    ckpt = torch.full((ss.glr_ckpt_numel(2, 5, L),), float("nan"), device=dev)
+    ss.glr_fwd(**p, ckpt=ckpt)
+    for stored in (None, ckpt):
+        got = ss.glr_bwd(dy=dy, dh_final=dh, ckpt=stored, **p)
+        torch.cuda.synchronize()
+        for name, v in want.items():
+            check(name + (" from stored states" if stored is not None else ""), f64(got[name]), v,
+                  HALF[io] if got[name].dtype == torch.bfloat16 else 0.0)
+        for name in set(got) - set(want):
+            assert got[name] is None, name
+
+
+@pytest.mark.parametrize("kind", ["convex", "normalised"])
+@pytest.mark.parametrize("batch,dim,L", [(3, 700, 5), (1, 2100, 300), (2, 513, 2500)])
+def test_many_rows(ss, dev, kind, batch, dim, L):
+    """Enough rows for the plan that gives each of them to one workgroup."""
+    import torch
+    p = problem(dev, 300 + L, batch, dim, L, "bf16", kind)
+    y, h = run_fwd(ss, p)
+    g = forward(p, adds(L))
+    check("y", f64(y), g["y"], HALF["bf16"])
+    check("h_final", f64(h), g["h"][..., -1], 0.0)
+    dy = torch.randn(p["x"].shape, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(dev)
+    got = ss.glr_bwd(dy=dy, **p)
+    torch.cuda.synchronize()
+    for name, v in backward(p, g, f64(dy), np.zeros((batch, dim)), adds(L)).items():
+        check(name, f64(got[name]), v, HALF["bf16"] if got[name].dtype == torch.bfloat16 else 0.0)
+
+
+def test_gradients_against_differences(ss, dev):
+    """The formulas' gradients, which the kernels are held to above, against central differences of the 64-bit forward."""
+    rng = np.random.default_rng(5)
+    B, D, L, eps = 2, 3, 6, 1e-6
+    for kind in ("convex", "normalised"):
+        import torch
+        base = {k: rng.standard_normal((B, D, L)) for k in ("x", "r", "i", "z")}
+        base["decay"] = rng.uniform(0.1, 0.9, D) if kind == "convex" else rng.uniform(-4, 1, D)
+        base["r_bias"], base["i_bias"], base["h0"] = rng.standard_normal(D), rng.standard_normal(D), rng.standard_normal((B, D))
+        dy, dh = rng.standard_normal((B, D, L)), rng.standard_normal((B, D))
+        as_t = lambda d: {k: torch.from_numpy(v) for k, v in d.items()}  # noqa: E731
+
+        def loss(d):
+            g = forward64(dict(as_t(d), kind=kind))
+            return float((g["y"].v * dy).sum() + (g["h"].v[..., -1] * dh).sum())
+
+        p = dict(as_t(base), kind=kind)
+        want = backward64(p, dy, dh)
+        for name, grad in (("x", "dx"), ("r", "dr"), ("i", "di"), ("z", "dz"), ("decay", "ddecay"), ("r_bias", "dr_bias"),
+                           ("i_bias", "di_bias"), ("h0", "dh0")):
+            num = np.empty_like(base[name])
+            for at in np.ndindex(num.shape):
+                up, dn = {k: v.copy() for k, v in base.items()}, {k: v.copy() for k, v in base.items()}
+                up[name][at] += eps
+                dn[name][at] -= eps
+                num[at] = (loss(up) - loss(dn)) / (2 * eps)
+            # differences of values near 10 with 1e-16 of them over 2e-6, and eps^2 of a third derivative
+            assert np.max(np.abs(num - want[grad].v)) < 1e-7, (kind, name)
+
+
+def _double(t):
+    return None if t is None else t.double().numpy() if hasattr(t, "double") else t
+
+
+def forward64(p):
+    global f64
+    keep, f64 = f64, _double
+    try:
+        return forward(p, 0)
+    finally:
+        f64 = keep
+
+
+def backward64(p, dy, dh):
+    global f64
+    keep, f64 = f64, _double
+    try:
+        return backward(p, forward(p, 0), dy, dh, 0)
+    finally:
+        f64 = keep
+
+
+@pytest.mark.parametrize("kind", ["convex", "normalised"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("i,z", [(True, True), (False, False)])
+@pytest.mark.parametrize("batch,dim", [(1, 1), (3, 37), (5, 1030)])
+def test_step_is_one_token_of_the_sequence(ss, dev, kind, io, i, z, batch, dim):
+    import torch
+    T = 4
+    p = problem(dev, 7, batch, dim, T, io, kind, i, z)
+    g = forward(p, adds(T))
+    state = p["h0"].clone()
+    for t in range(T):
+        tok = {k: None if p[k] is None else p[k][..., t].contiguous() for k in ("x", "r", "i", "z")}
+        vec = {k: p[k] for k in ("decay", "r_bias", "i_bias", "kind")}
+        other = torch.empty_like(state)
+        y2 = ss.glr_step(state, **tok, **vec, state_out=other)
+        kept = state.clone()
+        y = ss.glr_step(state, **tok, **vec)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(state, other) and not torch.equal(kept, state)
+        check("y %d" % t, f64(y), g["y"][..., t], HALF[io])
+    check("state", f64(state), g["h"][..., -1], 0.0)
+
+
+@pytest.mark.parametrize("kind,closed", [("convex", float("inf")), ("normalised", float("-inf"))])
+@pytest.mark.parametrize("L", [40, 3000])
+def test_padding_tokens_leave_the_state_alone(ss, dev, kind, closed, L):
+    """Rows padded behind, before and altogether: the state of the tokens that are there (exactly that of none), zero
+    gradients of the others, finite everywhere."""
+    import torch
+    p = problem(dev, 11, 3, 6, L, "f32", kind, z=False)
+    n = L - 13
+    p["r"][0, :, n:] = closed
+    p["r"][1, :, :n] = closed
+    p["r"][2] = closed
+    y, h = run_fwd(ss, p)
+    own = {k: v[:1, :, :n] if k in ("x", "r", "i") else v[:1] if k == "h0" else v for k, v in p.items()}
+    end = forward(own, adds(L))["h"][..., -1]
+    for name, v in (("y of the last token", y[:1, :, n - 1]), ("y of the last padding", y[:1, :, -1]), ("h_final", h[:1])):
+        check(name, f64(v), end, 0.0)
+    assert torch.equal(y[1, :, 0], p["h0"][1]) and torch.equal(y[1, :, n - 1], p["h0"][1])
+    assert torch.equal(h[2], p["h0"][2]) and torch.equal(y[2], p["h0"][2][:, None].expand(-1, L))
+    dy = torch.ones_like(y)
+    g = ss.glr_bwd(dy=dy, **p)
+    torch.cuda.synchronize()
+    for name in ("dx", "dr", "di"):
+        assert torch.isfinite(g[name]).all(), name
+        assert not g[name][0, :, n:].any() and not g[name][1, :, :n].any() and not g[name][2].any(), name
+    assert torch.equal(g["dh0"][2], torch.full_like(g["dh0"][2], float(L)))
+    for name in ("ddecay", "dr_bias", "di_bias"):
+        assert torch.isfinite(g[name]).all(), name
+
+
+def test_extreme_gates_and_decays(ss, dev):
+    """Gates of +-100, floors of 0 and 1, decays whose softplus underflows or is large: finite, and as the formulas say."""
+    import torch
+    for kind in ("convex", "normalised"):
+        p = problem(dev, 12, 2, 4, 96, "f32", kind)
+        p["r"][:, :, ::3] = 100.0
+        p["r"][:, :, 1::3] = -100.0
+        p["i"][:, :, ::5] = -100.0
+        p["z"][:, :, ::7] = -100.0
+        p["decay"] = torch.tensor([0.0, 1.0, 0.5, 0.999] if kind == "convex" else [-120.0, -60.0, 30.0, -9.0], device=dev)
+        y, h = run_fwd(ss, p)
+        g = forward(p, adds(96))
+        # what falls below 2^-126 is 0 in fp32, and the input's weight is a square root of such a product: at most
+        # sqrt(2 * 240 * 2^-126) = 2.4e-18 off (240 = 8 softplus(30)), times values and adjoints below 400
+        check("y", f64(y), g["y"], 2.0 ** -24, floor=1e-15)
+        got = ss.glr_bwd(dy=torch.ones_like(y), **p)
+        torch.cuda.synchronize()
+        for name, v in got.items():
+            assert torch.isfinite(v).all(), (kind, name)
+        want = backward(p, g, np.ones(y.shape), np.zeros((2, 4)), adds(96))
+        for name in ("dx", "dr", "di", "dz", "dh0"):
+            check(name, f64(got[name]), want[name], 2.0 ** -24, floor=1e-15)
+
+
+def test_a_nan_stays_in_its_row(ss, dev):
+    import torch
+    p = problem(dev, 13, 2, 9, 1000, "bf16", "normalised")
+    clean, _ = run_fwd(ss, p)
+    p["x"][1, 4, 500] = float("nan")
+    y, h = run_fwd(ss, p)
+    assert torch.isnan(y[1, 4, 500:]).all() and torch.isnan(h[1, 4])
+    y[1, 4] = clean[1, 4]
+    assert torch.equal(y, clean)
+
+
+def test_empty_sequence(ss, dev):
+    import torch
+    p = problem(dev, 14, 2, 3, 0, "bf16", "convex")
+    y, h = run_fwd(ss, p)
+    assert y.shape == (2, 3, 0) and torch.equal(h, p["h0"])
+    dh = torch.randn(2, 3, device=dev)
+    g = ss.glr_bwd(dy=p["x"], dh_final=dh, **p)
+    torch.cuda.synchronize()
+    assert torch.equal(g["dh0"], dh)
+    assert not any(g[k].any() for k in ("ddecay", "dr_bias", "di_bias"))
+    p["h0"] = None
+    assert not run_fwd(ss, p)[1].any()
+
+
+def test_outputs_stay_inside_their_rows(ss, dev):
+    """Nothing is written behind the last row or before the first, at lengths that end inside a vector."""
+    import torch
+    for L in (1, 5, 333, 2051):
+        p = problem(dev, 15, 3, 5, L, "bf16", "normalised")
+        n = p["x"].numel()
+        flat = torch.full((n + 64,), 7.0, dtype=torch.bfloat16, device=dev)
+        y = flat[32:32 + n].view(3, 5, L)
+        ss.glr_fwd(**p, y=y)
+        torch.cuda.synchronize()
+        assert (flat[:32] == 7).all() and (flat[32 + n:] == 7).all()
+        assert torch.equal(y, ss.glr_fwd(**p)[0])
+
+
+def test_repeats_and_graph_replays_are_bitwise_equal(ss, dev):
+    import torch
+    for batch, dim, L in ((2, 64, 300), (1, 8, 9000), (1, 600, 2500)):
+        p = problem(dev, 16, batch, dim, L, "bf16", "normalised")
+        dy = torch.randn_like(p["x"])
+        ckpt = torch.empty(ss.glr_ckpt_numel(batch, dim, L), device=dev)
+
+        def both():
+            y, h = ss.glr_fwd(**p, ckpt=ckpt)
+            return dict(ss.glr_bwd(dy=dy, ckpt=ckpt, **p), y=y, h=h)
+
+        want = {k: v.clone() for k, v in both().items()}
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            both()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        graph, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = both()
+        with torch.cuda.graph(second):
+            more = both()
+        for k in range(3):
+            for v in list(got.values()) + list(more.values()):
+                v.zero_()
+            graph.replay()
+            second.replay()
+            torch.cuda.synchronize()
+            for name in want:
+                assert torch.equal(got[name], want[name]) and torch.equal(more[name], want[name]), (name, k)
+            again = both()
+            torch.cuda.synchronize()
+            assert all(torch.equal(again[n], want[n]) for n in want)
+
+
+def test_two_streams_at_once(ss, dev):
+    import torch
+    a, b = problem(dev, 17, 1, 40, 5000, "bf16", "convex"), problem(dev, 18, 1, 40, 5000, "bf16", "convex")
+    ya, yb = run_fwd(ss, a)[0], run_fwd(ss, b)[0]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            y1 = ss.glr_fwd(**a)[0]
+        with torch.cuda.stream(s2):
+            y2 = ss.glr_fwd(**b)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(y1, ya) and torch.equal(y2, yb)
+
+
+def test_theorem_1_gated_recurrence_equals_the_scan(ss, dev):
+    """The scan with one state, A = -1, B = C = 1 and the zero-order hold is h = (1 - s(g)) h + s(g) x (Theorem 1 in the
+    reader's notes): the convex recurrence with r = -g."""
+    import torch
+    batch, D, L = 2, 24, 700
+    gen = torch.Generator().manual_seed(3)
+    x, g = (torch.randn(batch, D, L, generator=gen).to(dev) for _ in range(2))
+    one = torch.ones(batch, 1, L, device=dev)
+    y1, h1 = ss.scan_fwd(x, g, one, one, -torch.ones(D, 1, device=dev), zoh=True)
+    y2, h2 = ss.glr_fwd(x, -g, kind="convex")
+    torch.cuda.synchronize()
+    e = float((y1 - y2).double().norm() / y2.double().norm())
+    log("scan against recurrence: rel-L2 %.2e" % e)
+    assert e < 1e-5 and float((h1[..., 0] - h2).abs().max()) < 1e-4
+
+
+def test_tensor_checks(ss, dev):
+    import torch
+    p = problem(dev, 19, 2, 3, 16, "bf16", "normalised")
+    ok = dict(p)
+    for change, err in ((dict(r=p["r"].float()), TypeError), (dict(r=p["r"][..., :8]), ValueError),
+                        (dict(kind="other"), ValueError), (dict(decay=p["decay"].double()), TypeError),
+                        (dict(h0=p["h0"].t()), ValueError), (dict(i=p["i"].transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
+                        (dict(decay=None), ss.SsError), (dict(i=None), ss.SsError),
+                        (dict(x=p["x"].half()), TypeError), (dict(decay_scale=0.0), ss.SsError), (dict(y=p["x"]), ss.SsError)):
+        with pytest.raises(err):
+            ss.glr_fwd(**{**ok, **change})
+    with pytest.raises(ValueError):
+        ss.glr_fwd(**{k: v.cpu() if hasattr(v, "cpu") else v for k, v in p.items()})
+    with pytest.raises(ValueError):
+        ss.glr_bwd(dy=p["x"], workspace=torch.empty(8, dtype=torch.uint8, device=dev), **p)
