@@ -22,9 +22,23 @@ struct Raw {
   __device__ __forceinline__ float operator[](int j) const { return span_elem<IO>(w, j); }
 };
 
+// A lane's tokens as one or two 16-byte accesses.  Rows of odd length start at any
+// element, and gfx950 takes vector accesses at any address, so the type promises
+// the compiler no more than its elements' alignment.
+template <typename IO>
+struct __attribute__((packed, aligned(sizeof(typename IO::T)))) Words {
+  uint32_t w[Raw<IO>::kWords];
+};
+
 template <typename IO>
 __device__ __forceinline__ Raw<IO> load_raw(const typename IO::T* __restrict__ p, int valid) {
   Raw<IO> o;
+  if (valid >= kV) {
+    const Words<IO> v = *reinterpret_cast<const Words<IO>*>(p);
+#pragma unroll
+    for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = v.w[k];
+    return o;
+  }
 #pragma unroll
   for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = 0u;
 #pragma unroll
@@ -39,6 +53,18 @@ __device__ __forceinline__ Raw<IO> load_raw(const typename IO::T* __restrict__ p
 
 template <typename IO>
 __device__ __forceinline__ void store_raw(typename IO::T* __restrict__ p, int valid, const float (&v)[kV]) {
+  if (valid >= kV) {
+    Words<IO> o;
+    if constexpr (IO::kPerSpan == 4) {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) o.w[j] = __float_as_uint(v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; j += 2) o.w[j >> 1] = pack_bf16x2(v[j], v[j + 1]);
+    }
+    *reinterpret_cast<Words<IO>*>(p) = o;
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < kV; ++j)
     if (j < valid) store_one<IO>(p, j, v[j]);
