@@ -183,7 +183,7 @@ ss_status ss_qk_norm_rot(int64_t batch, int64_t seqlen, int heads_q, int heads_k
 
 size_t ss_qk_norm_rot_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim) {
   if (check_sizes(batch, seqlen, heads_q, heads_k, head_dim) != SS_OK || seqlen == 0) return 0;
-  return round256((size_t)qk_bwd_blocks(batch, seqlen, heads_q, heads_k) * 2 * head_dim * sizeof(float));
+  return round256((size_t)qk_bwd_plan(batch, seqlen, heads_q, heads_k).rows() * head_dim * sizeof(float));
 }
 
 ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim,

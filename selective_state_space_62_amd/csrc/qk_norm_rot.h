@@ -32,13 +32,30 @@ struct QkArgs {
   const int64_t* positions;  // nullable
   int64_t pos0;
   QkSide side[2];        // queries, keys
-  float* part;           // backward: (workgroups, 2, n) partial sums of dw
+  float* part;           // backward: rows of n partial sums of dw, those of each side together
+  int64_t part_row[2];   // backward: a side's first row and rows
+  int64_t part_rows[2];
 };
 
-// Workgroups of the backward, each with a row of partial sums.
-int64_t qk_bwd_blocks(int64_t batch, int64_t seqlen, int heads_q, int heads_k);
+// Head blocks of the backward and the most rows of partial sums that any of its kernels writes.
+struct QkBwdPlan {
+  int32_t heads_per_block;
+  int32_t blocks[2];     // head blocks of each side
+  int64_t token_blocks;  // most workgroups along the tokens
+  int64_t rows() const { return token_blocks * (blocks[0] + blocks[1]); }
+};
+QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k);
 
 hipError_t launch_qk_norm_rot(const QkArgs& a, hipStream_t s);
-hipError_t launch_qk_norm_rot_bwd(const QkArgs& a, hipStream_t s);
+// sets part_row and part_rows itself
+hipError_t launch_qk_norm_rot_bwd(QkArgs a, hipStream_t s);
+
+// The kernels behind them: feature-major outputs, token-major ones whose pairs come in
+// runs (false where they do not), and token-major ones of any shape.
+hipError_t launch_qk_cols(const QkArgs& a, hipStream_t s);
+hipError_t launch_qk_cols_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s);
+bool qk_rows_take(const QkArgs& a);
+hipError_t launch_qk_rows(const QkArgs& a, hipStream_t s);
+hipError_t launch_qk_rows_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s);
 
 }  // namespace ssscan

@@ -1,42 +1,18 @@
-// Norm and position rotation of queries and keys, forward and backward (gfx950).
+// Norm and position rotation of queries and keys: dispatch, the backward's sums, and
+// the kernels for token-major heads of any shape (gfx950).
 //
-// A wave takes one vector (the values of one head at one token) at a time; a lane
-// holds pairs of values that a rotation mixes, so that after the sum of squares
-// no value crosses lanes.
-#include "device_common.h"
-#include "internal.h"
-#include "qk_norm_rot.h"
+// Here a wave takes one vector (the values of one head at one token) at a time; a
+// lane holds pairs of values that a rotation mixes, so that after the sum of squares
+// no value crosses lanes.  It loads element by element, for shapes whose pairs do
+// not come in runs of two or more (an odd head_dim, an odd number of rotated pairs).
+#include "qk_device.h"
 
 namespace ssscan {
 namespace {
 
-using namespace dev;
+using namespace qk;
 
 constexpr int kSlots = 2;   // pairs per lane: head_dim <= 256
-
-// cos and sin of pos * freq (radians).  The angle in turns is formed and reduced
-// to an eighth of a turn in fp64 (an fp32 product is off by radians at positions
-// of millions); the rest is a Taylor polynomial on |x| <= pi/4, whose first dropped
-// terms are below 2e-9 (sin) and 3e-8 (cos).
-__device__ __forceinline__ void angle(double pos, double freq, float& c, float& s) {
-  const double turns = pos * (freq * 0.15915494309189533577);
-  const double f = turns - __builtin_rint(turns);
-  const double q = __builtin_rint(4.0 * f);
-  const float x = (float)(f - 0.25 * q) * 6.28318530717958647693f;
-  const float x2 = x * x;
-  float ps = fmaf(x2, 1.0f / 362880.0f, -1.0f / 5040.0f);
-  ps = fmaf(ps, x2, 1.0f / 120.0f);
-  ps = fmaf(ps, x2, -1.0f / 6.0f);
-  ps = fmaf(ps * x2, x, x);
-  float pc = fmaf(x2, 1.0f / 40320.0f, -1.0f / 720.0f);
-  pc = fmaf(pc, x2, 1.0f / 24.0f);
-  pc = fmaf(pc, x2, -0.5f);
-  pc = fmaf(pc, x2, 1.0f);
-  const int k = (int)q & 3;
-  const float cs = k & 1 ? ps : pc, sn = k & 1 ? pc : ps;
-  c = k == 1 || k == 2 ? -cs : cs;
-  s = k >= 2 ? -sn : sn;
-}
 
 __device__ __forceinline__ float wave_total(float v) {
 #pragma unroll
@@ -69,16 +45,6 @@ __device__ __forceinline__ Vec vec_of(const QkArgs& a, int64_t v, int heads) {
   return o;
 }
 
-// Where value j of the vector stands in the contiguous output layout.
-__device__ __forceinline__ int64_t out_index(const QkArgs& a, const Vec& v, int heads, int j) {
-  if (a.feature_major) return ((v.b * heads + v.h) * a.n + j) * a.seqlen + v.t;
-  return (v.tok * heads + v.h) * a.n + j;
-}
-
-__device__ __forceinline__ double position(const QkArgs& a, const Vec& v) {
-  return (double)(a.positions ? a.positions[v.tok] : a.pos0 + v.t);
-}
-
 template <typename IO>
 __global__ __launch_bounds__(256) void qk_fwd_kernel(QkArgs a) {
   using T = typename IO::T;
@@ -90,7 +56,7 @@ __global__ __launch_bounds__(256) void qk_fwd_kernel(QkArgs a) {
   for (int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); v < vectors; v += waves) {
     const Vec o = vec_of(a, v, sd.heads);
     const T* in = (const T*)sd.in + o.b * sd.stride[0] + o.t * sd.stride[1] + o.h * sd.stride[2];
-    T* out = (T*)sd.out;
+    T* out = (T*)sd.out + (o.tok * sd.heads + o.h) * a.n;
     float x[kSlots][2];
     float sq = 0.0f;
 #pragma unroll
@@ -103,8 +69,8 @@ __global__ __launch_bounds__(256) void qk_fwd_kernel(QkArgs a) {
       sq = fmaf(x[k][0], x[k][0], sq);
       sq = fmaf(x[k][1], x[k][1], sq);
     }
-    const float rho = 1.0f / __builtin_sqrtf(wave_total(sq) / (float)a.n + a.eps);
-    const double pos = position(a, o);
+    const float rho = inv_norm(wave_total(sq), a);
+    const double pos = position(a, o.tok, o.t);
 #pragma unroll
     for (int k = 0; k < kSlots; ++k) {
       const int p = lane + 64 * k;
@@ -120,8 +86,8 @@ __global__ __launch_bounds__(256) void qk_fwd_kernel(QkArgs a) {
         n2 = fmaf(n2, c, n1 * s);
         n1 = r1;
       }
-      store_one<IO>(out, out_index(a, o, sd.heads, j1), n1);
-      if (j2 >= 0) store_one<IO>(out, out_index(a, o, sd.heads, j2), n2);
+      store_one<IO>(out, j1, n1);
+      if (j2 >= 0) store_one<IO>(out, j2, n2);
     }
   }
 }
@@ -142,8 +108,8 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
     const Vec o = vec_of(a, v, sd.heads);
     const T* in = (const T*)sd.in + o.b * sd.stride[0] + o.t * sd.stride[1] + o.h * sd.stride[2];
     T* din = (T*)sd.din + o.b * sd.dstride[0] + o.t * sd.dstride[1] + o.h * sd.dstride[2];
-    const T* dout = (const T*)sd.dout;
-    const double pos = position(a, o);
+    const T* dout = (const T*)sd.dout + (o.tok * sd.heads + o.h) * a.n;
+    const double pos = position(a, o.tok, o.t);
     float x[kSlots][2], d[kSlots][2], pw[kSlots][2];
     float sq = 0.0f, pv = 0.0f;
 #pragma unroll
@@ -154,8 +120,8 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
       const bool one = p < pairs, two = one && j2 >= 0;
       x[k][0] = one ? load_one<IO>(in, j1) : 0.0f;
       x[k][1] = two ? load_one<IO>(in, j2) : 0.0f;
-      float d1 = one ? load_one<IO>(dout, out_index(a, o, sd.heads, j1)) : 0.0f;
-      float d2 = two ? load_one<IO>(dout, out_index(a, o, sd.heads, j2)) : 0.0f;
+      float d1 = one ? load_one<IO>(dout, j1) : 0.0f;
+      float d2 = two ? load_one<IO>(dout, j2) : 0.0f;
       if (p < a.half) {
         float c, s;
         angle(pos, a.inv_freq[p], c, s);
@@ -173,7 +139,7 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
         pv = fmaf(pw[k][h], x[k][h], pv);
       }
     }
-    const float rho = 1.0f / __builtin_sqrtf(wave_total(sq) / (float)a.n + a.eps);
+    const float rho = inv_norm(wave_total(sq), a);
     const float back = rho * rho * (wave_total(pv) / (float)a.n);
 #pragma unroll
     for (int k = 0; k < kSlots; ++k) {
@@ -198,37 +164,48 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
   __syncthreads();
   const int j = threadIdx.x;
   if (j < a.n)
-    a.part[((int64_t)blockIdx.x * 2 + blockIdx.z) * a.n + j] = (s_dw[0][j] + s_dw[1][j]) + (s_dw[2][j] + s_dw[3][j]);
+    a.part[(a.part_row[blockIdx.z] + blockIdx.x) * a.n + j] = (s_dw[0][j] + s_dw[1][j]) + (s_dw[2][j] + s_dw[3][j]);
 }
 
-// dw[j] of a side: the workgroups' partial sums in a fixed order, 16 runs of them
-// summed by 16 lanes and then joined.
-__global__ __launch_bounds__(256) void qk_reduce_kernel(QkArgs a, int64_t blocks) {
-  __shared__ float s_sum[16][16];
+// dw[j] of a side: its rows of partial sums in a fixed order, 64 runs of them summed
+// by 64 threads and then joined.
+__global__ __launch_bounds__(1024) void qk_reduce_kernel(QkArgs a) {
+  __shared__ float s_sum[64][16];
   const QkSide& sd = a.side[blockIdx.z];
   if (!sd.dw) return;
   const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
   const int j = (int)blockIdx.x * 16 + col;
   float v = 0.0f;
-  if (j < a.n)
-    for (int64_t b = run; b < blocks; b += 16) v += a.part[(b * 2 + blockIdx.z) * a.n + j];
+  if (j < a.n) {
+    const float* in = a.part + a.part_row[blockIdx.z] * a.n + j;
+#pragma unroll 4
+    for (int64_t b = run; b < a.part_rows[blockIdx.z]; b += 64) v += in[b * a.n];
+  }
   s_sum[run][col] = v;
   __syncthreads();
   if (run == 0 && j < a.n) {
-    for (int k = 1; k < 16; ++k) v += s_sum[k][col];
+    for (int k = 1; k < 64; ++k) v += s_sum[k][col];
     sd.dw[j] = v;
   }
 }
 
 }  // namespace
 
-int64_t qk_bwd_blocks(int64_t batch, int64_t seqlen, int heads_q, int heads_k) {
-  const int64_t vectors = batch * seqlen * (heads_q > heads_k ? heads_q : heads_k);
-  const int64_t blocks = (vectors + 3) / 4;
-  return blocks < 1024 ? blocks : 1024;
+// 4 heads of a token share its angles; at most about 2048 rows of partial sums.
+QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k) {
+  QkBwdPlan p;
+  const int64_t heads = (int64_t)heads_q + heads_k;
+  p.heads_per_block = heads <= 256 ? 4 : (int)((heads + 63) / 64);
+  p.blocks[0] = (heads_q + p.heads_per_block - 1) / p.heads_per_block;
+  p.blocks[1] = (heads_k + p.heads_per_block - 1) / p.heads_per_block;
+  p.token_blocks = 2048 / (p.blocks[0] + p.blocks[1]);
+  if (p.token_blocks > batch * seqlen) p.token_blocks = batch * seqlen;
+  return p;
 }
 
 hipError_t launch_qk_norm_rot(const QkArgs& a, hipStream_t s) {
+  if (a.feature_major) return launch_qk_cols(a, s);
+  if (qk_rows_take(a)) return launch_qk_rows(a, s);
   const int hmax = a.side[0].heads > a.side[1].heads ? a.side[0].heads : a.side[1].heads;
   int64_t blocks = (a.batch * a.seqlen * hmax + 3) / 4;
   if (blocks > 8192) blocks = 8192;
@@ -238,14 +215,23 @@ hipError_t launch_qk_norm_rot(const QkArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_qk_norm_rot_bwd(const QkArgs& a, hipStream_t s) {
-  const int64_t blocks = qk_bwd_blocks(a.batch, a.seqlen, a.side[0].heads, a.side[1].heads);
-  const dim3 g((unsigned)blocks, 1, 2);
-  if (a.io == kIoBf16) hipLaunchKernelGGL((qk_bwd_kernel<BF16>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((qk_bwd_kernel<F32>), g, dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
+hipError_t launch_qk_norm_rot_bwd(QkArgs a, hipStream_t s) {
+  const QkBwdPlan p = qk_bwd_plan(a.batch, a.seqlen, a.side[0].heads, a.side[1].heads);
+  hipError_t e;
+  if (a.feature_major) {
+    e = launch_qk_cols_bwd(a, p, s);
+  } else if (qk_rows_take(a)) {
+    e = launch_qk_rows_bwd(a, p, s);
+  } else {
+    for (int i = 0; i < 2; ++i) a.part_rows[i] = a.side[i].heads ? p.token_blocks : 0;
+    a.part_row[1] = a.part_rows[0];
+    const dim3 g((unsigned)p.token_blocks, 1, 2);
+    if (a.io == kIoBf16) hipLaunchKernelGGL((qk_bwd_kernel<BF16>), g, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((qk_bwd_kernel<F32>), g, dim3(256), 0, s, a);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess || (!a.side[0].dw && !a.side[1].dw)) return e;
-  hipLaunchKernelGGL(qk_reduce_kernel, dim3((unsigned)((a.n + 15) / 16), 1, 2), dim3(256), 0, s, a, blocks);
+  hipLaunchKernelGGL(qk_reduce_kernel, dim3((unsigned)((a.n + 15) / 16), 1, 2), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
