@@ -72,18 +72,33 @@ ss_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   return SS_OK;
 }
 
-// Backward scratch: the stored states of rows of several tiles, and the three
-// per-row sums behind the per-channel gradients.
+// Forward scratch: the memory through which split rows join.  Backward scratch: the
+// same, the states entering the tiles of rows of several, and the sums over each
+// row's (split: each tile's) tokens behind the per-channel gradients.
 struct GlrBwdLayout {
-  size_t ckpt, sums, total;
+  size_t chain, ckpt, sums, total;
 };
 
+size_t chain_bytes(int64_t rows, int64_t seqlen) {
+  return glr_split(rows, seqlen) ? round256(glr_chain_bytes(rows, seqlen)) : 0;
+}
+
 GlrBwdLayout bwd_layout(int64_t rows, int64_t seqlen) {
+  const size_t tiles = glr_split(rows, seqlen) ? glr_tiles(seqlen) : 1;
   GlrBwdLayout w{};
-  w.ckpt = 0;
-  w.sums = seqlen > kGlrCkptTokens ? round256((size_t)rows * ckpt_count(seqlen) * sizeof(float)) : 0;
-  w.total = w.sums + (seqlen > 0 ? round256((size_t)rows * 3 * sizeof(float)) : 0);
+  w.chain = 0;
+  w.ckpt = chain_bytes(rows, seqlen);
+  w.sums = w.ckpt + (seqlen > kGlrCkptTokens ? round256((size_t)rows * ckpt_count(seqlen) * sizeof(float)) : 0);
+  w.total = w.sums + (seqlen > 0 ? round256((size_t)rows * tiles * 3 * sizeof(float)) : 0);
   return w;
+}
+
+// The chain's slots start as zeros (a kernel, so that a captured call replays).
+hipError_t clear_chain(GlrArgs& a, void* ws, hipStream_t s) {
+  a.chain = nullptr;
+  if (!glr_split(a.rows, a.seqlen)) return hipSuccess;
+  a.chain = ws;
+  return launch_fill_zero(static_cast<float*>(ws), (int64_t)(glr_chain_bytes(a.rows, a.seqlen) / sizeof(float)), s);
 }
 
 GlrArgs base_args(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss_glr_kind kind, float decay_scale,
@@ -117,10 +132,8 @@ size_t ss_glr_ckpt_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
 }
 
 size_t ss_glr_fwd_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
-  (void)batch;
-  (void)dim;
-  (void)seqlen;
-  return 0;
+  if (!valid_sizes(batch, dim, seqlen)) return 0;
+  return chain_bytes(batch * dim, seqlen);
 }
 
 ss_status ss_glr_fwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss_glr_kind kind, float decay_scale,
@@ -158,7 +171,8 @@ ss_status ss_glr_fwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
   a.y = y;
   a.h_final = h_final;
   a.ckpt = ckpt;
-  const hipError_t e = launch_glr_fwd(a, s);
+  hipError_t e = clear_chain(a, workspace, s);
+  if (e == hipSuccess) e = launch_glr_fwd(a, s);
   return e == hipSuccess ? SS_OK : record_hip_error(e, "recurrence launch");
 }
 
@@ -225,7 +239,8 @@ ss_status ss_glr_bwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
     GlrArgs f = a;   // the forward again, storing its states only
     f.z = nullptr;
     f.ckpt = a.ckpt = reinterpret_cast<float*>(ws + wl.ckpt);
-    e = launch_glr_fwd(f, s);
+    e = clear_chain(f, ws, s);
+    if (e == hipSuccess) e = launch_glr_fwd(f, s);
     if (e != hipSuccess) return record_hip_error(e, "state sweep launch");
   }
   a.dy = dy;
@@ -236,10 +251,11 @@ ss_status ss_glr_bwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
   a.dz = dz;
   a.dh0 = dh0;
   a.sums = ddecay || dr_bias || di_bias ? reinterpret_cast<float*>(ws + wl.sums) : nullptr;
-  e = launch_glr_bwd(a, s);
+  e = clear_chain(a, ws, s);
+  if (e == hipSuccess) e = launch_glr_bwd(a, s);
   if (e != hipSuccess) return record_hip_error(e, "recurrence backward launch");
   if (a.sums) {
-    e = launch_glr_reduce(batch, dim, a.sums, ddecay, dr_bias, di_bias, s);
+    e = launch_glr_reduce(batch, dim, a.chain ? glr_tiles(seqlen) : 1, a.sums, ddecay, dr_bias, di_bias, s);
     if (e != hipSuccess) return record_hip_error(e, "per-channel sums launch");
   }
   return SS_OK;

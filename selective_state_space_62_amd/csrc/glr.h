@@ -37,14 +37,29 @@ struct GlrArgs {
   void* di;            // non-null exactly when i is
   void* dz;            // non-null exactly when z is
   float* dh0;          // nullable
-  float* sums;         // nullable: (3, rows) sums over a row's tokens: of decay, r_bias, i_bias
+  float* sums;         // nullable: (3, rows, parts) sums over pieces of a row: of decay, r_bias, i_bias
+  void* chain;         // split rows: glr_chain_bytes of zeros
 };
+
+constexpr int64_t glr_tiles(int64_t seqlen) { return (seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens; }
+// Long rows, when there are fewer of them than CUs, are split over workgroups, a tile
+// of kGlrCkptTokens each.  Kernel times of forward / backward from stored states, one
+// workgroup to a row -> split, fp32: 16 rows of 256K tokens 151 / 256 -> 33 / 38 us, 96 rows
+// of 300001 187 / 407 -> 117 / 176 us, whole calls of 192 rows of 128K 96 / 208 -> 107 / 187 us, of
+// 384 rows 175 / 320 -> 180 / 335 us; 64 rows of 5000 tokens 20 / 36 -> 22 / 35 us.
+constexpr bool glr_split(int64_t rows, int64_t seqlen) { return rows < 256 && seqlen > 4 * kGlrCkptTokens; }
+// Tiles joined from one state, and the memory through which the tiles of split rows join.
+constexpr int kGlrGroup = 32;
+constexpr size_t glr_chain_bytes(int64_t rows, int64_t seqlen) {
+  const int64_t tiles = glr_tiles(seqlen);
+  return (size_t)rows * (tiles + (tiles + kGlrGroup - 1) / kGlrGroup + 1) * sizeof(uint64_t);
+}
 
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t s);
 hipError_t launch_glr_step(const GlrArgs& a, hipStream_t s);
-// out[d] = sum over batch rows of sums[b, d], in order; null outputs are skipped
-hipError_t launch_glr_reduce(int64_t batch, int64_t dim, const float* sums, float* ddecay, float* dr_bias,
-                             float* di_bias, hipStream_t s);
+// out[d] = sum over batch rows and parts of sums[b, d, part] in a fixed order; null outputs are skipped
+hipError_t launch_glr_reduce(int64_t batch, int64_t dim, int64_t parts, const float* sums, float* ddecay,
+                             float* dr_bias, float* di_bias, hipStream_t s);
 
 }  // namespace ssscan

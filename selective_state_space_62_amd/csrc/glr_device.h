@@ -70,6 +70,12 @@ __device__ __forceinline__ void store_raw(typename IO::T* __restrict__ p, int va
     if (j < valid) store_one<IO>(p, j, v[j]);
 }
 
+// How many of a lane's kV tokens from t on are inside the row.
+__device__ __forceinline__ int lane_tokens(int64_t seqlen, int64_t t) {
+  const int64_t left = seqlen - t;
+  return left >= kV ? kV : left > 0 ? (int)left : 0;
+}
+
 // What a row's tokens share: the biases times -log2(e), and of the decay
 //   convex:     c0 = f, c1 = 1 - f
 //   normalised: c0 = -l log2(e), c1 = 2 l, with l = decay_scale softplus(decay)
@@ -195,6 +201,71 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// --- joining the tiles of a split row ---------------------------------------------
+// Each tile is a workgroup.  Workgroups take their row's tiles in order (a counter
+// for each row), publish their tile's map as soon as they have it, and join the maps
+// of the tiles before theirs: those of their group of 32 tiles, onto the state
+// entering the group, which the last tile of the group before has published.  A
+// workgroup waits only for ones that took their tile earlier and so already run, and
+// no map waits for anything: every wait ends.  What is joined does not depend on
+// timing, so neither does the result.  A slot is one 64-bit word, written and read
+// whole past the caches that are not shared, and never 0 once written.  A call that
+// shares its workspace with one that runs at the same time, which is not allowed,
+// could find its slots cleared: a wait gives up after seconds and enters NaN.
+constexpr int kMostPolls = 1 << 22;   // of about a microsecond each
+
+struct Chain {
+  uint64_t* map;      // (rows, tiles)
+  uint64_t* state;    // (rows, groups): the state entering each group
+  uint32_t* counter;  // (rows), 8 bytes apart
+  __device__ __forceinline__ Chain(const GlrArgs& p, int64_t tiles) {
+    const int64_t groups = (tiles + kGlrGroup - 1) / kGlrGroup;
+    map = (uint64_t*)p.chain;
+    state = map + p.rows * tiles;
+    counter = (uint32_t*)(state + p.rows * groups);
+  }
+};
+
+__device__ __forceinline__ uint64_t pack_map(float A, float B) {
+  const uint64_t v = (uint64_t)__float_as_uint(A) << 32 | __float_as_uint(B);
+  return v ? v : uint64_t(1) << 63;   // A = -0 for 0
+}
+
+__device__ __forceinline__ void publish(uint64_t* slot, uint64_t v) {
+  __hip_atomic_store(slot, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// For one wave: publishes tile n's map (A, B) of row `row` and returns the state
+// entering the tile; `first` is the one entering the row.
+__device__ __forceinline__ float chain_enter(const Chain& ch, int64_t row, int64_t n, int64_t tiles, float first, float A,
+                                             float B, int lane) {
+  const int64_t group = n / kGlrGroup, groups = (tiles + kGlrGroup - 1) / kGlrGroup;
+  const int before = (int)(n - group * kGlrGroup);   // tiles of the group before this one
+  uint64_t* map = ch.map + row * tiles + group * kGlrGroup;
+  if (lane == 0) publish(map + before, pack_map(A, B));
+  const bool reads = lane < before || (lane == kGlrGroup && group > 0);
+  uint64_t* slot = lane == kGlrGroup ? ch.state + row * groups + group : map + lane;
+  uint64_t v = 0;
+  for (int polls = 0;; ++polls) {
+    if (reads && v == 0) v = __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__ballot(reads && v == 0) == 0) break;
+    if (polls == kMostPolls) {
+      first = __builtin_nanf("");
+      v = pack_map(first, first);
+      break;
+    }
+    __builtin_amdgcn_s_sleep(1);
+  }
+  const float enter = group > 0 ? lane_value(__uint_as_float((uint32_t)v), kGlrGroup) : first;
+  float a = lane < before ? __uint_as_float((uint32_t)(v >> 32)) : 1.0f;
+  float b = lane < before ? __uint_as_float((uint32_t)v) : 0.0f;
+  scan_up(a, b);
+  const float h = fmaf(lane_value(a, 63), enter, lane_value(b, 63));
+  if (before == kGlrGroup - 1 && n + 1 < tiles && lane == 0)
+    publish(ch.state + row * groups + group + 1, pack_map(0.0f, fmaf(A, h, B)));
+  return h;
+}
+
 // --- launch shape ---------------------------------------------------------------
 // Workgroups of 256 threads hold 4 / W rows of W waves; a grid dimension's
 // threads are 32-bit, so large launches use two dimensions.
@@ -211,8 +282,6 @@ inline bool grid_of(int64_t blocks, dim3* g) {
 }
 
 __device__ __forceinline__ int64_t block_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
-
-inline int waves_for(int64_t seqlen) { return seqlen <= 64 * kV ? 1 : seqlen <= 128 * kV ? 2 : 4; }
 
 // OP<io, kind, has i, has z>::go(a, s) for the call's form.
 template <template <typename, int, bool, bool> class OP, typename IO, int KIND>

@@ -11,13 +11,70 @@ namespace ssscan {
 namespace glr {
 namespace {
 
-// W waves share a row, which is taken in tiles of W * 512 tokens.
-template <typename IO, int KIND, bool HI, bool HZ, int W>
-__global__ __launch_bounds__(256) void glr_fwd_kernel(GlrArgs p) {
+// A lane's operands of one tile.
+template <typename IO, bool HI, bool HZ>
+struct FwdTile {
+  Raw<IO> x, r, i, z;
+  int valid;   // tokens of the lane that are inside the row
+  __device__ __forceinline__ void load(const GlrArgs& p, int64_t base, int64_t t) {
+    using T = typename IO::T;
+    valid = lane_tokens(p.seqlen, t);
+    x = load_raw<IO>((const T*)p.x + base + t, valid);
+    r = load_raw<IO>((const T*)p.r + base + t, valid);
+    if constexpr (HI) i = load_raw<IO>((const T*)p.i + base + t, valid);
+    if constexpr (HZ) z = load_raw<IO>((const T*)p.z + base + t, valid);
+  }
+};
+
+// The decays and inputs of a lane's tokens, and their composition over the wave's lanes up to its own.
+template <int KIND, bool HI, typename TILE>
+__device__ __forceinline__ void lane_maps(const TILE& in, const RowConst& c, float (&a)[kV], float (&u)[kV], float& A,
+                                          float& B) {
+  A = 1.0f;
+  B = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    float m;
+    gate<KIND>(in.r[j], c, a[j], m);
+    u[j] = m * in.x[j];
+    if constexpr (HI) {
+      float e;
+      u[j] *= sigmoid_e(in.i[j], c.ib, e);
+    }
+    if (j >= in.valid) {
+      a[j] = 1.0f;
+      u[j] = 0.0f;
+    }
+    A *= a[j];
+    B = fmaf(a[j], B, u[j]);
+  }
+  scan_up(A, B);
+}
+
+// The lane's outputs, from the state entering it.
+template <typename IO, bool HZ, typename TILE>
+__device__ __forceinline__ void replay(const TILE& in, const float (&a)[kV], const float (&u)[kV], float h,
+                                       typename IO::T* __restrict__ out) {
+  float y[kV];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    h = fmaf(a[j], h, u[j]);
+    y[j] = h;
+    if constexpr (HZ) y[j] *= silu(in.z[j]);
+  }
+  store_raw<IO>(out, in.valid, y);
+}
+
+// W waves share a row, which is taken in tiles of W * 512 tokens; workgroups of four
+// waves hold 4 / W rows.  With MORE tiles than one, the next one's operands are loaded
+// while a tile is worked on (96 fp32 rows of 300001 tokens 245 -> 187 us); without, the
+// registers for it would only cost waves (2.8B-shaped layer, one tile to a row, 160 -> 197 us).
+template <typename IO, int KIND, bool HI, bool HZ, int W, bool MORE>
+__global__ __launch_bounds__(W > 4 ? W * 64 : 256) void glr_fwd_kernel(GlrArgs p) {
   using T = typename IO::T;
-  constexpr int R = 4 / W;
+  constexpr int R = W > 4 ? 1 : 4 / W;
   constexpr int64_t kTile = W * 64 * kV;
-  __shared__ float s_tot[2][4][2];
+  __shared__ float s_tot[2][R * W][2];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave % W;
@@ -28,67 +85,92 @@ __global__ __launch_bounds__(256) void glr_fwd_kernel(GlrArgs p) {
   const RowConst c = row_const<KIND>(p, row % p.dim);
   const int64_t base = row * p.seqlen;
   const int64_t ncheck = (p.seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens;
+  const int64_t mine = (part * 64 + lane) * kV;
   float carry = p.h0 ? p.h0[row] : 0.0f;
-  for (int64_t t0 = 0, n = 0; t0 < p.seqlen; t0 += kTile, ++n) {
-    if (p.ckpt && act && t0 % kGlrCkptTokens == 0 && part == 0 && lane == 0)
-      p.ckpt[row * ncheck + t0 / kGlrCkptTokens] = carry;
-    const int64_t t = t0 + (part * 64 + lane) * kV;
-    const int valid = (int)(p.seqlen - t < kV ? (p.seqlen - t > 0 ? p.seqlen - t : 0) : kV);
-    const Raw<IO> xv = load_raw<IO>((const T*)p.x + base + t, valid);
-    const Raw<IO> rv = load_raw<IO>((const T*)p.r + base + t, valid);
-    Raw<IO> iv, zv;
-    if constexpr (HI) iv = load_raw<IO>((const T*)p.i + base + t, valid);
-    if constexpr (HZ) zv = load_raw<IO>((const T*)p.z + base + t, valid);
-    float a[kV], u[kV];
-    float A = 1.0f, B = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      float m;
-      gate<KIND>(rv[j], c, a[j], m);
-      u[j] = m * xv[j];
-      if constexpr (HI) {
-        float e;
-        u[j] *= sigmoid_e(iv[j], c.ib, e);
-      }
-      if (j >= valid) {
-        a[j] = 1.0f;
-        u[j] = 0.0f;
-      }
-      A *= a[j];
-      B = fmaf(a[j], B, u[j]);
-    }
-    scan_up(A, B);
-    float h = fmaf(shift_up(1.0f, A), carry, shift_up(0.0f, B));
+  FwdTile<IO, HI, HZ> next;
+  next.load(p, base, mine);
+  for (int64_t t0 = 0, n = 0; MORE ? t0 < p.seqlen : n == 0; t0 += kTile, ++n) {
+    const FwdTile<IO, HI, HZ> in = next;
+    const int64_t t = t0 + mine;
+    if constexpr (MORE)
+      if (t0 + kTile < p.seqlen) next.load(p, base, t + kTile);
+    float a[kV], u[kV], A, B;
+    lane_maps<KIND, HI>(in, c, a, u, A, B);
     const float At = lane_value(A, 63), Bt = lane_value(B, 63);
+    float enter = carry;   // the state entering the wave's tokens
     if constexpr (W == 1) {
       carry = fmaf(At, carry, Bt);
     } else {
-      float(&tot)[4][2] = s_tot[n & 1];
+      float(&tot)[R * W][2] = s_tot[n & 1];
       if (lane == 0) {
         tot[wave][0] = At;
         tot[wave][1] = Bt;
       }
       __syncthreads();   // the other parity's totals are read before the next barrier only
-      float enter = carry;
 #pragma unroll
       for (int k = 0; k < W; ++k) {
         if (k == part) enter = carry;
         carry = fmaf(tot[wave - part + k][0], carry, tot[wave - part + k][1]);
       }
-      h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
     }
-    if (p.y) {
-      float y[kV];
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        h = fmaf(a[j], h, u[j]);
-        y[j] = h;
-        if constexpr (HZ) y[j] *= silu(zv[j]);
-      }
-      if (act) store_raw<IO>((T*)p.y + base + t, valid, y);
-    }
+    if (p.ckpt && act && lane == 0 && t % kGlrCkptTokens == 0 && t < p.seqlen)
+      p.ckpt[row * ncheck + t / kGlrCkptTokens] = enter;
+    const float h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
+    if (p.y && act) replay<IO, HZ>(in, a, u, h, (T*)p.y + base + t);
   }
   if (p.h_final && act && part == 0 && lane == 0) p.h_final[row] = carry;
+}
+
+// Split rows: a workgroup takes one tile of 2048 tokens.
+template <typename IO, int KIND, bool HI, bool HZ>
+__global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
+  using T = typename IO::T;
+  __shared__ float s_tot[4][2];
+  __shared__ float s_enter;
+  __shared__ uint32_t s_tile;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tiles = glr_tiles(p.seqlen);
+  const int64_t block = block_index();
+  if (block >= p.rows * tiles) return;
+  const int64_t row = block % p.rows;
+  const Chain chain(p, tiles);
+  if (threadIdx.x == 0)
+    s_tile = __hip_atomic_fetch_add(chain.counter + 2 * row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const RowConst c = row_const<KIND>(p, row % p.dim);
+  const float first = p.h0 ? p.h0[row] : 0.0f;
+  __syncthreads();
+  const int64_t n = __builtin_amdgcn_readfirstlane(s_tile);
+  if (n >= tiles) return;   // not without a call that shares the workspace
+  const int64_t base = row * p.seqlen, t = n * kGlrCkptTokens + (wave * 64 + lane) * kV;
+  FwdTile<IO, HI, HZ> in;
+  in.load(p, base, t);
+  float a[kV], u[kV], A, B;
+  lane_maps<KIND, HI>(in, c, a, u, A, B);
+  if (lane == 63) {
+    s_tot[wave][0] = A;
+    s_tot[wave][1] = B;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    float At = 1.0f, Bt = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      Bt = fmaf(s_tot[k][0], Bt, s_tot[k][1]);
+      At *= s_tot[k][0];
+    }
+    const float h = chain_enter(chain, row, n, tiles, first, At, Bt, lane);
+    if (lane == 0) {
+      s_enter = h;
+      if (p.ckpt) p.ckpt[row * tiles + n] = h;
+      if (p.h_final && n == tiles - 1) p.h_final[row] = fmaf(At, h, Bt);
+    }
+  }
+  __syncthreads();
+  float enter = s_enter;
+  for (int k = 0; k < wave; ++k) enter = fmaf(s_tot[k][0], enter, s_tot[k][1]);
+  const float h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
+  if (p.y) replay<IO, HZ>(in, a, u, h, (T*)p.y + base + t);
 }
 
 template <typename IO, int KIND, bool HI, bool HZ>
@@ -111,15 +193,38 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrArgs p) {
   }
 }
 
+// A row's waves.  Rows of up to 512 or 1024 tokens fit one or two.  bf16 rows of many
+// tiles take eight or sixteen: a tile of four waves is 4 KB of each tensor, which the loads of one
+// tile ahead do not keep the memory busy with (384 rows of 128K tokens 132 -> 116 us, 1536 of 32K 97 ->
+// 98 us; with sixteen 2048 rows of 256K 894 -> 850 us but 1536 of 32K 112 us).  In fp32 four are as
+// fast (384 rows of 128K 175, with eight 180 us).
+int waves_for(const GlrArgs& a) {
+  if (a.seqlen <= 128 * kV) return a.seqlen <= 64 * kV ? 1 : 2;
+  if (a.io != kIoBf16 || a.seqlen < (1 << 14)) return 4;
+  return a.seqlen < (1 << 17) ? 8 : 16;
+}
+
 template <typename IO, int KIND, bool HI, bool HZ>
 struct Fwd {
   static hipError_t go(const GlrArgs& a, hipStream_t s) {
-    const int w = waves_for(a.seqlen);
+    if (a.chain) {
+      dim3 g;
+      if (!grid_of(a.rows * glr_tiles(a.seqlen), &g)) return hipErrorInvalidValue;
+      hipLaunchKernelGGL((glr_fwd_split_kernel<IO, KIND, HI, HZ>), g, dim3(256), 0, s, a);
+      return hipGetLastError();
+    }
+    const int w = waves_for(a);
     dim3 g;
-    if (!grid_of((a.rows + 4 / w - 1) / (4 / w), &g)) return hipErrorInvalidValue;
-    if (w == 1) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 1>), g, dim3(256), 0, s, a);
-    else if (w == 2) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 2>), g, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 4>), g, dim3(256), 0, s, a);
+    if (!grid_of(w > 4 ? a.rows : (a.rows + 4 / w - 1) / (4 / w), &g)) return hipErrorInvalidValue;
+    const bool more = a.seqlen > w * 64 * kV;
+    if (w == 1) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 1, false>), g, dim3(256), 0, s, a);
+    else if (w == 2) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 2, false>), g, dim3(256), 0, s, a);
+    else if (!more) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 4, false>), g, dim3(256), 0, s, a);
+    else if (w == 4) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 4, true>), g, dim3(256), 0, s, a);
+    else if constexpr (IO::kPerSpan == 8) {
+      if (w == 8) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 8, true>), g, dim3(512), 0, s, a);
+      else hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 16, true>), g, dim3(1024), 0, s, a);
+    }
     return hipGetLastError();
   }
 };

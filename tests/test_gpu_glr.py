@@ -139,7 +139,7 @@ def run_fwd(ss, p, **kw):
 FORMS = [("convex", "f32", True, True, True), ("convex", "bf16", False, False, False), ("normalised", "f32", True, False, True),
          ("normalised", "bf16", True, True, True), ("normalised", "f32", False, True, False), ("convex", "bf16", True, False, True)]
 # one token, odd ones, the borders of a lane (8), of 16 lanes (128), a wave (512), two and four waves (1024, 2048), and past them
-LENGTHS = [1, 2, 7, 8, 9, 63, 127, 128, 129, 511, 512, 513, 1023, 1025, 2047, 2048, 2049, 4100, 6145]
+LENGTHS = [1, 2, 7, 8, 9, 63, 127, 128, 129, 511, 512, 513, 1023, 1025, 2047, 2048, 2049, 4100, 6145, 8193, 10247]
 
 
 @pytest.mark.parametrize("kind,io,i,z,h0", FORMS)
@@ -174,7 +174,7 @@ def test_backward(ss, dev, L, kind, io, i, z, h0):
 
 
 @pytest.mark.parametrize("kind", ["convex", "normalised"])
-@pytest.mark.parametrize("batch,dim,L", [(3, 700, 5), (1, 2100, 300), (2, 513, 2500)])
+@pytest.mark.parametrize("batch,dim,L", [(3, 700, 5), (1, 2100, 300), (2, 513, 2500), (1, 256, 16391)])
 def test_many_rows(ss, dev, kind, batch, dim, L):
     """Enough rows for the plan that gives each of them to one workgroup."""
     import torch
@@ -188,6 +188,71 @@ def test_many_rows(ss, dev, kind, batch, dim, L):
     torch.cuda.synchronize()
     for name, v in backward(p, g, f64(dy), np.zeros((batch, dim)), adds(L)).items():
         check(name, f64(got[name]), v, HALF["bf16"] if got[name].dtype == torch.bfloat16 else 0.0)
+
+
+@pytest.mark.parametrize("kind,io", [("convex", "f32"), ("normalised", "bf16")])
+def test_long_rows(ss, dev, kind, io):
+    """Tens of thousands of tokens in few rows: more tiles than are joined from one state."""
+    import torch
+    L = 2048 * 67 + 5
+    p = problem(dev, 21, 1, 3, L, io, kind)
+    y, h = run_fwd(ss, p)
+    g = forward(p, adds(L))
+    check("y", f64(y), g["y"], HALF[io])
+    check("h_final", f64(h), g["h"][..., -1], 0.0)
+    dy = torch.randn(p["x"].shape, generator=torch.Generator().manual_seed(1)).to(p["x"].dtype).to(dev)
+    dh = torch.ones(1, 3, device=dev)
+    want = backward(p, g, f64(dy), f64(dh), adds(L))
+    ckpt = torch.full((ss.glr_ckpt_numel(1, 3, L),), float("nan"), device=dev)
+    ss.glr_fwd(**p, ckpt=ckpt)
+    for stored in (None, ckpt):
+        got = ss.glr_bwd(dy=dy, dh_final=dh, ckpt=stored, **p)
+        torch.cuda.synchronize()
+        for name, v in want.items():
+            check(name, f64(got[name]), v, HALF[io] if got[name].dtype == torch.bfloat16 else 0.0)
+
+
+def test_sixteen_waves_to_a_row(ss, dev):
+    """bf16 rows of 2^17 tokens, enough of them to have a workgroup each: like the split of the same rows, up to the
+    rounding of y (half a step each) and of the states' joining (within 1e-4 of a row's largest, as the bounds above)."""
+    import torch
+    rows, L = 260, (1 << 17) + 3
+    p = problem(dev, 23, 1, rows, L, "bf16", "convex", z=False)
+    ckpt = torch.full((ss.glr_ckpt_numel(1, rows, L),), float("nan"), device=dev)
+    y, h = ss.glr_fwd(**p, ckpt=ckpt)
+    dy = torch.randn_like(p["x"])
+    g = ss.glr_bwd(dy=dy, ckpt=ckpt, **p)
+    few = {k: v[:, :9].contiguous() if torch.is_tensor(v) and v.dim() > 1 else v[:9].contiguous() if torch.is_tensor(v) else v
+           for k, v in p.items()}
+    y9, h9 = ss.glr_fwd(**few)
+    g9 = ss.glr_bwd(dy=dy[:, :9].contiguous(), **few)
+    torch.cuda.synchronize()
+    for name, a, b in [("y", y, y9), ("h", h, h9)] + [(k, g[k], g9[k]) for k in ("dx", "dr", "di", "dh0")]:
+        a, b = a[:, :9].float(), b.float()
+        top = b.abs().amax(-1, keepdim=True) if b.dim() == 3 else b.abs().max()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-4 * top).all(), name
+    for name in ("ddecay", "dr_bias", "di_bias"):
+        assert float((g[name][:9] - g9[name]).abs().max()) <= 1e-4 * float(g9[name].abs().max()) + 1e-2, name
+
+
+def test_zero_decays_join_across_tiles(ss, dev):
+    """Floors of 0 and closed gates make maps of all zeros, which still are maps."""
+    import torch
+    L = 5 * 2048
+    p = problem(dev, 22, 1, 4, L, "f32", "convex", z=False)
+    p["decay"].zero_()
+    p["r"][:, :, 2048:4096] = float("-inf")     # a = 0 throughout a tile
+    p["x"][:, 0, 2048:4096] = 0                 # and nothing enters
+    y, h = run_fwd(ss, p)
+    assert not y[0, 0, 2048:4096].any()
+    own = {k: v[:, :, 4096:] if k in ("x", "r", "i") else v for k, v in p.items()}
+    own["h0"] = y[:, :, 4095].contiguous()
+    g = forward(own, adds(L))
+    check("y", f64(y[:, :, 4096:]), g["y"], HALF["f32"])
+    gr = ss.glr_bwd(dy=torch.ones_like(y), **p)
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(v).all() for v in gr.values() if v is not None)
+    assert not gr["dh0"].isnan().any()
 
 
 def test_gradients_against_differences(ss, dev):

@@ -53,7 +53,9 @@ EVERY = [
     (dict(seqlen=-1), INVALID), (dict(y=None), INVALID), (dict(y=at(8, 1)), INVALID), (dict(h0=at(7, 2)), INVALID),
     (dict(h_final=at(9, 2)), INVALID), (dict(ckpt=at(10, 2)), INVALID), (dict(y=at(0)), INVALID),
     (dict(y=at(1, 2 * 64 * 300 * 2 - 16)), INVALID), (dict(h_final=at(7)), INVALID), (dict(ckpt=at(9)), INVALID),
-    (dict(h_final=at(8)), INVALID),
+    (dict(h_final=at(8)), INVALID), (dict(dim=1, seqlen=9000, ws=None), WORKSPACE),
+    (dict(dim=1, seqlen=9000, ws=at(21, 64)), WORKSPACE), (dict(dim=1, seqlen=9000, ws_bytes=64), WORKSPACE),
+    (dict(dim=1, seqlen=9000, h_final=at(21)), INVALID),
 ])
 def test_glr_fwd_refuses(case, status):
     st, msg = glr("fwd", **case)
@@ -92,7 +94,10 @@ def test_glr_sizes():
     assert b.ss_glr_ckpt_bytes(2, 3, 2048) == 2 * 3 * 4
     assert b.ss_glr_ckpt_bytes(2, 3, 2049) == 2 * 3 * 2 * 4
     assert b.ss_glr_ckpt_bytes(2, 3, 0) == 0 and b.ss_glr_ckpt_bytes(0, 3, 5) == 0 and b.ss_glr_ckpt_bytes(1, 1, -1) == 0
-    assert b.ss_glr_fwd_workspace_bytes(8, 5120, 2048) == 0
+    assert b.ss_glr_fwd_workspace_bytes(8, 5120, 2048) == 0 and b.ss_glr_fwd_workspace_bytes(1, 2048, 1 << 20) == 0
+    # 8 tiles of 2048 tokens and one group of them: a slot each, and a counter
+    assert b.ss_glr_fwd_workspace_bytes(1, 10, 16384) == (10 * (8 + 1 + 1) * 8 + 255) // 256 * 256
+    assert b.ss_glr_fwd_workspace_bytes(1, 10, 8192) == 0 and b.ss_glr_fwd_workspace_bytes(1, 0, 16384) == 0
     assert b.ss_glr_bwd_workspace_bytes(0, 1, 1) == 0 and b.ss_glr_bwd_workspace_bytes(2, 64, 300) >= 2 * 64 * 3 * 4
 
 
