@@ -308,9 +308,12 @@ SS_QK_INTERLEAVED = 1
 SS_QK_FEATURE_MAJOR = 2
 
 
+_Strides = _i64 * 3
+
+
 def _strides(s):
     """(batch, token, head) strides in elements as the C entry points take them; None without that side."""
-    return None if s is None else (_i64 * 3)(*s)
+    return None if s is None else _Strides(*s)
 
 
 def ss_qk_norm_rot(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, q_stride, k, k_stride, wq, wk,

@@ -8,25 +8,24 @@ from __future__ import annotations
 import torch
 
 from . import binding as _b
-from .recurrence import _on, _workspace
-from .torch_ops import _IO, _need, _ptr, _stream
+from ._marshal import io_code, launch, need, ptr, workspace as _workspace
 
 
 def _shape(t, name, dtype, dev):
     """(batch, seqlen, heads, head_dim) and (batch, token, head) strides of an input
     (batch, L, heads, N), (batch, L, N) of one head, or (batch, N) of one token's one head."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.device != dev:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    d = t.dim()
+    s, st = t.shape, t.stride()
+    d = len(s)
     if not 2 <= d <= 4:
         raise ValueError("%s has %d dimensions, expected 2 to 4" % (name, d))
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+    if st[-1] != 1 and s[-1] > 1 and t.numel():
         raise ValueError("%s must have unit stride in its last dimension" % name)
-    s, st = t.shape, t.stride()
     if d == 4:
-        return tuple(s), st[:3]
+        return s, st[:3]
     if d == 3:
         return (s[0], s[1], 1, s[2]), (st[0], st[1], 0)
     return (s[0], 1, 1, s[1]), (st[0], 0, 0)
@@ -46,30 +45,26 @@ def _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major):
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k are both None")
-    if ref.dtype not in _IO:
-        raise TypeError("%s must be float32 or bfloat16" % ("q" if q is not None else "k"))
-    dev = ref.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be on a GPU")
-    sides = [None if t is None else _shape(t, name, ref.dtype, dev) for t, name in ((q, "q"), (k, "k"))]
-    (batch, L, _, n), _ = sides[0] or sides[1]
-    if sides[0] and sides[1]:
-        if q.dim() != k.dim() or sides[1][0][:2] != (batch, L) or sides[1][0][3] != n:
-            raise ValueError("q %s and k %s differ in more than their heads" % (tuple(q.shape), tuple(k.shape)))
+    io, dev = io_code(ref, "q" if q is not None else "k")
+    dtype = ref.dtype
+    sq, stq = (None, None) if q is None else _shape(q, "q", dtype, dev)
+    sk, stk = (None, None) if k is None else _shape(k, "k", dtype, dev)
+    batch, L, _, n = sq or sk
+    if sq and sk and (sk[0] != batch or sk[1] != L or sk[3] != n or q.dim() != k.dim()):
+        raise ValueError("q %s and k %s differ in more than their heads" % (tuple(q.shape), tuple(k.shape)))
     rot = 0
     if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq has %d dimensions, expected 1" % inv_freq.dim())
+        need((("inv_freq", inv_freq),), torch.float64, inv_freq.shape, dev)
         rot = 2 * inv_freq.shape[0]
-        _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
-    _need(wq, "wq", torch.float32, (n,), dev)
-    _need(wk, "wk", torch.float32, (n,), dev)
+    need((("wq", wq), ("wk", wk)), torch.float32, (n,), dev)
     if positions is not None:
-        _need(positions, "positions", torch.int64, (batch,) if ref.dim() == 2 and positions.dim() == 1 else (batch, L), dev)
+        flat = ref.dim() == 2 and positions.dim() == 1
+        need((("positions", positions),), torch.int64, (batch,) if flat else (batch, L), dev)
     flags = (_b.SS_QK_INTERLEAVED if interleaved else 0) | (_b.SS_QK_FEATURE_MAJOR if feature_major else 0)
-    heads = [0 if s is None else s[0][2] for s in sides]
-    strides = [None if s is None else s[1] for s in sides]
-    return dev, ref.dtype, sides, (batch, L, heads[0], heads[1], n, rot, _IO[ref.dtype], flags), strides
+    head = (batch, L, sq[2] if sq else 0, sk[2] if sk else 0, n, rot, io, flags)
+    return dev, dtype, (sq, sk), head, (stq, stk)
 
 
 def qk_norm_rot(q, k, inv_freq=None, wq=None, wk=None, positions=None, pos0=0, *, eps=1e-6, interleaved=False,
@@ -95,14 +90,14 @@ def qk_norm_rot(q, k, inv_freq=None, wq=None, wk=None, positions=None, pos0=0, *
                 raise ValueError("%s is given without its input" % name)
             outs.append(None)
             continue
-        shape = _out_shape(t.dim(), side[0], feature_major)
+        shape = _out_shape(t.dim(), side, feature_major)
         if given is None:
             given = torch.empty(shape, dtype=dtype, device=dev)
         else:
-            _need(given, name, dtype, shape, dev)
+            need(((name, given),), dtype, shape, dev)
         outs.append(given)
-    _on(dev, _b.ss_qk_norm_rot, *head, eps, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(wq), _ptr(wk),
-        _ptr(inv_freq), _ptr(positions), pos0, _ptr(outs[0]), _ptr(outs[1]), _stream(dev))
+    launch(dev, _b.ss_qk_norm_rot, *head, eps, ptr(q), strides[0], ptr(k), strides[1], ptr(wq), ptr(wk), ptr(inv_freq),
+           ptr(positions), pos0, ptr(outs[0]), ptr(outs[1]))
     return outs[0], outs[1]
 
 
@@ -126,7 +121,7 @@ def qk_norm_rot_bwd(q, k, inv_freq, dq_out, dk_out, wq=None, wk=None, positions=
             continue
         if up is None:
             raise ValueError("%s_out is None" % name)
-        _need(up, name + "_out", dtype, _out_shape(t.dim(), side[0], feature_major), dev)
+        need(((name + "_out", up),), dtype, _out_shape(t.dim(), side, feature_major), dev)
         if given is None:
             given = torch.empty(t.shape, dtype=dtype, device=dev)
         elif given.shape != t.shape:
@@ -136,7 +131,7 @@ def qk_norm_rot_bwd(q, k, inv_freq, dq_out, dk_out, wq=None, wk=None, positions=
     batch, L, hq, hk, n = head[:5]
     dw = [torch.empty(n, dtype=torch.float32, device=dev) if need_dw and t is not None else None for t in (q, k)]
     keep, ws, nbytes = _workspace(workspace, _b.ss_qk_norm_rot_bwd_workspace_bytes(batch, L, hq, hk, n), dev)
-    _on(dev, _b.ss_qk_norm_rot_bwd, *head, eps, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(wq), _ptr(wk),
-        _ptr(inv_freq), _ptr(positions), pos0, _ptr(dq_out), _ptr(dk_out), _ptr(grads[0]), gst[0], _ptr(grads[1]), gst[1],
-        _ptr(dw[0]), _ptr(dw[1]), ws, nbytes, _stream(dev))
+    launch(dev, _b.ss_qk_norm_rot_bwd, *head, eps, ptr(q), strides[0], ptr(k), strides[1], ptr(wq), ptr(wk),
+           ptr(inv_freq), ptr(positions), pos0, ptr(dq_out), ptr(dk_out), ptr(grads[0]), gst[0], ptr(grads[1]), gst[1],
+           ptr(dw[0]), ptr(dw[1]), ws, nbytes)
     return dict(dq=grads[0], dk=grads[1], dwq=dw[0], dwk=dw[1])

@@ -9,52 +9,21 @@ from __future__ import annotations
 import torch
 
 from . import binding as _b
-from .torch_ops import _IO, _need, _ptr, _stream
+from ._marshal import io_code, launch, need, ptr, workspace as _workspace
 
 _KINDS = {"convex": _b.SS_GLR_CONVEX, "normalised": _b.SS_GLR_NORMALISED}
+_F32 = torch.float32
 
 
-def _on(dev, fn, *args):
-    """Call fn with dev as the current device (its launches go to dev's stream)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        fn(*args)
-    else:
-        with torch.cuda.device(dev):
-            fn(*args)
-
-
-def _checked(x, r, i, z, decay, r_bias, i_bias, kind, shape):
+def _checked(x, io_tensors, vectors, kind, shape):
     """The checks that all calls share; returns (device, I/O code, kind code)."""
-    if x.dtype not in _IO:
-        raise TypeError("x must be float32 or bfloat16")
-    dev = x.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be on a GPU")
-    if kind not in _KINDS:
+    io, dev = io_code(x, "x")
+    code = _KINDS.get(kind)
+    if code is None:
         raise ValueError("kind must be 'convex' or 'normalised', got %r" % (kind,))
-    dim = (shape[1],)
-    _need(x, "x", x.dtype, shape, dev)
-    _need(r, "r", x.dtype, shape, dev)
-    _need(i, "i", x.dtype, shape, dev)
-    _need(z, "z", x.dtype, shape, dev)
-    _need(decay, "decay", torch.float32, dim, dev)
-    _need(r_bias, "r_bias", torch.float32, dim, dev)
-    _need(i_bias, "i_bias", torch.float32, dim, dev)
-    return dev, _IO[x.dtype], _KINDS[kind]
-
-
-def _workspace(given, nbytes, dev):
-    """(address, bytes) of the caller's workspace, or of a new one; nothing where none is needed."""
-    if given is None and nbytes:
-        given = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if given is None:
-        return None, None, 0
-    have = given.numel() * given.element_size()
-    if have < nbytes:
-        raise ValueError("workspace has %d bytes, %d needed" % (have, nbytes))
-    if given.device != dev or not given.is_contiguous():
-        raise ValueError("workspace must be contiguous and on %s" % (dev,))
-    return given, given.data_ptr(), have
+    need(io_tensors, x.dtype, shape, dev)
+    need(vectors, _F32, shape[1:2], dev)
+    return dev, io, code
 
 
 def glr_ckpt_numel(batch, dim, seqlen) -> int:
@@ -77,21 +46,19 @@ def glr_fwd(x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=None,
     Returns (y, h_final); h_final (batch, D) is None when return_final_state is False.
     """
     batch, dim, L = x.shape
-    dev, io, k = _checked(x, r, i, z, decay, r_bias, i_bias, kind, (batch, dim, L))
-    _need(h0, "h0", torch.float32, (batch, dim), dev)
+    shape = x.shape
+    dev, io, k = _checked(x, (("x", x), ("r", r), ("i", i), ("z", z), ("y", y)),
+                          (("decay", decay), ("r_bias", r_bias), ("i_bias", i_bias)), kind, shape)
+    need((("h0", h0), ("h_final", h_final)), _F32, shape[:2], dev)
     if y is None:
         y = torch.empty_like(x)
-    else:
-        _need(y, "y", x.dtype, (batch, dim, L), dev)
-    if h_final is not None:
-        _need(h_final, "h_final", torch.float32, (batch, dim), dev)
-    elif return_final_state:
-        h_final = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+    if h_final is None and return_final_state:
+        h_final = torch.empty((batch, dim), dtype=_F32, device=dev)
     if ckpt is not None:
-        _need(ckpt, "ckpt", torch.float32, (glr_ckpt_numel(batch, dim, L),), dev)
+        need((("ckpt", ckpt),), _F32, (glr_ckpt_numel(batch, dim, L),), dev)
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_fwd_workspace_bytes(batch, dim, L), dev)
-    _on(dev, _b.ss_glr_fwd, batch, dim, L, io, k, decay_scale, _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(decay),
-        _ptr(r_bias), _ptr(i_bias), _ptr(h0), _ptr(y), _ptr(h_final), _ptr(ckpt), ws, nbytes, _stream(dev))
+    launch(dev, _b.ss_glr_fwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(decay),
+           ptr(r_bias), ptr(i_bias), ptr(h0), y.data_ptr(), ptr(h_final), ptr(ckpt), ws, nbytes)
     return y, h_final
 
 
@@ -107,25 +74,25 @@ def glr_bwd(x, r, dy, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=N
     i): (D,) and dh0 (batch, D) in float32 (None where not requested).
     """
     batch, dim, L = x.shape
-    dev, io, k = _checked(x, r, i, z, decay, r_bias, i_bias, kind, (batch, dim, L))
-    _need(dy, "dy", x.dtype, (batch, dim, L), dev)
-    _need(h0, "h0", torch.float32, (batch, dim), dev)
-    _need(dh_final, "dh_final", torch.float32, (batch, dim), dev)
+    shape = x.shape
+    dev, io, k = _checked(x, (("x", x), ("r", r), ("i", i), ("z", z), ("dy", dy)),
+                          (("decay", decay), ("r_bias", r_bias), ("i_bias", i_bias)), kind, shape)
+    need((("h0", h0), ("dh_final", dh_final)), _F32, shape[:2], dev)
     if ckpt is not None:
-        _need(ckpt, "ckpt", torch.float32, (glr_ckpt_numel(batch, dim, L),), dev)
+        need((("ckpt", ckpt),), _F32, (glr_ckpt_numel(batch, dim, L),), dev)
 
     def vec(wanted, *shape):
-        return torch.empty(shape, dtype=torch.float32, device=dev) if wanted else None
+        return torch.empty(shape, dtype=_F32, device=dev) if wanted else None
 
     out = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), di=None if i is None else torch.empty_like(x),
                dz=None if z is None else torch.empty_like(x), ddecay=vec(need_ddecay and decay is not None, dim),
                dr_bias=vec(need_dr_bias, dim), di_bias=vec(need_di_bias and i is not None, dim),
                dh0=vec(need_dh0, batch, dim))
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_bwd_workspace_bytes(batch, dim, L), dev)
-    _on(dev, _b.ss_glr_bwd, batch, dim, L, io, k, decay_scale, _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(decay),
-        _ptr(r_bias), _ptr(i_bias), _ptr(h0), _ptr(dy), _ptr(dh_final), _ptr(ckpt), _ptr(out["dx"]), _ptr(out["dr"]),
-        _ptr(out["di"]), _ptr(out["dz"]), _ptr(out["ddecay"]), _ptr(out["dr_bias"]), _ptr(out["di_bias"]),
-        _ptr(out["dh0"]), ws, nbytes, _stream(dev))
+    launch(dev, _b.ss_glr_bwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(decay),
+           ptr(r_bias), ptr(i_bias), ptr(h0), dy.data_ptr(), ptr(dh_final), ptr(ckpt), ptr(out["dx"]), ptr(out["dr"]),
+           ptr(out["di"]), ptr(out["dz"]), ptr(out["ddecay"]), ptr(out["dr_bias"]), ptr(out["di_bias"]), ptr(out["dh0"]),
+           ws, nbytes)
     return out
 
 
@@ -134,16 +101,13 @@ def glr_step(state, x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, 
     """One token of ``glr_fwd``: ``state`` (batch, D) float32 is updated in place, or the
     new state is written to state_out.  x, r, i, z: (batch, D).  Returns y (batch, D)."""
     batch, dim = x.shape
-    dev, io, k = _checked(x, r, i, z, decay, r_bias, i_bias, kind, (batch, dim))
-    _need(state, "state", torch.float32, (batch, dim), dev)
-    if state_out is None:
-        state_out = state
-    else:
-        _need(state_out, "state_out", torch.float32, (batch, dim), dev)
+    shape = x.shape
+    dev, io, k = _checked(x, (("x", x), ("r", r), ("i", i), ("z", z), ("y", y)),
+                          (("decay", decay), ("r_bias", r_bias), ("i_bias", i_bias)), kind, shape)
+    need((("state", state), ("state_out", state_out)), _F32, shape, dev)
     if y is None:
         y = torch.empty_like(x)
-    else:
-        _need(y, "y", x.dtype, (batch, dim), dev)
-    _on(dev, _b.ss_glr_step, batch, dim, io, k, decay_scale, _ptr(state), _ptr(state_out), _ptr(x), _ptr(r), _ptr(i),
-        _ptr(z), _ptr(decay), _ptr(r_bias), _ptr(i_bias), _ptr(y), _stream(dev))
+    launch(dev, _b.ss_glr_step, batch, dim, io, k, decay_scale, state.data_ptr(),
+           (state if state_out is None else state_out).data_ptr(), x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(decay),
+           ptr(r_bias), ptr(i_bias), y.data_ptr())
     return y
