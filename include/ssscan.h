@@ -398,7 +398,7 @@ ss_status ss_glr_step(int64_t batch, int64_t dim, ss_dtype io, ss_glr_kind kind,
  * positions (batch, seqlen) int64, NULL for pos0 + t; negative ones rotate
  * backwards.  Angles are formed in fp64 and reduced to a turn before anything is
  * rounded, so a position of 2^40 is as exact as a small one; all else is fp32,
- * each output rounded once.  eps must be positive and finite.
+ * each output rounded once.  eps must be a positive normal number.
  *
  * Inputs: value n of head h of token (b, t) of the queries is at
  * q[b q_stride[0] + t q_stride[1] + h q_stride[2] + n], strides in elements and

@@ -103,8 +103,8 @@ ss_status check_common(int64_t batch, int64_t seqlen, int heads_q, int heads_k, 
     return record_error(SS_ERR_UNSUPPORTED, "head_dim %d is not one of 1, 2, 4, 8, 16 (feature-major)", head_dim);
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
     return record_error(SS_ERR_INVALID_ARG, "rot_dim %d is not even and 0 to head_dim (%d)", rot_dim, head_dim);
-  if (!(eps > 0.0f) || !std::isfinite(eps))
-    return record_error(SS_ERR_INVALID_ARG, "eps %g is not positive and finite", (double)eps);
+  if (!(eps > 0.0f) || !std::isnormal(eps))
+    return record_error(SS_ERR_INVALID_ARG, "eps %g is not a positive normal number", (double)eps);
   if (rot_dim > 0 && !inv_freq) return record_error(SS_ERR_INVALID_ARG, "inv_freq is NULL");
   if (!aligned(inv_freq, 8) || !aligned(positions, 8))
     return record_error(SS_ERR_INVALID_ARG, "%s is not 8-byte aligned", aligned(inv_freq, 8) ? "positions" : "inv_freq");
@@ -127,6 +127,7 @@ QkArgs make_args(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int he
   a.interleaved = (flags & SS_QK_INTERLEAVED) != 0;
   a.feature_major = (flags & SS_QK_FEATURE_MAJOR) != 0;
   a.eps = eps;
+  a.inv_n = 1.0f / (float)head_dim;
   a.inv_freq = inv_freq;
   a.positions = positions;
   a.pos0 = pos0;
@@ -183,7 +184,8 @@ ss_status ss_qk_norm_rot(int64_t batch, int64_t seqlen, int heads_q, int heads_k
 
 size_t ss_qk_norm_rot_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim) {
   if (check_sizes(batch, seqlen, heads_q, heads_k, head_dim) != SS_OK || seqlen == 0) return 0;
-  return round256((size_t)qk_bwd_plan(batch, seqlen, heads_q, heads_k).rows() * head_dim * sizeof(float));
+  const QkBwdPlan p = qk_bwd_plan(batch, seqlen, heads_q, heads_k);
+  return round256((size_t)(p.blocks[0] + p.blocks[1]) * head_dim * sizeof(float));
 }
 
 ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim,

@@ -71,40 +71,76 @@ __device__ __forceinline__ void angles(const QkArgs& a, double pos, float (&c)[N
   }
 }
 
-template <typename IO, int N, int ORDER>
-__global__ __launch_bounds__(64) void qk_cols_fwd_kernel(QkArgs a) {
-  using T = typename IO::T;
-  const int64_t tokens = a.batch * a.seqlen;
-  for (int64_t tok = (int64_t)blockIdx.x * 64 + threadIdx.x; tok < tokens; tok += (int64_t)gridDim.x * 64) {
-    const int64_t b = tok / a.seqlen, t = tok - b * a.seqlen;
-    float c[N / 2 + 1], sn[N / 2 + 1];
-    angles<N>(a, position(a, tok, t), c, sn);
+// The lane's token of a turn of 64; past the last one, the last one again.
+struct Token {
+  int64_t tok, b, t;
+  bool act;
+  __device__ __forceinline__ Token(const QkArgs& a, int64_t turn) {
+    const int64_t tokens = a.batch * a.seqlen;
+    tok = turn * 64 + threadIdx.x;
+    act = tok < tokens;
+    tok = act ? tok : tokens - 1;
+    b = tok / a.seqlen;
+    t = tok - b * a.seqlen;
+  }
+};
+
+// The norm, weight and rotation of one vector.
+template <int N>
+__device__ __forceinline__ void forward(const QkArgs& a, const float (&w)[N], const float (&c)[N / 2 + 1],
+                                        const float (&sn)[N / 2 + 1], float (&x)[N]) {
+  float sq = 0.0f;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
+  for (int k = 0; k < N; ++k) sq = fmaf(x[k], x[k], sq);
+  const float rho = inv_norm(sq, a);
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = x[k] * rho * w[k];
+#pragma unroll
+  for (int p = 0; p < N / 2; ++p) {
+    if (p >= a.half) continue;
+    const float r = x[2 * p] * c[p] - x[2 * p + 1] * sn[p];
+    x[2 * p + 1] = fmaf(x[2 * p + 1], c[p], x[2 * p] * sn[p]);
+    x[2 * p] = r;
+  }
+}
+
+// Both sides' loads are out before the angles are formed: the rows' 64 bytes of B and C
+// are the wait (a million tokens, whole call: one side after the other 52.4, ahead 45.7, with
+// the registers for six waves to a SIMD 43.5 us; a copy of the same 64 bytes of each
+// 320-byte row 32 us).  Turning tiles in LDS for 16-byte stores took 54 us, for 16-byte pieces
+// of a row to neighbouring lanes 77 us, 4-byte stores of two tokens 51 us.
+template <typename IO, int N, int ORDER>
+__global__ __launch_bounds__(64, N == 16 && IO::kPerSpan == 4 ? 5 : 6) void qk_cols_fwd_kernel(QkArgs a, int64_t turns) {
+  using T = typename IO::T;
+  const int heads = a.side[0].heads + a.side[1].heads;
+  for (int64_t turn = blockIdx.x; turn < turns; turn += gridDim.x) {
+    const Token tk(a, turn);
+    // the token's vectors, queries first; one is loaded ahead
+    auto fetch = [&](int item, float (&x)[N]) {
+      const int side = item >= a.side[0].heads, h = item - (side ? a.side[0].heads : 0);
+      const QkSide& sd = a.side[side];
+      load_pairs<IO, N, ORDER>((const T*)sd.in + tk.b * sd.stride[0] + tk.t * sd.stride[1] + h * sd.stride[2], a.half, x);
+    };
+    float x[N], next[N];
+    fetch(0, x);
+    if (heads > 1) fetch(1, next);
+    float c[N / 2 + 1], sn[N / 2 + 1];
+    angles<N>(a, position(a, tk.tok, tk.t), c, sn);
+    for (int item = 0; item < heads; ++item) {
+      const int side = item >= a.side[0].heads, h = item - (side ? a.side[0].heads : 0);
       const QkSide& sd = a.side[side];
       float w[N];
       load_weight<N, ORDER>(sd.w, a.half, w);
-      for (int h = 0; h < sd.heads; ++h) {
-        float x[N];
-        load_pairs<IO, N, ORDER>((const T*)sd.in + b * sd.stride[0] + t * sd.stride[1] + h * sd.stride[2], a.half, x);
-        float sq = 0.0f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) sq = fmaf(x[k], x[k], sq);
-        const float rho = inv_norm(sq, a);
-        T* out = (T*)sd.out + (b * sd.heads + h) * N * a.seqlen + t;
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = x[k] * rho * w[k];
-#pragma unroll
-        for (int p = 0; p < N / 2; ++p) {
-          if (p >= a.half) continue;
-          const float r = x[2 * p] * c[p] - x[2 * p + 1] * sn[p];
-          x[2 * p + 1] = fmaf(x[2 * p + 1], c[p], x[2 * p] * sn[p]);
-          x[2 * p] = r;
-        }
+      forward<N>(a, w, c, sn, x);
+      T* out = (T*)sd.out + (tk.b * sd.heads + h) * N * a.seqlen;
+      if (tk.act) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          store_one<IO>(out, (N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)) * a.seqlen, x[k]);
+          store_one<IO>(out, (N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)) * a.seqlen + tk.t, x[k]);
       }
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = next[k];
+      if (item + 2 < heads) fetch(item + 2, next);
     }
   }
 }
@@ -112,14 +148,13 @@ __global__ __launch_bounds__(64) void qk_cols_fwd_kernel(QkArgs a) {
 // With n = rho w v and o the rotated n: dn is the gradient of o rotated back, and
 // with p = w dn, dv = rho p - rho^3 v mean(p v), dw = sum of dn rho v.
 template <typename IO, int N, int ORDER>
-__global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a) {
+__global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a, int64_t turns) {
   using T = typename IO::T;
-  const int64_t tokens = a.batch * a.seqlen;
   float dw[2][N] = {};
-  for (int64_t tok = (int64_t)blockIdx.x * 64 + threadIdx.x; tok < tokens; tok += (int64_t)gridDim.x * 64) {
-    const int64_t b = tok / a.seqlen, t = tok - b * a.seqlen;
+  for (int64_t turn = blockIdx.x; turn < turns; turn += gridDim.x) {
+    const Token tk(a, turn);
     float c[N / 2 + 1], sn[N / 2 + 1];
-    angles<N>(a, position(a, tok, t), c, sn);
+    angles<N>(a, position(a, tk.tok, tk.t), c, sn);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const QkSide& sd = a.side[side];
@@ -127,11 +162,12 @@ __global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a) {
       load_weight<N, ORDER>(sd.w, a.half, w);
       for (int h = 0; h < sd.heads; ++h) {
         float x[N], d[N];
-        load_pairs<IO, N, ORDER>((const T*)sd.in + b * sd.stride[0] + t * sd.stride[1] + h * sd.stride[2], a.half, x);
-        const T* dout = (const T*)sd.dout + (b * sd.heads + h) * N * a.seqlen + t;
+        load_pairs<IO, N, ORDER>((const T*)sd.in + tk.b * sd.stride[0] + tk.t * sd.stride[1] + h * sd.stride[2], a.half,
+                                 x);
+        const T* dout = (const T*)sd.dout + (tk.b * sd.heads + h) * N * a.seqlen;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          d[k] = load_one<IO>(dout, (N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)) * a.seqlen);
+          d[k] = load_one<IO>(dout, (N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)) * a.seqlen + tk.t);
 #pragma unroll
         for (int p = 0; p < N / 2; ++p) {
           if (p >= a.half) continue;
@@ -145,13 +181,16 @@ __global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a) {
           sq = fmaf(x[k], x[k], sq);
           pv = fmaf(d[k] * w[k], x[k], pv);
         }
-        const float rho = inv_norm(sq, a), back = rho * rho * (pv / (float)N);
+        const float rho = inv_norm(sq, a), back = rho * rho * (pv * (1.0f / N));
+        if (tk.act) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          dw[side][k] = fmaf(d[k], rho * x[k], dw[side][k]);
-          x[k] = rho * (d[k] * w[k] - x[k] * back);
+          for (int k = 0; k < N; ++k) {
+            dw[side][k] = fmaf(d[k], rho * x[k], dw[side][k]);
+            x[k] = rho * (d[k] * w[k] - x[k] * back);
+          }
+          store_pairs<IO, N, ORDER>((T*)sd.din + tk.b * sd.dstride[0] + tk.t * sd.dstride[1] + h * sd.dstride[2], a.half,
+                                    x);
         }
-        store_pairs<IO, N, ORDER>((T*)sd.din + b * sd.dstride[0] + t * sd.dstride[1] + h * sd.dstride[2], a.half, x);
       }
     }
   }
@@ -169,52 +208,64 @@ __global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a) {
   }
 }
 
+struct ColsShape {
+  int64_t turns;   // of 64 tokens
+  unsigned blocks;
+};
+
 template <typename IO, int N, int ORDER>
-void launch(const QkArgs& a, bool back, unsigned blocks, hipStream_t s) {
-  if (back) hipLaunchKernelGGL((qk_cols_bwd_kernel<IO, N, ORDER>), dim3(blocks), dim3(64), 0, s, a);
-  else hipLaunchKernelGGL((qk_cols_fwd_kernel<IO, N, ORDER>), dim3(blocks), dim3(64), 0, s, a);
+void launch(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
+  if (back) hipLaunchKernelGGL((qk_cols_bwd_kernel<IO, N, ORDER>), dim3(sh.blocks), dim3(64), 0, s, a, sh.turns);
+  else hipLaunchKernelGGL((qk_cols_fwd_kernel<IO, N, ORDER>), dim3(sh.blocks), dim3(64), 0, s, a, sh.turns);
 }
 
 template <typename IO, int N>
-void by_order(const QkArgs& a, bool back, unsigned blocks, hipStream_t s) {
+void by_order(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
   if constexpr (N <= 2) {   // one pair at most: every order is the same
-    launch<IO, N, kAdjacent>(a, back, blocks, s);
+    launch<IO, N, kAdjacent>(a, back, sh, s);
   } else {
-    if (a.interleaved || a.half == 0) launch<IO, N, kAdjacent>(a, back, blocks, s);
-    else if (2 * a.half == N) launch<IO, N, kHalves>(a, back, blocks, s);
-    else launch<IO, N, kPartial>(a, back, blocks, s);
+    if (a.interleaved || a.half == 0) launch<IO, N, kAdjacent>(a, back, sh, s);
+    else if (2 * a.half == N) launch<IO, N, kHalves>(a, back, sh, s);
+    else launch<IO, N, kPartial>(a, back, sh, s);
   }
 }
 
 template <typename IO>
-hipError_t by_dim(const QkArgs& a, bool back, unsigned blocks, hipStream_t s) {
+hipError_t by_dim(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
   switch (a.n) {
-    case 1: by_order<IO, 1>(a, back, blocks, s); break;
-    case 2: by_order<IO, 2>(a, back, blocks, s); break;
-    case 4: by_order<IO, 4>(a, back, blocks, s); break;
-    case 8: by_order<IO, 8>(a, back, blocks, s); break;
-    case 16: by_order<IO, 16>(a, back, blocks, s); break;
+    case 1: by_order<IO, 1>(a, back, sh, s); break;
+    case 2: by_order<IO, 2>(a, back, sh, s); break;
+    case 4: by_order<IO, 4>(a, back, sh, s); break;
+    case 8: by_order<IO, 8>(a, back, sh, s); break;
+    case 16: by_order<IO, 16>(a, back, sh, s); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }
 
-hipError_t go(const QkArgs& a, bool back, int64_t most, hipStream_t s) {
-  int64_t blocks = (a.batch * a.seqlen + 63) / 64;
-  if (blocks > most) blocks = most;
-  return a.io == kIoBf16 ? by_dim<BF16>(a, back, (unsigned)blocks, s) : by_dim<F32>(a, back, (unsigned)blocks, s);
+ColsShape shape_of(const QkArgs& a, int64_t most) {
+  ColsShape sh;
+  sh.turns = (a.batch * a.seqlen + 63) / 64;
+  sh.blocks = (unsigned)(sh.turns < most ? sh.turns : most);
+  return sh;
+}
+
+hipError_t go(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
+  return a.io == kIoBf16 ? by_dim<BF16>(a, back, sh, s) : by_dim<F32>(a, back, sh, s);
 }
 
 }  // namespace
 
-hipError_t launch_qk_cols(const QkArgs& a, hipStream_t s) { return go(a, false, 1 << 20, s); }
+hipError_t launch_qk_cols(const QkArgs& a, hipStream_t s) { return go(a, false, shape_of(a, 1 << 20), s); }
 
 hipError_t launch_qk_cols_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s) {
-  int64_t blocks = (a.batch * a.seqlen + 63) / 64;
-  if (blocks > p.token_blocks) blocks = p.token_blocks;
-  for (int i = 0; i < 2; ++i) a.part_rows[i] = a.side[i].heads ? blocks : 0;
+  int64_t most = 1 << 20;
+  for (int i = 0; i < 2; ++i)
+    if (a.side[i].heads && p.blocks[i] < most) most = p.blocks[i];
+  const ColsShape sh = shape_of(a, most);
+  for (int i = 0; i < 2; ++i) a.part_rows[i] = a.side[i].heads ? (int64_t)sh.blocks : 0;
   a.part_row[1] = a.part_rows[0];
-  return go(a, true, blocks, s);
+  return go(a, true, sh, s);
 }
 
 }  // namespace ssscan

@@ -40,9 +40,9 @@ __device__ __forceinline__ float wave_total(float v) {
   return v;
 }
 
-// 1 / sqrt(mean + eps), for the sum of n squares.
+// 1 / sqrt(mean + eps), for the sum of n squares (the hardware's root is within one step).
 __device__ __forceinline__ float inv_norm(float sum, const QkArgs& a) {
-  return 1.0f / __builtin_sqrtf(sum / (float)a.n + a.eps);
+  return __builtin_amdgcn_rsqf(fmaf(sum, a.inv_n, a.eps));
 }
 
 __device__ __forceinline__ double position(const QkArgs& a, int64_t tok, int64_t t) {

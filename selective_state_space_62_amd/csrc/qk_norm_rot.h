@@ -28,6 +28,7 @@ struct QkArgs {
   int32_t interleaved;
   int32_t feature_major;
   float eps;
+  float inv_n;           // 1 / head_dim
   const double* inv_freq;
   const int64_t* positions;  // nullable
   int64_t pos0;
@@ -37,14 +38,19 @@ struct QkArgs {
   int64_t part_rows[2];
 };
 
-// Head blocks of the backward and the most rows of partial sums that any of its kernels writes.
+// The most workgroups, each with a row of partial sums, that a side has in the backward.
 struct QkBwdPlan {
-  int32_t heads_per_block;
-  int32_t blocks[2];     // head blocks of each side
-  int64_t token_blocks;  // most workgroups along the tokens
-  int64_t rows() const { return token_blocks * (blocks[0] + blocks[1]); }
+  int64_t blocks[2];
 };
 QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k);
+
+// Launch of the kernels for pairs in runs: lanes to a vector, and of each side the
+// tokens of a workgroup and the workgroups.
+struct QkRowsShape {
+  int32_t lanes;
+  int32_t tokens[2];
+  int32_t blocks[2];
+};
 
 hipError_t launch_qk_norm_rot(const QkArgs& a, hipStream_t s);
 // sets part_row and part_rows itself

@@ -101,7 +101,8 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
   const QkSide& sd = a.side[blockIdx.z];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t vectors = a.batch * a.seqlen * sd.heads;
-  const int64_t waves = (int64_t)gridDim.x * 4;
+  if ((int64_t)blockIdx.x >= a.part_rows[blockIdx.z]) return;
+  const int64_t waves = a.part_rows[blockIdx.z] * 4;
   const int pairs = a.half + (a.n - 2 * a.half + 1) / 2;
   float dw[kSlots][2] = {};
   for (int64_t v = (int64_t)blockIdx.x * 4 + wave; v < vectors; v += waves) {
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
       }
     }
     const float rho = inv_norm(wave_total(sq), a);
-    const float back = rho * rho * (wave_total(pv) / (float)a.n);
+    const float back = rho * rho * (wave_total(pv) * a.inv_n);
 #pragma unroll
     for (int k = 0; k < kSlots; ++k) {
       const int p = lane + 64 * k;
@@ -191,15 +192,16 @@ __global__ __launch_bounds__(1024) void qk_reduce_kernel(QkArgs a) {
 
 }  // namespace
 
-// 4 heads of a token share its angles; at most about 2048 rows of partial sums.
+// About 1024 rows of partial sums, shared by the sides as their heads are: four workgroups
+// to a CU, which is what the registers of the kernel for runs allow (25 fp32 heads of 80 at 8188
+// tokens, whole call: 1024 rows 51.7, 2048 53.7, 4096 56.1 us).
 QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k) {
   QkBwdPlan p;
-  const int64_t heads = (int64_t)heads_q + heads_k;
-  p.heads_per_block = heads <= 256 ? 4 : (int)((heads + 63) / 64);
-  p.blocks[0] = (heads_q + p.heads_per_block - 1) / p.heads_per_block;
-  p.blocks[1] = (heads_k + p.heads_per_block - 1) / p.heads_per_block;
-  p.token_blocks = 2048 / (p.blocks[0] + p.blocks[1]);
-  if (p.token_blocks > batch * seqlen) p.token_blocks = batch * seqlen;
+  const int64_t heads = (int64_t)heads_q + heads_k, tokens = batch * seqlen;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t h = i ? heads_k : heads_q, n = 1024 * h / heads;
+    p.blocks[i] = h == 0 ? 0 : n < 1 ? 1 : n < tokens ? n : tokens;
+  }
   return p;
 }
 
@@ -223,9 +225,9 @@ hipError_t launch_qk_norm_rot_bwd(QkArgs a, hipStream_t s) {
   } else if (qk_rows_take(a)) {
     e = launch_qk_rows_bwd(a, p, s);
   } else {
-    for (int i = 0; i < 2; ++i) a.part_rows[i] = a.side[i].heads ? p.token_blocks : 0;
+    for (int i = 0; i < 2; ++i) a.part_rows[i] = p.blocks[i];
     a.part_row[1] = a.part_rows[0];
-    const dim3 g((unsigned)p.token_blocks, 1, 2);
+    const dim3 g((unsigned)(p.blocks[0] > p.blocks[1] ? p.blocks[0] : p.blocks[1]), 1, 2);
     if (a.io == kIoBf16) hipLaunchKernelGGL((qk_bwd_kernel<BF16>), g, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((qk_bwd_kernel<F32>), g, dim3(256), 0, s, a);
     e = hipGetLastError();

@@ -1,11 +1,13 @@
 // Norm and position rotation of queries and keys, token-major, for heads whose
 // rotated pairs come in runs of K = 2, 4 or 8 (gfx950).
 //
-// G lanes take the heads of one token in turn.  A lane holds K pairs of a vector: two
-// runs of K values (j .. j + K - 1 and the same at + half, or 2 K consecutive ones
-// where pairs are adjacent or not rotated), each one vector load; the sum of squares
-// crosses the G lanes and nothing else does.  The lane's K angles are formed once for
-// all of the token's heads.
+// A workgroup takes the heads of one side (queries or keys) of some consecutive
+// tokens, so that it reads and writes runs of whole rows.  Its threads first put the
+// tokens' cosines and sines into LDS, each formed once; then G lanes take a vector
+// (one head of one token) at a time.  A lane holds K pairs of it: two runs of K values (j .. j + K - 1
+// and the same at + half, or 2 K consecutive ones where pairs are adjacent or not
+// rotated), each one vector load; the sum of squares crosses the G lanes and nothing
+// else does.
 #include "qk_device.h"
 
 namespace ssscan {
@@ -79,95 +81,115 @@ __device__ __forceinline__ void load_weight(const float* __restrict__ w, int j1,
   }
 }
 
-template <int K>
-__device__ __forceinline__ void angles(const QkArgs& a, double pos, int c, bool rot, float (&cs)[K], float (&sn)[K]) {
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    cs[i] = 1.0f;
-    sn[i] = 0.0f;
-    if (rot) angle(pos, a.inv_freq[c * K + i], cs[i], sn[i]);
-  }
-}
+constexpr int kThreads = 256;
+constexpr int kAngles = 2048;   // pairs of a workgroup's tokens
+constexpr int kTokens = 64;     // most tokens of a workgroup
 
-// Heads of a workgroup: heads [y * per, ...) of the queries followed by the keys.
-template <typename IO, int K, bool INTER>
-__global__ __launch_bounds__(256) void qk_rows_fwd_kernel(QkArgs a, int g, int per) {
-  using T = typename IO::T;
-  constexpr int U = 4;   // vectors in flight
-  const int c = threadIdx.x & (g - 1);
-  const Lane<K, INTER> ln(a, c);
-  const int64_t tokens = a.batch * a.seqlen;
-  const int64_t step = (int64_t)gridDim.x * (256 / g);
-  const int first = blockIdx.y * per;
-  for (int64_t tok = (int64_t)blockIdx.x * (256 / g) + threadIdx.x / g; tok < tokens; tok += step) {
-    const int64_t b = tok / a.seqlen, t = tok - b * a.seqlen;
-    float cs[K], sn[K];
-    angles<K>(a, position(a, tok, t), c, ln.rot, cs, sn);
-    int lo = first, hi = first + per;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const QkSide& sd = a.side[side];
-      const int h0 = lo > 0 ? lo : 0, h1 = hi < sd.heads ? hi : sd.heads;
-      lo -= sd.heads;
-      hi -= sd.heads;
-      if (h0 >= h1) continue;
-      float w[2 * K];
-      load_weight<K>(sd.w, ln.j1, ln.j2, w);
-      const T* in = (const T*)sd.in + b * sd.stride[0] + t * sd.stride[1];
-      T* out = (T*)sd.out + tok * sd.heads * a.n;
-      for (int hb = h0; hb < h1; hb += U) {
-        float x[U][2 * K];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          load_two<IO, K>(in + (hb + u < h1 ? hb + u : h1 - 1) * sd.stride[2], ln.j1, ln.j2, ln.act, x[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (hb + u >= h1) break;
-          float sq = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 2 * K; ++k) sq = fmaf(x[u][k], x[u][k], sq);
-          const float rho = inv_norm(group_sum(sq, g), a);
-#pragma unroll
-          for (int i = 0; i < K; ++i) {
-            const int k1 = at<K, INTER>(i, 0), k2 = at<K, INTER>(i, 1);
-            const float n1 = x[u][k1] * rho * w[k1], n2 = x[u][k2] * rho * w[k2];
-            x[u][k1] = ln.rot ? n1 * cs[i] - n2 * sn[i] : n1;
-            x[u][k2] = ln.rot ? fmaf(n2, cs[i], n1 * sn[i]) : n2;
-          }
-          if (ln.act) store_two<IO, K>(out + (int64_t)(hb + u) * a.n, ln.j1, ln.j2, x[u]);
-        }
-      }
+// The tokens of a workgroup: cosines and sines, and where the tokens' rows start.
+struct Tokens {
+  float cos[kAngles], sin[kAngles];
+  double pos[kTokens];
+  int64_t in[kTokens], din[kTokens];
+
+  __device__ __forceinline__ void fill(const QkArgs& a, const QkSide& sd, int64_t tok0, int count) {
+    if ((int)threadIdx.x < count) {
+      const int64_t tok = tok0 + threadIdx.x, b = tok / a.seqlen, t = tok - b * a.seqlen;
+      pos[threadIdx.x] = position(a, tok, t);
+      in[threadIdx.x] = b * sd.stride[0] + t * sd.stride[1];
+      din[threadIdx.x] = b * sd.dstride[0] + t * sd.dstride[1];
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < count * a.half; k += kThreads) {
+      const int l = k / a.half, p = k - l * a.half;
+      float c, s;
+      angle(pos[l], a.inv_freq[p], c, s);
+      cos[k] = c;
+      sin[k] = s;
     }
   }
+};
+
+template <int K>
+__device__ __forceinline__ void load_angles(const Tokens& tk, int at, float (&cs)[K], float (&sn)[K]) {
+  const Run<F32, K> c = *reinterpret_cast<const Run<F32, K>*>(tk.cos + at);
+  const Run<F32, K> s = *reinterpret_cast<const Run<F32, K>*>(tk.sin + at);
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    cs[i] = c.v[i];
+    sn[i] = s.v[i];
+  }
 }
 
-// The backward (its formulas: qk_cols.hip).  A workgroup has heads of one side, and
-// keeps the sums of dw of its tokens; blockIdx.y counts the queries' head blocks, then the keys'.
+// blockIdx.x counts the queries' token blocks, then the keys'.
 template <typename IO, int K, bool INTER>
-__global__ __launch_bounds__(256) void qk_rows_bwd_kernel(QkArgs a, int g, int per, int q_blocks) {
+__global__ __launch_bounds__(kThreads) void qk_rows_fwd_kernel(QkArgs a, QkRowsShape sh) {
   using T = typename IO::T;
-  __shared__ float s_dw[4][256];
-  const int side = (int)blockIdx.y >= q_blocks;
-  const int block = (int)blockIdx.y - (side ? q_blocks : 0);
+  __shared__ Tokens tk;
+  const int side = (int)blockIdx.x >= sh.blocks[0];
   const QkSide& sd = a.side[side];
+  const int g = sh.lanes, groups = kThreads / g, mine = threadIdx.x / g;
   const int c = threadIdx.x & (g - 1);
   const Lane<K, INTER> ln(a, c);
+  float w[2 * K];
+  load_weight<K>(sd.w, ln.j1, ln.j2, w);
   const int64_t tokens = a.batch * a.seqlen;
-  const int64_t step = (int64_t)gridDim.x * (256 / g);
-  const int h0 = block * per, h1 = h0 + per < sd.heads ? h0 + per : sd.heads;
+  const int64_t step = (int64_t)sh.blocks[side] * sh.tokens[side];
+  for (int64_t tok0 = (int64_t)((int)blockIdx.x - (side ? sh.blocks[0] : 0)) * sh.tokens[side]; tok0 < tokens; tok0 += step) {
+    const int count = (int)(tokens - tok0 < sh.tokens[side] ? tokens - tok0 : sh.tokens[side]);
+    tk.fill(a, sd, tok0, count);
+    __syncthreads();
+    const int items = count * sd.heads;
+    T* out = (T*)sd.out + tok0 * sd.heads * a.n;
+    for (int it = mine; it < items; it += groups) {
+      const int tl = it / sd.heads;
+      float x[2 * K], cs[K], sn[K];
+      load_two<IO, K>((const T*)sd.in + tk.in[tl] + (it - tl * sd.heads) * sd.stride[2], ln.j1, ln.j2, ln.act, x);
+      if (ln.rot) load_angles<K>(tk, tl * a.half + c * K, cs, sn);
+      float sq = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2 * K; ++k) sq = fmaf(x[k], x[k], sq);
+      const float rho = inv_norm(group_sum(sq, g), a);
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const int k1 = at<K, INTER>(i, 0), k2 = at<K, INTER>(i, 1);
+        const float n1 = x[k1] * rho * w[k1], n2 = x[k2] * rho * w[k2];
+        x[k1] = ln.rot ? n1 * cs[i] - n2 * sn[i] : n1;
+        x[k2] = ln.rot ? fmaf(n2, cs[i], n1 * sn[i]) : n2;
+      }
+      if (ln.act) store_two<IO, K>(out + (int64_t)it * a.n, ln.j1, ln.j2, x);
+    }
+    __syncthreads();
+  }
+}
+
+// The backward (its formulas: qk_cols.hip); a workgroup keeps its sums of dw.
+template <typename IO, int K, bool INTER>
+__global__ __launch_bounds__(kThreads) void qk_rows_bwd_kernel(QkArgs a, QkRowsShape sh) {
+  using T = typename IO::T;
+  __shared__ Tokens tk;
+  __shared__ float s_dw[4][256];
+  const int side = (int)blockIdx.x >= sh.blocks[0];
+  const int block = (int)blockIdx.x - (side ? sh.blocks[0] : 0);
+  const QkSide& sd = a.side[side];
+  const int g = sh.lanes, groups = kThreads / g, mine = threadIdx.x / g;
+  const int c = threadIdx.x & (g - 1);
+  const Lane<K, INTER> ln(a, c);
   float w[2 * K], dw[2 * K] = {};
   load_weight<K>(sd.w, ln.j1, ln.j2, w);
-  for (int64_t tok = (int64_t)blockIdx.x * (256 / g) + threadIdx.x / g; tok < tokens; tok += step) {
-    const int64_t b = tok / a.seqlen, t = tok - b * a.seqlen;
-    float cs[K], sn[K];
-    angles<K>(a, position(a, tok, t), c, ln.rot, cs, sn);
-    const T* in = (const T*)sd.in + b * sd.stride[0] + t * sd.stride[1];
-    T* din = (T*)sd.din + b * sd.dstride[0] + t * sd.dstride[1];
-    const T* dout = (const T*)sd.dout + tok * sd.heads * a.n;
-    for (int h = h0; h < h1; ++h) {
-      float x[2 * K], d[2 * K];
-      load_two<IO, K>(in + h * sd.stride[2], ln.j1, ln.j2, ln.act, x);
-      load_two<IO, K>(dout + (int64_t)h * a.n, ln.j1, ln.j2, ln.act, d);
+  const int64_t tokens = a.batch * a.seqlen;
+  const int64_t step = (int64_t)sh.blocks[side] * sh.tokens[side];
+  for (int64_t tok0 = (int64_t)block * sh.tokens[side]; tok0 < tokens; tok0 += step) {
+    const int count = (int)(tokens - tok0 < sh.tokens[side] ? tokens - tok0 : sh.tokens[side]);
+    tk.fill(a, sd, tok0, count);
+    __syncthreads();
+    const int items = count * sd.heads;
+    const T* dout = (const T*)sd.dout + tok0 * sd.heads * a.n;
+    for (int it = mine; it < items; it += groups) {
+      const int tl = it / sd.heads, h = it - tl * sd.heads;
+      float x[2 * K], d[2 * K], cs[K], sn[K];
+      load_two<IO, K>((const T*)sd.in + tk.in[tl] + h * sd.stride[2], ln.j1, ln.j2, ln.act, x);
+      load_two<IO, K>(dout + (int64_t)it * a.n, ln.j1, ln.j2, ln.act, d);
+      if (ln.rot) load_angles<K>(tk, tl * a.half + c * K, cs, sn);
       float sq = 0.0f, pv = 0.0f;
 #pragma unroll
       for (int i = 0; i < K; ++i) {
@@ -182,14 +204,15 @@ __global__ __launch_bounds__(256) void qk_rows_bwd_kernel(QkArgs a, int g, int p
         pv = fmaf(d[k] * w[k], x[k], pv);
       }
       const float rho = inv_norm(group_sum(sq, g), a);
-      const float back = rho * rho * (group_sum(pv, g) / (float)a.n);
+      const float back = rho * rho * (group_sum(pv, g) * a.inv_n);
 #pragma unroll
       for (int k = 0; k < 2 * K; ++k) {
         dw[k] = fmaf(d[k], rho * x[k], dw[k]);
         x[k] = rho * (d[k] * w[k] - x[k] * back);
       }
-      if (ln.act) store_two<IO, K>(din + h * sd.dstride[2], ln.j1, ln.j2, x);
+      if (ln.act) store_two<IO, K>((T*)sd.din + tk.din[tl] + h * sd.dstride[2], ln.j1, ln.j2, x);
     }
+    __syncthreads();
   }
   if (!sd.dw) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -202,8 +225,7 @@ __global__ __launch_bounds__(256) void qk_rows_bwd_kernel(QkArgs a, int g, int p
   __syncthreads();
   const int j = threadIdx.x;
   if (j < a.n)
-    a.part[(a.part_row[side] + (int64_t)block * gridDim.x + blockIdx.x) * a.n + j] =
-        (s_dw[0][j] + s_dw[1][j]) + (s_dw[2][j] + s_dw[3][j]);
+    a.part[(a.part_row[side] + block) * a.n + j] = (s_dw[0][j] + s_dw[1][j]) + (s_dw[2][j] + s_dw[3][j]);
 }
 
 // The longest run that the shape allows: half and the rest's pairs in whole runs, and
@@ -220,24 +242,44 @@ int lanes_of(const QkArgs& a, int k) {
   return g;
 }
 
-struct Shape {
-  dim3 grid;
-  int g, per, q_blocks;
-};
+// A workgroup's tokens: two rounds of vectors for its groups of lanes, fewer where the
+// tokens would not give 1024 workgroups.  (40 bf16 heads of 128 at 16384 tokens: one round 73.7, two
+// 66.6, three 67.6 us; two or four vectors in flight to a group, which cost waves their registers,
+// 71 and 80 us.)
+QkRowsShape shape_of(const QkArgs& a, int k, const int64_t (&most)[2]) {
+  QkRowsShape sh{};
+  const int64_t tokens = a.batch * a.seqlen;
+  sh.lanes = lanes_of(a, k);
+  const int groups = kThreads / sh.lanes;
+  for (int i = 0; i < 2; ++i) {
+    const int heads = a.side[i].heads;
+    sh.tokens[i] = 1;
+    if (!heads) continue;
+    int64_t n = (2 * groups + heads - 1) / heads;
+    if (n > tokens / 1024) n = tokens / 1024;
+    if (a.half && n > kAngles / a.half) n = kAngles / a.half;
+    if (n > kTokens) n = kTokens;
+    sh.tokens[i] = n > 1 ? (int)n : 1;
+    int64_t blocks = (tokens + sh.tokens[i] - 1) / sh.tokens[i];
+    sh.blocks[i] = (int)(blocks < most[i] ? blocks : most[i]);
+  }
+  return sh;
+}
 
 template <typename IO, int K, bool INTER>
-void launch(const QkArgs& a, bool back, const Shape& sh, hipStream_t s) {
-  if (back) hipLaunchKernelGGL((qk_rows_bwd_kernel<IO, K, INTER>), sh.grid, dim3(256), 0, s, a, sh.g, sh.per, sh.q_blocks);
-  else hipLaunchKernelGGL((qk_rows_fwd_kernel<IO, K, INTER>), sh.grid, dim3(256), 0, s, a, sh.g, sh.per);
+void launch(const QkArgs& a, bool back, const QkRowsShape& sh, hipStream_t s) {
+  const dim3 g((unsigned)(sh.blocks[0] + sh.blocks[1]));
+  if (back) hipLaunchKernelGGL((qk_rows_bwd_kernel<IO, K, INTER>), g, dim3(kThreads), 0, s, a, sh);
+  else hipLaunchKernelGGL((qk_rows_fwd_kernel<IO, K, INTER>), g, dim3(kThreads), 0, s, a, sh);
 }
 
 template <typename IO, int K>
-void by_pairs(const QkArgs& a, bool back, const Shape& sh, hipStream_t s) {
+void by_pairs(const QkArgs& a, bool back, const QkRowsShape& sh, hipStream_t s) {
   if (a.interleaved) launch<IO, K, true>(a, back, sh, s);
   else launch<IO, K, false>(a, back, sh, s);
 }
 
-hipError_t go(const QkArgs& a, bool back, int k, const Shape& sh, hipStream_t s) {
+hipError_t go(const QkArgs& a, bool back, int k, const QkRowsShape& sh, hipStream_t s) {
   if (a.io == kIoBf16) {
     if (k == 8) by_pairs<BF16, 8>(a, back, sh, s);
     else if (k == 4) by_pairs<BF16, 4>(a, back, sh, s);
@@ -255,35 +297,13 @@ bool qk_rows_take(const QkArgs& a) { return run_of(a) > 0; }
 
 hipError_t launch_qk_rows(const QkArgs& a, hipStream_t s) {
   const int k = run_of(a);
-  const int64_t tokens = a.batch * a.seqlen;
-  const int heads = a.side[0].heads + a.side[1].heads;
-  Shape sh{};
-  sh.g = lanes_of(a, k);
-  // all heads of a token in one group, unless that leaves fewer than 2^18 lanes busy
-  const int64_t lanes = tokens * sh.g;
-  int64_t split = ((int64_t(1) << 18) + lanes - 1) / lanes;
-  if (split > heads) split = heads;
-  sh.per = (int)((heads + split - 1) / split);
-  int64_t blocks = (tokens + 256 / sh.g - 1) / (256 / sh.g);
-  if (blocks > (1 << 20)) blocks = 1 << 20;
-  sh.grid = dim3((unsigned)blocks, (unsigned)((heads + sh.per - 1) / sh.per));
-  if (sh.grid.y > 65535) {
-    sh.per = (heads + 65534) / 65535;
-    sh.grid.y = (unsigned)((heads + sh.per - 1) / sh.per);
-  }
-  return go(a, false, k, sh, s);
+  return go(a, false, k, shape_of(a, k, {1 << 20, 1 << 20}), s);
 }
 
 hipError_t launch_qk_rows_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s) {
   const int k = run_of(a);
-  Shape sh{};
-  sh.g = lanes_of(a, k);
-  sh.per = p.heads_per_block;
-  sh.q_blocks = p.blocks[0];
-  int64_t blocks = (a.batch * a.seqlen + 256 / sh.g - 1) / (256 / sh.g);
-  if (blocks > p.token_blocks) blocks = p.token_blocks;
-  sh.grid = dim3((unsigned)blocks, (unsigned)(p.blocks[0] + p.blocks[1]));
-  for (int i = 0; i < 2; ++i) a.part_rows[i] = blocks * p.blocks[i];
+  const QkRowsShape sh = shape_of(a, k, p.blocks);
+  for (int i = 0; i < 2; ++i) a.part_rows[i] = sh.blocks[i];
   a.part_row[1] = a.part_rows[0];
   return go(a, true, k, sh, s);
 }

@@ -121,7 +121,7 @@ COMMON = [
     (dict(hq=-1), INVALID), (dict(hq=0, hk=0), INVALID), (dict(hq=(1 << 20) + 1), INVALID), (dict(n=0), UNSUPPORTED),
     (dict(n=257), UNSUPPORTED), (dict(n=24, rot=16, flags=b.SS_QK_FEATURE_MAJOR), UNSUPPORTED), (dict(rot=-2), INVALID),
     (dict(rot=3), INVALID), (dict(rot=18), INVALID), (dict(eps=0.0), INVALID), (dict(eps=float("nan")), INVALID),
-    (dict(eps=float("inf")), INVALID), (dict(freq=None), INVALID), (dict(freq=at(3, 4)), INVALID), (dict(pos=at(4, 4)), INVALID),
+    (dict(eps=float("inf")), INVALID), (dict(eps=1e-40), INVALID), (dict(freq=None), INVALID), (dict(freq=at(3, 4)), INVALID), (dict(pos=at(4, 4)), INVALID),
     (dict(wq=at(1, 2)), INVALID), (dict(wk=at(2, 1)), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
     (dict(hk=0), INVALID), (dict(q=at(0, 1)), INVALID), (dict(qs=(480, -48, 16)), INVALID), (dict(ks=None), INVALID),
     (dict(qs=(1 << 62, 48, 16)), INVALID), (dict(batch=1 << 40, seqlen=1 << 30), INVALID),
