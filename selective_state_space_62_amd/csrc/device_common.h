@@ -238,5 +238,17 @@ __device__ __forceinline__ float silu(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + s);
 }
 
+// Sum over aligned groups of g lanes (a power of 2), in every lane of the group:
+// quad permutes, mirrors of 8 and of 16 lanes, then exchanges across rows.
+__device__ __forceinline__ float group_sum(float v, int g) {
+  if (g > 1) v += __builtin_amdgcn_update_dpp(0.0f, v, 0xB1, 0xf, 0xf, false);
+  if (g > 2) v += __builtin_amdgcn_update_dpp(0.0f, v, 0x4E, 0xf, 0xf, false);
+  if (g > 4) v += __builtin_amdgcn_update_dpp(0.0f, v, 0x141, 0xf, 0xf, false);
+  if (g > 8) v += __builtin_amdgcn_update_dpp(0.0f, v, 0x140, 0xf, 0xf, false);
+  if (g > 16) v += __shfl_xor(v, 16);
+  if (g > 32) v += __shfl_xor(v, 32);
+  return v;
+}
+
 }  // namespace dev
 }  // namespace ssscan

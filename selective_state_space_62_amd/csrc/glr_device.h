@@ -22,58 +22,77 @@ struct Raw {
   __device__ __forceinline__ float operator[](int j) const { return span_elem<IO>(w, j); }
 };
 
-// A lane's tokens as one or two 16-byte accesses.  Rows of odd length start at any
-// element, and gfx950 takes vector accesses at any address, so the type promises
-// the compiler no more than its elements' alignment.
+// A lane's tokens as one or two 16-byte accesses, for a lane whose tokens are all inside the
+// row; the lane at its end goes element by element.  A tile's loads stand together in one
+// branch for the first and one for the second: a branch for each of them made the
+// compiler wait for a load before it sent the next (2.8B-shaped layer, forward 177 -> 153 us; 40960 rows of 1000 bf16
+// tokens, backward, whose second wave holds the row's end, 246 -> 112 us).  Rows of odd length start
+// at any element, and gfx950 takes vector accesses at any address, so the type
+// promises the compiler no more than its elements' alignment.
 template <typename IO>
 struct __attribute__((packed, aligned(sizeof(typename IO::T)))) Words {
   uint32_t w[Raw<IO>::kWords];
 };
 
 template <typename IO>
-__device__ __forceinline__ Raw<IO> load_raw(const typename IO::T* __restrict__ p, int valid) {
+__device__ __forceinline__ Raw<IO> load_whole(const typename IO::T* __restrict__ p) {
   Raw<IO> o;
-  if (valid >= kV) {
-    const Words<IO> v = *reinterpret_cast<const Words<IO>*>(p);
+  const Words<IO> v = *reinterpret_cast<const Words<IO>*>(p);
 #pragma unroll
-    for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = v.w[k];
-    return o;
-  }
+  for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = v.w[k];
+  return o;
+}
+
+// The first `valid` elements; the others read as `pad`, the bits of two bf16 or of one
+// fp32 value.
+template <typename IO>
+__device__ __forceinline__ Raw<IO> load_part(const typename IO::T* __restrict__ p, int valid, uint32_t pad = 0u) {
+  Raw<IO> o;
 #pragma unroll
-  for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = 0u;
+  for (int k = 0; k < Raw<IO>::kWords; ++k) o.w[k] = pad;
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     if (j < valid) {
       if constexpr (IO::kPerSpan == 4) o.w[j] = __float_as_uint(p[j]);
-      else o.w[j >> 1] |= (uint32_t)p[j] << ((j & 1) * 16);
+      else o.w[j >> 1] = j & 1 ? (o.w[j >> 1] & 0xffffu) | (uint32_t)p[j] << 16 : (o.w[j >> 1] & 0xffff0000u) | p[j];
     }
   }
   return o;
 }
 
+// The r of tokens past a row's end: an infinite gate, which keeps the state exactly
+// (a = 1, m = 0), so that nothing after the load asks where the row ends.
+template <typename IO, int KIND>
+constexpr uint32_t gate_pad() {
+  constexpr uint32_t kSign = KIND == 0 ? 0u : 0x80000000u;
+  return IO::kPerSpan == 4 ? 0x7f800000u | kSign : 0x7f807f80u | kSign | kSign >> 16;
+}
+
 template <typename IO>
-__device__ __forceinline__ void store_raw(typename IO::T* __restrict__ p, int valid, const float (&v)[kV]) {
-  if (valid >= kV) {
-    Words<IO> o;
-    if constexpr (IO::kPerSpan == 4) {
+__device__ __forceinline__ void store_whole(typename IO::T* __restrict__ p, const float (&v)[kV]) {
+  Words<IO> o;
+  if constexpr (IO::kPerSpan == 4) {
 #pragma unroll
-      for (int j = 0; j < kV; ++j) o.w[j] = __float_as_uint(v[j]);
-    } else {
+    for (int j = 0; j < kV; ++j) o.w[j] = __float_as_uint(v[j]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < kV; j += 2) o.w[j >> 1] = pack_bf16x2(v[j], v[j + 1]);
-    }
-    *reinterpret_cast<Words<IO>*>(p) = o;
-    return;
+    for (int j = 0; j < kV; j += 2) o.w[j >> 1] = pack_bf16x2(v[j], v[j + 1]);
   }
+  *reinterpret_cast<Words<IO>*>(p) = o;
+}
+
+template <typename IO>
+__device__ __forceinline__ void store_part(typename IO::T* __restrict__ p, int valid, const float (&v)[kV]) {
 #pragma unroll
   for (int j = 0; j < kV; ++j)
     if (j < valid) store_one<IO>(p, j, v[j]);
 }
 
-// How many of a lane's kV tokens from t on are inside the row.
-__device__ __forceinline__ int lane_tokens(int64_t seqlen, int64_t t) {
-  const int64_t left = seqlen - t;
-  return left >= kV ? kV : left > 0 ? (int)left : 0;
+// How many of a lane's kV tokens are inside the row, when its wave's tokens start `left`
+// before the row's end.
+__device__ __forceinline__ int lane_tokens(int64_t left, int lane) {
+  const int n = (int)(left < 64 * kV ? left : 64 * kV) - lane * kV;
+  return n < 0 ? 0 : n > kV ? kV : n;
 }
 
 // What a row's tokens share: the biases times -log2(e), and of the decay
@@ -86,7 +105,8 @@ struct RowConst {
 template <int KIND>
 __device__ __forceinline__ RowConst row_const(const GlrArgs& p, int64_t d) {
   RowConst c;
-  c.rb = p.r_bias ? -kLog2e * p.r_bias[d] : 0.0f;
+  // an infinite bias is held to 2^126: the gate's infinity at the tokens past the end decides
+  c.rb = p.r_bias ? __builtin_amdgcn_fmed3f(-kLog2e * p.r_bias[d], -0x1p126f, 0x1p126f) : 0.0f;
   c.ib = p.i_bias ? -kLog2e * p.i_bias[d] : 0.0f;
   const float v = p.decay ? p.decay[d] : 0.0f;
   if constexpr (KIND == kConvex) {
@@ -106,7 +126,16 @@ __device__ __forceinline__ float sigmoid_e(float v, float nb, float& e) {
   return __builtin_amdgcn_rcpf(1.0f + e);   // 0 where e overflowed
 }
 
-// 1 - s of the sigmoid above without cancellation: e s where s is the larger
+// The same with e held to 2^126, for a gate whose 1 - s is wanted too: e s.  It is
+// never below 2^-126, so a gate of -inf passes that much instead of nothing.
+__device__ __forceinline__ float sigmoid_both(float v, float nb, float& minus) {
+  const float e = __builtin_amdgcn_exp2f(fminf(fmaf(v, -kLog2e, nb), 126.0f));
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  minus = e * s;
+  return s;
+}
+
+// 1 - s of the first sigmoid without cancellation: e s where s is the larger
 // half.  e s is never formed from an overflowed e (the comparison selects 1 - s).
 __device__ __forceinline__ float one_minus(float s, float e) { return e > 1.0f ? 1.0f - s : e * s; }
 
@@ -189,6 +218,67 @@ __device__ __forceinline__ void scan_down(float& A, float& B, int lane) {
 // The compositions of the lanes before (after) a lane's own, from those above.
 __device__ __forceinline__ float shift_up(float old, float v) { return dpp<0x138>(old, v); }     // wave_shr:1
 __device__ __forceinline__ float shift_down(float old, float v) { return dpp<0x130>(old, v); }   // wave_shl:1
+
+// --- the same over groups of S lanes, a power of 2 up to 32: a short row each -------
+// `l` is the lane's place in its group.
+
+template <int K>
+__device__ __forceinline__ void join_up(float& A, float& B, int l) {
+  float a, b;
+  if constexpr (K < 16) {
+    a = dpp<0x110 + K>(1.0f, A);
+    b = dpp<0x110 + K>(0.0f, B);
+  } else {
+    a = dpp<0x142, 0xa>(1.0f, A);
+    b = dpp<0x142, 0xa>(0.0f, B);
+  }
+  if (K < 16 && l < K) {
+    a = 1.0f;
+    b = 0.0f;
+  }
+  B = fmaf(A, b, B);
+  A *= a;
+}
+
+__device__ __forceinline__ void group_scan_up(float& A, float& B, int l, int S) {
+  if (S > 1) join_up<1>(A, B, l);
+  if (S > 2) join_up<2>(A, B, l);
+  if (S > 4) join_up<4>(A, B, l);
+  if (S > 8) join_up<8>(A, B, l);
+  if (S > 16) join_up<16>(A, B, l);
+}
+
+template <int K>
+__device__ __forceinline__ void join_down(float& A, float& B, int l, int S) {
+  float a = dpp<0x100 + K>(1.0f, A), b = dpp<0x100 + K>(0.0f, B);
+  if (l + K >= S) {
+    a = 1.0f;
+    b = 0.0f;
+  }
+  B = fmaf(A, b, B);
+  A *= a;
+}
+
+__device__ __forceinline__ void group_scan_down(float& A, float& B, int l, int S, int lane) {
+  if (S > 1) join_down<1>(A, B, l, S);
+  if (S > 2) join_down<2>(A, B, l, S);
+  if (S > 4) join_down<4>(A, B, l, S);
+  if (S > 8) join_down<8>(A, B, l, S);
+  if (S > 16) {   // the first 16 lanes with the total of the second
+    const float a1 = lane_value(A, 16), b1 = lane_value(B, 16), a3 = lane_value(A, 48), b3 = lane_value(B, 48);
+    const float a = l >= 16 ? 1.0f : lane < 32 ? a1 : a3;
+    const float b = l >= 16 ? 0.0f : lane < 32 ? b1 : b3;
+    B = fmaf(A, b, B);
+    A *= a;
+  }
+}
+
+// Rows of up to 256 tokens take the smallest group that holds them.
+inline int group_of(int64_t seqlen) {
+  int s = 1;
+  while (s * kV < seqlen) s <<= 1;
+  return s;
+}
 
 // Sum over the wave's lanes in a fixed order, in lane 63.
 __device__ __forceinline__ float wave_sum(float v) {

@@ -11,22 +11,30 @@ namespace ssscan {
 namespace glr {
 namespace {
 
-// A lane's operands of one tile.
-template <typename IO, bool HI, bool HZ>
+// A lane's operands of one tile.  `at` is the wave's first element, the same for all
+// lanes, so that every access is a scalar base and one 32-bit lane offset.
+template <typename IO, int KIND, bool HI, bool HZ>
 struct FwdTile {
   Raw<IO> x, r, i, z;
-  int valid;   // tokens of the lane that are inside the row
-  __device__ __forceinline__ void load(const GlrArgs& p, int64_t base, int64_t t) {
+  __device__ __forceinline__ void load(const GlrArgs& p, int64_t at, int64_t left, int lane) {
     using T = typename IO::T;
-    valid = lane_tokens(p.seqlen, t);
-    x = load_raw<IO>((const T*)p.x + base + t, valid);
-    r = load_raw<IO>((const T*)p.r + base + t, valid);
-    if constexpr (HI) i = load_raw<IO>((const T*)p.i + base + t, valid);
-    if constexpr (HZ) z = load_raw<IO>((const T*)p.z + base + t, valid);
+    const unsigned off = (unsigned)lane * kV;
+    const int valid = lane_tokens(left, lane);
+    if (valid >= kV) {
+      x = load_whole<IO>((const T*)p.x + at + off);
+      r = load_whole<IO>((const T*)p.r + at + off);
+      if constexpr (HI) i = load_whole<IO>((const T*)p.i + at + off);
+      if constexpr (HZ) z = load_whole<IO>((const T*)p.z + at + off);
+    } else {
+      x = load_part<IO>((const T*)p.x + at + off, valid);
+      r = load_part<IO>((const T*)p.r + at + off, valid, gate_pad<IO, KIND>());
+      if constexpr (HI) i = load_part<IO>((const T*)p.i + at + off, valid);
+      if constexpr (HZ) z = load_part<IO>((const T*)p.z + at + off, valid);
+    }
   }
 };
 
-// The decays and inputs of a lane's tokens, and their composition over the wave's lanes up to its own.
+// The decays and inputs of a lane's tokens, and their composition.
 template <int KIND, bool HI, typename TILE>
 __device__ __forceinline__ void lane_maps(const TILE& in, const RowConst& c, float (&a)[kV], float (&u)[kV], float& A,
                                           float& B) {
@@ -41,19 +49,14 @@ __device__ __forceinline__ void lane_maps(const TILE& in, const RowConst& c, flo
       float e;
       u[j] *= sigmoid_e(in.i[j], c.ib, e);
     }
-    if (j >= in.valid) {
-      a[j] = 1.0f;
-      u[j] = 0.0f;
-    }
     A *= a[j];
     B = fmaf(a[j], B, u[j]);
   }
-  scan_up(A, B);
 }
 
 // The lane's outputs, from the state entering it.
 template <typename IO, bool HZ, typename TILE>
-__device__ __forceinline__ void replay(const TILE& in, const float (&a)[kV], const float (&u)[kV], float h,
+__device__ __forceinline__ void replay(const TILE& in, const float (&a)[kV], const float (&u)[kV], float h, int64_t left, int lane,
                                        typename IO::T* __restrict__ out) {
   float y[kV];
 #pragma unroll
@@ -62,7 +65,10 @@ __device__ __forceinline__ void replay(const TILE& in, const float (&a)[kV], con
     y[j] = h;
     if constexpr (HZ) y[j] *= silu(in.z[j]);
   }
-  store_raw<IO>(out, in.valid, y);
+  out += (unsigned)lane * kV;
+  const int valid = lane_tokens(left, lane);
+  if (valid >= kV) store_whole<IO>(out, y);
+  else store_part<IO>(out, valid, y);
 }
 
 // W waves share a row, which is taken in tiles of W * 512 tokens; workgroups of four
@@ -85,17 +91,18 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void glr_fwd_kernel(GlrArgs p
   const RowConst c = row_const<KIND>(p, row % p.dim);
   const int64_t base = row * p.seqlen;
   const int64_t ncheck = (p.seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens;
-  const int64_t mine = (part * 64 + lane) * kV;
+  const int64_t mine = part * 64 * kV;
   float carry = p.h0 ? p.h0[row] : 0.0f;
-  FwdTile<IO, HI, HZ> next;
-  next.load(p, base, mine);
+  FwdTile<IO, KIND, HI, HZ> next;
+  next.load(p, base + mine, p.seqlen - mine, lane);
   for (int64_t t0 = 0, n = 0; MORE ? t0 < p.seqlen : n == 0; t0 += kTile, ++n) {
-    const FwdTile<IO, HI, HZ> in = next;
+    const FwdTile<IO, KIND, HI, HZ> in = next;
     const int64_t t = t0 + mine;
     if constexpr (MORE)
-      if (t0 + kTile < p.seqlen) next.load(p, base, t + kTile);
+      if (t0 + kTile < p.seqlen) next.load(p, base + t + kTile, p.seqlen - t - kTile, lane);
     float a[kV], u[kV], A, B;
     lane_maps<KIND, HI>(in, c, a, u, A, B);
+    scan_up(A, B);
     const float At = lane_value(A, 63), Bt = lane_value(B, 63);
     float enter = carry;   // the state entering the wave's tokens
     if constexpr (W == 1) {
@@ -116,9 +123,32 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void glr_fwd_kernel(GlrArgs p
     if (p.ckpt && act && lane == 0 && t % kGlrCkptTokens == 0 && t < p.seqlen)
       p.ckpt[row * ncheck + t / kGlrCkptTokens] = enter;
     const float h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
-    if (p.y && act) replay<IO, HZ>(in, a, u, h, (T*)p.y + base + t);
+    if (p.y && act) replay<IO, HZ>(in, a, u, h, p.seqlen - t, lane, (T*)p.y + (base + t));
   }
   if (p.h_final && act && part == 0 && lane == 0) p.h_final[row] = carry;
+}
+
+// Short rows: S lanes each, so that a wave holds 64 / S.
+template <typename IO, int KIND, bool HI, bool HZ>
+__global__ __launch_bounds__(256) void glr_fwd_short_kernel(GlrArgs p, int S) {
+  using T = typename IO::T;
+  const int l = threadIdx.x & (S - 1);
+  int64_t row = block_index() * (256 / S) + threadIdx.x / S;
+  const bool act = row < p.rows;
+  row = act ? row : p.rows - 1;   // padding lanes repeat the last row and store nothing
+  const RowConst c = row_const<KIND>(p, row % p.dim);
+  const float first = p.h0 ? p.h0[row] : 0.0f;
+  const int64_t base = row * p.seqlen;
+  FwdTile<IO, KIND, HI, HZ> in;
+  in.load(p, base, p.seqlen, l);
+  float a[kV], u[kV], A, B;
+  lane_maps<KIND, HI>(in, c, a, u, A, B);
+  group_scan_up(A, B, l, S);
+  const float Ab = shift_up(1.0f, A), Bb = shift_up(0.0f, B);
+  const float h = l == 0 ? first : fmaf(Ab, first, Bb);
+  if (p.y) replay<IO, HZ>(in, a, u, h, act ? p.seqlen : 0, l, (T*)p.y + base);
+  if (act && p.ckpt && l == 0) p.ckpt[row] = first;
+  if (act && p.h_final && l == S - 1) p.h_final[row] = fmaf(A, first, B);
 }
 
 // Split rows: a workgroup takes one tile of 2048 tokens.
@@ -142,11 +172,12 @@ __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
   __syncthreads();
   const int64_t n = __builtin_amdgcn_readfirstlane(s_tile);
   if (n >= tiles) return;   // not without a call that shares the workspace
-  const int64_t base = row * p.seqlen, t = n * kGlrCkptTokens + (wave * 64 + lane) * kV;
-  FwdTile<IO, HI, HZ> in;
-  in.load(p, base, t);
+  const int64_t base = row * p.seqlen, t = n * kGlrCkptTokens + wave * 64 * kV;
+  FwdTile<IO, KIND, HI, HZ> in;
+  in.load(p, base + t, p.seqlen - t, lane);
   float a[kV], u[kV], A, B;
   lane_maps<KIND, HI>(in, c, a, u, A, B);
+  scan_up(A, B);
   if (lane == 63) {
     s_tot[wave][0] = A;
     s_tot[wave][1] = B;
@@ -170,7 +201,7 @@ __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
   float enter = s_enter;
   for (int k = 0; k < wave; ++k) enter = fmaf(s_tot[k][0], enter, s_tot[k][1]);
   const float h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
-  if (p.y) replay<IO, HZ>(in, a, u, h, (T*)p.y + base + t);
+  if (p.y) replay<IO, HZ>(in, a, u, h, p.seqlen - t, lane, (T*)p.y + (base + t));
 }
 
 template <typename IO, int KIND, bool HI, bool HZ>
@@ -213,8 +244,14 @@ struct Fwd {
       hipLaunchKernelGGL((glr_fwd_split_kernel<IO, KIND, HI, HZ>), g, dim3(256), 0, s, a);
       return hipGetLastError();
     }
-    const int w = waves_for(a);
     dim3 g;
+    if (a.seqlen <= 32 * kV) {
+      const int S = group_of(a.seqlen);
+      if (!grid_of((a.rows + 256 / S - 1) / (256 / S), &g)) return hipErrorInvalidValue;
+      hipLaunchKernelGGL((glr_fwd_short_kernel<IO, KIND, HI, HZ>), g, dim3(256), 0, s, a, S);
+      return hipGetLastError();
+    }
+    const int w = waves_for(a);
     if (!grid_of(w > 4 ? a.rows : (a.rows + 4 / w - 1) / (4 / w), &g)) return hipErrorInvalidValue;
     const bool more = a.seqlen > w * 64 * kV;
     if (w == 1) hipLaunchKernelGGL((glr_fwd_kernel<IO, KIND, HI, HZ, 1, false>), g, dim3(256), 0, s, a);
