@@ -103,21 +103,26 @@ struct RowConst {
 };
 
 template <int KIND>
-__device__ __forceinline__ RowConst row_const(const GlrArgs& p, int64_t d) {
+__device__ __forceinline__ RowConst make_const(float r_bias, float i_bias, float decay, float decay_scale) {
   RowConst c;
   // an infinite bias is held to 2^126: the gate's infinity at the tokens past the end decides
-  c.rb = p.r_bias ? __builtin_amdgcn_fmed3f(-kLog2e * p.r_bias[d], -0x1p126f, 0x1p126f) : 0.0f;
-  c.ib = p.i_bias ? -kLog2e * p.i_bias[d] : 0.0f;
-  const float v = p.decay ? p.decay[d] : 0.0f;
+  c.rb = __builtin_amdgcn_fmed3f(-kLog2e * r_bias, -0x1p126f, 0x1p126f);
+  c.ib = -kLog2e * i_bias;
   if constexpr (KIND == kConvex) {
-    c.c0 = v;
-    c.c1 = 1.0f - v;
+    c.c0 = decay;
+    c.c1 = 1.0f - decay;
   } else {
-    const float l = p.decay_scale * softplus_dt(v, 0.0f);
+    const float l = decay_scale * softplus_dt(decay, 0.0f);
     c.c0 = -kLog2e * l;
     c.c1 = 2.0f * l;
   }
   return c;
+}
+
+template <int KIND>
+__device__ __forceinline__ RowConst row_const(const GlrArgs& p, int64_t d) {
+  return make_const<KIND>(p.r_bias ? p.r_bias[d] : 0.0f, p.i_bias ? p.i_bias[d] : 0.0f, p.decay ? p.decay[d] : 0.0f,
+                          p.decay_scale);
 }
 
 // sigmoid(v + bias), given nb = -log2(e) bias; e receives exp(-(v + bias)).
