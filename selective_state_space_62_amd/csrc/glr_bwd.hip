@@ -171,7 +171,7 @@ template <int KIND, int WAVES>
 __device__ __forceinline__ void store_sums(const GlrArgs& p, int64_t d, int64_t at, int64_t third, int wave, int part,
                                            int parts, int lane, bool act, float sum_d, float sum_r, float sum_i) {
   __shared__ float s_sum[WAVES][3];
-  const float sums[3] = {wave_sum(sum_d) * decay_factor<KIND>(p, d), wave_sum(sum_r), wave_sum(sum_i)};
+  const float sums[3] = {wave_sum(sum_d), wave_sum(sum_r), wave_sum(sum_i)};
   if (lane == 63) {
 #pragma unroll
     for (int k = 0; k < 3; ++k) s_sum[wave][k] = sums[k];
@@ -180,7 +180,7 @@ __device__ __forceinline__ void store_sums(const GlrArgs& p, int64_t d, int64_t 
   if (part == 0 && act && lane < 3) {
     float v = s_sum[wave][lane];
     for (int k = 1; k < parts; ++k) v += s_sum[wave + k][lane];
-    p.sums[lane * third + at] = v;
+    p.sums[lane * third + at] = lane == 0 ? v * decay_factor<KIND>(p, d) : v;
   }
 }
 

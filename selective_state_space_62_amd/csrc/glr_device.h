@@ -105,8 +105,10 @@ struct RowConst {
 template <int KIND>
 __device__ __forceinline__ RowConst make_const(float r_bias, float i_bias, float decay, float decay_scale) {
   RowConst c;
-  // an infinite bias is held to 2^126: the gate's infinity at the tokens past the end decides
-  c.rb = __builtin_amdgcn_fmed3f(-kLog2e * r_bias, -0x1p126f, 0x1p126f);
+  // an infinite bias is held to 2^126: the gate's infinity at the tokens past the end
+  // decides (a NaN stays one)
+  const float rb = -kLog2e * r_bias;
+  c.rb = fabsf(rb) > 0x1p126f ? copysignf(0x1p126f, rb) : rb;
   c.ib = -kLog2e * i_bias;
   if constexpr (KIND == kConvex) {
     c.c0 = decay;

@@ -394,6 +394,24 @@ def test_a_nan_stays_in_its_row(ss, dev):
     assert torch.equal(y, clean)
 
 
+@pytest.mark.parametrize("kind", ["convex", "normalised"])
+@pytest.mark.parametrize("L", [5, 300, 700, 2100, 9000])
+def test_infinite_and_nan_biases_end_with_the_row(ss, dev, kind, L):
+    """A channel whose gate's bias is infinite is open or closed at its tokens, however the row's end falls into a vector:
+    the final state is the last output.  A NaN spoils its channel alone."""
+    import torch
+    p = problem(dev, 24, 2, 4, L, "f32", kind, z=False)
+    clean, _ = run_fwd(ss, p)
+    p["r_bias"] = torch.tensor([float("inf"), float("-inf"), float("nan"), float(p["r_bias"][3])], device=dev)
+    y, h = run_fwd(ss, p)
+    assert torch.isfinite(y[:, :2]).all() and torch.isnan(y[:, 2]).all() and torch.isnan(h[:, 2]).all()
+    assert torch.equal(y[:, 3], clean[:, 3])
+    kept = 0 if kind == "convex" else 1          # the gate that keeps the state
+    assert torch.equal(h[:, kept], p["h0"][:, kept]) and torch.equal(y[:, kept, -1], p["h0"][:, kept])
+    other = 1 - kept                              # a and u are constants of the channel: one step from the last output but one
+    assert float((h[:, other] - y[:, other, -1]).abs().max()) <= 1e-5 * float(y[:, other].abs().max())
+
+
 def test_empty_sequence(ss, dev):
     import torch
     p = problem(dev, 14, 2, 3, 0, "bf16", "convex")
