@@ -22,13 +22,14 @@ struct Raw {
   __device__ __forceinline__ float operator[](int j) const { return span_elem<IO>(w, j); }
 };
 
-// A lane's tokens as one or two 16-byte accesses, for a lane whose tokens are all inside the
-// row; the lane at its end goes element by element.  A tile's loads stand together in one
-// branch for the first and one for the second: a branch for each of them made the
-// compiler wait for a load before it sent the next (2.8B-shaped layer, forward 177 -> 153 us; 40960 rows of 1000 bf16
-// tokens, backward, whose second wave holds the row's end, 246 -> 112 us).  Rows of odd length start
-// at any element, and gfx950 takes vector accesses at any address, so the type
-// promises the compiler no more than its elements' alignment.
+// A lane's tokens as one or two 16-byte accesses, for a lane whose tokens are all inside
+// the row; the lane at its end goes element by element.  A tile's loads stand together
+// in one branch for the first and one for the second: with a branch for each of them
+// the compiler waited for a load before it sent the next (2.8B-shaped layer, forward 177
+// -> 153 us), and with one for the wave as a whole a wave that holds a row's end went
+// element by element (40960 rows of 1000 bf16 tokens, backward, 246 -> 112 us).  Rows of
+// odd length start at any element, and gfx950 takes vector accesses at any address, so
+// the type promises the compiler no more than its elements' alignment.
 template <typename IO>
 struct __attribute__((packed, aligned(sizeof(typename IO::T)))) Words {
   uint32_t w[Raw<IO>::kWords];

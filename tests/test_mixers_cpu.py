@@ -76,7 +76,7 @@ def test_glr_bwd_refuses(case, status):
 
 
 @pytest.mark.parametrize("case,status", EVERY + [
-    (dict(state_in=None), INVALID), (dict(state_out=None), INVALID), (dict(y=None), INVALID), (dict(y=at(0)), INVALID),
+    (dict(batch=1, dim=(1 << 31) + 1), UNSUPPORTED), (dict(state_in=None), INVALID), (dict(state_out=None), INVALID), (dict(y=None), INVALID), (dict(y=at(0)), INVALID),
     (dict(state_out=at(22, 256)), INVALID), (dict(state_out=at(23, 2)), INVALID), (dict(y=at(22)), INVALID),
 ])
 def test_glr_step_refuses(case, status):
