@@ -11,19 +11,20 @@ current_stream = torch._C._cuda_getCurrentRawStream   # the stream's address, wi
 
 
 def io_code(t, name):
-    """The library's code of a tensor's I/O type, and the tensor's device, a GPU."""
-    io = _IO.get(t.dtype)
+    """The library's code of a tensor's I/O type, that type, and the tensor's device, a GPU."""
+    dtype = t.dtype
+    io = _IO.get(dtype)
     if io is None:
         raise TypeError("%s must be float32 or bfloat16" % name)
     if not t.is_cuda:
         raise ValueError("inputs must be on a GPU")
-    return io, t.device
+    return io, dtype, t.device
 
 
 def need(named, dtype, shape, device):
     """Every tensor of the (name, tensor or None) pairs has this type, shape and device and is contiguous."""
     for name, t in named:
-        if t is not None and not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous()):
             _need(t, name, dtype, shape, device)   # says which
 
 

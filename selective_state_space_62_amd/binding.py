@@ -8,6 +8,7 @@ missing this module raises ImportError: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import re
 from pathlib import Path
 
@@ -308,12 +309,14 @@ SS_QK_INTERLEAVED = 1
 SS_QK_FEATURE_MAJOR = 2
 
 
-_Strides = _i64 * 3
+@functools.lru_cache(maxsize=256)
+def _stride_array(s):
+    return (_i64 * 3)(*s)   # read only by the library
 
 
 def _strides(s):
     """(batch, token, head) strides in elements as the C entry points take them; None without that side."""
-    return None if s is None else _Strides(*s)
+    return None if s is None else _stride_array(s)
 
 
 def ss_qk_norm_rot(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, q_stride, k, k_stride, wq, wk,

@@ -34,19 +34,18 @@ def _shape(t, name, dtype, dev):
 def _out_shape(d, shape, feature_major):
     """The output's shape for an input of d dimensions."""
     batch, L, heads, n = shape
-    if d == 2:
-        return (batch, n)
+    if d == 4:
+        return (batch, heads, n, L) if feature_major else shape
     if d == 3:
         return (batch, n, L) if feature_major else (batch, L, n)
-    return (batch, heads, n, L) if feature_major else (batch, L, heads, n)
+    return (batch, n)
 
 
 def _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major):
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k are both None")
-    io, dev = io_code(ref, "q" if q is not None else "k")
-    dtype = ref.dtype
+    io, dtype, dev = io_code(ref, "q" if q is not None else "k")
     sq, stq = (None, None) if q is None else _shape(q, "q", dtype, dev)
     sk, stk = (None, None) if k is None else _shape(k, "k", dtype, dev)
     batch, L, _, n = sq or sk
@@ -54,10 +53,11 @@ def _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major):
         raise ValueError("q %s and k %s differ in more than their heads" % (tuple(q.shape), tuple(k.shape)))
     rot = 0
     if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq has %d dimensions, expected 1" % inv_freq.dim())
-        need((("inv_freq", inv_freq),), torch.float64, inv_freq.shape, dev)
-        rot = 2 * inv_freq.shape[0]
+        pairs = inv_freq.shape
+        if len(pairs) != 1:
+            raise ValueError("inv_freq has %d dimensions, expected 1" % len(pairs))
+        need((("inv_freq", inv_freq),), torch.float64, pairs, dev)
+        rot = 2 * pairs[0]
     need((("wq", wq), ("wk", wk)), torch.float32, (n,), dev)
     if positions is not None:
         flat = ref.dim() == 2 and positions.dim() == 1

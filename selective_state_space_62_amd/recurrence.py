@@ -17,11 +17,13 @@ _F32 = torch.float32
 
 def _checked(x, io_tensors, vectors, kind, shape):
     """The checks that all calls share; returns (device, I/O code, kind code)."""
-    io, dev = io_code(x, "x")
+    io, dtype, dev = io_code(x, "x")
     code = _KINDS.get(kind)
     if code is None:
         raise ValueError("kind must be 'convex' or 'normalised', got %r" % (kind,))
-    need(io_tensors, x.dtype, shape, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    need(io_tensors, dtype, shape, dev)
     need(vectors, _F32, shape[1:2], dev)
     return dev, io, code
 
@@ -47,7 +49,7 @@ def glr_fwd(x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=None,
     """
     batch, dim, L = x.shape
     shape = x.shape
-    dev, io, k = _checked(x, (("x", x), ("r", r), ("i", i), ("z", z), ("y", y)),
+    dev, io, k = _checked(x, (("r", r), ("i", i), ("z", z), ("y", y)),
                           (("decay", decay), ("r_bias", r_bias), ("i_bias", i_bias)), kind, shape)
     need((("h0", h0), ("h_final", h_final)), _F32, shape[:2], dev)
     if y is None:
@@ -57,7 +59,7 @@ def glr_fwd(x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=None,
     if ckpt is not None:
         need((("ckpt", ckpt),), _F32, (glr_ckpt_numel(batch, dim, L),), dev)
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_fwd_workspace_bytes(batch, dim, L), dev)
-    launch(dev, _b.ss_glr_fwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(decay),
+    launch(dev, _b.ss_glr_fwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
            ptr(r_bias), ptr(i_bias), ptr(h0), y.data_ptr(), ptr(h_final), ptr(ckpt), ws, nbytes)
     return y, h_final
 
@@ -75,7 +77,7 @@ def glr_bwd(x, r, dy, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=N
     """
     batch, dim, L = x.shape
     shape = x.shape
-    dev, io, k = _checked(x, (("x", x), ("r", r), ("i", i), ("z", z), ("dy", dy)),
+    dev, io, k = _checked(x, (("r", r), ("i", i), ("z", z), ("dy", dy)),
                           (("decay", decay), ("r_bias", r_bias), ("i_bias", i_bias)), kind, shape)
     need((("h0", h0), ("dh_final", dh_final)), _F32, shape[:2], dev)
     if ckpt is not None:
@@ -89,8 +91,8 @@ def glr_bwd(x, r, dy, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=N
                dr_bias=vec(need_dr_bias, dim), di_bias=vec(need_di_bias and i is not None, dim),
                dh0=vec(need_dh0, batch, dim))
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_bwd_workspace_bytes(batch, dim, L), dev)
-    launch(dev, _b.ss_glr_bwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(decay),
-           ptr(r_bias), ptr(i_bias), ptr(h0), dy.data_ptr(), ptr(dh_final), ptr(ckpt), ptr(out["dx"]), ptr(out["dr"]),
+    launch(dev, _b.ss_glr_bwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
+           ptr(r_bias), ptr(i_bias), ptr(h0), ptr(dy), ptr(dh_final), ptr(ckpt), ptr(out["dx"]), ptr(out["dr"]),
            ptr(out["di"]), ptr(out["dz"]), ptr(out["ddecay"]), ptr(out["dr_bias"]), ptr(out["di_bias"]), ptr(out["dh0"]),
            ws, nbytes)
     return out
@@ -102,12 +104,12 @@ def glr_step(state, x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, 
     new state is written to state_out.  x, r, i, z: (batch, D).  Returns y (batch, D)."""
     batch, dim = x.shape
     shape = x.shape
-    dev, io, k = _checked(x, (("x", x), ("r", r), ("i", i), ("z", z), ("y", y)),
+    dev, io, k = _checked(x, (("r", r), ("i", i), ("z", z), ("y", y)),
                           (("decay", decay), ("r_bias", r_bias), ("i_bias", i_bias)), kind, shape)
     need((("state", state), ("state_out", state_out)), _F32, shape, dev)
     if y is None:
         y = torch.empty_like(x)
-    launch(dev, _b.ss_glr_step, batch, dim, io, k, decay_scale, state.data_ptr(),
-           (state if state_out is None else state_out).data_ptr(), x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(decay),
+    launch(dev, _b.ss_glr_step, batch, dim, io, k, decay_scale, ptr(state),
+           (state if state_out is None else state_out).data_ptr(), x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
            ptr(r_bias), ptr(i_bias), y.data_ptr())
     return y
