@@ -72,9 +72,10 @@ ss_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   return SS_OK;
 }
 
-// Forward scratch: the memory through which split rows join.  Backward scratch: the
-// same, the states entering the tiles of rows of several, and the sums over each
-// row's (split: each tile's) tokens behind the per-channel gradients.
+// Forward scratch: the memory through which split rows join (their chain).  Backward
+// scratch: two of them (of the sweep that recomputes the states, and of the adjoint),
+// the states entering the tiles of rows of several, and the sums over each row's
+// (split: each tile's) tokens behind the per-channel gradients.
 struct GlrBwdLayout {
   size_t chain, ckpt, sums, total;
 };
@@ -86,19 +87,16 @@ size_t chain_bytes(int64_t rows, int64_t seqlen) {
 GlrBwdLayout bwd_layout(int64_t rows, int64_t seqlen) {
   const size_t tiles = glr_split(rows, seqlen) ? glr_tiles(seqlen) : 1;
   GlrBwdLayout w{};
-  w.chain = 0;
-  w.ckpt = chain_bytes(rows, seqlen);
+  w.chain = chain_bytes(rows, seqlen);
+  w.ckpt = 2 * w.chain;
   w.sums = w.ckpt + (seqlen > kGlrCkptTokens ? round256((size_t)rows * ckpt_count(seqlen) * sizeof(float)) : 0);
   w.total = w.sums + (seqlen > 0 ? round256((size_t)rows * tiles * 3 * sizeof(float)) : 0);
   return w;
 }
 
-// The chain's slots start as zeros (a kernel, so that a captured call replays).
-hipError_t clear_chain(GlrArgs& a, void* ws, hipStream_t s) {
-  a.chain = nullptr;
-  if (!glr_split(a.rows, a.seqlen)) return hipSuccess;
-  a.chain = ws;
-  return launch_fill_zero(static_cast<float*>(ws), (int64_t)(glr_chain_bytes(a.rows, a.seqlen) / sizeof(float)), s);
+// A chain's slots start as zeros (by a kernel, so that a captured call replays).
+hipError_t clear_chains(void* ws, size_t bytes, hipStream_t s) {
+  return bytes ? launch_fill_zero(static_cast<float*>(ws), (int64_t)(bytes / sizeof(float)), s) : hipSuccess;
 }
 
 GlrArgs base_args(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss_glr_kind kind, float decay_scale,
@@ -171,7 +169,8 @@ ss_status ss_glr_fwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
   a.y = y;
   a.h_final = h_final;
   a.ckpt = ckpt;
-  hipError_t e = clear_chain(a, workspace, s);
+  a.chain = need ? workspace : nullptr;
+  hipError_t e = clear_chains(workspace, need, s);
   if (e == hipSuccess) e = launch_glr_fwd(a, s);
   return e == hipSuccess ? SS_OK : record_hip_error(e, "recurrence launch");
 }
@@ -235,12 +234,16 @@ ss_status ss_glr_bwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
   char* ws = static_cast<char*>(workspace);
   GlrArgs a = base_args(batch, dim, seqlen, io, kind, decay_scale, x, r, i, z, decay, r_bias, i_bias, h0);
   a.ckpt = const_cast<float*>(ckpt);
-  if (!ckpt && seqlen > kGlrCkptTokens) {
+  const bool sweep = !ckpt && seqlen > kGlrCkptTokens;
+  e = clear_chains(ws, sweep ? 2 * wl.chain : wl.chain, s);
+  if (e != hipSuccess) return record_hip_error(e, "zero-fill launch");
+  a.chain = wl.chain ? ws : nullptr;
+  if (sweep) {
     GlrArgs f = a;   // the forward again, storing its states only
     f.z = nullptr;
     f.ckpt = a.ckpt = reinterpret_cast<float*>(ws + wl.ckpt);
-    e = clear_chain(f, ws, s);
-    if (e == hipSuccess) e = launch_glr_fwd(f, s);
+    if (f.chain) f.chain = ws + wl.chain;
+    e = launch_glr_fwd(f, s);
     if (e != hipSuccess) return record_hip_error(e, "state sweep launch");
   }
   a.dy = dy;
@@ -251,8 +254,7 @@ ss_status ss_glr_bwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
   a.dz = dz;
   a.dh0 = dh0;
   a.sums = ddecay || dr_bias || di_bias ? reinterpret_cast<float*>(ws + wl.sums) : nullptr;
-  e = clear_chain(a, ws, s);
-  if (e == hipSuccess) e = launch_glr_bwd(a, s);
+  e = launch_glr_bwd(a, s);
   if (e != hipSuccess) return record_hip_error(e, "recurrence backward launch");
   if (a.sums) {
     e = launch_glr_reduce(batch, dim, a.chain ? glr_tiles(seqlen) : 1, a.sums, ddecay, dr_bias, di_bias, s);

@@ -184,7 +184,7 @@ ss_status ss_qk_norm_rot(int64_t batch, int64_t seqlen, int heads_q, int heads_k
 
 size_t ss_qk_norm_rot_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim) {
   if (check_sizes(batch, seqlen, heads_q, heads_k, head_dim) != SS_OK || seqlen == 0) return 0;
-  const QkBwdPlan p = qk_bwd_plan(batch, seqlen, heads_q, heads_k);
+  const QkBwdPlan p = qk_bwd_plan(batch, seqlen, heads_q, heads_k, head_dim);
   return round256((size_t)(p.blocks[0] + p.blocks[1]) * head_dim * sizeof(float));
 }
 

@@ -336,32 +336,49 @@ __global__ __launch_bounds__(256) void glr_bwd_split_kernel(GlrArgs p) {
     store_sums<KIND, 4>(p, d, row * tiles + n, p.rows * tiles, wave, wave, 4, lane, true, sum_d, sum_r, sum_i);
 }
 
-// Rows of one part each: a thread sums a channel's batch rows in order.
-__global__ __launch_bounds__(256) void glr_reduce_kernel(int64_t batch, int64_t dim, const float* __restrict__ sums,
-                                                         float* ddecay, float* dr_bias, float* di_bias) {
+// Rows of one part each: 32 threads sum a channel's batch rows, every 32nd each, and are
+// joined in order.
+__global__ __launch_bounds__(1024) void glr_reduce_kernel(int64_t batch, int64_t dim, const float* __restrict__ sums,
+                                                          float* ddecay, float* dr_bias, float* di_bias) {
+  __shared__ float s_sum[32][32];
   float* out = blockIdx.y == 0 ? ddecay : blockIdx.y == 1 ? dr_bias : di_bias;
-  const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (!out || d >= dim) return;
-  const float* in = sums + (int64_t)blockIdx.y * batch * dim + d;
+  if (!out) return;
+  const int col = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int64_t d = (int64_t)blockIdx.x * 32 + col;
   float v = 0.0f;
-  for (int64_t b = 0; b < batch; ++b) v += in[b * dim];
-  out[d] = v;
+  if (d < dim) {
+    const float* in = sums + (int64_t)blockIdx.y * batch * dim + d;
+#pragma unroll 4
+    for (int64_t b = run; b < batch; b += 32) v += in[b * dim];
+  }
+  s_sum[run][col] = v;
+  __syncthreads();
+  if (run == 0 && d < dim) {
+    const int runs = batch < 32 ? (int)batch : 32;
+    for (int k = 1; k < runs; ++k) v += s_sum[k][col];
+    out[d] = v;
+  }
 }
 
-// Rows of several parts: a wave sums a channel, its lanes every 64th part.
-__global__ __launch_bounds__(64) void glr_reduce_parts_kernel(int64_t batch, int64_t dim, int64_t parts,
-                                                              const float* __restrict__ sums, float* ddecay,
-                                                              float* dr_bias, float* di_bias) {
+// Rows of several parts: a workgroup sums a channel, a thread every 256th part of all its batch rows.
+__global__ __launch_bounds__(256) void glr_reduce_parts_kernel(int64_t batch, int64_t dim, int64_t parts,
+                                                               const float* __restrict__ sums, float* ddecay,
+                                                               float* dr_bias, float* di_bias) {
+  __shared__ float s_sum[4];
   float* out = blockIdx.y == 0 ? ddecay : blockIdx.y == 1 ? dr_bias : di_bias;
   if (!out) return;
   const int64_t d = blockIdx.x;
+  const float* in = sums + ((int64_t)blockIdx.y * batch * dim + d) * parts;
   float v = 0.0f;
-  for (int64_t b = 0; b < batch; ++b) {
-    const float* in = sums + ((int64_t)blockIdx.y * batch * dim + b * dim + d) * parts;
-    for (int64_t k = threadIdx.x; k < parts; k += 64) v += in[k];
+#pragma unroll 4
+  for (int64_t e = threadIdx.x; e < batch * parts; e += 256) {
+    const int64_t b = e / parts;
+    v += in[b * dim * parts + (e - b * parts)];
   }
   v = wave_sum(v);
-  if (threadIdx.x == 63) out[d] = v;
+  if ((threadIdx.x & 63) == 63) s_sum[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) out[d] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
 }
 
 template <typename IO, int KIND, bool HI, bool HZ>
@@ -406,10 +423,10 @@ hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t s) { return glr::by_form
 hipError_t launch_glr_reduce(int64_t batch, int64_t dim, int64_t parts, const float* sums, float* ddecay,
                              float* dr_bias, float* di_bias, hipStream_t s) {
   if (parts == 1) {
-    hipLaunchKernelGGL(glr::glr_reduce_kernel, dim3((unsigned)((dim + 255) / 256), 3), dim3(256), 0, s, batch, dim,
+    hipLaunchKernelGGL(glr::glr_reduce_kernel, dim3((unsigned)((dim + 31) / 32), 3), dim3(1024), 0, s, batch, dim,
                        sums, ddecay, dr_bias, di_bias);
   } else {
-    hipLaunchKernelGGL(glr::glr_reduce_parts_kernel, dim3((unsigned)dim, 3), dim3(64), 0, s, batch, dim, parts, sums,
+    hipLaunchKernelGGL(glr::glr_reduce_parts_kernel, dim3((unsigned)dim, 3), dim3(256), 0, s, batch, dim, parts, sums,
                        ddecay, dr_bias, di_bias);
   }
   return hipGetLastError();

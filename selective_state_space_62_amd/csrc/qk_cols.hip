@@ -11,54 +11,36 @@ namespace {
 
 using namespace qk;
 
-// How a vector lies in registers: pair p is values 2p and 2p + 1 of the input
-// (kAdjacent: interleaved, or nothing rotated), p and p + N/2 (kHalves: all of it
-// rotated), or p and p + half up to half and 2p and 2p + 1 from there (kPartial,
-// whose element addresses depend on half, so it loads one by one).
-enum Order { kAdjacent, kHalves, kPartial };
-
-template <int N, int ORDER>
-__device__ __forceinline__ int place(int p, int h, int half) {
-  if constexpr (ORDER == kAdjacent) return 2 * p + h;
-  else if constexpr (ORDER == kHalves) return p + h * (N / 2);
-  else return p < half ? p + h * half : 2 * p + h;
+// How a vector's pairs lie in it: 2p and 2p + 1 (HALF 0: interleaved, or nothing
+// rotated), or p and p + HALF up to HALF and 2p and 2p + 1 from there.  A constant, so
+// that pairs are picked from vector loads by register (at 612000 tokens, half of 16 values
+// rotated: 37 us a whole call, element by element 60).
+template <int N, int HALF>
+__device__ __forceinline__ constexpr int place(int k) {   // of value k % 2 of pair k / 2
+  return N == 1 ? 0 : k / 2 < HALF ? k / 2 + k % 2 * HALF : k;
 }
 
 // x[2 p + h] = value h of pair p.
-template <typename IO, int N, int ORDER>
-__device__ __forceinline__ void load_pairs(const typename IO::T* __restrict__ in, int half, float (&x)[N]) {
-  if constexpr (N == 1) {
-    x[0] = load_one<IO>(in, 0);
-  } else if constexpr (ORDER == kPartial) {
+template <typename IO, int N, int HALF>
+__device__ __forceinline__ void load_pairs(const typename IO::T* __restrict__ in, float (&x)[N]) {
+  float v[N];
+  load_run<IO, N>(in, v);
 #pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = load_one<IO>(in, place<N, ORDER>(k >> 1, k & 1, half));
-  } else {
-    float v[N];
-    load_run<IO, N>(in, v);
-#pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = v[place<N, ORDER>(k >> 1, k & 1, half)];
-  }
+  for (int k = 0; k < N; ++k) x[k] = v[place<N, HALF>(k)];
 }
 
-template <typename IO, int N, int ORDER>
-__device__ __forceinline__ void store_pairs(typename IO::T* __restrict__ out, int half, const float (&x)[N]) {
-  if constexpr (N == 1) {
-    store_one<IO>(out, 0, x[0]);
-  } else if constexpr (ORDER == kPartial) {
+template <typename IO, int N, int HALF>
+__device__ __forceinline__ void store_pairs(typename IO::T* __restrict__ out, const float (&x)[N]) {
+  float v[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) store_one<IO>(out, place<N, ORDER>(k >> 1, k & 1, half), x[k]);
-  } else {
-    float v[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[place<N, ORDER>(k >> 1, k & 1, half)] = x[k];
-    store_run<IO, N>(out, v);
-  }
+  for (int k = 0; k < N; ++k) v[place<N, HALF>(k)] = x[k];
+  store_run<IO, N>(out, v);
 }
 
-template <int N, int ORDER>
-__device__ __forceinline__ void load_weight(const float* __restrict__ w, int half, float (&v)[N]) {
+template <int N, int HALF>
+__device__ __forceinline__ void load_weight(const float* __restrict__ w, float (&v)[N]) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = w ? w[N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, half)] : 1.0f;
+  for (int k = 0; k < N; ++k) v[k] = w ? w[place<N, HALF>(k)] : 1.0f;
 }
 
 template <int N>
@@ -71,13 +53,13 @@ __device__ __forceinline__ void angles(const QkArgs& a, double pos, float (&c)[N
   }
 }
 
-// The lane's token of a turn of 64; past the last one, the last one again.
+// The lane's token of a turn of blockDim.x; past the last one, the last one again.
 struct Token {
   int64_t tok, b, t;
   bool act;
   __device__ __forceinline__ Token(const QkArgs& a, int64_t turn) {
     const int64_t tokens = a.batch * a.seqlen;
-    tok = turn * 64 + threadIdx.x;
+    tok = turn * blockDim.x + threadIdx.x;
     act = tok < tokens;
     tok = act ? tok : tokens - 1;
     b = tok / a.seqlen;
@@ -109,7 +91,7 @@ __device__ __forceinline__ void forward(const QkArgs& a, const float (&w)[N], co
 // the registers for six waves to a SIMD 43.5 us; a copy of the same 64 bytes of each
 // 320-byte row 32 us).  Turning tiles in LDS for 16-byte stores took 54 us, for 16-byte pieces
 // of a row to neighbouring lanes 77 us, 4-byte stores of two tokens 51 us.
-template <typename IO, int N, int ORDER>
+template <typename IO, int N, int HALF>
 __global__ __launch_bounds__(64, N == 16 && IO::kPerSpan == 4 ? 5 : 6) void qk_cols_fwd_kernel(QkArgs a, int64_t turns) {
   using T = typename IO::T;
   const int heads = a.side[0].heads + a.side[1].heads;
@@ -119,7 +101,7 @@ __global__ __launch_bounds__(64, N == 16 && IO::kPerSpan == 4 ? 5 : 6) void qk_c
     auto fetch = [&](int item, float (&x)[N]) {
       const int side = item >= a.side[0].heads, h = item - (side ? a.side[0].heads : 0);
       const QkSide& sd = a.side[side];
-      load_pairs<IO, N, ORDER>((const T*)sd.in + tk.b * sd.stride[0] + tk.t * sd.stride[1] + h * sd.stride[2], a.half, x);
+      load_pairs<IO, N, HALF>((const T*)sd.in + tk.b * sd.stride[0] + tk.t * sd.stride[1] + h * sd.stride[2], x);
     };
     float x[N], next[N];
     fetch(0, x);
@@ -130,13 +112,13 @@ __global__ __launch_bounds__(64, N == 16 && IO::kPerSpan == 4 ? 5 : 6) void qk_c
       const int side = item >= a.side[0].heads, h = item - (side ? a.side[0].heads : 0);
       const QkSide& sd = a.side[side];
       float w[N];
-      load_weight<N, ORDER>(sd.w, a.half, w);
+      load_weight<N, HALF>(sd.w, w);
       forward<N>(a, w, c, sn, x);
       T* out = (T*)sd.out + (tk.b * sd.heads + h) * N * a.seqlen;
       if (tk.act) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          store_one<IO>(out, (N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)) * a.seqlen + tk.t, x[k]);
+          store_one<IO>(out, place<N, HALF>(k) * a.seqlen + tk.t, x[k]);
       }
 #pragma unroll
       for (int k = 0; k < N; ++k) x[k] = next[k];
@@ -147,9 +129,10 @@ __global__ __launch_bounds__(64, N == 16 && IO::kPerSpan == 4 ? 5 : 6) void qk_c
 
 // With n = rho w v and o the rotated n: dn is the gradient of o rotated back, and
 // with p = w dn, dv = rho p - rho^3 v mean(p v), dw = sum of dn rho v.
-template <typename IO, int N, int ORDER>
-__global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a, int64_t turns) {
+template <typename IO, int N, int HALF>
+__global__ __launch_bounds__(256) void qk_cols_bwd_kernel(QkArgs a, int64_t turns) {
   using T = typename IO::T;
+  __shared__ float s_dw[2][4][N];
   float dw[2][N] = {};
   for (int64_t turn = blockIdx.x; turn < turns; turn += gridDim.x) {
     const Token tk(a, turn);
@@ -159,15 +142,14 @@ __global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a, int64_t turns
     for (int side = 0; side < 2; ++side) {
       const QkSide& sd = a.side[side];
       float w[N];
-      load_weight<N, ORDER>(sd.w, a.half, w);
+      load_weight<N, HALF>(sd.w, w);
       for (int h = 0; h < sd.heads; ++h) {
         float x[N], d[N];
-        load_pairs<IO, N, ORDER>((const T*)sd.in + tk.b * sd.stride[0] + tk.t * sd.stride[1] + h * sd.stride[2], a.half,
-                                 x);
+        load_pairs<IO, N, HALF>((const T*)sd.in + tk.b * sd.stride[0] + tk.t * sd.stride[1] + h * sd.stride[2], x);
         const T* dout = (const T*)sd.dout + (tk.b * sd.heads + h) * N * a.seqlen;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          d[k] = load_one<IO>(dout, (N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)) * a.seqlen + tk.t);
+          d[k] = load_one<IO>(dout, place<N, HALF>(k) * a.seqlen + tk.t);
 #pragma unroll
         for (int p = 0; p < N / 2; ++p) {
           if (p >= a.half) continue;
@@ -188,64 +170,71 @@ __global__ __launch_bounds__(64) void qk_cols_bwd_kernel(QkArgs a, int64_t turns
             dw[side][k] = fmaf(d[k], rho * x[k], dw[side][k]);
             x[k] = rho * (d[k] * w[k] - x[k] * back);
           }
-          store_pairs<IO, N, ORDER>((T*)sd.din + tk.b * sd.dstride[0] + tk.t * sd.dstride[1] + h * sd.dstride[2], a.half,
-                                    x);
+          store_pairs<IO, N, HALF>((T*)sd.din + tk.b * sd.dstride[0] + tk.t * sd.dstride[1] + h * sd.dstride[2], x);
         }
       }
     }
   }
+  const int wave = threadIdx.x >> 6;
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     if (!a.side[side].dw) continue;
-    float* part = a.part + (a.part_row[side] + blockIdx.x) * N;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       float v = dw[side][k];
 #pragma unroll
       for (int step = 1; step < 64; step <<= 1) v += __shfl_xor(v, step);
-      if (threadIdx.x == 0) part[N == 1 ? 0 : place<N, ORDER>(k >> 1, k & 1, a.half)] = v;
+      if ((threadIdx.x & 63) == 0) s_dw[side][wave][place<N, HALF>(k)] = v;
     }
+  }
+  __syncthreads();
+  const int side = threadIdx.x / N, j = threadIdx.x % N;
+  if (side < 2 && a.side[side].dw) {
+    float v = s_dw[side][0][j];
+    for (int k = 1; k < (int)blockDim.x / 64; ++k) v += s_dw[side][k][j];
+    a.part[(a.part_row[side] + blockIdx.x) * N + j] = v;
   }
 }
 
 struct ColsShape {
-  int64_t turns;   // of 64 tokens
-  unsigned blocks;
+  int64_t turns;   // of a workgroup's threads, a token each
+  unsigned blocks, threads;
 };
 
-template <typename IO, int N, int ORDER>
+template <typename IO, int N, int HALF>
 void launch(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
-  if (back) hipLaunchKernelGGL((qk_cols_bwd_kernel<IO, N, ORDER>), dim3(sh.blocks), dim3(64), 0, s, a, sh.turns);
-  else hipLaunchKernelGGL((qk_cols_fwd_kernel<IO, N, ORDER>), dim3(sh.blocks), dim3(64), 0, s, a, sh.turns);
+  if (back) hipLaunchKernelGGL((qk_cols_bwd_kernel<IO, N, HALF>), dim3(sh.blocks), dim3(sh.threads), 0, s, a, sh.turns);
+  else hipLaunchKernelGGL((qk_cols_fwd_kernel<IO, N, HALF>), dim3(sh.blocks), dim3(64), 0, s, a, sh.turns);
 }
 
-template <typename IO, int N>
-void by_order(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
-  if constexpr (N <= 2) {   // one pair at most: every order is the same
-    launch<IO, N, kAdjacent>(a, back, sh, s);
+// The kernel for this half: HALF down to 1 where pairs lie apart, or 0.
+template <typename IO, int N, int HALF = N / 2>
+void by_half(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
+  if constexpr (N >= 4 && HALF > 0) {   // one pair at most lies as adjacent ones do
+    if (!a.interleaved && a.half == HALF) launch<IO, N, HALF>(a, back, sh, s);
+    else by_half<IO, N, HALF - 1>(a, back, sh, s);
   } else {
-    if (a.interleaved || a.half == 0) launch<IO, N, kAdjacent>(a, back, sh, s);
-    else if (2 * a.half == N) launch<IO, N, kHalves>(a, back, sh, s);
-    else launch<IO, N, kPartial>(a, back, sh, s);
+    launch<IO, N, 0>(a, back, sh, s);
   }
 }
 
 template <typename IO>
 hipError_t by_dim(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
   switch (a.n) {
-    case 1: by_order<IO, 1>(a, back, sh, s); break;
-    case 2: by_order<IO, 2>(a, back, sh, s); break;
-    case 4: by_order<IO, 4>(a, back, sh, s); break;
-    case 8: by_order<IO, 8>(a, back, sh, s); break;
-    case 16: by_order<IO, 16>(a, back, sh, s); break;
+    case 1: by_half<IO, 1>(a, back, sh, s); break;
+    case 2: by_half<IO, 2>(a, back, sh, s); break;
+    case 4: by_half<IO, 4>(a, back, sh, s); break;
+    case 8: by_half<IO, 8>(a, back, sh, s); break;
+    case 16: by_half<IO, 16>(a, back, sh, s); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }
 
-ColsShape shape_of(const QkArgs& a, int64_t most) {
+ColsShape shape_of(const QkArgs& a, unsigned threads, int64_t most) {
   ColsShape sh;
-  sh.turns = (a.batch * a.seqlen + 63) / 64;
+  sh.threads = threads;
+  sh.turns = (a.batch * a.seqlen + threads - 1) / threads;
   sh.blocks = (unsigned)(sh.turns < most ? sh.turns : most);
   return sh;
 }
@@ -256,13 +245,16 @@ hipError_t go(const QkArgs& a, bool back, const ColsShape& sh, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_qk_cols(const QkArgs& a, hipStream_t s) { return go(a, false, shape_of(a, 1 << 20), s); }
+hipError_t launch_qk_cols(const QkArgs& a, hipStream_t s) { return go(a, false, shape_of(a, 64, 1 << 20), s); }
 
 hipError_t launch_qk_cols_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s) {
   int64_t most = 1 << 20;
   for (int i = 0; i < 2; ++i)
     if (a.side[i].heads && p.blocks[i] < most) most = p.blocks[i];
-  const ColsShape sh = shape_of(a, most);
+  // the workgroups are few, each with a row of sums: four waves each where the tokens fill
+  // them (320860 tokens, half of 16 values rotated, whole call: one wave 53.9, four
+  // 35.2 us)
+  const ColsShape sh = shape_of(a, a.batch * a.seqlen >= 256 * most ? 256 : 64, most);
   for (int i = 0; i < 2; ++i) a.part_rows[i] = a.side[i].heads ? (int64_t)sh.blocks : 0;
   a.part_row[1] = a.part_rows[0];
   return go(a, true, sh, s);

@@ -42,7 +42,7 @@ struct QkArgs {
 struct QkBwdPlan {
   int64_t blocks[2];
 };
-QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k);
+QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int n);
 
 // Launch of the kernels for pairs in runs: lanes to a vector, and of each side the
 // tokens of a workgroup and the workgroups.

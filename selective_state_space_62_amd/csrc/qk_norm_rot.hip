@@ -194,13 +194,14 @@ __global__ __launch_bounds__(1024) void qk_reduce_kernel(QkArgs a) {
 
 // About 1024 rows of partial sums, shared by the sides as their heads are: four workgroups
 // to a CU, which is what the registers of the kernel for runs allow (25 fp32 heads of 80 at 8188
-// tokens, whole call: 1024 rows 51.7, 2048 53.7, 4096 56.1 us).
-QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k) {
+// tokens, whole call: 1024 rows 51.7, 2048 53.7, 4096 56.1 us).  Twice as many for the short
+// heads of the feature-major kernel, which needs less of both.
+QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int n) {
   QkBwdPlan p;
   const int64_t heads = (int64_t)heads_q + heads_k, tokens = batch * seqlen;
   for (int i = 0; i < 2; ++i) {
-    const int64_t h = i ? heads_k : heads_q, n = 1024 * h / heads;
-    p.blocks[i] = h == 0 ? 0 : n < 1 ? 1 : n < tokens ? n : tokens;
+    const int64_t h = i ? heads_k : heads_q, most = (n <= 16 ? 2048 : 1024) * h / heads;
+    p.blocks[i] = h == 0 ? 0 : most < 1 ? 1 : most < tokens ? most : tokens;
   }
   return p;
 }
@@ -218,7 +219,7 @@ hipError_t launch_qk_norm_rot(const QkArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_qk_norm_rot_bwd(QkArgs a, hipStream_t s) {
-  const QkBwdPlan p = qk_bwd_plan(a.batch, a.seqlen, a.side[0].heads, a.side[1].heads);
+  const QkBwdPlan p = qk_bwd_plan(a.batch, a.seqlen, a.side[0].heads, a.side[1].heads, a.n);
   hipError_t e;
   if (a.feature_major) {
     e = launch_qk_cols_bwd(a, p, s);

@@ -216,10 +216,11 @@ __global__ __launch_bounds__(kThreads) void qk_rows_bwd_kernel(QkArgs a, QkRowsS
     a.part[(a.part_row[side] + block) * a.n + j] = (s_dw[0][j] + s_dw[1][j]) + (s_dw[2][j] + s_dw[3][j]);
 }
 
-// The longest run that the shape allows: half and the rest's pairs in whole runs, and
-// 16 bytes at most.  0: none.
-int run_of(const QkArgs& a) {
-  for (int k = a.io == kIoBf16 ? 8 : 4; k >= 2; k >>= 1)
+// The longest run that the shape allows: half and the rest's pairs in whole runs, and 16
+// bytes at most; in the backward 4 values, whose registers leave room for more waves (6 bf16 heads
+// of 128 at 21879 tokens: runs of 8 42.0, of 4 33.1 us; 40 at 16384 142.5 and 139.7 us).  0: none.
+int run_of(const QkArgs& a, bool back) {
+  for (int k = a.io == kIoBf16 && !back ? 8 : 4; k >= 2; k >>= 1)
     if (a.half % k == 0 && (a.n - 2 * a.half) % (2 * k) == 0) return k;
   return 0;
 }
@@ -230,25 +231,34 @@ int lanes_of(const QkArgs& a, int k) {
   return g;
 }
 
-// A workgroup's tokens: two rounds of vectors for its groups of lanes, fewer where the
-// tokens would not give 1024 workgroups.  (40 bf16 heads of 128 at 16384 tokens: one round 73.7, two
-// 66.6, three 67.6 us; two or four vectors in flight to a group, which cost waves their registers,
-// 71 and 80 us.)
-QkRowsShape shape_of(const QkArgs& a, int k, const int64_t (&most)[2]) {
+// A workgroup's tokens.  Forward: two rounds of vectors for its groups of lanes, fewer
+// where the tokens would not give 1024 workgroups.  (40 bf16 heads of 128 at 16384 tokens: one
+// round 73.7, two 66.6, three 67.6 us; two or four vectors in flight to a group, which cost
+// waves their registers, 71 and 80 us.)  Backward, where the workgroups are few and keep
+// their sums: an equal share of the tokens, in as few turns as the angles' LDS allows.
+QkRowsShape shape_of(const QkArgs& a, int k, bool back, const int64_t (&most)[2]) {
   QkRowsShape sh{};
   const int64_t tokens = a.batch * a.seqlen;
   sh.lanes = lanes_of(a, k);
   const int groups = kThreads / sh.lanes;
+  const int64_t cap = a.half && kAngles / a.half < kTokens ? kAngles / a.half : kTokens;
   for (int i = 0; i < 2; ++i) {
     const int heads = a.side[i].heads;
     sh.tokens[i] = 1;
     if (!heads) continue;
-    int64_t n = (2 * groups + heads - 1) / heads;
-    if (n > tokens / 1024) n = tokens / 1024;
-    if (a.half && n > kAngles / a.half) n = kAngles / a.half;
-    if (n > kTokens) n = kTokens;
+    int64_t n;
+    if (back) {
+      const int64_t share = (tokens + most[i] - 1) / most[i], turns = (share + cap - 1) / cap;
+      const int64_t least = (groups + heads - 1) / heads;
+      n = (share + turns - 1) / turns;
+      if (n < least) n = least;
+    } else {
+      n = (2 * groups + heads - 1) / heads;
+      if (n > tokens / 1024) n = tokens / 1024;
+    }
+    if (n > cap) n = cap;
     sh.tokens[i] = n > 1 ? (int)n : 1;
-    int64_t blocks = (tokens + sh.tokens[i] - 1) / sh.tokens[i];
+    const int64_t blocks = (tokens + sh.tokens[i] - 1) / sh.tokens[i];
     sh.blocks[i] = (int)(blocks < most[i] ? blocks : most[i]);
   }
   return sh;
@@ -257,8 +267,13 @@ QkRowsShape shape_of(const QkArgs& a, int k, const int64_t (&most)[2]) {
 template <typename IO, int K, bool INTER>
 void launch(const QkArgs& a, bool back, const QkRowsShape& sh, hipStream_t s) {
   const dim3 g((unsigned)(sh.blocks[0] + sh.blocks[1]));
-  if (back) hipLaunchKernelGGL((qk_rows_bwd_kernel<IO, K, INTER>), g, dim3(kThreads), 0, s, a, sh);
-  else hipLaunchKernelGGL((qk_rows_fwd_kernel<IO, K, INTER>), g, dim3(kThreads), 0, s, a, sh);
+  if constexpr (K <= 4) {
+    if (back) {
+      hipLaunchKernelGGL((qk_rows_bwd_kernel<IO, K, INTER>), g, dim3(kThreads), 0, s, a, sh);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((qk_rows_fwd_kernel<IO, K, INTER>), g, dim3(kThreads), 0, s, a, sh);
 }
 
 template <typename IO, int K>
@@ -281,16 +296,16 @@ hipError_t go(const QkArgs& a, bool back, int k, const QkRowsShape& sh, hipStrea
 
 }  // namespace
 
-bool qk_rows_take(const QkArgs& a) { return run_of(a) > 0; }
+bool qk_rows_take(const QkArgs& a) { return run_of(a, false) > 0; }
 
 hipError_t launch_qk_rows(const QkArgs& a, hipStream_t s) {
-  const int k = run_of(a);
-  return go(a, false, k, shape_of(a, k, {1 << 20, 1 << 20}), s);
+  const int k = run_of(a, false);
+  return go(a, false, k, shape_of(a, k, false, {1 << 20, 1 << 20}), s);
 }
 
 hipError_t launch_qk_rows_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s) {
-  const int k = run_of(a);
-  const QkRowsShape sh = shape_of(a, k, p.blocks);
+  const int k = run_of(a, true);
+  const QkRowsShape sh = shape_of(a, k, true, p.blocks);
   for (int i = 0; i < 2; ++i) a.part_rows[i] = sh.blocks[i];
   a.part_row[1] = a.part_rows[0];
   return go(a, true, k, sh, s);
