@@ -92,7 +92,7 @@ def qk_norm_rot(q, k, inv_freq=None, wq=None, wk=None, positions=None, pos0=0, *
             continue
         shape = _out_shape(t.dim(), side, feature_major)
         if given is None:
-            given = torch.empty(shape, dtype=dtype, device=dev)
+            given = t.new_empty(shape)
         else:
             need(((name, given),), dtype, shape, dev)
         outs.append(given)
@@ -123,7 +123,7 @@ def qk_norm_rot_bwd(q, k, inv_freq, dq_out, dk_out, wq=None, wk=None, positions=
             raise ValueError("%s_out is None" % name)
         need(((name + "_out", up),), dtype, _out_shape(t.dim(), side, feature_major), dev)
         if given is None:
-            given = torch.empty(t.shape, dtype=dtype, device=dev)
+            given = t.new_empty(t.shape)
         elif given.shape != t.shape:
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(given.shape), tuple(t.shape)))
         grads.append(given)

@@ -55,7 +55,7 @@ def glr_fwd(x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=None,
     if y is None:
         y = torch.empty_like(x)
     if h_final is None and return_final_state:
-        h_final = torch.empty((batch, dim), dtype=_F32, device=dev)
+        h_final = torch.empty_like(h0) if h0 is not None else torch.empty((batch, dim), dtype=_F32, device=dev)
     if ckpt is not None:
         need((("ckpt", ckpt),), _F32, (glr_ckpt_numel(batch, dim, L),), dev)
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_fwd_workspace_bytes(batch, dim, L), dev)

@@ -426,6 +426,37 @@ def test_empty_sequence(ss, dev):
     assert not run_fwd(ss, p)[1].any()
 
 
+@pytest.mark.parametrize("L", [37, 2100])
+def test_offsets_past_32_bits(ss, dev, L):
+    """More than 2^31 elements: the last rows of a large call are bit for bit those of a call of their own."""
+    import torch
+    rows = (1 << 31) // L + 1000
+    p = problem(dev, 25, 1, 5, L, "bf16", "convex", z=False)
+    big = {k: None if v is None else torch.zeros((1, rows, L), dtype=v.dtype, device=dev) for k, v in p.items() if k in ("x", "r", "i", "z")}
+    vec = {k: torch.zeros(rows, device=dev) for k in ("decay", "r_bias", "i_bias")}
+    h0 = torch.zeros(1, rows, device=dev)
+    for k, v in big.items():
+        if v is not None:
+            v[:, -5:] = p[k]
+    for k, v in vec.items():
+        v[-5:] = p[k]
+    h0[:, -5:] = p["h0"]
+    y, h = ss.glr_fwd(**big, **vec, h0=h0, kind="convex")
+    y5, h5 = run_fwd(ss, p)
+    assert torch.equal(y[:, -5:], y5) and torch.equal(h[:, -5:], h5) and not y[:, :-5].any()
+    del y
+    dy = torch.zeros_like(big["x"])
+    dy[:, -5:] = p["x"]
+    g = ss.glr_bwd(dy=dy, **big, **vec, h0=h0, kind="convex")
+    g5 = ss.glr_bwd(dy=p["x"], **p)
+    torch.cuda.synchronize()
+    for k in ("dx", "dr", "di"):
+        assert torch.equal(g[k][:, -5:], g5[k]), k
+    for k in ("ddecay", "dr_bias", "di_bias"):
+        assert torch.equal(g[k][-5:], g5[k]), k
+    assert torch.equal(g["dh0"][:, -5:], g5["dh0"])
+
+
 def test_outputs_stay_inside_their_rows(ss, dev):
     """Nothing is written behind the last row or before the first, at lengths that end inside a vector."""
     import torch

@@ -237,6 +237,29 @@ def test_gradient_into_columns_of_one_buffer(ss, dev):
         assert (rows[..., :8] == 7).all() and (rows[..., 8 + (hq + hk) * N:] == 7).all()
 
 
+@pytest.mark.parametrize("fm,N,hq,hk", [(True, 16, 1, 1), (False, 64, 2, 1), (False, 7, 1, 1)])
+def test_offsets_past_32_bits(ss, dev, fm, N, hq, hk):
+    """Rows whose last ones start more than 2^31 elements on: as from contiguous copies, gradients into such rows too."""
+    import torch
+    B, L, width = 2, 1100, 1 << 20
+    p = problem(dev, 16, B, L, hq, hk, N, N // 2 * 2, "bf16")
+    rows = torch.empty(B, L, width, dtype=torch.bfloat16, device=dev)
+    n = (hq + hk) * N
+    wide = rows[..., -n:]
+    far = dict(p, q=wide[..., :hq * N].unflatten(-1, (hq, N)), k=wide[..., hq * N:].unflatten(-1, (hk, N)))
+    far["q"].copy_(p["q"])
+    far["k"].copy_(p["k"])
+    want, got = ss.qk_norm_rot(**p, feature_major=fm), ss.qk_norm_rot(**far, feature_major=fm)
+    dq, dk = grads_like(dev, 17, p, fm)
+    gw = ss.qk_norm_rot_bwd(dq_out=dq, dk_out=dk, **p, feature_major=fm)
+    grad = torch.empty_like(rows)
+    dst = [grad[..., a:a + h * N].unflatten(-1, (h, N)) for a, h in ((0, hq), (hq * N, hk))]
+    gg = ss.qk_norm_rot_bwd(dq_out=dq, dk_out=dk, **far, feature_major=fm, dq=dst[0], dk=dst[1])
+    torch.cuda.synchronize()
+    for a, b in ((want[0], got[0]), (want[1], got[1]), *((gw[k], gg[k]) for k in gw)):
+        assert torch.equal(a, b)
+
+
 def test_broadcast_inputs(ss, dev):
     """One row shared by all tokens (stride 0) and heads apart by more than their values."""
     import torch
