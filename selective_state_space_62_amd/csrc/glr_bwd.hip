@@ -338,25 +338,30 @@ __global__ __launch_bounds__(256) void glr_bwd_split_kernel(GlrArgs p) {
 
 // Rows of one part each: 32 threads sum a channel's batch rows, every 32nd each, and are
 // joined in order.
+constexpr int64_t kReduceBlocks = int64_t(1) << 20;   // a grid axis holds fewer than 2^32 threads
+
 __global__ __launch_bounds__(1024) void glr_reduce_kernel(int64_t batch, int64_t dim, const float* __restrict__ sums,
                                                           float* ddecay, float* dr_bias, float* di_bias) {
   __shared__ float s_sum[32][32];
   float* out = blockIdx.y == 0 ? ddecay : blockIdx.y == 1 ? dr_bias : di_bias;
   if (!out) return;
   const int col = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int64_t d = (int64_t)blockIdx.x * 32 + col;
-  float v = 0.0f;
-  if (d < dim) {
-    const float* in = sums + (int64_t)blockIdx.y * batch * dim + d;
+  for (int64_t first = (int64_t)blockIdx.x * 32; first < dim; first += (int64_t)gridDim.x * 32) {
+    const int64_t d = first + col;
+    float v = 0.0f;
+    if (d < dim) {
+      const float* in = sums + (int64_t)blockIdx.y * batch * dim + d;
 #pragma unroll 4
-    for (int64_t b = run; b < batch; b += 32) v += in[b * dim];
-  }
-  s_sum[run][col] = v;
-  __syncthreads();
-  if (run == 0 && d < dim) {
-    const int runs = batch < 32 ? (int)batch : 32;
-    for (int k = 1; k < runs; ++k) v += s_sum[k][col];
-    out[d] = v;
+      for (int64_t b = run; b < batch; b += 32) v += in[b * dim];
+    }
+    s_sum[run][col] = v;
+    __syncthreads();
+    if (run == 0 && d < dim) {
+      const int runs = batch < 32 ? (int)batch : 32;
+      for (int k = 1; k < runs; ++k) v += s_sum[k][col];
+      out[d] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -423,8 +428,9 @@ hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t s) { return glr::by_form
 hipError_t launch_glr_reduce(int64_t batch, int64_t dim, int64_t parts, const float* sums, float* ddecay,
                              float* dr_bias, float* di_bias, hipStream_t s) {
   if (parts == 1) {
-    hipLaunchKernelGGL(glr::glr_reduce_kernel, dim3((unsigned)((dim + 31) / 32), 3), dim3(1024), 0, s, batch, dim,
-                       sums, ddecay, dr_bias, di_bias);
+    const int64_t blocks = (dim + 31) / 32;
+    const dim3 g((unsigned)(blocks < glr::kReduceBlocks ? blocks : glr::kReduceBlocks), 3);
+    hipLaunchKernelGGL(glr::glr_reduce_kernel, g, dim3(1024), 0, s, batch, dim, sums, ddecay, dr_bias, di_bias);
   } else {
     hipLaunchKernelGGL(glr::glr_reduce_parts_kernel, dim3((unsigned)dim, 3), dim3(256), 0, s, batch, dim, parts, sums,
                        ddecay, dr_bias, di_bias);

@@ -457,6 +457,28 @@ def test_offsets_past_32_bits(ss, dev, L):
     assert torch.equal(g["dh0"][:, -5:], g5["dh0"])
 
 
+def test_channels_past_a_grid_of_sums(ss, dev):
+    """Per-channel gradients of more channels than 2^22 workgroups of 32: the last ones are those of a call of their own,
+    the others, whose inputs are zeros, are zeros."""
+    import torch
+    dim = (1 << 27) + 40
+    p = problem(dev, 26, 1, 5, 1, "bf16", "convex", z=False, h0=False)
+    p["i"] = p["i_bias"] = None
+    wide = {k: torch.zeros((1, dim, 1), dtype=p[k].dtype, device=dev) for k in ("x", "r")}
+    vec = {k: torch.zeros(dim, device=dev) for k in ("decay", "r_bias")}
+    dy = torch.zeros_like(wide["x"])
+    for k in wide:
+        wide[k][:, -5:] = p[k]
+    for k in vec:
+        vec[k][-5:] = p[k]
+    dy[:, -5:] = p["r"]
+    g = ss.glr_bwd(dy=dy, **wide, **vec, kind="convex")
+    g5 = ss.glr_bwd(dy=p["r"], **p)
+    torch.cuda.synchronize()
+    for k in ("ddecay", "dr_bias"):
+        assert torch.equal(g[k][-5:], g5[k]) and not g[k][:-5].any(), k
+
+
 def test_outputs_stay_inside_their_rows(ss, dev):
     """Nothing is written behind the last row or before the first, at lengths that end inside a vector."""
     import torch
