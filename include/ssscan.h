@@ -397,8 +397,10 @@ ss_status ss_glr_step(int64_t batch, int64_t dim, ss_dtype io, ss_glr_kind kind,
  * with 2j + 1 under SS_QK_INTERLEAVED.  rot_dim is even, 0 <= rot_dim <= head_dim;
  * inv_freq (rot_dim/2, fp64, radians per token) may be NULL when it is 0.
  * positions (batch, seqlen) int64, NULL for pos0 + t; negative ones rotate
- * backwards.  Angles are formed in fp64 and reduced to a turn before anything is
- * rounded, so a position of 2^40 is as exact as a small one; all else is fp32,
+ * backwards.  Angles are formed in fp64, within 2^-51 of their size, and reduced to a
+ * turn before they are rounded to fp32: up to 2^26 radians that rounding is the
+ * larger, at 2^40 an angle is within 2^-11 radians.  Positions are exact up to 2^53;
+ * a pos0 with which they leave that range is refused.  All else is fp32,
  * each output rounded once.  eps must be a positive normal number.
  *
  * Inputs: value n of head h of token (b, t) of the queries is at

@@ -11,6 +11,7 @@ using namespace ssscan;
 
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxHeads = 1 << 20;
+constexpr int64_t kMaxPosition = int64_t(1) << 53;   // exact in fp64
 
 bool scan_dstate(int n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
 
@@ -92,7 +93,7 @@ bool columns_of_one(int64_t batch, int64_t seqlen, int n, int heads_q, const int
 ss_status check_common(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim, ss_dtype io,
                        uint32_t flags, float eps, const void* q, const int64_t* q_stride, const void* k,
                        const int64_t* k_stride, const float* wq, const float* wk, const double* inv_freq,
-                       const int64_t* positions, int64_t* q_span, int64_t* k_span) {
+                       const int64_t* positions, int64_t pos0, int64_t* q_span, int64_t* k_span) {
   if (io != SS_F32 && io != SS_BF16)
     return record_error(SS_ERR_UNSUPPORTED, "io dtype %d is not SS_F32 or SS_BF16", (int)io);
   if (flags & ~(uint32_t)(SS_QK_INTERLEAVED | SS_QK_FEATURE_MAJOR))
@@ -105,6 +106,8 @@ ss_status check_common(int64_t batch, int64_t seqlen, int heads_q, int heads_k, 
     return record_error(SS_ERR_INVALID_ARG, "rot_dim %d is not even and 0 to head_dim (%d)", rot_dim, head_dim);
   if (!(eps > 0.0f) || !std::isnormal(eps))
     return record_error(SS_ERR_INVALID_ARG, "eps %g is not a positive normal number", (double)eps);
+  if (!positions && (pos0 < -kMaxPosition || pos0 > kMaxPosition - seqlen))
+    return record_error(SS_ERR_INVALID_ARG, "positions from pos0 %lld on are past 2^53", (long long)pos0);
   if (rot_dim > 0 && !inv_freq) return record_error(SS_ERR_INVALID_ARG, "inv_freq is NULL");
   if (!aligned(inv_freq, 8) || !aligned(positions, 8))
     return record_error(SS_ERR_INVALID_ARG, "%s is not 8-byte aligned", aligned(inv_freq, 8) ? "positions" : "inv_freq");
@@ -154,7 +157,7 @@ ss_status ss_qk_norm_rot(int64_t batch, int64_t seqlen, int heads_q, int heads_k
                          const int64_t* positions, int64_t pos0, void* q_out, void* k_out, void* stream) {
   int64_t q_span, k_span;
   ss_status st = check_common(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, q_stride, k,
-                              k_stride, wq, wk, inv_freq, positions, &q_span, &k_span);
+                              k_stride, wq, wk, inv_freq, positions, pos0, &q_span, &k_span);
   if (st != SS_OK) return st;
   const int64_t eb = elem_bytes(io), tokens = batch * seqlen;
   void* out[2] = {q_out, k_out};
@@ -197,7 +200,7 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
                              size_t workspace_bytes, void* stream) {
   int64_t q_span, k_span, dq_span, dk_span;
   ss_status st = check_common(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags, eps, q, q_stride, k,
-                              k_stride, wq, wk, inv_freq, positions, &q_span, &k_span);
+                              k_stride, wq, wk, inv_freq, positions, pos0, &q_span, &k_span);
   if (st != SS_OK) return st;
   if ((st = check_side("dq", dq, dq_stride, batch, seqlen, heads_q, head_dim, io, &dq_span)) != SS_OK) return st;
   if ((st = check_side("dk", dk, dk_stride, batch, seqlen, heads_k, head_dim, io, &dk_span)) != SS_OK) return st;

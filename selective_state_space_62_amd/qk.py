@@ -41,7 +41,7 @@ def _out_shape(d, shape, feature_major):
     return (batch, n)
 
 
-def _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major):
+def _common(q, k, inv_freq, wq, wk, positions, pos0, interleaved, feature_major):
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k are both None")
@@ -62,6 +62,8 @@ def _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major):
     if positions is not None:
         flat = ref.dim() == 2 and positions.dim() == 1
         need((("positions", positions),), torch.int64, (batch,) if flat else (batch, L), dev)
+    if not -1 << 63 <= pos0 < 1 << 63:
+        raise ValueError("pos0 %r is not a 64-bit integer" % (pos0,))
     flags = (_b.SS_QK_INTERLEAVED if interleaved else 0) | (_b.SS_QK_FEATURE_MAJOR if feature_major else 0)
     head = (batch, L, sq[2] if sq else 0, sk[2] if sk else 0, n, rot, io, flags)
     return dev, dtype, (sq, sk), head, (stq, stk)
@@ -77,12 +79,12 @@ def qk_norm_rot(q, k, inv_freq=None, wq=None, wk=None, positions=None, pos0=0, *
     None.  wq, wk: (N,) float32 or None.  inv_freq: (R/2,) float64, radians per token of
     each rotated pair (None: no rotation): value j pairs with j + R/2, or 2j with 2j + 1
     when interleaved; values from R on are normed only.  positions: (batch, L) int64
-    ((batch,) with (batch, N) inputs), or None for pos0 + t.
+    ((batch,) with (batch, N) inputs), or None for pos0 + t (within 2^53).
 
     Returns (q, k) contiguous in the inputs' shapes, or with feature_major (N one of 1, 2,
     4, 8, 16) as (batch, heads, N, L) or (batch, N, L): the scan's C and B.
     """
-    dev, dtype, sides, head, strides = _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major)
+    dev, dtype, sides, head, strides = _common(q, k, inv_freq, wq, wk, positions, pos0, interleaved, feature_major)
     outs = []
     for t, side, given, name in ((q, sides[0], q_out, "q_out"), (k, sides[1], k_out, "k_out")):
         if t is None:
@@ -110,7 +112,7 @@ def qk_norm_rot_bwd(q, k, inv_freq, dq_out, dk_out, wq=None, wk=None, positions=
     of their own (columns of one buffer).  Returns a dict: dq, dk in the inputs' dtype and
     shapes; dwq, dwk (N,) float32 (None where there is no input, or need_dw is False).
     """
-    dev, dtype, sides, head, strides = _common(q, k, inv_freq, wq, wk, positions, interleaved, feature_major)
+    dev, dtype, sides, head, strides = _common(q, k, inv_freq, wq, wk, positions, pos0, interleaved, feature_major)
     grads, gst = [], []
     for t, side, up, given, name in ((q, sides[0], dq_out, dq, "dq"), (k, sides[1], dk_out, dk, "dk")):
         if t is None:

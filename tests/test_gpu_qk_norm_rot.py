@@ -409,3 +409,15 @@ def test_tensor_checks(ss, dev):
     with pytest.raises(ss.SsError):
         shared = torch.empty(2, 4, 1, 64, dtype=torch.bfloat16, device=dev).expand(2, 4, 2, 64)
         ss.qk_norm_rot_bwd(dq_out=dq, dk_out=dk, dq=shared, **p)
+
+
+@pytest.mark.parametrize("pos0", [1 << 64, -(1 << 63) - 1, (1 << 64) + 5])
+def test_pos0_of_more_than_64_bits_is_refused(ss, dev, pos0):
+    p = problem(dev, 18, 1, 4, 1, 1, 16, 16, "f32")
+    p["positions"] = None
+    with pytest.raises(ValueError):
+        ss.qk_norm_rot(**p, pos0=pos0)
+    with pytest.raises(ValueError):
+        ss.qk_norm_rot_bwd(dq_out=p["q"], dk_out=p["k"], **p, pos0=pos0)
+    with pytest.raises(ss.SsError):
+        ss.qk_norm_rot(**p, pos0=1 << 60)

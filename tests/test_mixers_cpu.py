@@ -176,6 +176,16 @@ def test_qk_sizes():
     assert 0 < n < 1 << 30      # bounded, however long the sequence
 
 
+@pytest.mark.parametrize("entry", ["fwd", "bwd"])
+@pytest.mark.parametrize("pos0", [(1 << 53) - 9, (1 << 63) - 1, -(1 << 53) - 1, -(1 << 63)])
+def test_positions_past_fp64(entry, pos0):
+    """pos0 + t of ten tokens beyond 2^53, where fp64 holds no odd position and 64 bits end; given positions are used instead of it."""
+    st, msg = qk(entry, pos=None, pos0=pos0)
+    assert st == INVALID and "pos0" in msg, (st, msg)
+    assert "pos0" not in qk(entry, pos0=pos0, qo=None, dqo=None)[1]
+    assert "pos0" not in qk(entry, pos=None, pos0=(1 << 53) - 10, qo=None, dqo=None)[1]
+
+
 def test_strides_marshal():
     assert b._strides(None) is None
     assert list(b._strides((1, 2, 3))) == [1, 2, 3] and isinstance(b._strides((1, 2, 3)), ctypes.Array)
