@@ -412,6 +412,30 @@ def test_infinite_and_nan_biases_end_with_the_row(ss, dev, kind, L):
     assert float((h[:, other] - y[:, other, -1]).abs().max()) <= 1e-5 * float(y[:, other].abs().max())
 
 
+@pytest.mark.parametrize("rows,L", [(5, 33), (5, 700), (5, 1500), (5, 5003), (5, 70001), (300, 17001)])
+def test_a_nan_goes_one_way(ss, dev, rows, L):
+    """A NaN input spoils the outputs from its token on, a NaN upstream gradient dx up to its token, and neither any other bit,
+    in the kernels for groups of lanes, for one to eight waves and for split rows."""
+    import torch
+    p = problem(dev, 27, 1, rows, L, "bf16", "convex", z=False)
+    y0, _ = run_fwd(ss, p)
+    g0 = ss.glr_bwd(dy=p["i"], **p)
+    for t in (0, 7, L // 2, L - 1):
+        bad = dict(p, x=p["x"].clone())
+        bad["x"][0, 3, t] = float("nan")
+        y, h = run_fwd(ss, bad)
+        assert torch.isnan(y[0, 3, t:]).all() and torch.isnan(h[0, 3])
+        y[0, 3, t:] = y0[0, 3, t:]
+        assert torch.equal(y, y0)
+        dy = p["i"].clone()
+        dy[0, 3, t] = float("nan")
+        g = ss.glr_bwd(dy=dy, **p)
+        torch.cuda.synchronize()
+        assert torch.isnan(g["dx"][0, 3, :t + 1]).all() and torch.isnan(g["dh0"][0, 3])
+        g["dx"][0, 3, :t + 1] = g0["dx"][0, 3, :t + 1]
+        assert torch.equal(g["dx"], g0["dx"])
+
+
 def test_empty_sequence(ss, dev):
     import torch
     p = problem(dev, 14, 2, 3, 0, "bf16", "convex")
