@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import torch
 
+from .binding import _check
 from .torch_ops import _IO, _need
 
 current_device = torch._C._cuda_getDevice
@@ -48,10 +49,12 @@ def workspace(given, nbytes, device):
 
 
 def launch(device, fn, *args):
-    """fn(*args, stream) on torch's current stream of `device`, which is made the current device for it."""
+    """fn(*args, stream), of the library, on torch's current stream of `device`, which is made the current device for it."""
     index = device.index
     if index == current_device():
-        fn(*args, current_stream(index))
+        status = fn(*args, current_stream(index))
     else:
         with torch.cuda.device(device):
-            fn(*args, current_stream(index))
+            status = fn(*args, current_stream(index))
+    if status:
+        _check(status)

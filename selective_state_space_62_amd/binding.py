@@ -275,10 +275,12 @@ def ss_scan_shard_combine(batch, dim, dstate, nshards, A, dsum, h_end, h0, h_in,
 SS_GLR_CONVEX, SS_GLR_NORMALISED = 0, 1
 
 
+@functools.lru_cache(maxsize=256)
 def ss_glr_ckpt_bytes(batch, dim, seqlen) -> int:
     return int(lib.ss_glr_ckpt_bytes(batch, dim, seqlen))
 
 
+@functools.lru_cache(maxsize=256)
 def ss_glr_fwd_workspace_bytes(batch, dim, seqlen) -> int:
     return int(lib.ss_glr_fwd_workspace_bytes(batch, dim, seqlen))
 
@@ -289,6 +291,7 @@ def ss_glr_fwd(batch, dim, seqlen, io, kind, decay_scale, x, r, i, z, decay, r_b
                           ckpt, workspace, workspace_bytes, stream))
 
 
+@functools.lru_cache(maxsize=256)
 def ss_glr_bwd_workspace_bytes(batch, dim, seqlen) -> int:
     return int(lib.ss_glr_bwd_workspace_bytes(batch, dim, seqlen))
 
@@ -325,6 +328,7 @@ def ss_qk_norm_rot(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, flags
                               k, _strides(k_stride), wq, wk, inv_freq, positions, pos0, q_out, k_out, stream))
 
 
+@functools.lru_cache(maxsize=256)
 def ss_qk_norm_rot_bwd_workspace_bytes(batch, seqlen, heads_q, heads_k, head_dim) -> int:
     return int(lib.ss_qk_norm_rot_bwd_workspace_bytes(batch, seqlen, heads_q, heads_k, head_dim))
 

@@ -66,7 +66,7 @@ def _common(q, k, inv_freq, wq, wk, positions, pos0, interleaved, feature_major)
         raise ValueError("pos0 %r is not a 64-bit integer" % (pos0,))
     flags = (_b.SS_QK_INTERLEAVED if interleaved else 0) | (_b.SS_QK_FEATURE_MAJOR if feature_major else 0)
     head = (batch, L, sq[2] if sq else 0, sk[2] if sk else 0, n, rot, io, flags)
-    return dev, dtype, (sq, sk), head, (stq, stk)
+    return dev, dtype, (sq, sk), head, (_b._strides(stq), _b._strides(stk))
 
 
 def qk_norm_rot(q, k, inv_freq=None, wq=None, wk=None, positions=None, pos0=0, *, eps=1e-6, interleaved=False,
@@ -98,8 +98,8 @@ def qk_norm_rot(q, k, inv_freq=None, wq=None, wk=None, positions=None, pos0=0, *
         else:
             need(((name, given),), dtype, shape, dev)
         outs.append(given)
-    launch(dev, _b.ss_qk_norm_rot, *head, eps, ptr(q), strides[0], ptr(k), strides[1], ptr(wq), ptr(wk), ptr(inv_freq),
-           ptr(positions), pos0, ptr(outs[0]), ptr(outs[1]))
+    launch(dev, _b.lib.ss_qk_norm_rot, *head, eps, ptr(q), strides[0], ptr(k), strides[1], ptr(wq), ptr(wk),
+           ptr(inv_freq), ptr(positions), pos0, ptr(outs[0]), ptr(outs[1]))
     return outs[0], outs[1]
 
 
@@ -129,11 +129,11 @@ def qk_norm_rot_bwd(q, k, inv_freq, dq_out, dk_out, wq=None, wk=None, positions=
         elif given.shape != t.shape:
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(given.shape), tuple(t.shape)))
         grads.append(given)
-        gst.append(_shape(given, name, dtype, dev)[1])
+        gst.append(_b._strides(_shape(given, name, dtype, dev)[1]))
     batch, L, hq, hk, n = head[:5]
     dw = [torch.empty(n, dtype=torch.float32, device=dev) if need_dw and t is not None else None for t in (q, k)]
     keep, ws, nbytes = _workspace(workspace, _b.ss_qk_norm_rot_bwd_workspace_bytes(batch, L, hq, hk, n), dev)
-    launch(dev, _b.ss_qk_norm_rot_bwd, *head, eps, ptr(q), strides[0], ptr(k), strides[1], ptr(wq), ptr(wk),
+    launch(dev, _b.lib.ss_qk_norm_rot_bwd, *head, eps, ptr(q), strides[0], ptr(k), strides[1], ptr(wq), ptr(wk),
            ptr(inv_freq), ptr(positions), pos0, ptr(dq_out), ptr(dk_out), ptr(grads[0]), gst[0], ptr(grads[1]), gst[1],
            ptr(dw[0]), ptr(dw[1]), ws, nbytes)
     return dict(dq=grads[0], dk=grads[1], dwq=dw[0], dwk=dw[1])

@@ -59,7 +59,7 @@ def glr_fwd(x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=None,
     if ckpt is not None:
         need((("ckpt", ckpt),), _F32, (glr_ckpt_numel(batch, dim, L),), dev)
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_fwd_workspace_bytes(batch, dim, L), dev)
-    launch(dev, _b.ss_glr_fwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
+    launch(dev, _b.lib.ss_glr_fwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
            ptr(r_bias), ptr(i_bias), ptr(h0), y.data_ptr(), ptr(h_final), ptr(ckpt), ws, nbytes)
     return y, h_final
 
@@ -91,7 +91,7 @@ def glr_bwd(x, r, dy, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=N
                dr_bias=vec(need_dr_bias, dim), di_bias=vec(need_di_bias and i is not None, dim),
                dh0=vec(need_dh0, batch, dim))
     keep, ws, nbytes = _workspace(workspace, _b.ss_glr_bwd_workspace_bytes(batch, dim, L), dev)
-    launch(dev, _b.ss_glr_bwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
+    launch(dev, _b.lib.ss_glr_bwd, batch, dim, L, io, k, decay_scale, x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
            ptr(r_bias), ptr(i_bias), ptr(h0), ptr(dy), ptr(dh_final), ptr(ckpt), ptr(out["dx"]), ptr(out["dr"]),
            ptr(out["di"]), ptr(out["dz"]), ptr(out["ddecay"]), ptr(out["dr_bias"]), ptr(out["di_bias"]), ptr(out["dh0"]),
            ws, nbytes)
@@ -109,7 +109,7 @@ def glr_step(state, x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, 
     need((("state", state), ("state_out", state_out)), _F32, shape, dev)
     if y is None:
         y = torch.empty_like(x)
-    launch(dev, _b.ss_glr_step, batch, dim, io, k, decay_scale, ptr(state),
-           (state if state_out is None else state_out).data_ptr(), x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
+    launch(dev, _b.lib.ss_glr_step, batch, dim, io, k, decay_scale, ptr(state),
+           ptr(state if state_out is None else state_out), x.data_ptr(), ptr(r), ptr(i), ptr(z), ptr(decay),
            ptr(r_bias), ptr(i_bias), y.data_ptr())
     return y
