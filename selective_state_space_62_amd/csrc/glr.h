@@ -43,9 +43,9 @@ struct GlrArgs {
 
 constexpr int64_t glr_tiles(int64_t seqlen) { return (seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens; }
 // Long rows, when there are fewer of them than CUs, are split over workgroups, a tile
-// of kGlrCkptTokens each.  Kernel times of forward / backward from stored states, one
+// of one or more times kGlrCkptTokens each.  Kernel times of forward / backward from stored states, one
 // workgroup to a row -> split, fp32: 16 rows of 256K tokens 151 / 256 -> 33 / 38 us, 96 rows
-// of 300001 187 / 407 -> 117 / 176 us, whole calls of 192 rows of 128K 96 / 208 -> 107 / 187 us, of
+// of 300001 187 / 407 -> 106 / 166 us, whole calls of 192 rows of 128K 96 / 208 -> 107 / 187 us, of
 // 384 rows 175 / 320 -> 180 / 335 us; 64 rows of 5000 tokens 20 / 36 -> 22 / 35 us.
 constexpr bool glr_split(int64_t rows, int64_t seqlen) { return rows < 256 && seqlen > 4 * kGlrCkptTokens; }
 // Tiles joined from one state, and the memory through which the tiles of split rows join.

@@ -151,16 +151,20 @@ __global__ __launch_bounds__(256) void glr_fwd_short_kernel(GlrArgs p, int S) {
   if (act && p.h_final && l == S - 1) p.h_final[row] = fmaf(A, first, B);
 }
 
-// Split rows: a workgroup takes one tile of 2048 tokens.
-template <typename IO, int KIND, bool HI, bool HZ>
+// Split rows: a workgroup takes SEG pieces of 2048 tokens each, whose loads are in flight together.
+// It waits for its ticket, its loads and the tiles before it in turn, so the bytes in flight are the
+// rate: 64 bf16 rows of a million tokens, SEG 1, 2, 3, 4: 149, 109, 101, 95 us; 4 of four million 122, 77,
+// 65, 65; 96 fp32 rows of 300001 120, 110, 107, 106.  Rows of fewer pieces, whose tiles all run at once,
+// wait longer for each: 240 bf16 rows of 31949 tokens 22, 23, 26, 22; 36 of 155719 29, 26, 24, 25 us.
+template <typename IO, int KIND, bool HI, bool HZ, int SEG>
 __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
   using T = typename IO::T;
-  __shared__ float s_tot[4][2];
+  __shared__ float s_tot[SEG * 4][2];
   __shared__ float s_enter;
   __shared__ uint32_t s_tile;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tiles = glr_tiles(p.seqlen);
+  const int64_t pieces = glr_tiles(p.seqlen), tiles = (pieces + SEG - 1) / SEG;
   const int64_t block = block_index();
   if (block >= p.rows * tiles) return;
   const int64_t row = block % p.rows;
@@ -172,36 +176,49 @@ __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
   __syncthreads();
   const int64_t n = __builtin_amdgcn_readfirstlane(s_tile);
   if (n >= tiles) return;   // not without a call that shares the workspace
-  const int64_t base = row * p.seqlen, t = n * kGlrCkptTokens + wave * 64 * kV;
-  FwdTile<IO, KIND, HI, HZ> in;
-  in.load(p, base + t, p.seqlen - t, lane);
-  float a[kV], u[kV], A, B;
-  lane_maps<KIND, HI>(in, c, a, u, A, B);
-  scan_up(A, B);
-  if (lane == 63) {
-    s_tot[wave][0] = A;
-    s_tot[wave][1] = B;
+  const int64_t base = row * p.seqlen, t = n * SEG * kGlrCkptTokens + wave * 64 * kV;
+  FwdTile<IO, KIND, HI, HZ> in[SEG];
+#pragma unroll
+  for (int s = 0; s < SEG; ++s) in[s].load(p, base + t + s * kGlrCkptTokens, p.seqlen - t - s * kGlrCkptTokens, lane);
+  float a[SEG][kV], u[SEG][kV], A[SEG], B[SEG];
+#pragma unroll
+  for (int s = 0; s < SEG; ++s) {
+    lane_maps<KIND, HI>(in[s], c, a[s], u[s], A[s], B[s]);
+    scan_up(A[s], B[s]);
+    if (lane == 63) {
+      s_tot[s * 4 + wave][0] = A[s];
+      s_tot[s * 4 + wave][1] = B[s];
+    }
   }
   __syncthreads();
   if (wave == 0) {
     float At = 1.0f, Bt = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < SEG * 4; ++k) {
       Bt = fmaf(s_tot[k][0], Bt, s_tot[k][1]);
       At *= s_tot[k][0];
     }
     const float h = chain_enter(chain, row, n, tiles, first, At, Bt, lane);
     if (lane == 0) {
       s_enter = h;
-      if (p.ckpt) p.ckpt[row * tiles + n] = h;
       if (p.h_final && n == tiles - 1) p.h_final[row] = fmaf(At, h, Bt);
     }
   }
   __syncthreads();
   float enter = s_enter;
-  for (int k = 0; k < wave; ++k) enter = fmaf(s_tot[k][0], enter, s_tot[k][1]);
-  const float h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
-  if (p.y) replay<IO, HZ>(in, a, u, h, p.seqlen - t, lane, (T*)p.y + (base + t));
+#pragma unroll
+  for (int s = 0; s < SEG; ++s) {
+    if (p.ckpt && threadIdx.x == 0 && n * SEG + s < pieces) p.ckpt[row * pieces + n * SEG + s] = enter;
+    float mine = enter;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k == wave) mine = enter;
+      enter = fmaf(s_tot[s * 4 + k][0], enter, s_tot[s * 4 + k][1]);
+    }
+    const float h = fmaf(shift_up(1.0f, A[s]), mine, shift_up(0.0f, B[s]));
+    const int64_t at = t + s * kGlrCkptTokens;
+    if (p.y) replay<IO, HZ>(in[s], a[s], u[s], h, p.seqlen - at, lane, (T*)p.y + (base + at));
+  }
 }
 
 // One token.  A lane takes two neighbouring channels of two batch rows, so that it forms
@@ -311,12 +328,17 @@ int waves_for(const GlrArgs& a) {
 
 template <typename IO, int KIND, bool HI, bool HZ>
 struct Fwd {
+  template <int SEG>
+  static hipError_t split(const GlrArgs& a, hipStream_t s) {
+    dim3 g;
+    if (!grid_of(a.rows * ((glr_tiles(a.seqlen) + SEG - 1) / SEG), &g)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((glr_fwd_split_kernel<IO, KIND, HI, HZ, SEG>), g, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   static hipError_t go(const GlrArgs& a, hipStream_t s) {
     if (a.chain) {
-      dim3 g;
-      if (!grid_of(a.rows * glr_tiles(a.seqlen), &g)) return hipErrorInvalidValue;
-      hipLaunchKernelGGL((glr_fwd_split_kernel<IO, KIND, HI, HZ>), g, dim3(256), 0, s, a);
-      return hipGetLastError();
+      const int64_t pieces = glr_tiles(a.seqlen);   // figures: the kernel's comment
+      return pieces >= 128 ? split<4>(a, s) : pieces >= 64 ? split<2>(a, s) : split<1>(a, s);
     }
     dim3 g;
     if (a.seqlen <= 32 * kV) {

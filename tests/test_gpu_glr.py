@@ -212,6 +212,24 @@ def test_long_rows(ss, dev, kind, io):
             check(name, f64(got[name]), v, HALF[io] if got[name].dtype == torch.bfloat16 else 0.0)
 
 
+@pytest.mark.parametrize("pieces,extra,kind,io", [(64, 1, "convex", "bf16"), (127, 0, "normalised", "f32"), (128, 9, "normalised", "bf16"),
+                                                  (131, -3, "convex", "f32"), (132, 0, "normalised", "bf16")])
+def test_split_rows_of_several_pieces(ss, dev, pieces, extra, kind, io):
+    """Rows split into tiles of two and four times 2048 tokens, the last tile whole or missing some of its pieces; states stored
+    every 2048 tokens."""
+    import torch
+    L = 2048 * pieces + extra
+    p = problem(dev, 28, 2, 1, L, io, kind)
+    ckpt = torch.full((ss.glr_ckpt_numel(2, 1, L),), float("nan"), device=dev)
+    y, h = run_fwd(ss, p, ckpt=ckpt)
+    g = forward(p, adds(L))
+    check("y", f64(y), g["y"], HALF[io])
+    check("h_final", f64(h), g["h"][..., -1], 0.0)
+    states = ckpt.view(2, 1, -1)
+    assert torch.equal(states[..., 0], p["h0"])
+    check("ckpt", f64(states[..., 1:]), g["h"][..., 2047:L - 1:2048], 0.0)
+
+
 def test_sixteen_waves_to_a_row(ss, dev):
     """bf16 rows of 2^17 tokens, enough of them to have a workgroup each: like the split of the same rows, up to the
     rounding of y (half a step each) and of the states' joining (within 1e-4 of a row's largest, as the bounds above)."""
