@@ -42,12 +42,15 @@ struct GlrArgs {
 };
 
 constexpr int64_t glr_tiles(int64_t seqlen) { return (seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens; }
-// Long rows, when there are fewer of them than CUs, are split over workgroups, a tile
+// Long rows, when there are about as many as CUs or fewer, are split over workgroups, a tile
 // of one or more times kGlrCkptTokens each.  Kernel times of forward / backward from stored states, one
 // workgroup to a row -> split, fp32: 16 rows of 256K tokens 151 / 256 -> 33 / 38 us, 96 rows
-// of 300001 187 / 407 -> 106 / 166 us, whole calls of 192 rows of 128K 96 / 208 -> 107 / 187 us, of
-// 384 rows 175 / 320 -> 180 / 335 us; 64 rows of 5000 tokens 20 / 36 -> 22 / 35 us.
-constexpr bool glr_split(int64_t rows, int64_t seqlen) { return rows < 256 && seqlen > 4 * kGlrCkptTokens; }
+// of 300001 187 / 407 -> 106 / 166 us; 64 rows of 5000 tokens 20 / 36 -> 22 / 35 us.  Past 256 rows some
+// CUs have two: training steps (whole calls) of 297 rows of 116288 tokens 373 -> 321, bf16 239 -> 216, of 40000
+// 134 -> 124, bf16 90 -> 83, of 10000 42 -> 50; of 384 rows of 131072 451 -> 451, bf16 277 -> 297 us.
+constexpr bool glr_split(int64_t rows, int64_t seqlen) {
+  return seqlen > (rows < 256 ? 4 : 16) * kGlrCkptTokens && rows < 320;
+}
 // Tiles joined from one state, and the memory through which the tiles of split rows join.
 constexpr int kGlrGroup = 32;
 constexpr size_t glr_chain_bytes(int64_t rows, int64_t seqlen) {

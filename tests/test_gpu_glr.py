@@ -253,6 +253,33 @@ def test_sixteen_waves_to_a_row(ss, dev):
         assert float((g[name][:9] - g9[name]).abs().max()) <= 1e-4 * float(g9[name].abs().max()) + 1e-2, name
 
 
+@pytest.mark.parametrize("rows,L,kind,io", [(319, 32771, "normalised", "bf16"), (257, 40000, "convex", "f32"), (330, (1 << 17) + 3, "convex", "bf16"),
+                                            (320, 32771, "normalised", "bf16"), (320, 33000, "convex", "f32")])
+def test_about_as_many_long_rows_as_compute_units(ss, dev, rows, L, kind, io):
+    """Rows on both sides of the border between a workgroup to each and the split: like the split of the last nine of them, up to
+    the rounding of y (half a step each) and of the states' joining (within 1e-4 of a row's largest, as the bounds above)."""
+    import torch
+    p = problem(dev, 29, 1, rows, L, io, kind, z=False)
+    ckpt = torch.full((ss.glr_ckpt_numel(1, rows, L),), float("nan"), device=dev)
+    y, h = ss.glr_fwd(**p, ckpt=ckpt)
+    dy = torch.randn_like(p["x"])
+    g = ss.glr_bwd(dy=dy, **p)
+    stored = ss.glr_bwd(dy=dy, ckpt=ckpt, **p)
+    few = {k: v[:, -9:].contiguous() if torch.is_tensor(v) and v.dim() > 1 else v[-9:].contiguous() if torch.is_tensor(v) else v
+           for k, v in p.items()}
+    y9, h9 = ss.glr_fwd(**few)
+    g9 = ss.glr_bwd(dy=dy[:, -9:].contiguous(), **few)
+    torch.cuda.synchronize()
+    for k in ("dx", "dr", "di", "dh0", "ddecay", "dr_bias", "di_bias"):
+        assert torch.equal(g[k], stored[k]), k
+    for name, a, b in [("y", y, y9), ("h", h, h9)] + [(k, g[k], g9[k]) for k in ("dx", "dr", "di", "dh0")]:
+        a, b = a[:, -9:].float(), b.float()
+        top = b.abs().amax(-1, keepdim=True) if b.dim() == 3 else b.abs().max()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-4 * top).all(), name
+    for name in ("ddecay", "dr_bias", "di_bias"):
+        assert float((g[name][-9:] - g9[name]).abs().max()) <= 1e-4 * float(g9[name].abs().max()) + 1e-2, name
+
+
 def test_zero_decays_join_across_tiles(ss, dev):
     """Floors of 0 and closed gates make maps of all zeros, which still are maps."""
     import torch
