@@ -598,6 +598,37 @@ def test_repeats_and_graph_replays_are_bitwise_equal(ss, dev):
             assert all(torch.equal(again[n], want[n]) for n in want)
 
 
+@pytest.mark.parametrize("rows,L", [(3, 2048 * 70 + 1), (2, 2048 * 130 + 5), (300, 33000)])
+def test_split_rows_in_a_graph(ss, dev, rows, L):
+    """Tiles of two and four pieces, and more rows than compute units: replays between eager calls, each as the first."""
+    import torch
+    p = problem(dev, 30, 1, rows, L, "bf16", "convex")
+    dy = torch.randn_like(p["x"])
+
+    def both():
+        y, h = ss.glr_fwd(**p)
+        return dict(ss.glr_bwd(dy=dy, **p), y=y, h=h)
+
+    want = {k: v.clone() for k, v in both().items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for k in range(3):
+        for v in got.values():
+            v.zero_()
+        graph.replay()
+        eager = both()
+        torch.cuda.synchronize()
+        for name in want:
+            assert torch.equal(got[name], want[name]) and torch.equal(eager[name], want[name]), (name, k)
+
+
 def test_two_streams_at_once(ss, dev):
     import torch
     a, b = problem(dev, 17, 1, 40, 5000, "bf16", "convex"), problem(dev, 18, 1, 40, 5000, "bf16", "convex")
