@@ -135,9 +135,10 @@ __device__ __forceinline__ float sigmoid_e(float v, float nb, float& e) {
 }
 
 // The same with e held to 2^126, for a gate whose 1 - s is wanted too: e s.  It is
-// never below 2^-126, so a gate of -inf passes that much instead of nothing.
+// never below 2^-126, so a gate of -inf passes that much instead of nothing.  The
+// minimum of a NaN is a NaN (one v_minimum3; fminf's would be 126, and the gate a number).
 __device__ __forceinline__ float sigmoid_both(float v, float nb, float& minus) {
-  const float e = __builtin_amdgcn_exp2f(fminf(fmaf(v, -kLog2e, nb), 126.0f));
+  const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(fmaf(v, -kLog2e, nb), 126.0f));
   const float s = __builtin_amdgcn_rcpf(1.0f + e);
   minus = e * s;
   return s;

@@ -675,3 +675,54 @@ def test_tensor_checks(ss, dev):
         ss.glr_fwd(**{k: v.cpu() if hasattr(v, "cpu") else v for k, v in p.items()})
     with pytest.raises(ValueError):
         ss.glr_bwd(dy=p["x"], workspace=torch.empty(8, dtype=torch.uint8, device=dev), **p)
+
+
+# where a NaN in one operand of token t (or of the channel) goes: the tokens of each result from, up to and at t, or all of them; a
+# result that is not named stays as it was
+NAN_GOES = {
+    "x": dict(y="from", h="all", dr="from", di="at", dz="from", ddecay="all", dr_bias="all", di_bias="all"),
+    "r": dict(y="from", h="all", dx="upto", dr="all", di="upto", dz="from", ddecay="all", dr_bias="all", di_bias="all", dh0="all"),
+    "i": dict(y="from", h="all", dx="at", dr="from", di="at", dz="from", ddecay="all", dr_bias="all", di_bias="all"),
+    "z": dict(y="at", dx="upto", dr="upto", di="upto", dz="at", ddecay="all", dr_bias="all", di_bias="all", dh0="all"),
+    "h0": dict(y="all", h="all", dr="all", dz="all", ddecay="all", dr_bias="all"),
+    "i_bias": dict(y="all", h="all", dx="all", dr="all", di="all", dz="all", ddecay="all", dr_bias="all", di_bias="all"),
+    "r_bias": {k: "all" for k in ("y", "h", "dx", "dr", "di", "dz", "ddecay", "dr_bias", "di_bias", "dh0")},
+    "decay": {k: "all" for k in ("y", "h", "dx", "dr", "di", "dz", "ddecay", "dr_bias", "di_bias", "dh0")},
+}
+
+
+@pytest.mark.parametrize("rows,L,kind,io", [(5, 33, "convex", "bf16"), (5, 37, "normalised", "f32"), (5, 700, "normalised", "bf16"), (5, 1500, "convex", "f32"),
+                                            (5, 5003, "normalised", "f32"), (5, 5003, "convex", "bf16"), (300, 17001, "normalised", "bf16"), (5, 2048 * 5 + 9, "convex", "f32"),
+                                            (4, 2048 * 70 + 1, "normalised", "bf16"), (4, 2048 * 131 + 5, "convex", "bf16"), (321, (1 << 17) + 3, "normalised", "bf16")])
+def test_where_a_nan_goes(ss, dev, rows, L, kind, io):
+    """A NaN in any operand reaches exactly the results that the formulas carry it to, in every plan: groups of lanes, one to
+    sixteen waves to a row, split rows in tiles of one, two and four pieces."""
+    import torch
+    p = problem(dev, 31, 1, rows, L, io, kind)
+    dy = p["i"]
+
+    def both(p):
+        ckpt = torch.empty(ss.glr_ckpt_numel(1, rows, L), device=dev)
+        y, h = ss.glr_fwd(**p, ckpt=ckpt)
+        out = dict(ss.glr_bwd(dy=dy, **p), y=y, h=h)
+        stored = ss.glr_bwd(dy=dy, ckpt=ckpt, **p)
+        return out, dict(stored, y=y, h=h)
+
+    clean = both(p)[0]
+    for name, goes in NAN_GOES.items():
+        for t in (0, L // 2 + 1, L - 1) if p[name].dim() == 3 and rows * L < 1 << 20 else (L - 2,):
+            bad = dict(p, **{name: p[name].clone()})
+            if bad[name].dim() == 3:
+                bad[name][0, 3, t] = float("nan")
+            else:
+                bad[name].view(-1)[3] = float("nan")
+            for got in both(bad):
+                torch.cuda.synchronize()
+                for k, v in got.items():
+                    part = {"all": slice(None), "from": slice(t, None), "upto": slice(0, t + 1), "at": slice(t, t + 1), None: slice(0, 0)}[goes.get(k)]
+                    at = (0, 3, part) if v.dim() == 3 else ((0, 3) if v.dim() == 2 else (3,))
+                    if goes.get(k):
+                        assert torch.isnan(v[at]).all(), (name, t, k)
+                        v = v.clone()
+                        v[at] = clean[k][at]
+                    assert torch.equal(v, clean[k]), (name, t, k)
