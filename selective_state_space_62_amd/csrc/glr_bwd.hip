@@ -84,7 +84,7 @@ struct BwdTile {
         p2[j] = oms;
         p3[j] = c.c1 * s;
       } else {
-        p1[j] = a[j] * a[j] * (k * ix);
+        p1[j] = a[j] * a[j] * k * ix;   // from the left: a 0 takes k, at rates of 2^126 too, before x could overflow it
         p2[j] = a[j] * ls;
         p3[j] = oms;
       }

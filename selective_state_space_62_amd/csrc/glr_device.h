@@ -115,7 +115,10 @@ __device__ __forceinline__ RowConst make_const(float r_bias, float i_bias, float
     c.c0 = decay;
     c.c1 = 1.0f - decay;
   } else {
-    const float l = decay_scale * softplus_dt(decay, 0.0f);
+    // an infinite rate is held to 2^126 (a NaN stays one): a closed gate's 0 times it is 0, so
+    // that padding and the tokens past the end keep the state, and an open gate still
+    // forgets it all
+    const float l = __builtin_elementwise_minimum(decay_scale * softplus_dt(decay, 0.0f), 0x1p126f);
     c.c0 = -kLog2e * l;
     c.c1 = 2.0f * l;
   }

@@ -726,3 +726,49 @@ def test_where_a_nan_goes(ss, dev, rows, L, kind, io):
                         v = v.clone()
                         v[at] = clean[k][at]
                     assert torch.equal(v, clean[k]), (name, t, k)
+
+
+@pytest.mark.parametrize("L", [1, 5, 300, 700, 2100, 9000, 16391, 2048 * 70 + 1])
+def test_infinite_rates_end_with_the_row(ss, dev, L):
+    """A normalised channel whose rate is infinite (a decay of +inf, or one whose product with the scale overflows) forgets at every
+    token and keeps the state at padding; one whose rate is zero (-inf) keeps it throughout.  Against the formulas in 64 bits,
+    however the row's end falls into a vector, and the single token like the sequence."""
+    import torch
+    p = problem(dev, 32, 2, 4, L, "f32", "normalised", z=False)
+    p["decay"] = torch.tensor([float("inf"), 1e38, float("-inf"), -3.0], device=dev)
+    p["r"][:, :, 2::3] = float("-inf")           # padding
+    if L > 4:
+        p["r"][1, :, L - 2:] = float("-inf")
+    state = p["h0"].clone()
+    y, h = run_fwd(ss, p)
+    dy = torch.randn(y.shape, generator=torch.Generator().manual_seed(6)).to(dev)
+    dh = torch.ones(2, 4, device=dev)
+    ckpt = torch.empty(ss.glr_ckpt_numel(2, 4, L), device=dev)
+    ss.glr_fwd(**p, ckpt=ckpt)
+    grads = [ss.glr_bwd(dy=dy, dh_final=dh, ckpt=c, **p) for c in (None, ckpt)]
+    torch.cuda.synchronize()
+    open_ = np.isfinite(f64(p["r"][:, :3]))
+    a = np.where(np.arange(3)[:, None] < 2, 1.0 - open_, 1.0)          # exactly 0 or 1, and m is the other
+    gm = lambda v: v * V(1.0 - a)  # noqa: E731
+    iota = sigmoid(V(f64(p["i"][:, :3])) + V(f64(p["i_bias"][:3, None])))
+    ix = V(f64(p["x"][:, :3])) * iota
+    hh, _ = recur(V(a), gm(ix), V(f64(p["h0"][:, :3])), adds(L))
+    check("y", f64(y[:, :3]), hh, 2.0 ** -24)
+    assert torch.equal(h[:, :3], y[:, :3, -1]) and torch.isfinite(h).all() and torch.isfinite(y).all()
+    G, after = recur(V(a[..., ::-1]), (V(a) * V(f64(dy[:, :3])))[..., ::-1], V(np.ones((2, 3))), adds(L))
+    g = V(f64(dy[:, :3])) + after[..., ::-1]
+    for got in grads:
+        check("dx", f64(got["dx"][:, :3]), gm(g) * iota, 2.0 ** -24)
+        check("di", f64(got["di"][:, :3]), gm(g) * ix * (V(1.0) - iota), 2.0 ** -24)
+        check("dh0", f64(got["dh0"][:, :3]), G[..., -1], 2.0 ** -24)
+        for k in ("dr", "ddecay", "dr_bias"):    # the decay is flat there
+            v = got[k][:, :3] if got[k].dim() == 3 else got[k][:3]
+            assert not v.any(), k
+        assert all(torch.isfinite(v).all() for v in got.values() if v is not None)
+    if L <= 5:
+        for t in range(L):
+            yt = ss.glr_step(state, *(p[k][..., t].contiguous() for k in ("x", "r", "i")), decay=p["decay"], r_bias=p["r_bias"],
+                             i_bias=p["i_bias"])
+            check("step", f64(yt[:, :3]), hh[..., t], 2.0 ** -24)
+        torch.cuda.synchronize()
+        assert torch.isfinite(state).all()
