@@ -417,10 +417,11 @@ ss_status ss_glr_step(int64_t batch, int64_t dim, ss_dtype io, ss_glr_kind kind,
  *
  * The backward takes the forward's inputs and the gradients dq_out, dk_out of
  * its outputs in their layout, and writes dq, dk (batch, seqlen, heads, head_dim)
- * under strides of their own, which may be interleaved columns of one buffer's
- * rows (no two values may share an address), and, where not NULL, dwq and dwk
- * (head_dim, fp32), the gradients of the weights (also of weights that are NULL),
- * summed in a fixed order.  Its workspace (ss_qk_norm_rot_bwd_workspace_bytes,
+ * under strides of their own (no two values may share an address), and, where not
+ * NULL, dwq and dwk (head_dim, fp32), the gradients of the weights (also of weights
+ * that are NULL), summed in a fixed order.  dq and dk may be columns of one buffer's
+ * rows under the same batch and token strides: all heads of one behind those of the
+ * other, or head by head under one head stride (q, k and v of a head, then the next).  Its workspace (ss_qk_norm_rot_bwd_workspace_bytes,
  * 256-byte aligned) holds their partial sums. */
 typedef enum { SS_QK_INTERLEAVED = 1u, SS_QK_FEATURE_MAJOR = 2u } ss_qk_flags;
 

@@ -1,5 +1,6 @@
 // C ABI of the norm and rotation of queries and keys: argument checks and launches.  See include/ssscan.h.
 #include <cmath>
+#include <utility>
 
 #include "api_checks.h"
 #include "internal.h"
@@ -57,20 +58,18 @@ ss_status check_side(const char* name, const void* p, const int64_t* st, int64_t
   return SS_OK;
 }
 
-// Whether no two values share an address under these strides.
-bool distinct(int64_t batch, int64_t seqlen, int heads, int n, const int64_t* st) {
-  int64_t size[3] = {batch, seqlen, heads}, stride[3] = {st[0], st[1], st[2]};
-  for (int i = 0; i < 3; ++i)       // by stride, ascending
-    for (int j = i + 1; j < 3; ++j)
+// Whether runs of n values, one for each index of D dimensions, are disjoint: by stride,
+// ascending, each dimension has to step over all that the ones before it reach.
+template <int D>
+bool distinct(int64_t n, int64_t (&size)[D], int64_t (&stride)[D]) {
+  for (int i = 0; i < D; ++i)
+    for (int j = i + 1; j < D; ++j)
       if (stride[j] < stride[i]) {
-        const int64_t s = stride[i], z = size[i];
-        stride[i] = stride[j];
-        size[i] = size[j];
-        stride[j] = s;
-        size[j] = z;
+        std::swap(stride[i], stride[j]);
+        std::swap(size[i], size[j]);
       }
   int64_t reach = n;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < D; ++i) {
     if (size[i] <= 1) continue;
     if (stride[i] < reach) return false;
     reach += stride[i] * (size[i] - 1);
@@ -78,16 +77,22 @@ bool distinct(int64_t batch, int64_t seqlen, int heads, int n, const int64_t* st
   return true;
 }
 
-// Whether two strided gradients are columns of the same rows: the same batch and
-// token strides, each token's values of both within one token's stride, no column shared.
+// Whether two strided gradients, each without shared addresses and dk's first value `apart` after
+// dq's, share none: with the same batch and token strides, either all heads of the one lie behind
+// those of the other in each token's columns, or their heads alternate under one head stride.
 bool columns_of_one(int64_t batch, int64_t seqlen, int n, int heads_q, const int64_t* sq, int heads_k,
                     const int64_t* sk, int64_t apart) {
+  if ((batch > 1 && sq[0] != sk[0]) || (seqlen > 1 && sq[1] != sk[1])) return false;
   const int64_t eq = (heads_q - 1) * sq[2] + n, ek = (heads_k - 1) * sk[2] + n;
-  if (apart >= 0 ? apart < eq : -apart < ek) return false;
-  const int64_t lo = apart < 0 ? apart : 0, hi = apart + ek > eq ? apart + ek : eq;
-  if (seqlen > 1 && (sq[1] != sk[1] || hi - lo > sq[1])) return false;
-  const int64_t row = seqlen > 1 ? (seqlen - 1) * sq[1] + (hi - lo) : hi - lo;
-  return batch == 1 || (sq[0] == sk[0] && row <= sq[0]);
+  if (apart >= 0 ? apart >= eq : -apart >= ek) {
+    const int64_t lo = apart < 0 ? apart : 0, hi = apart + ek > eq ? apart + ek : eq;
+    int64_t size[] = {batch, seqlen}, stride[] = {sq[0], sq[1]};
+    if (distinct(hi - lo, size, stride)) return true;
+  }
+  if (heads_q > 1 && heads_k > 1 && sq[2] != sk[2]) return false;
+  int64_t size[] = {batch, seqlen, heads_q > heads_k ? heads_q : heads_k, 2};
+  int64_t stride[] = {sq[0], sq[1], heads_q > 1 ? sq[2] : sk[2], apart < 0 ? -apart : apart};
+  return distinct(n, size, stride);
 }
 
 ss_status check_common(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim, ss_dtype io,
@@ -218,8 +223,11 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
     if (heads[i] == 0 && dw[i])
       return record_error(SS_ERR_INVALID_ARG, "%s is given with 0 heads", i ? "dwk" : "dwq");
     if (!aligned(dw[i], 4)) return record_error(SS_ERR_INVALID_ARG, "%s is not 4-byte aligned", i ? "dwk" : "dwq");
-    if (heads[i] && !distinct(batch, seqlen, heads[i], head_dim, dst[i]))
-      return record_error(SS_ERR_INVALID_ARG, "values of %s share addresses under its strides", i ? "dk" : "dq");
+    if (heads[i]) {
+      int64_t size[] = {batch, seqlen, heads[i]}, stride[] = {dst[i][0], dst[i][1], dst[i][2]};
+      if (!distinct(head_dim, size, stride))
+        return record_error(SS_ERR_INVALID_ARG, "values of %s share addresses under its strides", i ? "dk" : "dq");
+    }
   }
   const size_t need = ss_qk_norm_rot_bwd_workspace_bytes(batch, seqlen, heads_q, heads_k, head_dim);
   if (need > 0) {

@@ -109,7 +109,7 @@ def qk_norm_rot_bwd(q, k, inv_freq, dq_out, dk_out, wq=None, wk=None, positions=
     outputs, contiguous), given the forward's inputs.
 
     dq, dk: optional tensors shaped like q and k that receive the gradients, under strides
-    of their own (columns of one buffer).  Returns a dict: dq, dk in the inputs' dtype and
+    of their own (columns of one buffer, side by side or head by head).  Returns a dict: dq, dk in the inputs' dtype and
     shapes; dwq, dwk (N,) float32 (None where there is no input, or need_dw is False).
     """
     dev, dtype, sides, head, strides = _common(q, k, inv_freq, wq, wk, positions, pos0, interleaved, feature_major)

@@ -421,3 +421,31 @@ def test_pos0_of_more_than_64_bits_is_refused(ss, dev, pos0):
         ss.qk_norm_rot_bwd(dq_out=p["q"], dk_out=p["k"], **p, pos0=pos0)
     with pytest.raises(ss.SsError):
         ss.qk_norm_rot(**p, pos0=1 << 60)
+
+
+@pytest.mark.parametrize("fm,N,order", [(False, 40, "b t h s"), (True, 16, "b t h s"), (False, 64, "t b h s"), (False, 33, "b h s t")])
+def test_gradient_between_the_heads_of_one_buffer(ss, dev, fm, N, order):
+    """q, k and v of a head side by side, head after head, batch row or token first: inputs and gradients there are those of
+    contiguous ones, and what lies at v is left alone."""
+    import torch
+    size = dict(b=2, t=37, h=3, s=3)
+    axes = order.split()
+    gen = torch.Generator().manual_seed(19)
+
+    def halves(t):
+        t = t.permute(*(axes.index(a) for a in "bths"), 4)
+        return t[..., 0, :], t[..., 1, :], t[..., 2, :]
+
+    buf = torch.randn([size[a] for a in axes] + [N], generator=gen).to(torch.bfloat16).to(dev)
+    grad = torch.full_like(buf, 7.0)
+    q, k, _ = halves(buf)
+    gq, gk, gv = halves(grad)
+    freq = torch.linspace(0.5, 0.01, N // 4, dtype=torch.float64, device=dev)
+    dq, dk = grads_like(dev, 20, dict(q=q, k=k), fm)
+    want = ss.qk_norm_rot_bwd(q.contiguous(), k.contiguous(), freq, dq, dk, feature_major=fm)
+    got = ss.qk_norm_rot_bwd(q, k, freq, dq, dk, feature_major=fm, dq=gq, dk=gk)
+    out, ref = ss.qk_norm_rot(q, k, freq, feature_major=fm), ss.qk_norm_rot(q.contiguous(), k.contiguous(), freq, feature_major=fm)
+    torch.cuda.synchronize()
+    assert torch.equal(gq, want["dq"]) and torch.equal(gk, want["dk"]) and (gv == 7).all()
+    assert torch.equal(got["dwq"], want["dwq"]) and torch.equal(got["dwk"], want["dwk"])
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])

@@ -189,3 +189,53 @@ def test_positions_past_fp64(entry, pos0):
 def test_strides_marshal():
     assert b._strides(None) is None
     assert list(b._strides((1, 2, 3))) == [1, 2, 3] and isinstance(b._strides((1, 2, 3)), ctypes.Array)
+
+
+# dq and dk in one buffer without a shared address: (dq's strides, dk's strides, dk's elements after dq), 2 heads and 1 unless given
+INTERLEAVED = [
+    (dict(hq=4, hk=4), (1920, 192, 48), (1920, 192, 48), 16),        # (batch, token, head, [q k v]): heads alternate
+    (dict(hq=4, hk=4), (1920, 192, 48), (1920, 192, 48), -16),       # [k q v]
+    (dict(hq=4, hk=4), (1280, 128, 32), (1280, 128, 32), 16),        # [q k], nothing between
+    (dict(hq=4, hk=1), (800, 80, 16), (800, 80, 16), -16),           # the key's columns first, the last head's end the row's
+    (dict(hq=1, hk=3), (960, 96, 16), (960, 96, 32), 16),            # one query before three keys 32 apart
+    ({}, (48, 96, 16), (48, 96, 16), 32),                            # (token, batch, columns)
+    (dict(hq=4, hk=4), (192, 384, 48), (192, 384, 48), 16),          # (token, batch, head, [q k v])
+    (dict(hq=3, hk=3), (1280, 16, 320), (1280, 16, 320), 160),       # (batch, head, [q k], token)
+    (dict(seqlen=1), (48, 0, 16), (48, 0, 16), 32),
+    (dict(batch=1, hq=2, hk=2), (0, 64, 32), (7, 64, 32), 16),       # a batch of one has no stride
+]
+
+
+@pytest.mark.parametrize("sizes,dqs,dks,apart", INTERLEAVED)
+def test_interleaved_gradients_pass_the_overlap_check(sizes, dqs, dks, apart):
+    """Only dwk is refused, which lies on the workspace and is looked at after dq and dk; and by counting, no two values share an
+    address."""
+    st, msg = qk("bwd", dq=at(9, 1024), dk=at(9, 1024 + 2 * apart), dqs=dqs, dks=dks, dwk=at(13), **sizes)
+    assert st == INVALID and "dwk overlaps workspace" in msg, (st, msg)
+    assert _shared(dict(dict(batch=2, seqlen=10, hq=2, hk=1), **sizes), dqs, dks, apart) == 0
+
+
+def _shared(sizes, dqs, dks, apart):
+    import numpy as np
+    seen = []
+    for heads, s, off in ((sizes["hq"], dqs, 0), (sizes["hk"], dks, apart)):
+        b, t, h, j = np.ogrid[:sizes["batch"], :sizes["seqlen"], :heads, :16]
+        seen.append((off + b * s[0] + t * s[1] + h * s[2] + j).ravel())
+    seen = np.concatenate(seen)
+    return seen.size - np.unique(seen).size
+
+
+@pytest.mark.parametrize("sizes,dqs,dks,apart", [
+    (dict(hq=4, hk=4), (1920, 192, 48), (1920, 192, 48), 8),         # half a vector shared
+    (dict(hq=4, hk=4), (1920, 192, 48), (1920, 192, 48), 40),        # into the next head
+    (dict(hq=4, hk=4), (1920, 192, 48), (1920, 192, 48), 48),        # the next head itself
+    (dict(hq=4, hk=4), (1920, 192, 48), (1920, 192, 48), 176 + 8),   # into the next token
+    (dict(hq=4, hk=4), (192, 384, 48), (192, 384, 48), 192),         # the other batch row
+    (dict(hq=1, hk=3), (960, 96, 16), (960, 96, 32), 32 + 8),
+    (dict(hq=3, hk=3), (1280, 16, 320), (1280, 16, 320), 144),
+    (dict(seqlen=1), (48, 0, 16), (48, 0, 16), 24),
+])
+def test_shared_gradients_are_refused(sizes, dqs, dks, apart):
+    assert _shared(dict(dict(batch=2, seqlen=10, hq=2, hk=1), **sizes), dqs, dks, apart) > 0
+    st, msg = qk("bwd", dq=at(9, 1024), dk=at(9, 1024 + 2 * apart), dqs=dqs, dks=dks, **sizes)
+    assert st == INVALID and "overlaps dk" in msg, (st, msg)
