@@ -357,7 +357,7 @@ ss_status ss_scan_bwd_seg(int64_t batch, int64_t dim, int dstate, int64_t seqlen
  *    recomputed.  The workspace (ss_glr_bwd_workspace_bytes) is as above; its size
  *    does not depend on ckpt.
  *  ss_glr_step: one token.  state_out may be state_in itself (updated in place).
- *    dim above 2^31 returns SS_ERR_UNSUPPORTED.
+ *    dim above 2^31 - 128 returns SS_ERR_UNSUPPORTED.
  *
  * Each size query returns 0 for invalid sizes. */
 typedef enum { SS_GLR_CONVEX = 0, SS_GLR_NORMALISED = 1 } ss_glr_kind;

@@ -269,7 +269,8 @@ ss_status ss_glr_step(int64_t batch, int64_t dim, ss_dtype io, ss_glr_kind kind,
                       void* stream) {
   ss_status st = check_glr(batch, dim, 1, io, kind, decay_scale, i, decay, i_bias);
   if (st != SS_OK) return st;
-  if (dim > (int64_t(1) << 31)) return record_error(SS_ERR_UNSUPPORTED, "dim %lld exceeds 2^31", (long long)dim);
+  if (dim > kGlrStepDim)
+    return record_error(SS_ERR_UNSUPPORTED, "dim %lld exceeds %lld", (long long)dim, (long long)kGlrStepDim);
   const Named req[] = {{"state_in", state_in}, {"state_out", state_out}, {"x", x}, {"r", r}, {"y", y}};
   for (const Named& n : req)
     if (!n.p) return record_error(SS_ERR_INVALID_ARG, "%s is NULL", n.name);

@@ -60,6 +60,9 @@ constexpr size_t glr_chain_bytes(int64_t rows, int64_t seqlen) {
 
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t s);
+// The single token's most channels: its workgroups take 128 each, and a grid dimension holds fewer than 2^32
+// threads, 256 to a workgroup.
+constexpr int64_t kGlrStepDim = ((int64_t(1) << 24) - 1) * 128;
 hipError_t launch_glr_step(const GlrArgs& a, hipStream_t s);
 // out[d] = sum over batch rows and parts of sums[b, d, part] in a fixed order; null outputs are skipped
 hipError_t launch_glr_reduce(int64_t batch, int64_t dim, int64_t parts, const float* sums, float* ddecay,

@@ -227,6 +227,7 @@ __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
 // four rows 6.7, four channels of two rows 7.4; a loop over rows, which held the loads back behind the
 // constants, 10.7); 4096 x 5120: 68 us, 5.5 TB/s (one channel of four rows 76, four of one row 70).
 constexpr int kStepC = 2, kStepB = 2;
+static_assert(kGlrStepDim == ((int64_t(1) << 24) - 1) * 64 * kStepC, "64 lanes side by side");
 
 template <typename T>
 struct __attribute__((packed, aligned(sizeof(T)))) Few {
@@ -368,7 +369,7 @@ struct Step {
     const int64_t batch = a.rows / a.dim, x = (a.dim + 64 * kStepC - 1) / (64 * kStepC);
     const int64_t groups = (batch + 4 * kStepB - 1) / (4 * kStepB);
     const int64_t y = groups < 65535 ? groups : 65535, z = (groups + y - 1) / y;
-    if (x >= (int64_t(1) << 24) || z > 65535) return hipErrorInvalidValue;   // a grid dimension has 2^32 threads at most
+    if (a.dim > kGlrStepDim || z > 65535) return hipErrorInvalidValue;
     hipLaunchKernelGGL((glr_step_kernel<IO, KIND, HI, HZ>), dim3((unsigned)x, (unsigned)y, (unsigned)z), dim3(256), 0, s,
                        a, batch);
     return hipGetLastError();

@@ -239,3 +239,12 @@ def test_shared_gradients_are_refused(sizes, dqs, dks, apart):
     assert _shared(dict(dict(batch=2, seqlen=10, hq=2, hk=1), **sizes), dqs, dks, apart) > 0
     st, msg = qk("bwd", dq=at(9, 1024), dk=at(9, 1024 + 2 * apart), dqs=dqs, dks=dks, **sizes)
     assert st == INVALID and "overlaps dk" in msg, (st, msg)
+
+
+@pytest.mark.parametrize("dim", [(1 << 31) - 127, 1 << 31])
+def test_glr_step_refuses_more_channels_than_a_grid(dim):
+    """A workgroup takes 128 channels and a grid dimension has fewer than 2^32 threads, so fewer than 2^24 of its workgroups."""
+    st, msg = glr("step", batch=1, dim=dim)
+    assert st == UNSUPPORTED and "dim" in msg, (st, msg)
+    st, msg = glr("step", batch=1, dim=(1 << 31) - 128, y=None)
+    assert st == INVALID and "y is NULL" in msg, (st, msg)
