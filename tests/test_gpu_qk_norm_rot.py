@@ -449,3 +449,27 @@ def test_gradient_between_the_heads_of_one_buffer(ss, dev, fm, N, order):
     assert torch.equal(gq, want["dq"]) and torch.equal(gk, want["dk"]) and (gv == 7).all()
     assert torch.equal(got["dwq"], want["dwq"]) and torch.equal(got["dwk"], want["dwk"])
     assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
+@pytest.mark.parametrize("B,L,hq,hk,N,rot,fm", [(3, 20011, 1, 1, 16, 16, True), (1, 70001, 2, 1, 8, 4, True), (2, 333, 1, 2, 2, 2, True), (5, 1, 1, 1, 16, 16, True),
+                                                (2, 4099, 8, 2, 64, 64, False), (1, 20011, 1, 1, 16, 16, False), (4, 2047, 20, 5, 80, 32, False), (3, 5003, 3, 1, 256, 128, False),
+                                                (1, 9001, 2, 1, 33, 10, False), (7, 1, 4, 4, 40, 40, False)])
+@pytest.mark.parametrize("io,interleaved", [("f32", False), ("bf16", True)])
+def test_every_vector_counts_in_the_weights_gradient(ss, dev, B, L, hq, hk, N, rot, fm, io, interleaved):
+    """Values of +-1 under an eps of 3 make every norm 2, positions of 0 turn nothing, and the gradients are odd whole numbers: each
+    term of dw is +-1/2 or +-3/2, and each partial sum exact in fp32 (below 2^23).  So a single vector lost or doubled shows."""
+    import torch
+    gen = torch.Generator().manual_seed(N + L)
+    dt = torch.float32 if io == "f32" else torch.bfloat16
+    freq = torch.linspace(1.0, 0.1, rot // 2, dtype=torch.float64, device=dev)
+    pos = torch.zeros(B, L, dtype=torch.int64, device=dev)
+    w = torch.randn(N, generator=gen).to(dev)
+    v = {s: (2 * torch.randint(0, 2, (B, L, h, N), generator=gen) - 1) for s, h in (("q", hq), ("k", hk))}
+    d = {s: (2 * torch.randint(-2, 2, (B, L, h, N), generator=gen) + 1) for s, h in (("q", hq), ("k", hk))}
+    up = {s: (t.permute(0, 2, 3, 1) if fm else t).to(dt).to(dev).contiguous() for s, t in d.items()}
+    got = ss.qk_norm_rot_bwd(v["q"].to(dt).to(dev), v["k"].to(dt).to(dev), freq, up["q"], up["k"], wq=w, positions=pos, eps=3.0,
+                             interleaved=interleaved, feature_major=fm)
+    torch.cuda.synchronize()
+    for s in "qk":
+        assert 1.5 * B * L * max(hq, hk) < 1 << 23
+        assert torch.equal(got["dw" + s].cpu().double() * 2, (v[s] * d[s]).sum((0, 1, 2)).double()), s
