@@ -772,3 +772,53 @@ def test_infinite_rates_end_with_the_row(ss, dev, L):
             check("step", f64(yt[:, :3]), hh[..., t], 2.0 ** -24)
         torch.cuda.synchronize()
         assert torch.isfinite(state).all()
+
+
+# Sums over tokens and batch rows of which every term counts: the gates are 0 (r = -inf) at even tokens and 1/2 (r = 0) at odd ones,
+# the floor 0, the input gate 1/2, and x and dy small odd and even whole numbers, so that each term of the three sums is a multiple
+# of 1/16 that is not zero (dr is, where the gate is 0), and each partial sum is exact in fp32: below 2^24 / 16 in size.  A single
+# term lost, doubled or taken from another channel changes the result.
+def counted(dev, batch, dim, L, io):
+    import torch
+    gen = torch.Generator().manual_seed(batch + L)
+    dt = torch.float32 if io == "f32" else torch.bfloat16
+    even = torch.arange(L) % 2 == 0
+
+    def whole(odd):    # odd numbers from -3 to 3, or even ones from -4 to 4
+        return torch.where(odd, 2 * torch.randint(-2, 2, (batch, dim, L), generator=gen) + 1, 4 * torch.randint(-1, 1, (batch, dim, L), generator=gen) + 2)
+
+    x, dy = whole(even), whole(torch.ones(L, dtype=torch.bool))
+    r = torch.where(even, -torch.inf, 0.0).expand(batch, dim, L)
+    as_io = lambda t: t.to(dt).to(dev).contiguous()  # noqa: E731
+    p = dict(x=as_io(x), r=as_io(r), i=torch.zeros(batch, dim, L, dtype=dt, device=dev), kind="convex", decay=torch.zeros(dim, device=dev))
+    # in 64 bits: a is 0 or 1/2 and m = 1 - a
+    x, dy, a = x.double().numpy(), dy.double().numpy(), torch.where(even, 0.0, 0.5).double().numpy()
+    ix, before = x / 2, np.zeros_like(x)
+    h = np.zeros((batch, dim))
+    g, G = np.empty_like(x), np.zeros((batch, dim))
+    for t in range(L):
+        before[..., t] = h
+        h = a[t] * h + (1 - a[t]) * ix[..., t]
+    for t in range(L - 1, -1, -1):
+        g[..., t] = dy[..., t] + G
+        G = a[t] * g[..., t]
+    dd = g * (before - ix) * (1 - a)
+    terms = dict(ddecay=dd, dr_bias=dd * a, di_bias=g * (1 - a) * x / 4)
+    return p, as_io(torch.from_numpy(dy)), terms
+
+
+# batch rows past one pass of the sums' 32 threads, and past two; split rows of more parts than one pass of 256 threads takes
+@pytest.mark.parametrize("batch,dim,L,io", [(33, 5, 37, "f32"), (70, 37, 4, "bf16"), (299, 3, 1, "f32"), (65, 2, 700, "bf16"), (2, 3, 6145, "f32"), (40, 3, 2048 * 7 + 5, "bf16"),
+                                            (37, 1, 2048 * 7 + 1, "f32"), (1, 4, 2048 * 260 + 3, "bf16")])
+def test_every_token_counts_in_the_sums(ss, dev, batch, dim, L, io):
+    import torch
+    p, dy, terms = counted(dev, batch, dim, L, io)
+    ckpt = torch.empty(ss.glr_ckpt_numel(batch, dim, L), device=dev)
+    ss.glr_fwd(**p, ckpt=ckpt)
+    for stored in (None, ckpt):
+        got = ss.glr_bwd(dy=dy, ckpt=stored, **p)
+        torch.cuda.synchronize()
+        for k, v in terms.items():
+            there = slice(1, None, 2) if k == "dr_bias" else slice(1, None)    # token 0 has no state before it, but an input
+            assert (v[..., there] != 0).all() and np.abs(v).sum((0, 2)).max() < 2 ** 20 and (v * 16 % 1 == 0).all(), k
+            assert np.array_equal(f64(got[k]), v.sum((0, 2))), k

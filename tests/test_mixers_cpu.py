@@ -248,3 +248,18 @@ def test_glr_step_refuses_more_channels_than_a_grid(dim):
     assert st == UNSUPPORTED and "dim" in msg, (st, msg)
     st, msg = glr("step", batch=1, dim=(1 << 31) - 128, y=None)
     assert st == INVALID and "y is NULL" in msg, (st, msg)
+
+
+@pytest.mark.parametrize("batch,dim,L,io", [(33, 5, 37, "f32"), (2, 3, 6145, "f32"), (40, 3, 2048 * 7 + 5, "bf16")])
+def test_a_lost_term_would_show_in_the_counted_sums(batch, dim, L, io):
+    """The inputs of the recurrence's sums over tokens: no term is 0 where the gate is not, each is exact in fp32, and the sum of their
+    sizes is too, so that fp32 sums of them in any order are exact and one term less is another value."""
+    import numpy as np
+    import torch
+    from test_gpu_glr import counted
+    p, _, terms = counted(torch.device("cpu"), batch, dim, L, io)
+    for k, v in terms.items():
+        shown = v[..., 1::2] if k == "dr_bias" else v
+        assert (shown != 0).all() and np.array_equal(v.astype(np.float32), v), k
+        assert (v * 16 == np.rint(v * 16)).all() and np.abs(v).sum((0, 2)).max() < 2 ** 20, k
+    assert p["x"].dtype == (torch.float32 if io == "f32" else torch.bfloat16)
