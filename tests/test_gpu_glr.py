@@ -822,3 +822,30 @@ def test_every_token_counts_in_the_sums(ss, dev, batch, dim, L, io):
             there = slice(1, None, 2) if k == "dr_bias" else slice(1, None)    # token 0 has no state before it, but an input
             assert (v[..., there] != 0).all() and np.abs(v).sum((0, 2)).max() < 2 ** 20 and (v * 16 % 1 == 0).all(), k
             assert np.array_equal(f64(got[k]), v.sum((0, 2))), k
+
+
+@pytest.mark.parametrize("kind,i,z", [("normalised", True, True), ("convex", False, False)])
+def test_sixteen_waves_against_the_formulas(ss, dev, kind, i, z):
+    """bf16 rows of 2^17 tokens and more, 321 of them so that each has a workgroup: sixteen waves forward, eight backward.  Three
+    of the rows, element by element."""
+    import torch
+    rows, L = 321, (1 << 17) + 3
+    p = problem(dev, 33, 1, rows, L, "bf16", kind, i, z)
+    ckpt = torch.full((ss.glr_ckpt_numel(1, rows, L),), float("nan"), device=dev)
+    y, h = ss.glr_fwd(**p, ckpt=ckpt)
+    gen = torch.Generator().manual_seed(34)
+    dy = torch.randn(p["x"].shape, generator=gen).to(torch.bfloat16).to(dev)
+    dh = torch.randn((1, rows), generator=gen).to(dev)
+    grads = [ss.glr_bwd(dy=dy, dh_final=dh, ckpt=c, **p) for c in (None, ckpt)]
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 160, 320], device=dev)
+    some = lambda t: None if t is None else t[at] if t.dim() == 1 else t[:, at]  # noqa: E731
+    few = {k: some(v) if k != "kind" else v for k, v in p.items()}
+    g = forward(few, adds(L))
+    check("y", f64(some(y)), g["y"], HALF["bf16"])
+    check("h_final", f64(some(h)), g["h"][..., -1], 0.0)
+    check("ckpt", f64(some(ckpt.view(1, rows, -1))[..., 1:]), g["h"][..., 2047:L - 1:2048], 0.0)
+    want = backward(few, g, f64(some(dy)), f64(some(dh)), adds(L))
+    for got in grads:
+        for name, v in want.items():
+            check(name, f64(some(got[name])), v, HALF["bf16"] if got[name].dtype == torch.bfloat16 else 0.0)
