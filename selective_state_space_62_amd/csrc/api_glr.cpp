@@ -37,8 +37,6 @@ bool valid_sizes(int64_t batch, int64_t dim, int64_t seqlen) {
          (__int128)batch * dim * (seqlen > 0 ? seqlen : 1) * 16 <= ((__int128)1 << 62);
 }
 
-int64_t ckpt_count(int64_t seqlen) { return (seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens; }
-
 struct Named {
   const char* name;
   const void* p;
@@ -89,7 +87,7 @@ GlrBwdLayout bwd_layout(int64_t rows, int64_t seqlen) {
   GlrBwdLayout w{};
   w.chain = chain_bytes(rows, seqlen);
   w.ckpt = 2 * w.chain;
-  w.sums = w.ckpt + (seqlen > kGlrCkptTokens ? round256((size_t)rows * ckpt_count(seqlen) * sizeof(float)) : 0);
+  w.sums = w.ckpt + (seqlen > kGlrCkptTokens ? round256((size_t)rows * glr_tiles(seqlen) * sizeof(float)) : 0);
   w.total = w.sums + (seqlen > 0 ? round256((size_t)rows * tiles * 3 * sizeof(float)) : 0);
   return w;
 }
@@ -126,7 +124,7 @@ extern "C" {
 
 size_t ss_glr_ckpt_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
   if (!valid_sizes(batch, dim, seqlen)) return 0;
-  return (size_t)batch * dim * ckpt_count(seqlen) * sizeof(float);
+  return (size_t)batch * dim * glr_tiles(seqlen) * sizeof(float);
 }
 
 size_t ss_glr_fwd_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen) {
@@ -156,7 +154,7 @@ ss_status ss_glr_fwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
                        rng("decay", decay, dim * 4), rng("r_bias", r_bias, dim * 4), rng("i_bias", i_bias, dim * 4),
                        rng("h0", h0, rows * 4)};
   const Range outs[] = {rng("y", y, seq), rng("h_final", h_final, rows * 4),
-                        rng("ckpt", ckpt, rows * ckpt_count(seqlen) * 4), rng("workspace", workspace, (int64_t)need)};
+                        rng("ckpt", ckpt, rows * glr_tiles(seqlen) * 4), rng("workspace", workspace, (int64_t)need)};
   if ((st = check_overlap(ins, outs)) != SS_OK) return st;
 
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -214,7 +212,7 @@ ss_status ss_glr_bwd(int64_t batch, int64_t dim, int64_t seqlen, ss_dtype io, ss
   const Range ins[] = {rng("x", x, seq), rng("r", r, seq), rng("i", i, seq), rng("z", z, seq),
                        rng("decay", decay, dim * 4), rng("r_bias", r_bias, dim * 4), rng("i_bias", i_bias, dim * 4),
                        rng("h0", h0, rows * 4), rng("dy", dy, seq), rng("dh_final", dh_final, rows * 4),
-                       rng("ckpt", ckpt, rows * ckpt_count(seqlen) * 4)};
+                       rng("ckpt", ckpt, rows * glr_tiles(seqlen) * 4)};
   const Range outs[] = {rng("dx", dx, seq), rng("dr", dr, seq), rng("di", di, seq), rng("dz", dz, seq),
                         rng("ddecay", ddecay, dim * 4), rng("dr_bias", dr_bias, dim * 4),
                         rng("di_bias", di_bias, dim * 4), rng("dh0", dh0, rows * 4),

@@ -90,7 +90,6 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void glr_fwd_kernel(GlrArgs p
   const int64_t row = act ? first + wave / W : p.rows - 1;   // a padding wave repeats a row and stores nothing
   const RowConst c = row_const<KIND>(p, row % p.dim);
   const int64_t base = row * p.seqlen;
-  const int64_t ncheck = (p.seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens;
   const int64_t mine = part * 64 * kV;
   float carry = p.h0 ? p.h0[row] : 0.0f;
   FwdTile<IO, KIND, HI, HZ> next;
@@ -121,7 +120,7 @@ __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void glr_fwd_kernel(GlrArgs p
       }
     }
     if (p.ckpt && act && lane == 0 && t % kGlrCkptTokens == 0 && t < p.seqlen)
-      p.ckpt[row * ncheck + t / kGlrCkptTokens] = enter;
+      p.ckpt[row * glr_tiles(p.seqlen) + t / kGlrCkptTokens] = enter;
     const float h = fmaf(shift_up(1.0f, A), enter, shift_up(0.0f, B));
     if (p.y && act) replay<IO, HZ>(in, a, u, h, p.seqlen - t, lane, (T*)p.y + (base + t));
   }

@@ -181,9 +181,7 @@ __global__ __launch_bounds__(256) void qk_cols_bwd_kernel(QkArgs a, int64_t turn
     if (!a.side[side].dw) continue;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      float v = dw[side][k];
-#pragma unroll
-      for (int step = 1; step < 64; step <<= 1) v += __shfl_xor(v, step);
+      const float v = wave_total(dw[side][k]);
       if ((threadIdx.x & 63) == 0) s_dw[side][wave][place<N, HALF>(k)] = v;
     }
   }

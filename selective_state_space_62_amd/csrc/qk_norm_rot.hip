@@ -14,12 +14,6 @@ using namespace qk;
 
 constexpr int kSlots = 2;   // pairs per lane: head_dim <= 256
 
-__device__ __forceinline__ float wave_total(float v) {
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k);
-  return v;
-}
-
 // The places of pair p's two values; the second is -1 for a last single value.
 __device__ __forceinline__ void places(const QkArgs& a, int p, int& j1, int& j2) {
   if (p < a.half) {
