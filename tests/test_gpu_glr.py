@@ -849,3 +849,36 @@ def test_sixteen_waves_against_the_formulas(ss, dev, kind, i, z):
     for got in grads:
         for name, v in want.items():
             check(name, f64(some(got[name])), v, HALF["bf16"] if got[name].dtype == torch.bfloat16 else 0.0)
+
+
+def test_c_names_of_the_binding(ss, dev):
+    """The C entry points under their own names: as the tensor calls, in place and through a workspace."""
+    import torch
+    B, D, L = 1, 3, 9000
+    p = problem(dev, 35, B, D, L, "bf16", "normalised")
+    y, h = run_fwd(ss, p)
+    dy = p["i"]
+    want = ss.glr_bwd(dy=dy, **p)
+    s = torch.cuda.current_stream().cuda_stream
+    a = lambda *names: [p[n].data_ptr() for n in names]  # noqa: E731
+    new = {k: torch.empty_like(v) for k, v in dict(want, y=y, h=h).items()}
+    ckpt = torch.empty(ss.ss_glr_ckpt_bytes(B, D, L) // 4, device=dev)
+    ws = torch.empty(max(ss.ss_glr_fwd_workspace_bytes(B, D, L), ss.ss_glr_bwd_workspace_bytes(B, D, L)), dtype=torch.uint8, device=dev)
+    head = (B, D, L, ss.SS_BF16, ss.SS_GLR_NORMALISED, SCALE)
+    ins = a("x", "r", "i", "z", "decay", "r_bias", "i_bias")
+    ss.ss_glr_fwd(*head, *ins, *a("h0"), new["y"].data_ptr(), new["h"].data_ptr(), ckpt.data_ptr(), ws.data_ptr(), ws.numel(), s)
+    ss.ss_glr_bwd(*head, *ins, *a("h0"), dy.data_ptr(), None, ckpt.data_ptr(),
+                  *(new[k].data_ptr() for k in ("dx", "dr", "di", "dz", "ddecay", "dr_bias", "di_bias", "dh0")), ws.data_ptr(), ws.numel(), s)
+    torch.cuda.synchronize()
+    for k, v in dict(want, y=y, h=h).items():
+        assert torch.equal(new[k], v), k
+    one = problem(dev, 36, 3, 5, 1, "bf16", "normalised", step=True)
+    state, other = one.pop("h0"), torch.empty(3, 5, device=dev)
+    out = torch.empty_like(one["x"])
+    ss.ss_glr_step(3, 5, ss.SS_BF16, ss.SS_GLR_NORMALISED, SCALE, state.data_ptr(), other.data_ptr(),
+                   *(one[k].data_ptr() for k in ("x", "r", "i", "z", "decay", "r_bias", "i_bias")), out.data_ptr(), s)
+    again = ss.glr_step(state, **one)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again) and torch.equal(other, state)
+    with pytest.raises(ss.SsError):
+        ss.ss_glr_step(3, 5, ss.SS_BF16, 7, SCALE, state.data_ptr(), other.data_ptr(), *[None] * 7, out.data_ptr(), s)

@@ -473,3 +473,26 @@ def test_every_vector_counts_in_the_weights_gradient(ss, dev, B, L, hq, hk, N, r
     for s in "qk":
         assert 1.5 * B * L * max(hq, hk) < 1 << 23
         assert torch.equal(got["dw" + s].cpu().double() * 2, (v[s] * d[s]).sum((0, 1, 2)).double()), s
+
+
+def test_c_names_of_the_binding(ss, dev):
+    """The C entry points under their own names, with strides as three numbers: as the tensor calls."""
+    import torch
+    B, L, hq, hk, N, rot = 2, 33, 3, 1, 40, 32
+    p = problem(dev, 21, B, L, hq, hk, N, rot, "bf16", 8, True)
+    dq, dk = grads_like(dev, 22, p, False)
+    q, k = ss.qk_norm_rot(**p, interleaved=True)
+    want = ss.qk_norm_rot_bwd(dq_out=dq, dk_out=dk, **p, interleaved=True)
+    new = {n: torch.empty_like(v) for n, v in dict(want, q=q, k=k).items()}
+    ws = torch.empty(ss.ss_qk_norm_rot_bwd_workspace_bytes(B, L, hq, hk, N), dtype=torch.uint8, device=dev)
+    s = torch.cuda.current_stream().cuda_stream
+    head = (B, L, hq, hk, N, rot, ss.SS_BF16, ss.SS_QK_INTERLEAVED, EPS, p["q"].data_ptr(), p["q"].stride()[:3], p["k"].data_ptr(),
+            p["k"].stride()[:3], *(p[n].data_ptr() for n in ("wq", "wk", "inv_freq", "positions")), 0)
+    ss.ss_qk_norm_rot(*head, new["q"].data_ptr(), new["k"].data_ptr(), s)
+    ss.ss_qk_norm_rot_bwd(*head, dq.data_ptr(), dk.data_ptr(), new["dq"].data_ptr(), new["dq"].stride()[:3], new["dk"].data_ptr(),
+                          new["dk"].stride()[:3], new["dwq"].data_ptr(), new["dwk"].data_ptr(), ws.data_ptr(), ws.numel(), s)
+    torch.cuda.synchronize()
+    for n, v in dict(want, q=q, k=k).items():
+        assert torch.equal(new[n], v), n
+    with pytest.raises(ss.SsError):
+        ss.ss_qk_norm_rot(*head[:5], 3, *head[6:], new["q"].data_ptr(), new["k"].data_ptr(), s)
