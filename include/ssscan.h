@@ -335,10 +335,12 @@ ss_status ss_scan_bwd_seg(int64_t batch, int64_t dim, int dstate, int64_t seqlen
  * needs i.  decay_scale must be positive and finite with SS_GLR_NORMALISED and is
  * not read otherwise.  The state and all arithmetic are fp32; y and the gradients
  * of I/O tensors are rounded once.  Tensors need only their elements' alignment
- * (4 bytes for fp32 vectors and states), and any seqlen >= 0 runs at full
- * vector width.  A token that must not change the state (padding) has r = +inf
- * (convex) or r = -inf (normalised) and a finite x: its decay is exactly 1 and
- * its input exactly 0, and its gradients of x, r and i are zero.
+ * (4 bytes for fp32 vectors and states), and any seqlen >= 0 runs: at full vector
+ * width but for the tokens behind a row's last whole 8, which go one by one.  A token
+ * that must not change the state (padding) has r = +inf (convex) or r = -inf
+ * (normalised) and finite x, i and z: its decay is exactly 1 and its input exactly 0,
+ * whatever the channel's bias and decay are short of NaN, and its gradients of x, r
+ * and i are zero where its state and adjoint are finite.
  *
  * Ownership, streams, errors and overlaps are as for ss_scan_fwd.  Results are
  * deterministic: every sum runs in a fixed order.

@@ -6,7 +6,8 @@
 
 namespace ssscan {
 
-// Tokens between two stored states (ckpt), and of the widest tile of a row.
+// Tokens between two stored states (ckpt): a piece of a row.  A tile is one, two or four pieces, or a
+// shorter row as a whole.
 constexpr int64_t kGlrCkptTokens = 2048;
 
 // Operands of one call.  Row = (batch row, channel), rows = batch * dim; I/O
@@ -43,11 +44,11 @@ struct GlrArgs {
 
 constexpr int64_t glr_tiles(int64_t seqlen) { return (seqlen + kGlrCkptTokens - 1) / kGlrCkptTokens; }
 // Long rows, when there are about as many as CUs or fewer, are split over workgroups, a tile
-// of one or more times kGlrCkptTokens each.  Kernel times of forward / backward from stored states, one
-// workgroup to a row -> split, fp32: 16 rows of 256K tokens 151 / 256 -> 33 / 38 us, 96 rows
-// of 300001 187 / 407 -> 106 / 166 us; 64 rows of 5000 tokens 20 / 36 -> 22 / 35 us.  Past 256 rows some
-// CUs have two: training steps (whole calls) of 297 rows of 116288 tokens 373 -> 321, bf16 239 -> 216, of 40000
-// 134 -> 124, bf16 90 -> 83, of 10000 42 -> 50; of 384 rows of 131072 451 -> 451, bf16 277 -> 297 us.
+// of one or more times kGlrCkptTokens each.  Whole calls, one after another, of the normalised kind with an
+// input gate, one workgroup to a row -> split, fp32 forward / backward from stored states: 16 rows of 256K
+// tokens 160 / 278 -> 25 / 44 us, 96 rows of 300001 191 / 447 -> 106 / 184; 64 rows of 5000 12 / 26 -> 18 / 31.
+// Past 256 rows some CUs have two: training steps of 297 rows of 116288 tokens 373 -> 316, bf16 239 -> 208, of
+// 40000 133 -> 122, bf16 89 -> 81, of 10000 37 -> 48; of 384 rows of 131072 451 -> 445, bf16 275 -> 286 us.
 constexpr bool glr_split(int64_t rows, int64_t seqlen) {
   return seqlen > (rows < 256 ? 4 : 16) * kGlrCkptTokens && rows < 320;
 }

@@ -412,8 +412,10 @@ struct Bwd {
     }
     if (a.seqlen <= 64 * kV) return rows<1>(a, s);
     if (a.seqlen <= 128 * kV) return rows<2>(a, s);
-    // bf16 rows of many tiles take eight waves: 384 rows of 128K tokens 251 -> 208 us, 2048 of 256K 1632 ->
-    // 1568 us; in fp32 four are as fast (384 rows of 128K 320, with eight 350 us)
+    // bf16 rows of many tiles take eight waves.  Whole calls from stored states, four -> eight, normalised
+    // with an input gate: 384 rows of 128K tokens 204 -> 180 us, 1536 of 32K 154 -> 145, 2048 of 256K 1573 ->
+    // 1514; 384 of 128K convex without gates 149 -> 120, but with both gates 234 -> 257.  In fp32 four are as
+    // fast (384 rows of 128K with an input gate 292, with eight 305 us)
     if constexpr (IO::kPerSpan == 8)
       if (a.seqlen >= (1 << 14)) return rows<8>(a, s);
     return rows<4>(a, s);

@@ -25,9 +25,10 @@ struct Raw {
 // A lane's tokens as one or two 16-byte accesses, for a lane whose tokens are all inside
 // the row; the lane at its end goes element by element.  A tile's loads stand together
 // in one branch for the first and one for the second: with a branch for each of them
-// the compiler waited for a load before it sent the next (2.8B-shaped layer, forward 177
-// -> 153 us), and with one for the wave as a whole a wave that holds a row's end went
-// element by element (40960 rows of 1000 bf16 tokens, backward, 246 -> 112 us).  Rows of
+// the compiler waited for a load before it sent the next (2.8B-shaped bf16 layer with
+// both gates, forward 177 -> 153 us), and with one for the wave as a whole a wave that
+// holds a row's end went element by element (40960 rows of 1000 bf16 tokens, normalised,
+// input gate, forward 124 -> 85 us, backward 274 -> 150).  Rows of
 // odd length start at any element, and gfx950 takes vector accesses at any address, so
 // the type promises the compiler no more than its elements' alignment.
 template <typename IO>
@@ -154,7 +155,8 @@ __device__ __forceinline__ float one_minus(float s, float e) { return e > 1.0f ?
 // 1 - a^2 of the normalised kind, with w = 2 l s and a = e^(-w/2).  1 - a a loses
 // digits as a nears 1 (the usual case: decays of 0.9 to 0.999), so below w = 1/8 it
 // is the Taylor polynomial of 1 - e^-w, whose first dropped term is w^5/720, 4.3e-8
-// relative there; above, a's rounding costs at most 6e-8/0.117 in 1 - a^2.
+// relative there; above, a is at most 0.94 and within one step, 2^-24, which moves a^2 by
+// 1.1e-7, 9.5e-7 of 1 - a^2 and half as much of its root.
 __device__ __forceinline__ float one_minus_sq(float w, float a) {
   float t = fmaf(w, 1.0f / 120.0f, -1.0f / 24.0f);
   t = fmaf(t, w, 1.0f / 6.0f);

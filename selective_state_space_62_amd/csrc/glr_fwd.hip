@@ -73,8 +73,9 @@ __device__ __forceinline__ void replay(const TILE& in, const float (&a)[kV], con
 
 // W waves share a row, which is taken in tiles of W * 512 tokens; workgroups of four
 // waves hold 4 / W rows.  With MORE tiles than one, the next one's operands are loaded
-// while a tile is worked on (96 fp32 rows of 300001 tokens 245 -> 187 us); without, the
-// registers for it would only cost waves (2.8B-shaped layer, one tile to a row, 160 -> 197 us).
+// while a tile is worked on (96 fp32 rows of 300001 tokens, a workgroup to each, normalised,
+// input gate, 260 -> 190 us); without, the registers for it would only cost waves (2.8B-shaped
+// bf16 layer with both gates, one tile to a row, 156 -> 161 us).
 template <typename IO, int KIND, bool HI, bool HZ, int W, bool MORE>
 __global__ __launch_bounds__(W > 4 ? W * 64 : 256) void glr_fwd_kernel(GlrArgs p) {
   using T = typename IO::T;
@@ -152,9 +153,10 @@ __global__ __launch_bounds__(256) void glr_fwd_short_kernel(GlrArgs p, int S) {
 
 // Split rows: a workgroup takes SEG pieces of 2048 tokens each, whose loads are in flight together.
 // It waits for its ticket, its loads and the tiles before it in turn, so the bytes in flight are the
-// rate: 64 bf16 rows of a million tokens, SEG 1, 2, 3, 4: 149, 109, 101, 95 us; 4 of four million 122, 77,
-// 65, 65; 96 fp32 rows of 300001 120, 110, 107, 106.  Rows of fewer pieces, whose tiles all run at once,
-// wait longer for each: 240 bf16 rows of 31949 tokens 22, 23, 26, 22; 36 of 155719 29, 26, 24, 25 us.
+// rate: 64 bf16 rows of a million tokens without gates, SEG 1, 2, 3, 4: 149, 109, 101, 95 us; 4 of four
+// million with both 122, 77, 65, 65; 96 fp32 rows of 300001 with an input gate, convex, 120, 110, 107, 106.
+// Rows of fewer pieces, whose tiles all run at once, wait longer for each: 240 bf16 rows of 31949 tokens with
+// an input gate 22, 23, 26, 22; 36 of 155719 with both 29, 26, 24, 25 us.
 template <typename IO, int KIND, bool HI, bool HZ, int SEG>
 __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
   using T = typename IO::T;
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(256) void glr_fwd_split_kernel(GlrArgs p) {
 
 // One token.  A lane takes two neighbouring channels of two batch rows, so that it forms
 // the channels' constants once and has all its loads in flight together; the last of an odd
-// number of channels goes by itself.  256 x 5120 bf16: 6.8 us (one channel of one row 8.0, of
+// number of channels goes by itself.  256 x 5120 bf16, normalised, both gates: 6.8 us (one channel of one row 8.0, of
 // four rows 6.7, four channels of two rows 7.4; a loop over rows, which held the loads back behind the
 // constants, 10.7); 4096 x 5120: 68 us, 5.5 TB/s (one channel of four rows 76, four of one row 70).
 constexpr int kStepC = 2, kStepB = 2;
@@ -317,9 +319,10 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrArgs p, int64_t batch)
 
 // A row's waves.  Rows of up to 512 or 1024 tokens fit one or two.  bf16 rows of many
 // tiles take eight or sixteen: a tile of four waves is 4 KB of each tensor, which the loads of one
-// tile ahead do not keep the memory busy with (384 rows of 128K tokens 132 -> 116 us, 1536 of 32K 97 ->
-// 98 us; with sixteen 2048 rows of 256K 894 -> 850 us but 1536 of 32K 112 us).  In fp32 four are as
-// fast (384 rows of 128K 175, with eight 180 us).
+// tile ahead do not keep the memory busy with.  Whole calls of four, eight and sixteen, normalised with an
+// input gate: 384 rows of 128K tokens 117, 112, 114 us, 1536 of 32K 86, 86, 92, 2048 of 256K 883, 876, 833;
+// 384 of 128K with both gates 129, 118, 122, convex without 76, 64, 67.  In fp32 four are as fast (384 rows
+// of 128K with an input gate 165, 169, 178).
 int waves_for(const GlrArgs& a) {
   if (a.seqlen <= 128 * kV) return a.seqlen <= 64 * kV ? 1 : 2;
   if (a.io != kIoBf16 || a.seqlen < (1 << 14)) return 4;

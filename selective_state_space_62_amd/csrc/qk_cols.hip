@@ -13,8 +13,8 @@ using namespace qk;
 
 // How a vector's pairs lie in it: 2p and 2p + 1 (HALF 0: interleaved, or nothing
 // rotated), or p and p + HALF up to HALF and 2p and 2p + 1 from there.  A constant, so
-// that pairs are picked from vector loads by register (at 612000 tokens, half of 16 values
-// rotated: 37 us a whole call, element by element 60).
+// that pairs are picked from vector loads by register (612000 tokens cut from rows of 192
+// values, half of 16 rotated, whole call: bf16 28 us, element by element 51; fp32 40 and 62).
 template <int N, int HALF>
 __device__ __forceinline__ constexpr int place(int k) {   // of value k % 2 of pair k / 2
   return N == 1 ? 0 : k / 2 < HALF ? k / 2 + k % 2 * HALF : k;
@@ -87,9 +87,9 @@ __device__ __forceinline__ void forward(const QkArgs& a, const float (&w)[N], co
 }
 
 // Both sides' loads are out before the angles are formed: the rows' 64 bytes of B and C
-// are the wait (a million tokens, whole call: one side after the other 52.4, ahead 45.7, with
-// the registers for six waves to a SIMD 43.5 us; a copy of the same 64 bytes of each
-// 320-byte row 32 us).  Turning tiles in LDS for 16-byte stores took 54 us, for 16-byte pieces
+// are the wait (a million bf16 tokens, half of 16 values rotated, interleaved, whole call:
+// one side after the other 52.4, ahead 45.7, with the registers for six waves to a SIMD
+// 43.5 us; a copy of the same 64 bytes of each 320-byte row 32 us).  Turning tiles in LDS for 16-byte stores took 54 us, for 16-byte pieces
 // of a row to neighbouring lanes 77 us, 4-byte stores of two tokens 51 us.
 template <typename IO, int N, int HALF>
 __global__ __launch_bounds__(64, N == 16 && IO::kPerSpan == 4 ? 5 : 6) void qk_cols_fwd_kernel(QkArgs a, int64_t turns) {
@@ -250,8 +250,8 @@ hipError_t launch_qk_cols_bwd(QkArgs& a, const QkBwdPlan& p, hipStream_t s) {
   for (int i = 0; i < 2; ++i)
     if (a.side[i].heads && p.blocks[i] < most) most = p.blocks[i];
   // the workgroups are few, each with a row of sums: four waves each where the tokens fill
-  // them (320860 tokens, half of 16 values rotated, whole call: one wave 53.9, four
-  // 35.2 us)
+  // them (whole call, one wave -> four: 320860 tokens, half of 16 values rotated, bf16 42.8 ->
+  // 36.9 us, fp32 43.5 -> 48.2; a million, all rotated, bf16 167 -> 123, fp32 147 -> 131)
   const ColsShape sh = shape_of(a, a.batch * a.seqlen >= 256 * most ? 256 : 64, most);
   for (int i = 0; i < 2; ++i) a.part_rows[i] = a.side[i].heads ? (int64_t)sh.blocks : 0;
   a.part_row[1] = a.part_rows[0];

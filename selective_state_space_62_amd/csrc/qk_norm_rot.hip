@@ -188,7 +188,7 @@ __global__ __launch_bounds__(1024) void qk_reduce_kernel(QkArgs a) {
 
 // About 1024 rows of partial sums, shared by the sides as their heads are: four workgroups
 // to a CU, which is what the registers of the kernel for runs allow (25 fp32 heads of 80 at 8188
-// tokens, whole call: 1024 rows 51.7, 2048 53.7, 4096 56.1 us).  Twice as many for the short
+// tokens counted from pos0, whole call: 1024 rows 46, 2048 50, 4096 53 us).  Twice as many for the short
 // heads of the feature-major kernel, which needs less of both.
 QkBwdPlan qk_bwd_plan(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int n) {
   QkBwdPlan p;

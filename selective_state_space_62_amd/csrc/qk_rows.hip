@@ -217,8 +217,9 @@ __global__ __launch_bounds__(kThreads) void qk_rows_bwd_kernel(QkArgs a, QkRowsS
 }
 
 // The longest run that the shape allows: half and the rest's pairs in whole runs, and 16
-// bytes at most; in the backward 4 values, whose registers leave room for more waves (6 bf16 heads
-// of 128 at 21879 tokens: runs of 8 42.0, of 4 33.1 us; 40 at 16384 142.5 and 139.7 us).  0: none.
+// bytes at most (40 bf16 heads of 128 at 16384 tokens, forward: runs of 4 73, of 8 68 us); in the
+// backward 4 values, whose registers leave room for more waves (6 bf16 heads of 128 at 21879 tokens: runs
+// of 8 43.8, of 4 35.2 us; 40 at 16384 142.9 and 141.3 us).  0: none.
 int run_of(const QkArgs& a, bool back) {
   for (int k = a.io == kIoBf16 && !back ? 8 : 4; k >= 2; k >>= 1)
     if (a.half % k == 0 && (a.n - 2 * a.half) % (2 * k) == 0) return k;
@@ -233,7 +234,7 @@ int lanes_of(const QkArgs& a, int k) {
 
 // A workgroup's tokens.  Forward: two rounds of vectors for its groups of lanes, fewer
 // where the tokens would not give 1024 workgroups.  (40 bf16 heads of 128 at 16384 tokens: one
-// round 73.7, two 66.6, three 67.6 us; two or four vectors in flight to a group, which cost
+// round 76, two 68, three 69 us; two or four vectors in flight to a group, which cost
 // waves their registers, 71 and 80 us.)  Backward, where the workgroups are few and keep
 // their sums: an equal share of the tokens, in as few turns as the angles' LDS allows.
 QkRowsShape shape_of(const QkArgs& a, int k, bool back, const int64_t (&most)[2]) {

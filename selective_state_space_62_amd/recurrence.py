@@ -44,7 +44,7 @@ def glr_fwd(x, r, i=None, z=None, decay=None, r_bias=None, i_bias=None, h0=None,
     x, r, i, z: (batch, D, L), all float32 or all bfloat16; decay, r_bias, i_bias: (D,)
     and h0: (batch, D) float32.  ckpt: optional float32 tensor of glr_ckpt_numel(...)
     elements that receives the states glr_bwd starts from.  A padding token has
-    r = +inf (convex) or -inf (normalised) and a finite x: it leaves the state alone.
+    r = +inf (convex) or -inf (normalised) and finite x, i and z: it leaves the state alone.
     Returns (y, h_final); h_final (batch, D) is None when return_final_state is False.
     """
     batch, dim, L = x.shape
