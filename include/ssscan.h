@@ -444,6 +444,96 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
                              float* dwq, float* dwk,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gated delta rule: a recurrence whose state is a matrix for every head, dim_k keys
+ * by dim_v values (fp32), for recurrent layers that stand next to the scan.  In the
+ * attention view of a selective model (first abstract of the "Mamba models" page)
+ * the scan's state sums outer products of B_t and x_t; here every token first takes
+ * back what the state already returns for its key:
+ *
+ *     S'_t = exp(g_t) S_(t-1)
+ *     u_t  = beta_t (v_t - S'_t^T k_t)
+ *     S_t  = S'_t + k_t u_t^T
+ *     o_t  = scale S_t^T q_t
+ *
+ * for every batch row and value head; value head h reads key head h / (heads_v /
+ * heads_k), heads_v being a multiple of heads_k.  g (log decays, NULL = all zero) and
+ * beta are (batch, seqlen, heads_v) fp32, h0, h_final and the states (batch, heads_v,
+ * dim_k, dim_v) fp32 with NULL h0 = zero; o is (batch, seqlen, heads_v, dim_v) in the
+ * I/O dtype, 16-byte aligned.  q, k (heads_k heads of dim_k) and v (heads_v of dim_v):
+ * value n of head h of token (b, t) of q is at q[b q_stride[0] + t q_stride[1] +
+ * h q_stride[2] + n], strides in elements and nonnegative, so they may be columns of a
+ * projection's rows, and are what ss_qk_norm_rot writes token-major (weights of
+ * 1/sqrt(dim_k) make keys of unit length).  dim_k is 1 to 128, dim_v 1 to 65536;
+ * batch, heads and columns together make fewer than 2^23 workgroups.
+ * The state and all sums are fp32, outputs rounded once.  g of -inf forgets the state;
+ * a padding token has beta = 0, g = 0 and finite q, k and v.
+ * Keys are not normed here: with beta |k|^2 above 2 the recurrence itself grows.
+ *
+ * Ownership, streams, errors and overlaps are as for ss_scan_fwd.  Results are
+ * deterministic: every sum runs in a fixed order.
+ *
+ *  ss_gdr_fwd: h_final (nullable) is the state after the last token (h0 when seqlen is
+ *    0).  The workspace has ss_gdr_fwd_workspace_bytes (which may be 0), 256-byte aligned.
+ *  ss_gdr_step: one token, q, k, v, g, beta and o without their seqlen dimension
+ *    (the strides' second entry is not used).  state_out may be state_in itself. */
+size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v);
+ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
+                     float scale, const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                     const void* v, const int64_t* v_stride, const float* g, const float* beta, const float* h0,
+                     void* o, float* h_final, void* workspace, size_t workspace_bytes, void* stream);
+ss_status ss_gdr_step(int64_t batch, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io, float scale,
+                      const float* state_in, float* state_out, const void* q, const int64_t* q_stride,
+                      const void* k, const int64_t* k_stride, const void* v, const int64_t* v_stride,
+                      const float* g, const float* beta, void* o, void* stream);
+
+/* Norms before and after a block of a model (the pages' blocks are "homogeneous" and
+ * gated: reader's notes on the Mamba paper, kurisu.si, "Architecture"), each in one
+ * pass.  n is a row's length, 1 to 8192, eps a positive normal number, all arithmetic
+ * fp32, outputs rounded once, sums over rows in a fixed order.
+ *
+ *  ss_gated_norm: for every token and head, with norm(a) = a / sqrt(mean(a^2) + eps),
+ *      y = w norm(x) silu(z), or w norm(x silu(z)) under SS_NORM_GATE_FIRST;
+ *    without z (NULL) y = w norm(x).  x and z under (batch, token, head) strides as
+ *    ss_qk_norm_rot's q, so z may be columns of the projection's rows; y is
+ *    contiguous (batch, seqlen, heads, n).  w fp32, NULL = ones: (n), or (heads, n)
+ *    under SS_NORM_HEAD_WEIGHTS.  Fewer than 2^32 rows.
+ *  ss_gated_norm_bwd: dy as y; writes dx, dz (given exactly when z is) under strides of
+ *    their own (no two values may share an address) and, where not NULL, dw shaped as
+ *    w, also of a w that is NULL.  Only dw needs the workspace.
+ *
+ *  ss_residual_norm: rows of a residual stream between two blocks,
+ *      r = res + alpha scale m,   y = w norm(r),
+ *    with m = x, or under SS_NORM_POST m = w_post norm(x) (a norm after the block).
+ *    x and y (rows, n) in the I/O dtype, res (NULL = zeros) and res_out (nullable,
+ *    receives r; may be res itself) in the residual's dtype rio, SS_F32 or the I/O
+ *    dtype; scale, w and w_post (n) fp32, NULL = ones.  r is rounded to rio before it
+ *    is normed, so that the backward sees the forward's r.
+ *  ss_residual_norm_bwd: res is the forward's res_out, dy and dres_out (nullable) the
+ *    gradients of y and of res_out.  Writes dres (that of r, hence of res; may be dres_out itself),
+ *    dx, and dw, dw_post, dscale, each nullable; x may be NULL where neither
+ *    SS_NORM_POST nor dscale needs it.  Only those three need the workspace.
+ * All tensors need only their elements' alignment, the workspace 256 bytes. */
+typedef enum { SS_NORM_GATE_FIRST = 1u, SS_NORM_HEAD_WEIGHTS = 2u, SS_NORM_POST = 4u } ss_norm_flags;
+
+ss_status ss_gated_norm(int64_t batch, int64_t seqlen, int heads, int n, ss_dtype io, uint32_t flags, float eps,
+                        const void* x, const int64_t* x_stride, const void* z, const int64_t* z_stride,
+                        const float* w, void* y, void* stream);
+size_t ss_gated_norm_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads, int n, uint32_t flags);
+ss_status ss_gated_norm_bwd(int64_t batch, int64_t seqlen, int heads, int n, ss_dtype io, uint32_t flags, float eps,
+                            const void* x, const int64_t* x_stride, const void* z, const int64_t* z_stride,
+                            const float* w, const void* dy, void* dx, const int64_t* dx_stride,
+                            void* dz, const int64_t* dz_stride, float* dw,
+                            void* workspace, size_t workspace_bytes, void* stream);
+ss_status ss_residual_norm(int64_t rows, int n, ss_dtype io, ss_dtype rio, uint32_t flags, float eps, float alpha,
+                           const void* x, const void* res, const float* w, const float* w_post, const float* scale,
+                           void* y, void* res_out, void* stream);
+size_t ss_residual_norm_bwd_workspace_bytes(int64_t rows, int n);
+ss_status ss_residual_norm_bwd(int64_t rows, int n, ss_dtype io, ss_dtype rio, uint32_t flags, float eps, float alpha,
+                               const void* x, const void* res, const float* w, const float* w_post, const float* scale,
+                               const void* dy, const void* dres_out, void* dx, void* dres,
+                               float* dw, float* dw_post, float* dscale,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the static device scratch array behind ss_scan_fwd_noalloc (32 MiB per GPU). */
 #define SS_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
 

@@ -115,6 +115,28 @@ def _load():
     lib.ss_qk_norm_rot_bwd_workspace_bytes.argtypes = [_i64, _i64, _int, _int, _int]
     lib.ss_qk_norm_rot_bwd.restype = _int
     lib.ss_qk_norm_rot_bwd.argtypes = _qk + [_vp, _vp, _vp, _st, _vp, _st, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    _sz = ctypes.c_size_t
+    _u32 = ctypes.c_uint32
+    _rows = [_vp, _st]
+    lib.ss_gdr_fwd_workspace_bytes.restype = _sz
+    lib.ss_gdr_fwd_workspace_bytes.argtypes = [_i64, _i64] + [_int] * 4
+    lib.ss_gdr_fwd.restype = _int
+    lib.ss_gdr_fwd.argtypes = [_i64, _i64] + [_int] * 5 + [_f32] + _rows * 3 + [_vp] * 6 + [_sz, _vp]
+    lib.ss_gdr_step.restype = _int
+    lib.ss_gdr_step.argtypes = [_i64] + [_int] * 5 + [_f32, _vp, _vp] + _rows * 3 + [_vp] * 4
+    lib.ss_gated_norm.restype = _int
+    lib.ss_gated_norm.argtypes = [_i64, _i64, _int, _int, _int, _u32, _f32] + _rows * 2 + [_vp] * 3
+    lib.ss_gated_norm_bwd_workspace_bytes.restype = _sz
+    lib.ss_gated_norm_bwd_workspace_bytes.argtypes = [_i64, _i64, _int, _int, _u32]
+    lib.ss_gated_norm_bwd.restype = _int
+    lib.ss_gated_norm_bwd.argtypes = ([_i64, _i64, _int, _int, _int, _u32, _f32] + _rows * 2 + [_vp, _vp] + _rows * 2
+                                      + [_vp, _vp, _sz, _vp])
+    lib.ss_residual_norm.restype = _int
+    lib.ss_residual_norm.argtypes = [_i64, _int, _int, _int, _u32, _f32, _f32] + [_vp] * 8
+    lib.ss_residual_norm_bwd_workspace_bytes.restype = _sz
+    lib.ss_residual_norm_bwd_workspace_bytes.argtypes = [_i64, _int]
+    lib.ss_residual_norm_bwd.restype = _int
+    lib.ss_residual_norm_bwd.argtypes = [_i64, _int, _int, _int, _u32, _f32, _f32] + [_vp] * 13 + [_sz, _vp]
     lib.ss_timing_enable.restype = _int
     lib.ss_timing_enable.argtypes = [_int]
     lib.ss_timing_reset.restype = _int
@@ -340,6 +362,61 @@ def ss_qk_norm_rot_bwd(batch, seqlen, heads_q, heads_k, head_dim, rot_dim, io, f
                                   _strides(q_stride), k, _strides(k_stride), wq, wk, inv_freq, positions, pos0, dq_out,
                                   dk_out, dq, _strides(dq_stride), dk, _strides(dk_stride), dwq, dwk, workspace,
                                   workspace_bytes, stream))
+
+
+@functools.lru_cache(maxsize=256)
+def ss_gdr_fwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) -> int:
+    return int(lib.ss_gdr_fwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v))
+
+
+def ss_gdr_fwd(batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, q_stride, k, k_stride, v, v_stride, g, beta,
+               h0, o, h_final, workspace, workspace_bytes, stream=None):
+    _check(lib.ss_gdr_fwd(batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, _strides(q_stride), k,
+                          _strides(k_stride), v, _strides(v_stride), g, beta, h0, o, h_final, workspace,
+                          workspace_bytes, stream))
+
+
+def ss_gdr_step(batch, heads_k, heads_v, dim_k, dim_v, io, scale, state_in, state_out, q, q_stride, k, k_stride, v,
+                v_stride, g, beta, o, stream=None):
+    _check(lib.ss_gdr_step(batch, heads_k, heads_v, dim_k, dim_v, io, scale, state_in, state_out, q, _strides(q_stride),
+                           k, _strides(k_stride), v, _strides(v_stride), g, beta, o, stream))
+
+
+SS_NORM_GATE_FIRST = 1
+SS_NORM_HEAD_WEIGHTS = 2
+SS_NORM_POST = 4
+
+
+def ss_gated_norm(batch, seqlen, heads, n, io, flags, eps, x, x_stride, z, z_stride, w, y, stream=None):
+    _check(lib.ss_gated_norm(batch, seqlen, heads, n, io, flags, eps, x, _strides(x_stride), z, _strides(z_stride), w, y,
+                             stream))
+
+
+@functools.lru_cache(maxsize=256)
+def ss_gated_norm_bwd_workspace_bytes(batch, seqlen, heads, n, flags) -> int:
+    return int(lib.ss_gated_norm_bwd_workspace_bytes(batch, seqlen, heads, n, flags))
+
+
+def ss_gated_norm_bwd(batch, seqlen, heads, n, io, flags, eps, x, x_stride, z, z_stride, w, dy, dx, dx_stride, dz,
+                      dz_stride, dw, workspace, workspace_bytes, stream=None):
+    _check(lib.ss_gated_norm_bwd(batch, seqlen, heads, n, io, flags, eps, x, _strides(x_stride), z, _strides(z_stride),
+                                 w, dy, dx, _strides(dx_stride), dz, _strides(dz_stride), dw, workspace,
+                                 workspace_bytes, stream))
+
+
+def ss_residual_norm(rows, n, io, rio, flags, eps, alpha, x, res, w, w_post, scale, y, res_out, stream=None):
+    _check(lib.ss_residual_norm(rows, n, io, rio, flags, eps, alpha, x, res, w, w_post, scale, y, res_out, stream))
+
+
+@functools.lru_cache(maxsize=256)
+def ss_residual_norm_bwd_workspace_bytes(rows, n) -> int:
+    return int(lib.ss_residual_norm_bwd_workspace_bytes(rows, n))
+
+
+def ss_residual_norm_bwd(rows, n, io, rio, flags, eps, alpha, x, res, w, w_post, scale, dy, dres_out, dx, dres, dw,
+                         dw_post, dscale, workspace, workspace_bytes, stream=None):
+    _check(lib.ss_residual_norm_bwd(rows, n, io, rio, flags, eps, alpha, x, res, w, w_post, scale, dy, dres_out, dx,
+                                    dres, dw, dw_post, dscale, workspace, workspace_bytes, stream))
 
 
 def ss_timing_enable(enable: bool):

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 #include "ssscan.h"
 
@@ -30,5 +31,34 @@ inline bool overlap(const Range& a, const Range& b) {
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 40;
+
+// Elements from the first to one past the last value under these strides, or -1
+// where that overflows.
+inline int64_t span_of(int64_t batch, int64_t seqlen, int heads, int n, const int64_t* st) {
+  if (heads == 0 || seqlen == 0) return 0;
+  __int128 last = n;
+  last += (__int128)(batch - 1) * st[0] + (__int128)(seqlen - 1) * st[1] + (__int128)(heads - 1) * st[2];
+  return last > ((__int128)1 << 58) ? -1 : (int64_t)last;
+}
+
+// Whether runs of n values, one for each index of D dimensions, are disjoint: by stride,
+// ascending, each dimension has to step over all that the ones before it reach.
+template <int D>
+bool distinct(int64_t n, int64_t (&size)[D], int64_t (&stride)[D]) {
+  for (int i = 0; i < D; ++i)
+    for (int j = i + 1; j < D; ++j)
+      if (stride[j] < stride[i]) {
+        std::swap(stride[i], stride[j]);
+        std::swap(size[i], size[j]);
+      }
+  int64_t reach = n;
+  for (int i = 0; i < D; ++i) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < reach) return false;
+    reach += stride[i] * (size[i] - 1);
+  }
+  return true;
+}
+
 
 }  // namespace ssscan

@@ -1,0 +1,169 @@
+// C ABI of the gated delta rule: argument checks and launches.  See include/ssscan.h.
+#include <cmath>
+
+#include "api_rows.h"
+#include "gdr.h"
+
+namespace {
+
+using namespace ssscan;
+
+constexpr int kMaxDimK = 128;
+constexpr int kMaxDimV = 1 << 16;
+constexpr int kMaxHeads = 1 << 20;
+constexpr int64_t kMaxBlocks = int64_t(1) << 23;   // of 256 or 512 threads, fewer than 2^32 of them
+
+ss_status check_sizes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
+  if (batch < 1 || seqlen < 0)
+    return record_error(SS_ERR_INVALID_ARG, "sizes must be batch >= 1, seqlen >= 0 (got %lld, %lld)",
+                        (long long)batch, (long long)seqlen);
+  if (heads_k < 1 || heads_v < 1 || heads_v > kMaxHeads || heads_v % heads_k)
+    return record_error(SS_ERR_INVALID_ARG, "heads_v %d is not 1 to 2^20 and a multiple of heads_k %d", heads_v, heads_k);
+  if (dim_k < 1 || dim_k > kMaxDimK) return record_error(SS_ERR_UNSUPPORTED, "dim_k %d is not 1 to %d", dim_k, kMaxDimK);
+  if (dim_v < 1 || dim_v > kMaxDimV) return record_error(SS_ERR_UNSUPPORTED, "dim_v %d is not 1 to %d", dim_v, kMaxDimV);
+  if (batch > kMaxDim || seqlen > kMaxDim ||
+      (__int128)batch * (seqlen > 0 ? seqlen : 1) * heads_v * (dim_k + (int64_t)dim_v) * 8 > ((__int128)1 << 62) ||
+      (__int128)batch * heads_v * dim_k * dim_v * 4 * (1 + seqlen / 64) > ((__int128)1 << 62))
+    return record_error(SS_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte offsets");
+  return SS_OK;
+}
+
+struct Inputs {
+  int64_t batch, seqlen;
+  int heads_k, heads_v, dim_k, dim_v;
+  ss_dtype io;
+  float scale;
+  const void* q;
+  const int64_t* q_stride;
+  const void* k;
+  const int64_t* k_stride;
+  const void* v;
+  const int64_t* v_stride;
+  const float* g;
+  const float* beta;
+  const float* h0;
+};
+
+int64_t gates(const Inputs& in) { return in.batch * in.seqlen * in.heads_v; }
+int64_t state_numel(const Inputs& in) { return in.batch * in.heads_v * in.dim_k * in.dim_v; }
+
+// The checks that all calls share, and the inputs' spans (ranges[0..5]: q, k, v, g, beta, h0).
+ss_status check_inputs(const Inputs& in, Range (&ranges)[6]) {
+  if (in.io != SS_F32 && in.io != SS_BF16)
+    return record_error(SS_ERR_UNSUPPORTED, "io dtype %d is not SS_F32 or SS_BF16", (int)in.io);
+  ss_status st = check_sizes(in.batch, in.seqlen, in.heads_k, in.heads_v, in.dim_k, in.dim_v);
+  if (st != SS_OK) return st;
+  if (!std::isfinite(in.scale)) return record_error(SS_ERR_INVALID_ARG, "scale %g is not finite", (double)in.scale);
+  int64_t sq, sk, sv;
+  const int64_t eb = elem_bytes(in.io);
+  if ((st = check_rows("q", in.q, in.q_stride, in.batch, in.seqlen, in.heads_k, in.dim_k, in.io, &sq)) != SS_OK) return st;
+  if ((st = check_rows("k", in.k, in.k_stride, in.batch, in.seqlen, in.heads_k, in.dim_k, in.io, &sk)) != SS_OK) return st;
+  if ((st = check_rows("v", in.v, in.v_stride, in.batch, in.seqlen, in.heads_v, in.dim_v, in.io, &sv)) != SS_OK) return st;
+  if (in.seqlen > 0 && !in.beta) return record_error(SS_ERR_INVALID_ARG, "beta is NULL");
+  const struct { const char* name; const float* p; } vecs[] = {{"g", in.g}, {"beta", in.beta}, {"h0", in.h0}};
+  for (const auto& n : vecs)
+    if (!aligned(n.p, 4)) return record_error(SS_ERR_INVALID_ARG, "%s is not 4-byte aligned", n.name);
+  ranges[0] = rng("q", in.q, sq * eb);
+  ranges[1] = rng("k", in.k, sk * eb);
+  ranges[2] = rng("v", in.v, sv * eb);
+  ranges[3] = rng("g", in.g, gates(in) * 4);
+  ranges[4] = rng("beta", in.beta, gates(in) * 4);
+  ranges[5] = rng("h0", in.h0, state_numel(in) * 4);
+  return SS_OK;
+}
+
+GdrArgs make_args(const Inputs& in) {
+  GdrArgs a{};
+  a.batch = in.batch;
+  a.seqlen = in.seqlen;
+  a.hk = in.heads_k;
+  a.hv = in.heads_v;
+  a.dk = in.dim_k;
+  a.dv = in.dim_v;
+  a.io = in.io == SS_BF16 ? kIoBf16 : kIoF32;
+  a.scale = in.scale;
+  a.q = in.q;
+  a.k = in.k;
+  a.v = in.v;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = in.q_stride[i];
+    a.ks[i] = in.k_stride[i];
+    a.vs[i] = in.v_stride[i];
+  }
+  a.g = in.g;
+  a.beta = in.beta;
+  a.h0 = in.h0;
+  return a;
+}
+
+ss_status check_blocks(int64_t blocks) {
+  if (blocks >= kMaxBlocks)
+    return record_error(SS_ERR_UNSUPPORTED, "%lld workgroups (of batch rows, heads and columns) exceed 2^23", (long long)blocks);
+  return SS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
+  if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK) return 0;
+  return 0;
+}
+
+ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
+                     float scale, const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                     const void* v, const int64_t* v_stride, const float* g, const float* beta, const float* h0, void* o,
+                     float* h_final, void* workspace, size_t workspace_bytes, void* stream) {
+  const Inputs in{batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, q_stride, k, k_stride, v, v_stride, g, beta, h0};
+  Range ins[6];
+  ss_status st = check_inputs(in, ins);
+  if (st != SS_OK) return st;
+  if (seqlen > 0 && !o) return record_error(SS_ERR_INVALID_ARG, "o is NULL");
+  if (!aligned(o, 16)) return record_error(SS_ERR_INVALID_ARG, "o is not 16-byte aligned");
+  if (!aligned(h_final, 4)) return record_error(SS_ERR_INVALID_ARG, "h_final is not 4-byte aligned");
+  const size_t need = ss_gdr_fwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v);
+  if ((st = check_scratch(workspace, workspace_bytes, need)) != SS_OK) return st;
+  const Range outs[] = {rng("o", o, batch * seqlen * heads_v * dim_v * elem_bytes(io)),
+                        rng("h_final", h_final, state_numel(in) * 4), rng("workspace", workspace, (int64_t)need)};
+  if ((st = check_disjoint(ins, 6, outs, 3)) != SS_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (seqlen == 0) {
+    if (h_final) e = h0 ? launch_copy_state(state_numel(in), h0, h_final, s) : launch_fill_zero(h_final, state_numel(in), s);
+    return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
+  }
+  if ((st = check_blocks(gdr_recur_blocks(batch, heads_v, dim_v))) != SS_OK) return st;
+  GdrArgs a = make_args(in);
+  a.o = o;
+  a.h_final = h_final;
+  e = launch_gdr_recur(a, s);
+  return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule launch");
+}
+
+ss_status ss_gdr_step(int64_t batch, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io, float scale,
+                      const float* state_in, float* state_out, const void* q, const int64_t* q_stride, const void* k,
+                      const int64_t* k_stride, const void* v, const int64_t* v_stride, const float* g,
+                      const float* beta, void* o, void* stream) {
+  const Inputs in{batch, 1, heads_k, heads_v, dim_k, dim_v, io, scale, q, q_stride, k, k_stride, v, v_stride, g, beta, state_in};
+  Range ins[6];
+  ss_status st = check_inputs(in, ins);
+  if (st != SS_OK) return st;
+  if (!state_in || !state_out || !o)
+    return record_error(SS_ERR_INVALID_ARG, "%s is NULL", !state_in ? "state_in" : !state_out ? "state_out" : "o");
+  if (!aligned(o, 16)) return record_error(SS_ERR_INVALID_ARG, "o is not 16-byte aligned");
+  if (!aligned(state_out, 4)) return record_error(SS_ERR_INVALID_ARG, "state_out is not 4-byte aligned");
+  ins[5].name = "state_in";
+  const Range outs[] = {rng("o", o, batch * heads_v * dim_v * elem_bytes(io)),
+                        rng("state_out", state_out, state_numel(in) * 4)};
+  if ((st = check_disjoint(ins, state_out == state_in ? 5 : 6, outs, 2)) != SS_OK) return st;
+  if (overlap(outs[0], ins[5])) return record_error(SS_ERR_INVALID_ARG, "o overlaps input state_in");
+  if ((st = check_blocks(gdr_recur_blocks(batch, heads_v, dim_v))) != SS_OK) return st;
+  GdrArgs a = make_args(in);
+  a.o = o;
+  a.h_final = state_out;
+  const hipError_t e = launch_gdr_recur(a, reinterpret_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule step launch");
+}
+
+}  // extern "C"

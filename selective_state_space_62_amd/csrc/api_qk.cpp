@@ -1,6 +1,5 @@
 // C ABI of the norm and rotation of queries and keys: argument checks and launches.  See include/ssscan.h.
 #include <cmath>
-#include <utility>
 
 #include "api_checks.h"
 #include "internal.h"
@@ -31,15 +30,6 @@ ss_status check_sizes(int64_t batch, int64_t seqlen, int heads_q, int heads_k, i
   return SS_OK;
 }
 
-// Elements from the first to one past the last value under these strides, or -1
-// where that overflows.
-int64_t span_of(int64_t batch, int64_t seqlen, int heads, int n, const int64_t* st) {
-  if (heads == 0 || seqlen == 0) return 0;
-  __int128 last = n;
-  last += (__int128)(batch - 1) * st[0] + (__int128)(seqlen - 1) * st[1] + (__int128)(heads - 1) * st[2];
-  return last > ((__int128)1 << 58) ? -1 : (int64_t)last;
-}
-
 ss_status check_side(const char* name, const void* p, const int64_t* st, int64_t batch, int64_t seqlen, int heads,
                      int n, ss_dtype io, int64_t* span) {
   *span = 0;
@@ -56,25 +46,6 @@ ss_status check_side(const char* name, const void* p, const int64_t* st, int64_t
   *span = span_of(batch, seqlen, heads, n, st);
   if (*span < 0) return record_error(SS_ERR_INVALID_ARG, "the strides of %s overflow 64-bit byte offsets", name);
   return SS_OK;
-}
-
-// Whether runs of n values, one for each index of D dimensions, are disjoint: by stride,
-// ascending, each dimension has to step over all that the ones before it reach.
-template <int D>
-bool distinct(int64_t n, int64_t (&size)[D], int64_t (&stride)[D]) {
-  for (int i = 0; i < D; ++i)
-    for (int j = i + 1; j < D; ++j)
-      if (stride[j] < stride[i]) {
-        std::swap(stride[i], stride[j]);
-        std::swap(size[i], size[j]);
-      }
-  int64_t reach = n;
-  for (int i = 0; i < D; ++i) {
-    if (size[i] <= 1) continue;
-    if (stride[i] < reach) return false;
-    reach += stride[i] * (size[i] - 1);
-  }
-  return true;
 }
 
 // Whether two strided gradients, each without shared addresses and dk's first value `apart` after

@@ -1,0 +1,33 @@
+// Internal interface of the gated delta rule (include/ssscan.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <cstdint>
+
+namespace ssscan {
+
+// Strides in elements: batch row, token, head.
+struct GdrArgs {
+  int64_t batch;
+  int64_t seqlen;
+  int32_t hk, hv;        // key heads; value heads, a multiple of them
+  int32_t dk, dv;
+  int32_t io;            // IoType
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t qs[3], ks[3], vs[3];
+  const float* g;        // (batch, seqlen, hv), nullable
+  const float* beta;
+  const float* h0;       // (batch, hv, dk, dv), nullable
+  void* o;               // (batch, seqlen, hv, dv)
+  float* h_final;        // nullable
+};
+
+// Token by token, the state in registers: one token of a serving loop, and short sequences.
+hipError_t launch_gdr_recur(const GdrArgs& a, hipStream_t s);
+// Workgroups of its launch.
+int64_t gdr_recur_blocks(int64_t batch, int hv, int dv);
+
+}  // namespace ssscan
