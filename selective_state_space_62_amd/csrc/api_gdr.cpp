@@ -98,8 +98,25 @@ GdrArgs make_args(const Inputs& in) {
 
 ss_status check_blocks(int64_t blocks) {
   if (blocks >= kMaxBlocks)
-    return record_error(SS_ERR_UNSUPPORTED, "%lld workgroups (of batch rows, heads and columns) exceed 2^23", (long long)blocks);
+    return record_error(SS_ERR_UNSUPPORTED, "2^23 workgroups (of batch rows, heads, and columns or 64 tokens) and more are not supported");
   return SS_OK;
+}
+
+// Up to this many tokens go one by one.
+constexpr int64_t kRecurTokens = 16;
+
+int64_t chunks_of(int64_t seqlen) { return (seqlen + kGdrChunk - 1) / kGdrChunk; }
+
+// Scratch of the chunked forward: the inverses, then the vectors.
+struct FwdLayout {
+  size_t vecs, total;
+};
+
+FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v) {
+  FwdLayout l;
+  l.vecs = round256(gdr_tri_bytes(batch, seqlen, heads_v));
+  l.total = l.vecs + round256(gdr_vecs_bytes(batch, seqlen, heads_v));
+  return l;
 }
 
 }  // namespace
@@ -107,8 +124,8 @@ ss_status check_blocks(int64_t blocks) {
 extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
-  if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK) return 0;
-  return 0;
+  if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen <= kRecurTokens) return 0;
+  return fwd_layout(batch, seqlen, heads_v).total;
 }
 
 ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
@@ -133,11 +150,21 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     if (h_final) e = h0 ? launch_copy_state(state_numel(in), h0, h_final, s) : launch_fill_zero(h_final, state_numel(in), s);
     return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
   }
-  if ((st = check_blocks(gdr_recur_blocks(batch, heads_v, dim_v))) != SS_OK) return st;
+  const bool one_by_one = seqlen <= kRecurTokens;
+  if ((st = check_blocks(one_by_one ? gdr_recur_blocks(batch, heads_v, dim_v) : batch * heads_v * chunks_of(seqlen))) != SS_OK)
+    return st;
   GdrArgs a = make_args(in);
   a.o = o;
   a.h_final = h_final;
-  e = launch_gdr_recur(a, s);
+  if (one_by_one) {
+    e = launch_gdr_recur(a, s);
+  } else {
+    a.chunks = chunks_of(seqlen);
+    a.tri = workspace;
+    a.vecs = reinterpret_cast<float*>(static_cast<char*>(workspace) + fwd_layout(batch, seqlen, heads_v).vecs);
+    e = launch_gdr_prep(a, s);
+    if (e == hipSuccess) e = launch_gdr_chunk(a, s);
+  }
   return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule launch");
 }
 

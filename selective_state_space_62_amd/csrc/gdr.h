@@ -6,6 +6,9 @@
 
 namespace ssscan {
 
+// Tokens that the chunked kernels take at once.
+constexpr int kGdrChunk = 64;
+
 // Strides in elements: batch row, token, head.
 struct GdrArgs {
   int64_t batch;
@@ -23,7 +26,17 @@ struct GdrArgs {
   const float* h0;       // (batch, hv, dk, dv), nullable
   void* o;               // (batch, seqlen, hv, dv)
   float* h_final;        // nullable
+  // chunked: what the preparation leaves for every (batch row, head, chunk)
+  int64_t chunks;        // of a row
+  void* tri;             // operand blocks of the inverse
+  float* vecs;           // kVecs vectors
 };
+
+// Chunk by chunk on the matrix cores: what needs no state for all chunks at once, then the states in turn.
+size_t gdr_tri_bytes(int64_t batch, int64_t seqlen, int hv);
+size_t gdr_vecs_bytes(int64_t batch, int64_t seqlen, int hv);
+hipError_t launch_gdr_prep(const GdrArgs& a, hipStream_t s);
+hipError_t launch_gdr_chunk(const GdrArgs& a, hipStream_t s);
 
 // Token by token, the state in registers: one token of a serving loop, and short sequences.
 hipError_t launch_gdr_recur(const GdrArgs& a, hipStream_t s);
