@@ -102,8 +102,18 @@ ss_status check_blocks(int64_t blocks) {
   return SS_OK;
 }
 
-// Up to this many tokens go one by one.
+// Up to this many tokens go one by one, and tokens so far apart that 64 of them pass 2^31 bytes.
 constexpr int64_t kRecurTokens = 16;
+constexpr int64_t kMostStride = int64_t(1) << 22;
+
+bool one_by_one(const Inputs& in) {
+  return in.seqlen <= kRecurTokens || in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride;
+}
+
+bool aligned_rows(const void* p, const int64_t* st, ss_dtype io) {
+  const int64_t eb = elem_bytes(io);
+  return aligned(p, 4) && st[0] * eb % 4 == 0 && st[1] * eb % 4 == 0 && st[2] * eb % 4 == 0;
+}
 
 int64_t chunks_of(int64_t seqlen) { return (seqlen + kGdrChunk - 1) / kGdrChunk; }
 
@@ -150,16 +160,17 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     if (h_final) e = h0 ? launch_copy_state(state_numel(in), h0, h_final, s) : launch_fill_zero(h_final, state_numel(in), s);
     return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
   }
-  const bool one_by_one = seqlen <= kRecurTokens;
-  if ((st = check_blocks(one_by_one ? gdr_recur_blocks(batch, heads_v, dim_v) : batch * heads_v * chunks_of(seqlen))) != SS_OK)
+  const bool recur = one_by_one(in);
+  if ((st = check_blocks(recur ? gdr_recur_blocks(batch, heads_v, dim_v) : batch * heads_v * chunks_of(seqlen))) != SS_OK)
     return st;
   GdrArgs a = make_args(in);
   a.o = o;
   a.h_final = h_final;
-  if (one_by_one) {
+  if (recur) {
     e = launch_gdr_recur(a, s);
   } else {
     a.chunks = chunks_of(seqlen);
+    a.whole = dim_k % 8 == 0 && aligned_rows(q, q_stride, io) && aligned_rows(k, k_stride, io);
     a.tri = workspace;
     a.vecs = reinterpret_cast<float*>(static_cast<char*>(workspace) + fwd_layout(batch, seqlen, heads_v).vecs);
     e = launch_gdr_prep(a, s);

@@ -15,20 +15,19 @@ using namespace gdr;
 constexpr int kThreads = 256;
 constexpr int kCols = 128;               // of a workgroup
 
-template <typename IO, int KP>
-__global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
+template <typename IO, int KP, bool WHOLE>
+__global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) void gdr_chunk_kernel(GdrArgs a) {
   using T = typename IO::T;
-  constexpr int NP = planes_of<IO>(), kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
+  // What leads to O alone is rounded to bf16 where the I/O is: there one fp16 plane (2^-12) of S, U and P does.
+  constexpr int NP = planes_of<IO>(), NO = NP, kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
   __shared__ alignas(16) char s_k[NP][2 * kSteps * kBlock], s_q[NP][2 * kSteps * kBlock], s_kt[NP][kTiles * 4 * kBlock];
-  __shared__ alignas(16) char s_t[kTBlocks * 1024], s_p[kTBlocks * 1024];
+  __shared__ alignas(16) char s_t[kTBlocks * 1024], s_p[NO][kTBlocks * 512];
   __shared__ alignas(16) float s_vec[kVecs][kC], s_qinv[kC];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, half = lane >> 5, low = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t bh = blockIdx.x;
   const int64_t b = bh / a.hv;
   const int h = (int)(bh - b * a.hv), hkey = h / (a.hv / a.hk);
   const int col0 = blockIdx.y * kCols + 32 * wave;
-  const bool active = col0 < a.dv;
-  const int col = col0 + low;
 
   const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hkey * a.qs[2];
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hkey * a.ks[2];
@@ -36,45 +35,66 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
 
   acc16 st[kTiles];                      // the state is st 2^ce
   int ce = 0;
+  {
+    const int lane = threadIdx.x & 63, col = col0 + (lane & 31);
+    const float* h0 = a.h0 + bh * a.dk * a.dv;
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+    for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = 32 * m + tile_row(r, lane);
-      st[m][r] = a.h0 && row < a.dk && col < a.dv ? a.h0[(bh * a.dk + row) * a.dv + col] : 0.0f;
-    }
+      for (int r = 0; r < 16; ++r) {
+        const int row = 32 * m + tile_row(r, lane);
+        st[m][r] = a.h0 && row < a.dk && col < a.dv ? h0[(uint32_t)(row * a.dv + col)] : 0.0f;
+      }
+  }
 
-  // what this thread brings of the next chunk: 4 tokens by 8 values of k, a quarter of a token's runs of q
-  const int kg = tid & 15, kc = tid >> 4, qtok = tid >> 2, qsub = tid & 3;
+  // What this thread brings of a chunk: 4 tokens by 8 values of k, a quarter of a token's runs of q, its share of T and of
+  // the vectors.
+  const uint32_t krow = (uint32_t)a.ks[1] * sizeof(T), qrow = (uint32_t)a.qs[1] * sizeof(T), vrow = (uint32_t)a.vs[1] * sizeof(T);
   Raw8<IO> rk[4], rq[kRuns];
   uint4 rt[3];
   float4 rs;
   float rv[3];
   auto fetch = [&](int64_t chunk) {
-    const int64_t first = chunk * kC;
-    const int valid = a.seqlen - first < kC ? (int)(a.seqlen - first) : kC;
-    const int64_t at = bh * a.chunks + chunk;
+    const int tid = anew(threadIdx.x), kg = tid & 15, kc = tid >> 4, qtok = tid >> 2, qsub = tid & 3;
+    const int64_t first = chunk * kC, at = bh * a.chunks + chunk;
+    const int valid = (int)min(a.seqlen - first, (int64_t)kC);
     const float* vec = a.vecs + at * (kVecs * kC);
+    const __amdgpu_buffer_rsrc_t kr = chunk_rows<IO>(k + first * a.ks[1], a.ks[1], valid, a.dk);
+    const __amdgpu_buffer_rsrc_t qr = chunk_rows<IO>(q + first * a.qs[1], a.qs[1], valid, a.dk);
     if (kc < KP / 8) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        rk[t] = load_raw8<IO>(k + (first + 4 * kg + t) * a.ks[1], 8 * kc, 4 * kg + t < valid ? a.dk : 0);
+      for (int t = 0; t < 4; ++t) rk[t] = buf_load8<IO, WHOLE>(kr, 4 * kg * krow, t * here(krow), 8 * kc, a.dk);
       rs = *reinterpret_cast<const float4*>(vec + kVecS * kC + 4 * kg);
     }
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) rq[r] = load_raw8<IO>(q + (first + qtok) * a.qs[1], 8 * (qsub + 4 * r), qtok < valid ? a.dk : 0);
+    for (int r = 0; r < kRuns; ++r) rq[r] = buf_load8<IO, WHOLE>(qr, qtok * qrow, 0, 8 * (qsub + 4 * r), a.dk);
     const uint4* tri = reinterpret_cast<const uint4*>(static_cast<const _Float16*>(a.tri) + at * kTHalfs);
 #pragma unroll
     for (int i = 0; i < 3; ++i) rt[i] = tri[tid + kThreads * i];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (tid + kThreads * i < kVecs * kC) rv[i] = vec[tid + kThreads * i];
+    for (int i = 0; i < 3; ++i) rv[i] = vec[min(tid + kThreads * i, kVecs * kC - 1)];
+  };
+  // V, as the result tiles stand; columns behind the last repeat it
+  T rvv[2][16];
+  auto fetch_v = [&](int64_t chunk) {
+    const int lane = anew(threadIdx.x & 63), col = col0 + (lane & 31);
+    const uint32_t vcol = 4 * (lane >> 5) * vrow + (uint32_t)(col < a.dv ? col : a.dv - 1) * sizeof(T);
+    const int64_t first = chunk * kC;
+    const int valid = (int)min(a.seqlen - first, (int64_t)kC);
+    const uint32_t row = here(vrow);
+    const __amdgpu_buffer_rsrc_t vr = chunk_rows<IO>(v + first * a.vs[1], a.vs[1], valid, a.dv);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) rvv[i][r] = buf_load1<IO>(vr, vcol, (32 * i + tile_row(r, 0)) * row);
   };
 
   fetch(0);
   for (int64_t chunk = 0; chunk < a.chunks; ++chunk) {
     const int64_t first = chunk * kC;
     const int valid = a.seqlen - first < kC ? (int)(a.seqlen - first) : kC;
+    const int tid = anew(threadIdx.x), lane = tid & 63, half = lane >> 5, low = lane & 31;
+    const int kg = tid & 15, kc = tid >> 4, qtok = tid >> 2, qsub = tid & 3;
     __syncthreads();
     if (kc < KP / 8) {
       const float s[4] = {rs.x, rs.y, rs.z, rs.w};
@@ -119,34 +139,15 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
     for (int i = 0; i < 3; ++i)
       if (tid + kThreads * i < kVecs * kC) (&s_vec[0][0])[tid + kThreads * i] = rv[i];
     __syncthreads();
-    if (chunk + 1 < a.chunks) fetch(chunk + 1);
-
-    // V, as the result tiles stand.  Rows behind the last token repeat it (their beta is 0), columns behind the last the last.
-    float vx[2][16];
-    if (active) {
-      const T* vc = v + first * a.vs[1] + (col < a.dv ? col : a.dv - 1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int row = 32 * i + tile_row(r, lane);
-          vx[i][r] = load_one<IO>(vc + (row < valid ? row : valid - 1) * a.vs[1], 0);
-        }
-    }
-
+    fetch_v(chunk);
     // P, a tile to a wave, transposed: a lane has a query i and 16 keys j
     if (wave < 3) {
       const int ti = wave > 0, tj = wave > 1;
       acc16 acc = zero16();
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        Planes x, y;
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-          (n ? x.lo : x.hi) = *reinterpret_cast<const h8*>(s_k[n] + (tj * kSteps + s) * kBlock + lane * 16);
-          (n ? y.lo : y.hi) = *reinterpret_cast<const h8*>(s_q[n] + (ti * kSteps + s) * kBlock + lane * 16);
-        }
-        acc = mm<NP, NP>(x, y, acc);
+        acc = mm<NP, NP>(operand<NP>(s_k[0] + (tj * kSteps + s) * kBlock, lane, sizeof(s_k[0])),
+                         operand<NP>(s_q[0] + (ti * kSteps + s) * kBlock, lane, sizeof(s_q[0])), acc);
       }
       const int i = 32 * ti + low;
       const float hi = s_vec[kVecHi][i] - s_vec[kVecGrow][i], lo = s_vec[kVecLo][i];
@@ -158,65 +159,64 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const Planes p = split(acc, s, 1.0f);
-        *reinterpret_cast<h8*>(s_p + ((wave * 2 + s) * 2 + 0) * 1024 + lane * 16) = p.hi;
-        *reinterpret_cast<h8*>(s_p + ((wave * 2 + s) * 2 + 1) * 1024 + lane * 16) = p.lo;
+        const Planes p = split<NO>(acc, s, 1.0f);
+        *reinterpret_cast<h8*>(s_p[0] + (wave * 2 + s) * 1024 + lane * 16) = p.hi;
+        if constexpr (NO == 2) *reinterpret_cast<h8*>(s_p[NO - 1] + (wave * 2 + s) * 1024 + lane * 16) = p.lo;
       }
     }
 
-    acc16 R[2] = {zero16(), zero16()}, O[2] = {zero16(), zero16()}, U[2] = {zero16(), zero16()};
+    acc16 R[2], O[2], U[2];
+    Planes sp[kSteps];
     float mS = 0.0f;
     int er = 0, es = 0;
-    if (active) {
+    {
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) mS = max_of(st[m], mS);
       mS = wave_max(mS);
       const Scale cs = scale_of(mS, 100);
       es = cs.e;
+      R[0] = R[1] = zero16();
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const Planes sp = split(st[s >> 1], s & 1, cs.f);
+        sp[s] = split(st[s >> 1], s & 1, cs.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          Planes x, y;
-#pragma unroll
-          for (int n = 0; n < NP; ++n) {
-            (n ? x.lo : x.hi) = *reinterpret_cast<const h8*>(s_k[n] + (i * kSteps + s) * kBlock + lane * 16);
-            (n ? y.lo : y.hi) = *reinterpret_cast<const h8*>(s_q[n] + (i * kSteps + s) * kBlock + lane * 16);
-          }
-          R[i] = mm<NP, 2>(x, sp, R[i]);
-          O[i] = mm<2, NP>(sp, y, O[i]);
-        }
+        for (int i = 0; i < 2; ++i) R[i] = mm<NP, 2>(operand<NP>(s_k[0] + (i * kSteps + s) * kBlock, lane, sizeof(s_k[0])), sp[s], R[i]);
+        if (s & 1) step_end();
       }
       const float back = pow2(ce - es);
-      float mR = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int row = 32 * i + tile_row(r, lane);
-          R[i][r] = s_vec[kVecF1][row] * vx[i][r] - s_vec[kVecF2][row] * (back * R[i][r]);
+          R[i][r] = s_vec[kVecF1][row] * load_one<IO>(&rvv[i][r], 0) - s_vec[kVecF2][row] * (back * R[i][r]);
         }
-        mR = max_of(R[i], mR);
-      }
-      const Scale cr = scale_of(wave_max(mR), 100);
+    }
+    if (chunk + 1 < a.chunks) fetch(chunk + 1);
+    {
+      const Scale cr = scale_of(wave_max(max_of(R[1], max_of(R[0], 0.0f))), 100);
       er = cr.e;
+      U[0] = U[1] = zero16();
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const Planes rp = split(R[s >> 1], s & 1, cr.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i == 0 && s >= 2) continue;
+        for (int i = s >> 1; i < 2; ++i) {
           const int blk = (i + (s >> 1)) * 2 + (s & 1);    // tiles (0, 0), (1, 0), (1, 1)
-          Planes t;
-          t.hi = *reinterpret_cast<const h8*>(s_t + (blk * 2 + 0) * 1024 + lane * 16);
-          t.lo = *reinterpret_cast<const h8*>(s_t + (blk * 2 + 1) * 1024 + lane * 16);
-          U[i] = mm<2, 2>(t, rp, U[i]);
+          U[i] = mm<2, 2>(operand<2>(s_t + blk * 2048, lane, 1024), rp, U[i]);
         }
+        step_end();
       }
     }
     __syncthreads();                                       // P stands
-    if (active) {
+    {
+      O[0] = O[1] = zero16();
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) O[i] = mm<NO, NP>(sp[s], operand<NP>(s_q[0] + (i * kSteps + s) * kBlock, lane, sizeof(s_q[0])), O[i]);
+        if (s & 1) step_end();
+      }
       const int lsk = exponent(s_vec[kVecS][0]) - (int)s_vec[kVecRel][0];
       const Scale cu = scale_of(wave_max(max_of(U[1], max_of(U[0], 0.0f))), min(20, 40 - (ce - es + er + lsk)));
       const float join = pow2(ce - es + er + lsk + cu.e);
@@ -229,16 +229,11 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
       }
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const Planes up = split(U[s >> 1], s & 1, cu.f);
+        const Planes up = split<NO>(U[s >> 1], s & 1, cu.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i == 0 && s >= 2) continue;
-          const int blk = (i + (s >> 1)) * 2 + (s & 1);
-          Planes p;
-          p.hi = *reinterpret_cast<const h8*>(s_p + (blk * 2 + 0) * 1024 + lane * 16);
-          p.lo = *reinterpret_cast<const h8*>(s_p + (blk * 2 + 1) * 1024 + lane * 16);
-          O[i] = mm<2, 2>(up, p, O[i]);
-        }
+        for (int i = s >> 1; i < 2; ++i)
+          O[i] = mm<NO, NO>(up, operand<NO>(s_p[0] + ((i + (s >> 1)) * 2 + (s & 1)) * 1024, lane, sizeof(s_p[0])), O[i]);
+        step_end();
       }
       float mE = 0.0f;
 #pragma unroll
@@ -259,12 +254,9 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
       for (int s = 0; s < 4; ++s) {
         const Planes up = split(U[s >> 1], s & 1, ue.f);
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          Planes x;
-#pragma unroll
-          for (int n = 0; n < NP; ++n) (n ? x.lo : x.hi) = *reinterpret_cast<const h8*>(s_kt[n] + (m * 4 + s) * kBlock + lane * 16);
-          st[m] = mm<NP, 2>(x, up, st[m]);
-        }
+        for (int m = 0; m < kTiles; ++m)
+          st[m] = mm<NP, 2>(operand<NP>(s_kt[0] + (m * 4 + s) * kBlock, lane, sizeof(s_kt[0])), up, st[m]);
+        step_end();
       }
       // O, transposed: a lane has a token and runs of four columns
 #pragma unroll
@@ -294,14 +286,16 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
       ce = -(er + ue.e);
     }
   }
+  const int lane = anew(threadIdx.x & 63), col = col0 + (lane & 31);
   if (a.h_final && col < a.dv) {
     const float f = pow2(ce);
+    float* hf = a.h_final + bh * a.dk * a.dv;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 32 * m + tile_row(r, lane);
-        if (row < a.dk) a.h_final[(bh * a.dk + row) * a.dv + col] = st[m][r] * f;
+        if (row < a.dk) hf[(uint32_t)(row * a.dv + col)] = st[m][r] * f;
       }
   }
 }
@@ -309,11 +303,9 @@ __global__ __launch_bounds__(kThreads) void gdr_chunk_kernel(GdrArgs a) {
 template <typename IO>
 hipError_t launch(const GdrArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.hv), (unsigned)((a.dv + kCols - 1) / kCols));
-  if (a.dk <= 32) gdr_chunk_kernel<IO, 32><<<grid, kThreads, 0, s>>>(a);
-  else if (a.dk <= 64) gdr_chunk_kernel<IO, 64><<<grid, kThreads, 0, s>>>(a);
-  else if (a.dk <= 96) gdr_chunk_kernel<IO, 96><<<grid, kThreads, 0, s>>>(a);
-  else gdr_chunk_kernel<IO, 128><<<grid, kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
+    gdr_chunk_kernel<IO, decltype(kp)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>(a);
+  });
 }
 
 }  // namespace

@@ -12,6 +12,8 @@
 // that stands in LDS or memory stands in that order: one block of 64 lanes times 8 values for 32 rows by 16 columns.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "gdr.h"
 #include "internal.h"
@@ -46,14 +48,15 @@ __device__ __forceinline__ acc16 mm(const Planes& a, const Planes& b, acc16 acc)
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a.hi, b.hi, acc, 0, 0, 0);
 }
 
-// Values 8 half .. 8 half + 7 of a result tile as an operand, scaled.
+// Values 8 half .. 8 half + 7 of a result tile as an operand of N planes, scaled.
+template <int N = 2>
 __device__ __forceinline__ Planes split(const acc16& v, int half, float s) {
   Planes p;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x = v[8 * half + j];
     p.hi[j] = (_Float16)(x * s);
-    p.lo[j] = (_Float16)fmaf(x, s, -(float)p.hi[j]);
+    if constexpr (N == 2) p.lo[j] = (_Float16)fmaf(x, s, -(float)p.hi[j]);
   }
   return p;
 }
@@ -65,19 +68,32 @@ __device__ __forceinline__ acc16 zero16() {
   return z;
 }
 
+// The operand block of this lane in LDS, in N planes (of which lo is `apart` bytes behind hi).
+template <int N>
+__device__ __forceinline__ Planes operand(const char* p, int lane, int apart) {
+  Planes o;
+  o.hi = *reinterpret_cast<const h8*>(p + lane * 16);
+  if constexpr (N == 2) o.lo = *reinterpret_cast<const h8*>(p + apart + lane * 16);
+  return o;
+}
+
+// Nothing is moved over this line: the steps of a product keep their loads one step ahead, and no more of them, in registers.
+__device__ __forceinline__ void step_end() { __builtin_amdgcn_sched_barrier(0); }
+
 // Row (of 32) of register r in a result tile.
 __device__ __forceinline__ int tile_row(int r, int lane) { return (r & 3) + 8 * (r >> 2) + 4 * (lane >> 5); }
 
-// Largest |value| over the wave, NaN left out.
+// Largest of nonnegative values over the wave, NaN left out, in a scalar register: quad permutes and mirrors of 8 and of
+// 16 lanes, then the four rows' (as integers, which order nonnegative floats as they are).
 __device__ __forceinline__ float wave_max(float v) {
-  // quad permutes, mirrors of 8 and of 16 lanes, then exchanges across rows
   v = fmaxf(v, __builtin_amdgcn_update_dpp(0.0f, v, 0xB1, 0xf, 0xf, false));
   v = fmaxf(v, __builtin_amdgcn_update_dpp(0.0f, v, 0x4E, 0xf, 0xf, false));
   v = fmaxf(v, __builtin_amdgcn_update_dpp(0.0f, v, 0x141, 0xf, 0xf, false));
   v = fmaxf(v, __builtin_amdgcn_update_dpp(0.0f, v, 0x140, 0xf, 0xf, false));
-  v = fmaxf(v, __shfl_xor(v, 16));
-  v = fmaxf(v, __shfl_xor(v, 32));
-  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+  const int i = __float_as_int(v);
+  const int a = __builtin_amdgcn_readlane(i, 0), b = __builtin_amdgcn_readlane(i, 16);
+  const int c = __builtin_amdgcn_readlane(i, 32), d = __builtin_amdgcn_readlane(i, 48);
+  return __int_as_float(max(max(a, b), max(c, d)));
 }
 
 __device__ __forceinline__ float max_of(const acc16& v, float m) {
@@ -127,33 +143,66 @@ struct __attribute__((packed, aligned(sizeof(typename IO::T)))) Raw8 {
   uint32_t w[8 * sizeof(typename IO::T) / 4];
 };
 
-// Values at .. at + 7 of a row of n, zeros from n on.
+// Rows of a chunk as a buffer: what lies behind the last token reads as zero, and a row is a 32-bit offset away (the host sees
+// to it that 64 rows stay below 2^31 bytes).
 template <typename IO>
-__device__ __forceinline__ Raw8<IO> load_raw8(const typename IO::T* __restrict__ row, int at, int n) {
-  if (at + 8 <= n) return *reinterpret_cast<const Raw8<IO>*>(row + at);
-  Raw8<IO> r;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const typename IO::T* base, int64_t stride, int valid, int n) {
+  return make_rsrc(base, ((valid - 1) * stride + n) * (int64_t)sizeof(typename IO::T));
+}
+
+constexpr uint32_t kNowhere = 0x80000000u;    // an offset behind every such buffer
+
+// Values at .. at + 7 of the row at byte offset voff + soff, zeros from n on.  WHOLE: n is a multiple of 8 and rows are aligned
+// to 4 bytes.
+template <typename IO, bool WHOLE>
+__device__ __forceinline__ Raw8<IO> buf_load8(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, int at, int n) {
+  constexpr int kSize = sizeof(typename IO::T);
+  Raw8<IO> o;
+  if constexpr (WHOLE) {
+    const uint32_t off = at < n ? voff + at * kSize : kNowhere;
 #pragma unroll
-  for (int j = 0; j < (int)(sizeof(r.w) / 4); ++j) r.w[j] = 0u;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (at + j < n) {
-      if constexpr (IO::kPerSpan == 4) r.w[j] = __float_as_uint(row[at + j]);
-      else r.w[j >> 1] |= (uint32_t)row[at + j] << ((j & 1) * 16);
+    for (int w = 0; w < (int)sizeof(o) / 4; w += 4) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off + w * 4, soff, 0);
+      o.w[w] = v[0]; o.w[w + 1] = v[1]; o.w[w + 2] = v[2]; o.w[w + 3] = v[3];
     }
-  return r;
+    return o;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t off = at + j < n ? voff + (at + j) * kSize : kNowhere;
+    if constexpr (kSize == 4) {
+      o.w[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, soff, 0);
+    } else {
+      const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, soff, 0);
+      o.w[j >> 1] = j & 1 ? o.w[j >> 1] | v << 16 : v;
+    }
+  }
+  return o;
+}
+
+// The value again, in a scalar register that nothing formed from it leaves the loop around: products with it are formed where they
+// are used instead of being kept.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// The same for a lane's value.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+template <typename IO>
+__device__ __forceinline__ typename IO::T buf_load1(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  if constexpr (IO::kPerSpan == 4) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0));
+  else return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
 }
 
 template <typename IO>
 __device__ __forceinline__ float raw_value(const Raw8<IO>& r, int j) {
   if constexpr (IO::kPerSpan == 4) return __uint_as_float(r.w[j]);
   else return (j & 1) ? __uint_as_float(r.w[j >> 1] & 0xffff0000u) : __uint_as_float(r.w[j >> 1] << 16);
-}
-
-template <typename IO>
-__device__ __forceinline__ void load8(const typename IO::T* __restrict__ row, int at, int n, float (&x)[8]) {
-  const Raw8<IO> r = load_raw8<IO>(row, at, n);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = raw_value<IO>(r, j);
 }
 
 // Run c (8 values, of index 8 c on) of row `row` (0..63) into the operand blocks of a chunk's rows: tiles of 32 rows,
@@ -172,6 +221,21 @@ __device__ __forceinline__ void store_operand_rows(char* hi, char* lo, int row, 
     *reinterpret_cast<h4*>(p + 512 * h) = v;
     if constexpr (planes_of<IO>() == 2) *reinterpret_cast<h4*>(p + (lo - hi) + 512 * h) = w;
   }
+}
+
+// f with dk as the kernels pad it, and whether whole runs of 8 values can be loaded.
+template <typename F>
+hipError_t by_keys(int dk, bool whole, F f) {
+  using std::integral_constant;
+  auto g = [&](auto kp) {
+    if (whole) f(kp, integral_constant<bool, true>());
+    else f(kp, integral_constant<bool, false>());
+  };
+  if (dk <= 32) g(integral_constant<int, 32>());
+  else if (dk <= 64) g(integral_constant<int, 64>());
+  else if (dk <= 96) g(integral_constant<int, 96>());
+  else g(integral_constant<int, 128>());
+  return hipGetLastError();
 }
 
 // The vectors that belong to a chunk of a head, kC floats each, as the preparation leaves them.  c_j scales column j of

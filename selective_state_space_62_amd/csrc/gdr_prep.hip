@@ -17,7 +17,7 @@ using namespace gdr;
 constexpr int kThreads = 256;
 constexpr int kPitch = 68;               // floats of a row in LDS
 
-template <typename IO, int KP>
+template <typename IO, int KP, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   using T = typename IO::T;
   constexpr int NP = planes_of<IO>(), kSteps = KP / 16, kRuns = KP / 32;
@@ -35,14 +35,20 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   // four lanes to a token, each every fourth run of 8 values
   {
     const int tok = tid >> 2, sub = tid & 3;
-    const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + (first + tok) * a.ks[1] + hkey * a.ks[2];
+    const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + first * a.ks[1] + hkey * a.ks[2];
+    const __amdgpu_buffer_rsrc_t kr = chunk_rows<IO>(k, a.ks[1], valid, a.dk);
+    Raw8<IO> raw[kRuns];
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r)
+      raw[r] = buf_load8<IO, WHOLE>(kr, tok * (uint32_t)a.ks[1] * sizeof(T), 0, 8 * (sub + 4 * r), a.dk);
     float x[kRuns][8], m = 0.0f;
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      load8<IO>(k, 8 * (sub + 4 * r), tok < valid ? a.dk : 0, x[r]);
+    for (int r = 0; r < kRuns; ++r)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[r][j]));
-    }
+      for (int j = 0; j < 8; ++j) {
+        x[r][j] = raw_value<IO>(raw[r], j);
+        m = fmaxf(m, fabsf(x[r][j]));
+      }
     m = quad_max(m);
     const float s = row_scale(m);
     if (sub == 0) s_scale[tok] = s;
@@ -224,11 +230,9 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
 template <typename IO>
 hipError_t launch(const GdrArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.hv * a.chunks));
-  if (a.dk <= 32) gdr_prep_kernel<IO, 32><<<grid, kThreads, 0, s>>>(a);
-  else if (a.dk <= 64) gdr_prep_kernel<IO, 64><<<grid, kThreads, 0, s>>>(a);
-  else if (a.dk <= 96) gdr_prep_kernel<IO, 96><<<grid, kThreads, 0, s>>>(a);
-  else gdr_prep_kernel<IO, 128><<<grid, kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
+    gdr_prep_kernel<IO, decltype(kp)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>(a);
+  });
 }
 
 }  // namespace
