@@ -170,7 +170,8 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     e = launch_gdr_recur(a, s);
   } else {
     a.chunks = chunks_of(seqlen);
-    a.whole = dim_k % 8 == 0 && aligned_rows(q, q_stride, io) && aligned_rows(k, k_stride, io);
+    a.whole = dim_k % 8 == 0 && dim_v % 8 == 0 && aligned_rows(q, q_stride, io) && aligned_rows(k, k_stride, io) &&
+              aligned_rows(v, v_stride, io);
     a.tri = workspace;
     a.vecs = reinterpret_cast<float*>(static_cast<char*>(workspace) + fwd_layout(batch, seqlen, heads_v).vecs);
     e = launch_gdr_prep(a, s);

@@ -28,7 +28,7 @@ struct GdrArgs {
   float* h_final;        // nullable
   // chunked: what the preparation leaves for every (batch row, head, chunk)
   int64_t chunks;        // of a row
-  int32_t whole;         // dk is a multiple of 8 and the rows of q and k are aligned to 4 bytes
+  int32_t whole;         // dk and dv are multiples of 8 and the rows of q, k and v are aligned to 4 bytes
   void* tri;             // operand blocks of the inverse
   float* vecs;           // kVecs vectors
 };

@@ -22,7 +22,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   constexpr int NP = planes_of<IO>(), NO = NP, kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
   __shared__ alignas(16) char s_k[NP][2 * kSteps * kBlock], s_q[NP][2 * kSteps * kBlock], s_kt[NP][kTiles * 4 * kBlock];
   __shared__ alignas(16) char s_t[kTBlocks * 1024], s_p[NO][kTBlocks * 512];
-  __shared__ alignas(16) float s_vec[kVecs][kC], s_qinv[kC];
+  __shared__ alignas(16) float s_vecs[2][kVecs][kC], s_qinv[kC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t bh = blockIdx.x;
   const int64_t b = bh / a.hv;
@@ -48,12 +48,10 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   }
 
   // What this thread brings of a chunk: 4 tokens by 8 values of k, a quarter of a token's runs of q, its share of T and of
-  // the vectors.
+  // the vectors, those straight to LDS.
   const uint32_t krow = (uint32_t)a.ks[1] * sizeof(T), qrow = (uint32_t)a.qs[1] * sizeof(T), vrow = (uint32_t)a.vs[1] * sizeof(T);
   Raw8<IO> rk[4], rq[kRuns];
-  uint4 rt[3];
   float4 rs;
-  float rv[3];
   auto fetch = [&](int64_t chunk) {
     const int tid = anew(threadIdx.x), kg = tid & 15, kc = tid >> 4, qtok = tid >> 2, qsub = tid & 3;
     const int64_t first = chunk * kC, at = bh * a.chunks + chunk;
@@ -61,32 +59,27 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     const float* vec = a.vecs + at * (kVecs * kC);
     const __amdgpu_buffer_rsrc_t kr = chunk_rows<IO>(k + first * a.ks[1], a.ks[1], valid, a.dk);
     const __amdgpu_buffer_rsrc_t qr = chunk_rows<IO>(q + first * a.qs[1], a.qs[1], valid, a.dk);
-    if (kc < KP / 8) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) rk[t] = buf_load8<IO, WHOLE>(kr, 4 * kg * krow, t * here(krow), 8 * kc, a.dk);
-      rs = *reinterpret_cast<const float4*>(vec + kVecS * kC + 4 * kg);
-    }
+    for (int t = 0; t < 4; ++t) rk[t] = buf_load8<IO, WHOLE>(kr, 4 * kg * krow, t * here(krow), 8 * kc, a.dk);
+    rs = *reinterpret_cast<const float4*>(vec + kVecS * kC + 4 * kg);
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) rq[r] = buf_load8<IO, WHOLE>(qr, qtok * qrow, 0, 8 * (qsub + 4 * r), a.dk);
-    const uint4* tri = reinterpret_cast<const uint4*>(static_cast<const _Float16*>(a.tri) + at * kTHalfs);
+    const char* tri = static_cast<const char*>(a.tri) + at * (kTHalfs * 2) + tid * 16;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) rt[i] = tri[tid + kThreads * i];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) rv[i] = vec[min(tid + kThreads * i, kVecs * kC - 1)];
+    for (int i = 0; i < 3; ++i) load_to_lds(tri + 4096 * i, s_t + 4096 * i + wave * 1024);
+    if (wave < 3) load_to_lds(reinterpret_cast<const char*>(vec) + tid * 16, reinterpret_cast<char*>(&s_vecs[chunk & 1][0][0]) + wave * 1024);
   };
-  // V, as the result tiles stand; columns behind the last repeat it
-  T rvv[2][16];
+  // V, as it is turned
+  Raw8<IO> rvv[2][2];
   auto fetch_v = [&](int64_t chunk) {
-    const int lane = anew(threadIdx.x & 63), col = col0 + (lane & 31);
-    const uint32_t vcol = 4 * (lane >> 5) * vrow + (uint32_t)(col < a.dv ? col : a.dv - 1) * sizeof(T);
     const int64_t first = chunk * kC;
-    const int valid = (int)min(a.seqlen - first, (int64_t)kC);
-    const uint32_t row = here(vrow);
+    const int lane = anew(threadIdx.x & 63), valid = (int)min(a.seqlen - first, (int64_t)kC);
     const __amdgpu_buffer_rsrc_t vr = chunk_rows<IO>(v + first * a.vs[1], a.vs[1], valid, a.dv);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) rvv[i][r] = buf_load1<IO>(vr, vcol, (32 * i + tile_row(r, 0)) * row);
+      for (int s = 0; s < 2; ++s)
+        rvv[i][s] = buf_load8<IO, WHOLE>(vr, (32 * i + (lane & 31)) * vrow, 0, col0 + 16 * (lane >> 5) + 8 * s, a.dv);
   };
 
   fetch(0);
@@ -95,6 +88,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     const int valid = a.seqlen - first < kC ? (int)(a.seqlen - first) : kC;
     const int tid = anew(threadIdx.x), lane = tid & 63, half = lane >> 5, low = lane & 31;
     const int kg = tid & 15, kc = tid >> 4, qtok = tid >> 2, qsub = tid & 3;
+    const float(&s_vec)[kVecs][kC] = s_vecs[chunk & 1];
     __syncthreads();
     if (kc < KP / 8) {
       const float s[4] = {rs.x, rs.y, rs.z, rs.w};
@@ -133,11 +127,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
       for (int r = 0; r < kRuns; ++r) store_operand_rows<IO>(s_q[0], s_q[NP - 1], qtok, qsub + 4 * r, kSteps, x[r], s);
     }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) reinterpret_cast<uint4*>(s_t)[tid + kThreads * i] = rt[i];
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (tid + kThreads * i < kVecs * kC) (&s_vec[0][0])[tid + kThreads * i] = rv[i];
+    loads_stand();
     __syncthreads();
     fetch_v(chunk);
     // P, a tile to a wave, transposed: a lane has a query i and 16 keys j
@@ -150,11 +140,11 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
                          operand<NP>(s_q[0] + (ti * kSteps + s) * kBlock, lane, sizeof(s_q[0])), acc);
       }
       const int i = 32 * ti + low;
-      const float hi = s_vec[kVecHi][i] - s_vec[kVecGrow][i], lo = s_vec[kVecLo][i];
+      const float hi = s_vec[kVecHi][i], lo = s_vec[kVecLo][i];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int j = 32 * tj + tile_row(r, lane);
-        const float e = (hi - (s_vec[kVecHi][j] + s_vec[kVecRel][j])) + (lo - s_vec[kVecLo][j]);
+        const float e = (hi - s_vec[kVecHiJ][j]) + (lo - s_vec[kVecLoJ][j]);
         acc[r] = j <= i ? acc[r] * __builtin_amdgcn_exp2f(e) : 0.0f;
       }
 #pragma unroll
@@ -185,14 +175,15 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
       }
       const float back = pow2(ce - es);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        const acc16 V = turn<IO>(rvv[i], lane);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int row = 32 * i + tile_row(r, lane);
-          R[i][r] = s_vec[kVecF1][row] * load_one<IO>(&rvv[i][r], 0) - s_vec[kVecF2][row] * (back * R[i][r]);
+          R[i][r] = s_vec[kVecF1][row] * V[r] - s_vec[kVecF2][row] * (back * R[i][r]);
         }
+      }
     }
-    if (chunk + 1 < a.chunks) fetch(chunk + 1);
     {
       const Scale cr = scale_of(wave_max(max_of(R[1], max_of(R[0], 0.0f))), 100);
       er = cr.e;
@@ -210,6 +201,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     }
     __syncthreads();                                       // P stands
     {
+      if (chunk + 1 < a.chunks) fetch(chunk + 1);          // T has been read
       O[0] = O[1] = zero16();
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {

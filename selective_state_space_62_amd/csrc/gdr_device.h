@@ -193,10 +193,46 @@ __device__ __forceinline__ int anew(int v) {
   return v;
 }
 
+// 16 bytes of every lane's own from memory to LDS, to the wave's place there plus 16 times the lane, past the registers.  They stand
+// in LDS for the workgroup after loads_stand and a barrier.
+__device__ __forceinline__ void load_to_lds(const void* from, void* wave_place) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)wave_place, 16, 0, 0);
+}
+
+__device__ __forceinline__ void loads_stand() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+
+// A 32x32 tile as it is loaded, a lane a row and runs of 8 columns, into a result tile, by a product with the identity in bf16: an
+// fp32 value is the sum of three bf16 exactly.  Lane l brings columns 16 (l >> 5) + 8 s .. + 7 for s = 0, 1.
 template <typename IO>
-__device__ __forceinline__ typename IO::T buf_load1(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
-  if constexpr (IO::kPerSpan == 4) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0));
-  else return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+__device__ __forceinline__ acc16 turn(const Raw8<IO> (&x)[2], int lane) {
+  acc16 acc = zero16();
+  const int off = (lane & 31) - 16 * (lane >> 5);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    b8 one;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) one[j] = (__bf16)(off == 8 * s + j ? 1.0f : 0.0f);
+    if constexpr (IO::kPerSpan == 8) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, x[s]), one, acc, 0, 0, 0);
+    } else {
+      b8 p[3];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float v = __uint_as_float(x[s].w[j]);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+          p[n][j] = (__bf16)v;
+          v -= (float)p[n][j];
+        }
+      }
+#pragma unroll
+      for (int n = 2; n >= 0; --n) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(p[n], one, acc, 0, 0, 0);
+    }
+  }
+  return acc;
 }
 
 template <typename IO>
@@ -244,15 +280,17 @@ enum Vec {
   kVecF1,      // beta_j / c_j
   kVecF2,      // beta_j 2^gam_j / (c_j s_j)
   kVecEnd,     // 2^(gam_C - gam_j) / s_j
-  kVecHi,      // gam_j = hi + lo
+  kVecHi,      // gam_i - p_i = hi + lo, for i
   kVecLo,
+  kVecHiJ,     // gam_j + rel_j = hi + lo, for j
+  kVecLoJ,
   kVecRel,     // log2 of s_j over the chunk's smallest
   kVecInto,    // 2^gam_j
   kVecS,       // s_j
   kVecGrow,    // whole number p_i >= 0 with gam_i - gam_j - rel_j <= p_i for every j <= i: 0 where no gate grows
-  kVecBeta,    // beta_j
-  kVecs
+  kVecs = 12   // as far apart: a whole number of waves' 16-byte loads
 };
+static_assert(kVecGrow < kVecs && kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
 
 // The inverse's operand blocks: tiles (0, 0), (1, 0), (1, 1), of each two steps of 16, of each two planes.
 constexpr int kTBlocks = 3 * 2 * 2;

@@ -195,18 +195,20 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
       if (lane >= d) low = o < low ? o : low;
     }
     const double grow = ceil(gam - low);
-    const float hi = (float)gam;
+    const double pi = grow > 0.0 ? grow : 0.0, gi = gam - pi, gj = gam + (double)rel;
+    const float hi = (float)gi, hij = (float)gj;
     float* v = a.vecs + ((int64_t)blockIdx.x * kVecs) * kC + tid;
     v[kVecF1 * kC] = beta / c;
     v[kVecF2 * kC] = beta * into / c * inv_s;
     v[kVecEnd * kC] = __builtin_amdgcn_exp2f((float)(end - gam)) * inv_s;
     v[kVecHi * kC] = hi;
-    v[kVecLo * kC] = (float)(gam - (double)hi);
+    v[kVecLo * kC] = (float)(gi - (double)hi);
+    v[kVecHiJ * kC] = hij;
+    v[kVecLoJ * kC] = (float)(gj - (double)hij);
     v[kVecRel * kC] = rel;
     v[kVecInto * kC] = into;
     v[kVecS * kC] = s;
-    v[kVecGrow * kC] = grow > 0.0 ? (float)grow : 0.0f;
-    v[kVecBeta * kC] = beta;
+    v[kVecGrow * kC] = (float)pi;
   }
   __syncthreads();
   // tiles as operands: slot (tile, step, lane)
