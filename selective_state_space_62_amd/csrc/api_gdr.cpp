@@ -115,17 +115,24 @@ bool aligned_rows(const void* p, const int64_t* st, ss_dtype io) {
   return aligned(p, 4) && st[0] * eb % 4 == 0 && st[1] * eb % 4 == 0 && st[2] * eb % 4 == 0;
 }
 
+bool whole_runs(const Inputs& in) {
+  return in.dim_k % 8 == 0 && in.dim_v % 8 == 0 && aligned_rows(in.q, in.q_stride, in.io) &&
+         aligned_rows(in.k, in.k_stride, in.io) && aligned_rows(in.v, in.v_stride, in.io);
+}
+
 int64_t chunks_of(int64_t seqlen) { return (seqlen + kGdrChunk - 1) / kGdrChunk; }
 
-// Scratch of the chunked forward: the inverses, then the vectors.
+// Scratch of the chunked forward: the inverses, P, then the vectors.  P is taken as large as either I/O type needs it.
 struct FwdLayout {
-  size_t vecs, total;
+  size_t p, vecs, total;
 };
 
 FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v) {
+  const int64_t n = batch * heads_v * chunks_of(seqlen);
   FwdLayout l;
-  l.vecs = round256(gdr_tri_bytes(batch, seqlen, heads_v));
-  l.total = l.vecs + round256(gdr_vecs_bytes(batch, seqlen, heads_v));
+  l.p = round256(gdr_tri_bytes(n));
+  l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, false));
+  l.total = l.vecs + round256(gdr_vecs_bytes(n));
   return l;
 }
 
@@ -169,13 +176,15 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   if (recur) {
     e = launch_gdr_recur(a, s);
   } else {
+    const FwdLayout l = fwd_layout(batch, seqlen, heads_v);
+    char* ws = static_cast<char*>(workspace);
     a.chunks = chunks_of(seqlen);
-    a.whole = dim_k % 8 == 0 && dim_v % 8 == 0 && aligned_rows(q, q_stride, io) && aligned_rows(k, k_stride, io) &&
-              aligned_rows(v, v_stride, io);
-    a.tri = workspace;
-    a.vecs = reinterpret_cast<float*>(static_cast<char*>(workspace) + fwd_layout(batch, seqlen, heads_v).vecs);
-    e = launch_gdr_prep(a, s);
-    if (e == hipSuccess) e = launch_gdr_chunk(a, s);
+    a.whole = whole_runs(in);
+    a.tri = ws;
+    a.p = ws + l.p;
+    a.vecs = reinterpret_cast<float*>(ws + l.vecs);
+    e = launch_gdr_prep(a, false, s);
+    if (e == hipSuccess) e = launch_gdr_chunk(a, false, s);
   }
   return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule launch");
 }

@@ -29,15 +29,27 @@ struct GdrArgs {
   // chunked: what the preparation leaves for every (batch row, head, chunk)
   int64_t chunks;        // of a row
   int32_t whole;         // dk and dv are multiples of 8 and the rows of q, k and v are aligned to 4 bytes
-  void* tri;             // operand blocks of the inverse
+  void* tri;             // operand blocks of the inverse T
+  void* tri_t;           // backward: of T transposed
+  void* p;               // operand blocks of P; backward: of P transposed
   float* vecs;           // kVecs vectors
+  // backward, for every chunk of a head: rows of ldv columns (dv rounded up to tiles of 32), and of each tile the largest
+  // |value| (of every kind in a run of its own, max_apart floats behind the one before)
+  int64_t ldv;
+  float* states;         // the state before it
+  float* u;              // U
+  float* maxima;
+  int64_t max_apart;
 };
 
+enum GdrMax { kMaxS, kMaxU };
+
 // Chunk by chunk on the matrix cores: what needs no state for all chunks at once, then the states in turn.
-size_t gdr_tri_bytes(int64_t batch, int64_t seqlen, int hv);
-size_t gdr_vecs_bytes(int64_t batch, int64_t seqlen, int hv);
-hipError_t launch_gdr_prep(const GdrArgs& a, hipStream_t s);
-hipError_t launch_gdr_chunk(const GdrArgs& a, hipStream_t s);
+size_t gdr_tri_bytes(int64_t chunk_heads);                    // of tri, tri_t
+size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward);
+size_t gdr_vecs_bytes(int64_t chunk_heads);
+hipError_t launch_gdr_prep(const GdrArgs& a, bool backward, hipStream_t s);
+hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s);
 
 // Token by token, the state in registers: one token of a serving loop, and short sequences.
 hipError_t launch_gdr_recur(const GdrArgs& a, hipStream_t s);

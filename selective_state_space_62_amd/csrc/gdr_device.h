@@ -202,6 +202,24 @@ __device__ __forceinline__ void load_to_lds(const void* from, void* wave_place) 
 
 __device__ __forceinline__ void loads_stand() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// Values 8 c .. 8 c + 7 of tokens 4 g .. 4 g + 3 (as x[token][value], with a scale each) into the blocks of the transposed rows:
+// tiles of 32 values, of each four steps of 16 tokens.
+template <typename IO>
+__device__ __forceinline__ void store_operand_turned(char* hi, char* lo, int g, int c, const float (&x)[4][8], const float (&s)[4]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    char* p = hi + ((c >> 2) * 4 + (g >> 2)) * kBlock + (8 * (c & 3) + j + 32 * (g & 1)) * 16 + (g >> 1 & 1) * 8;
+    h4 v, w;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v[t] = (_Float16)(x[t][j] * s[t]);
+      if constexpr (planes_of<IO>() == 2) w[t] = (_Float16)fmaf(x[t][j], s[t], -(float)v[t]);
+    }
+    *reinterpret_cast<h4*>(p) = v;
+    if constexpr (planes_of<IO>() == 2) *reinterpret_cast<h4*>(p + (lo - hi)) = w;
+  }
+}
+
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 // A 32x32 tile as it is loaded, a lane a row and runs of 8 columns, into a result tile, by a product with the identity in bf16: an
@@ -233,6 +251,49 @@ __device__ __forceinline__ acc16 turn(const Raw8<IO> (&x)[2], int lane) {
     }
   }
   return acc;
+}
+
+// The identity as an operand whose summed index is in the order of a result's rows, step s of the tile.
+__device__ __forceinline__ h8 identity(int s, int lane) {
+  const int n = lane & 31, at = (n >> 4) == s && ((n >> 2) & 1) == (lane >> 5) ? ((n >> 3) & 1) * 4 + (n & 3) : -1;
+  h8 o;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = (_Float16)(at == j ? 1.0f : 0.0f);
+  return o;
+}
+
+// A result tile that has been split (both steps), back as fp32 and transposed: a lane has a row of the tile and 16 of its columns,
+// runs of four at 8 g + 4 (lane >> 5).
+template <int N = 2>
+__device__ __forceinline__ acc16 transposed(const Planes& p0, const Planes& p1, int lane) {
+  const h8 e0 = identity(0, lane), e1 = identity(1, lane);
+  acc16 acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p0.hi, e0, zero16(), 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p1.hi, e1, acc, 0, 0, 0);
+  if constexpr (N == 2) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p0.lo, e0, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p1.lo, e1, acc, 0, 0, 0);
+  }
+  return acc;
+}
+
+// Runs of four of such a lane's columns at `at`, times f, to a row of n in the I/O type.
+template <typename IO>
+__device__ __forceinline__ void store_runs(typename IO::T* row, int at, int n, const acc16& v, float f) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int c = at + 8 * g;
+    const float x[4] = {v[4 * g] * f, v[4 * g + 1] * f, v[4 * g + 2] * f, v[4 * g + 3] * f};
+    if (n % 4 == 0) {                                      // the tensor is 16-byte aligned: runs of four are too
+      if (c < n) {
+        if constexpr (IO::kPerSpan == 4) *reinterpret_cast<float4*>(row + c) = make_float4(x[0], x[1], x[2], x[3]);
+        else *reinterpret_cast<uint2*>(row + c) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < n) store_one<IO>(row, c + j, x[j]);
+    }
+  }
 }
 
 template <typename IO>
@@ -274,27 +335,28 @@ hipError_t by_keys(int dk, bool whole, F f) {
   return hipGetLastError();
 }
 
-// The vectors that belong to a chunk of a head, kC floats each, as the preparation leaves them.  c_j scales column j of
-// the inverse T, s_j row j of k, gam_j the sum of log decays up to j (over log 2), gam_C the whole chunk's.
+// The vectors that belong to a chunk of a head, kC floats each, as the preparation leaves them.  c_j scales column j of the
+// inverse T, s_j row j of k, z_i row i of q (powers of 2); gam_j is the sum of log decays up to j (over log 2), gam_C the
+// whole chunk's; s the smallest s_j, and p_i >= 0 a whole number with gam_i - gam_j <= p_i + log2(s_j / s) for j <= i, 0 where no
+// gate grows.  The operand P holds q_i.k_j s z_i 2^(gam_i - gam_j - p_i).
 enum Vec {
   kVecF1,      // beta_j / c_j
   kVecF2,      // beta_j 2^gam_j / (c_j s_j)
   kVecEnd,     // 2^(gam_C - gam_j) / s_j
-  kVecHi,      // gam_i - p_i = hi + lo, for i
-  kVecLo,
-  kVecHiJ,     // gam_j + rel_j = hi + lo, for j
-  kVecLoJ,
-  kVecRel,     // log2 of s_j over the chunk's smallest
   kVecInto,    // 2^gam_j
   kVecS,       // s_j
-  kVecGrow,    // whole number p_i >= 0 with gam_i - gam_j - rel_j <= p_i for every j <= i: 0 where no gate grows
+  kVecZ,       // z_i
+  kVecOut,     // scale 2^p_i / (z_i s)
+  kVecQ,       // scale 2^gam_i / z_i
+  kVecJoin,    // kVecQ / kVecOut
+  kVecC,       // 1 / c_j
   kVecs = 12   // as far apart: a whole number of waves' 16-byte loads
 };
-static_assert(kVecGrow < kVecs && kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
+static_assert(kVecC < kVecs && kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
 
-// The inverse's operand blocks: tiles (0, 0), (1, 0), (1, 1), of each two steps of 16, of each two planes.
-constexpr int kTBlocks = 3 * 2 * 2;
-constexpr int64_t kTHalfs = kTBlocks * 512;      // fp16 values of one chunk's
+// The operand blocks of a triangular matrix of a chunk: tiles (0, 0), (1, 0), (1, 1), of each two steps of 16; two planes.
+constexpr int kTriBlocks = 3 * 2;
+constexpr int kTriBytes = kTriBlocks * 1024;     // of a plane
 
 }  // namespace gdr
 }  // namespace ssscan

@@ -2,9 +2,9 @@
 //
 // Within a chunk u_i = beta_i (v_i - 2^gam_i S^T k_i - sum over j < i of 2^(gam_i - gam_j) (k_i.k_j) u_j), S being the
 // state before the chunk and gam the sums of log decays: (I + A) U = R with A the strict lower triangle of
-// beta_i 2^(gam_i - gam_j) k_i.k_j.  This kernel makes T = (I + A)^-1 and the decays' vectors, a workgroup to each chunk of a
-// head.  k.k^T is a matrix product; the inverse is by 16x16 triangles on the diagonal, a lane to a column, and then
-// by twice joining neighbours, T21 = -T22 A21 T11, all of it in fp32.
+// beta_i 2^(gam_i - gam_j) k_i.k_j.  This kernel makes T = (I + A)^-1, P, the lower triangle of 2^(gam_i - gam_j) q_i.k_j, and the
+// decays' vectors, a workgroup to each chunk of a head.  k.k^T and q.k^T are matrix products; the inverse is by 16x16
+// triangles on the diagonal, a lane to a column, and then by twice joining neighbours, T21 = -T22 A21 T11, in fp32.
 // Sums of log decays are formed in fp64 and kept as two floats: a forgotten state (a decay of -inf, held to -2000 here)
 // must not cost the decays behind it their digits.
 #include "gdr_device.h"
@@ -17,14 +17,26 @@ using namespace gdr;
 constexpr int kThreads = 256;
 constexpr int kPitch = 68;               // floats of a row in LDS
 
-template <typename IO, int KP, bool WHOLE>
+// A sum of log decays in two floats.
+struct Two {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Two two(double v) {
+  const float hi = (float)v;
+  return {hi, (float)(v - (double)hi)};
+}
+
+template <typename IO, int KP, bool WHOLE, bool BWD>
 __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   using T = typename IO::T;
   constexpr int NP = planes_of<IO>(), kSteps = KP / 16, kRuns = KP / 32;
-  __shared__ alignas(16) char s_k[NP][2 * kSteps * kBlock];
-  __shared__ alignas(16) float s_a[kC][kPitch], s_t[kC][kPitch];
-  __shared__ double s_gam[kC];
-  __shared__ float s_beta[kC], s_scale[kC], s_max[4][kC], s_col[kC];
+  constexpr int kSide = 2 * kSteps * kBlock, kRows = 2 * NP * kSide, kTile = kC * kPitch * 4;
+  __shared__ alignas(16) char s_rows[kRows > kTile ? kRows : kTile];      // rows of k, of q; then T
+  __shared__ alignas(16) float s_a[kC][kPitch];
+  __shared__ alignas(16) float s_hi[3][kC], s_lo[3][kC], s_beta[kC];      // of A's row, of P's row, of a column
+  __shared__ float s_scale[2][kC], s_max[4][kC], s_col[kC];
+  float(&s_t)[kC][kPitch] = *reinterpret_cast<float(*)[kC][kPitch]>(s_rows);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t bh = blockIdx.x / a.chunks, chunk = blockIdx.x - bh * a.chunks;
   const int64_t b = bh / a.hv;
@@ -32,73 +44,127 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   const int64_t first = chunk * kC;
   const int valid = a.seqlen - first < kC ? (int)(a.seqlen - first) : kC;
 
-  // four lanes to a token, each every fourth run of 8 values
+  // four lanes to a token, each every fourth run of 8 values; k, then q
   {
     const int tok = tid >> 2, sub = tid & 3;
-    const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + first * a.ks[1] + hkey * a.ks[2];
-    const __amdgpu_buffer_rsrc_t kr = chunk_rows<IO>(k, a.ks[1], valid, a.dk);
-    Raw8<IO> raw[kRuns];
+    Raw8<IO> raw[2][kRuns];
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r)
-      raw[r] = buf_load8<IO, WHOLE>(kr, tok * (uint32_t)a.ks[1] * sizeof(T), 0, 8 * (sub + 4 * r), a.dk);
-    float x[kRuns][8], m = 0.0f;
+    for (int n = 0; n < 2; ++n) {
+      const int64_t* st = n ? a.qs : a.ks;
+      const T* base = static_cast<const T*>(n ? a.q : a.k) + b * st[0] + first * st[1] + hkey * st[2];
+      const __amdgpu_buffer_rsrc_t rows = chunk_rows<IO>(base, st[1], valid, a.dk);
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r)
+      for (int r = 0; r < kRuns; ++r)
+        raw[n][r] = buf_load8<IO, WHOLE>(rows, tok * (uint32_t)st[1] * sizeof(T), 0, 8 * (sub + 4 * r), a.dk);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[r][j] = raw_value<IO>(raw[r], j);
-        m = fmaxf(m, fabsf(x[r][j]));
-      }
-    m = quad_max(m);
-    const float s = row_scale(m);
-    if (sub == 0) s_scale[tok] = s;
+    for (int n = 0; n < 2; ++n) {
+      float x[kRuns][8], m = 0.0f;
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) store_operand_rows<IO>(s_k[0], NP == 2 ? s_k[NP - 1] : nullptr, tok, sub + 4 * r, kSteps, x[r], s);
+      for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[r][j] = raw_value<IO>(raw[n][r], j);
+          m = fmaxf(m, fabsf(x[r][j]));
+        }
+      const float s = row_scale(quad_max(m));
+      if (sub == 0) s_scale[n][tok] = s;
+      char* rows = s_rows + n * NP * kSide;
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) store_operand_rows<IO>(rows, rows + (NP - 1) * kSide, tok, sub + 4 * r, kSteps, x[r], s);
+    }
   }
-  if (tid < kC) {
-    const int64_t at = (b * a.seqlen + first + tid) * a.hv + h;
-    const float beta = tid < valid ? a.beta[at] : 0.0f;
-    float g = tid < valid && a.g ? a.g[at] : 0.0f;
+  __syncthreads();
+
+  // products: tasks 0-2 the tiles of A, 3-5 those of P, two to each of the first two waves; then the vectors by the last wave
+  acc16 acc[2] = {zero16(), zero16()};
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int task = wave + 4 * n;
+    if (task > 5) break;
+    const int tile = task % 3, ti = tile > 0, tj = tile > 1;
+    const bool of_p = task > 2, turned = of_p && !BWD;     // P as the forward reads it is made transposed
+    const char* pi = s_rows + (of_p ? NP * kSide : 0) + ti * kSteps * kBlock;
+    const char* pj = s_rows + tj * kSteps * kBlock;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      acc[n] = mm<NP, NP>(operand<NP>((turned ? pj : pi) + s * kBlock, lane, kSide),
+                          operand<NP>((turned ? pi : pj) + s * kBlock, lane, kSide), acc[n]);
+  }
+  double gam = 0.0, end = 0.0;
+  float beta = 0.0f, into = 0.0f, sk = 1.0f, sq = 1.0f, grow = 0.0f;
+  int least = 0;
+  if (wave == 3) {
+    const int64_t at = (b * a.seqlen + first + lane) * a.hv + h;
+    beta = lane < valid ? a.beta[at] : 0.0f;
+    float g = lane < valid && a.g ? a.g[at] : 0.0f;
     g = g < -2000.0f ? -2000.0f : g;                       // a NaN stays one
-    double gam = (double)g * 1.4426950408889634074;
+    gam = (double)g * 1.4426950408889634074;
 #pragma unroll
     for (int d = 1; d < kC; d <<= 1) {
       const double o = __shfl_up(gam, d);
       if (lane >= d) gam += o;
     }
-    s_gam[tid] = gam;
-    s_beta[tid] = beta;
+    end = __shfl(gam, kC - 1);
+    sk = s_scale[0][lane];
+    sq = s_scale[1][lane];
+    const int es = exponent(sk);
+    least = es;
+    double low = gam + (double)es;                         // the smallest gam_j + log2 s_j up to here
+#pragma unroll
+    for (int d = 1; d < kC; d <<= 1) {
+      const int o = __shfl_xor(least, d);
+      least = o < least ? o : least;
+      const double l = __shfl_up(low, d);
+      if (lane >= d) low = l < low ? l : low;
+    }
+    const double p = fmax(ceil(gam - (low - (double)least)), 0.0);
+    grow = (float)p;
+    const Two ri = two(gam - (double)es), pi = two(gam - p + (double)least), cj = two(gam + (double)es);
+    s_hi[0][lane] = ri.hi; s_lo[0][lane] = ri.lo;
+    s_hi[1][lane] = pi.hi; s_lo[1][lane] = pi.lo;
+    s_hi[2][lane] = cj.hi; s_lo[2][lane] = cj.lo;
+    s_beta[lane] = beta;
+    into = __builtin_amdgcn_exp2f((float)gam);
   }
   __syncthreads();
-
-  // A, tile by tile: wave 0 (0, 0), wave 1 (1, 0), wave 2 (1, 1)
-  if (wave < 3) {
-    const int ti = wave > 0, tj = wave > 1;
-    acc16 acc = zero16();
+  const int64_t at = blockIdx.x;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      Planes p, q;
-      p.hi = *reinterpret_cast<const h8*>(s_k[0] + (ti * kSteps + s) * kBlock + lane * 16);
-      q.hi = *reinterpret_cast<const h8*>(s_k[0] + (tj * kSteps + s) * kBlock + lane * 16);
-      if constexpr (NP == 2) {
-        p.lo = *reinterpret_cast<const h8*>(s_k[1] + (ti * kSteps + s) * kBlock + lane * 16);
-        q.lo = *reinterpret_cast<const h8*>(s_k[1] + (tj * kSteps + s) * kBlock + lane * 16);
+  for (int n = 0; n < 2; ++n) {
+    const int task = wave + 4 * n;
+    if (task > 5) break;
+    const int tile = task % 3, ti = tile > 0, tj = tile > 1;
+    if (task > 2) {
+      const int v = !BWD ? 1 : 2, w = 3 - v;               // the vector of a lane's column, of its 16 rows
+      const int c = 32 * (BWD ? tj : ti) + (lane & 31), r0 = 32 * (BWD ? ti : tj);
+      const float sign = BWD ? -1.0f : 1.0f, hi = s_hi[v][c], lo = s_lo[v][c];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = r0 + tile_row(r, lane);
+        const float e = sign * ((hi - s_hi[w][row]) + (lo - s_lo[w][row]));
+        acc[n][r] = (BWD ? c <= row : row <= c) ? acc[n][r] * __builtin_amdgcn_exp2f(e) : 0.0f;
       }
-      acc = mm<NP, NP>(p, q, acc);
-    }
-    const int j = 32 * tj + (lane & 31);
-    const double gj = s_gam[j];
-    const float inv_j = 1.0f / s_scale[j];                 // powers of 2
+      constexpr int NO = BWD ? 2 : NP;
+      char* out = static_cast<char*>(a.p) + at * (NO * kTriBytes) + tile * 2048 + lane * 16;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = 32 * ti + tile_row(r, lane);
-      const float d = __builtin_amdgcn_exp2f((float)(s_gam[i] - gj));
-      s_a[i][j] = j < i ? s_beta[i] * ((acc[r] * (1.0f / s_scale[i])) * inv_j) * d : 0.0f;
+      for (int s = 0; s < 2; ++s) {
+        const Planes p = split<NO>(acc[n], s, 1.0f);
+        *reinterpret_cast<h8*>(out + s * 1024) = p.hi;
+        if constexpr (NO == 2) *reinterpret_cast<h8*>(out + kTriBytes + s * 1024) = p.lo;
+      }
+    } else {
+      const int j = 32 * tj + (lane & 31);
+      const float hi = s_hi[2][j], lo = s_lo[2][j];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int i = 32 * ti + tile_row(r, lane);
+        const float e = (s_hi[0][i] - hi) + (s_lo[0][i] - lo);
+        s_a[i][j] = j < i ? s_beta[i] * (acc[n][r] * __builtin_amdgcn_exp2f(e)) : 0.0f;
+      }
     }
-  } else {
-    // above the diagonal T stays zero
-    for (int e = lane; e < 32 * 32; e += 64) s_t[e >> 5][32 + (e & 31)] = 0.0f;
   }
+  // above the diagonal T stays zero (the rows of k and q have been read)
+  for (int e = tid; e < 32 * 32; e += kThreads) s_t[e >> 5][32 + (e & 31)] = 0.0f;
   __syncthreads();
 
   // 16x16 triangles: lane 16 q + c solves column c of triangle q
@@ -174,81 +240,64 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
     s_max[part][col] = m;
   }
   __syncthreads();
-  if (tid < kC) {
-    const float m = fmaxf(fmaxf(s_max[0][tid], s_max[1][tid]), fmaxf(s_max[2][tid], s_max[3][tid]));
-    const float c = pow2(-exponent(m));
-    s_col[tid] = c;
-    const double gam = s_gam[tid], end = s_gam[kC - 1];
-    const float beta = s_beta[tid], s = s_scale[tid], inv_s = 1.0f / s, into = __builtin_amdgcn_exp2f((float)gam);
-    const int es = exponent(s);
-    int least = es;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_xor(least, d);
-      least = o < least ? o : least;
-    }
-    const float rel = (float)(es - least);
-    double low = gam + (double)rel;                        // the smallest gam_j + rel_j up to here
-#pragma unroll
-    for (int d = 1; d < kC; d <<= 1) {
-      const double o = __shfl_up(low, d);
-      if (lane >= d) low = o < low ? o : low;
-    }
-    const double grow = ceil(gam - low);
-    const double pi = grow > 0.0 ? grow : 0.0, gi = gam - pi, gj = gam + (double)rel;
-    const float hi = (float)gi, hij = (float)gj;
-    float* v = a.vecs + ((int64_t)blockIdx.x * kVecs) * kC + tid;
-    v[kVecF1 * kC] = beta / c;
-    v[kVecF2 * kC] = beta * into / c * inv_s;
+  if (wave == 3) {
+    const float m = fmaxf(fmaxf(s_max[0][lane], s_max[1][lane]), fmaxf(s_max[2][lane], s_max[3][lane]));
+    const int ec = exponent(m), es = exponent(sk), ez = exponent(sq), p = (int)grow;
+    s_col[lane] = pow2(-ec);
+    const float inv_c = pow2(ec), inv_s = pow2(-es), inv_z = pow2(-ez), scaled = a.scale * inv_z;
+    float* v = a.vecs + at * (kVecs * kC) + lane;
+    v[kVecF1 * kC] = beta * inv_c;
+    v[kVecF2 * kC] = beta * into * inv_c * inv_s;
     v[kVecEnd * kC] = __builtin_amdgcn_exp2f((float)(end - gam)) * inv_s;
-    v[kVecHi * kC] = hi;
-    v[kVecLo * kC] = (float)(gi - (double)hi);
-    v[kVecHiJ * kC] = hij;
-    v[kVecLoJ * kC] = (float)(gj - (double)hij);
-    v[kVecRel * kC] = rel;
     v[kVecInto * kC] = into;
-    v[kVecS * kC] = s;
-    v[kVecGrow * kC] = (float)pi;
+    v[kVecS * kC] = sk;
+    v[kVecZ * kC] = sq;
+    v[kVecOut * kC] = scaled * pow2(p - least);
+    v[kVecQ * kC] = scaled * into;
+    v[kVecJoin * kC] = into * pow2(least - p);
+    v[kVecC * kC] = inv_c;
   }
   __syncthreads();
   // tiles as operands: slot (tile, step, lane)
-  _Float16* out = static_cast<_Float16*>(a.tri) + (int64_t)blockIdx.x * kTHalfs;
-  for (int e = tid; e < 3 * 2 * 64; e += kThreads) {
-    const int tile = e >> 7, step = (e >> 6) & 1, l = e & 63;
-    const int i = 32 * (tile > 0) + (l & 31), j0 = 32 * (tile > 1) + 16 * step + 4 * (l >> 5);
+  for (int e = tid; e < kTriBlocks * 64 * (BWD ? 2 : 1); e += kThreads) {
+    const int turned = e / (kTriBlocks * 64), slot = e % (kTriBlocks * 64);
+    const int tile = slot >> 7, step = (slot >> 6) & 1, l = slot & 63, ti = tile > 0, tj = tile > 1;
+    const int row = 32 * (turned ? tj : ti) + (l & 31), j0 = 32 * (turned ? ti : tj) + 16 * step + 4 * (l >> 5);
     Planes p;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int col = j0 + (j & 3) + 8 * (j >> 2);
-      const float x = s_t[i][col] * s_col[col];
+      const int k = j0 + (j & 3) + 8 * (j >> 2);
+      const float x = turned ? s_t[k][row] * s_col[row] : s_t[row][k] * s_col[k];
       p.hi[j] = (_Float16)x;
       p.lo[j] = (_Float16)(x - (float)p.hi[j]);
     }
-    *reinterpret_cast<h8*>(out + ((tile * 2 + step) * 2 + 0) * 512 + l * 8) = p.hi;
-    *reinterpret_cast<h8*>(out + ((tile * 2 + step) * 2 + 1) * 512 + l * 8) = p.lo;
+    char* out = static_cast<char*>(turned ? a.tri_t : a.tri) + at * (2 * kTriBytes) + slot * 16;
+    *reinterpret_cast<h8*>(out) = p.hi;
+    *reinterpret_cast<h8*>(out + kTriBytes) = p.lo;
   }
 }
 
 template <typename IO>
-hipError_t launch(const GdrArgs& a, hipStream_t s) {
+hipError_t launch(const GdrArgs& a, bool backward, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.hv * a.chunks));
   return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
-    gdr_prep_kernel<IO, decltype(kp)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>(a);
+    if (backward) gdr_prep_kernel<IO, decltype(kp)::value, decltype(whole)::value, true><<<grid, kThreads, 0, s>>>(a);
+    else gdr_prep_kernel<IO, decltype(kp)::value, decltype(whole)::value, false><<<grid, kThreads, 0, s>>>(a);
   });
 }
 
 }  // namespace
 
-size_t gdr_tri_bytes(int64_t batch, int64_t seqlen, int hv) {
-  return (size_t)(batch * hv * ((seqlen + kC - 1) / kC)) * kTHalfs * 2;
+size_t gdr_tri_bytes(int64_t chunk_heads) { return (size_t)chunk_heads * 2 * kTriBytes; }
+
+size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward) {
+  return (size_t)chunk_heads * kTriBytes * (backward || io == kIoF32 ? 2 : 1);
 }
 
-size_t gdr_vecs_bytes(int64_t batch, int64_t seqlen, int hv) {
-  return (size_t)(batch * hv * ((seqlen + kC - 1) / kC)) * kVecs * kC * sizeof(float);
-}
+size_t gdr_vecs_bytes(int64_t chunk_heads) { return (size_t)chunk_heads * kVecs * kC * sizeof(float); }
 
-hipError_t launch_gdr_prep(const GdrArgs& a, hipStream_t s) {
-  return a.io == kIoBf16 ? launch<BF16>(a, s) : launch<F32>(a, s);
+hipError_t launch_gdr_prep(const GdrArgs& a, bool backward, hipStream_t s) {
+  return a.io == kIoBf16 ? launch<BF16>(a, backward, s) : launch<F32>(a, backward, s);
 }
 
 }  // namespace ssscan
