@@ -465,8 +465,11 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
  * projection's rows, and are what ss_qk_norm_rot writes token-major (weights of
  * 1/sqrt(dim_k) make keys of unit length).  dim_k is 1 to 128, dim_v 1 to 65536;
  * batch, heads and columns together make fewer than 2^23 workgroups.
- * The state and all sums are fp32, outputs rounded once.  g of -inf forgets the state;
- * a padding token has beta = 0, g = 0 and finite q, k and v.
+ * The state and all sums are fp32, outputs rounded once; sequences of more than 16
+ * tokens are taken in chunks of 64, with products in pairs of fp16 (22 bits).  g of
+ * -inf forgets the state; a padding token has beta = 0, g = 0 and finite q, k and v.
+ * Anything infinite or NaN in a token may reach all outputs of its head from the 64
+ * tokens (of t / 64) that it is among onwards, in the backward also those before.
  * Keys are not normed here: with beta |k|^2 above 2 the recurrence itself grows.
  *
  * Ownership, streams, errors and overlaps are as for ss_scan_fwd.  Results are
@@ -474,6 +477,12 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
  *
  *  ss_gdr_fwd: h_final (nullable) is the state after the last token (h0 when seqlen is
  *    0).  The workspace has ss_gdr_fwd_workspace_bytes (which may be 0), 256-byte aligned.
+ *  ss_gdr_bwd: given dout (as o, 16-byte aligned) and dh_final (as h_final; NULL =
+ *    zero), writes dq, dk (batch, seqlen, heads_k, dim_k; summed over a key head's value
+ *    heads) and dv (batch, seqlen, heads_v, dim_v), contiguous and 16-byte aligned, and,
+ *    where not NULL, the fp32 gradients dg (also of a g that is NULL), dbeta and dh0.  The workspace
+ *    (ss_gdr_bwd_workspace_bytes) holds two states for every 64 tokens.  Tokens of q, k
+ *    or v, or of a row of v, 2^22 values and more apart return SS_ERR_UNSUPPORTED.
  *  ss_gdr_step: one token, q, k, v, g, beta and o without their seqlen dimension
  *    (the strides' second entry is not used).  state_out may be state_in itself. */
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v);
@@ -481,6 +490,12 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
                      float scale, const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
                      const void* v, const int64_t* v_stride, const float* g, const float* beta, const float* h0,
                      void* o, float* h_final, void* workspace, size_t workspace_bytes, void* stream);
+size_t ss_gdr_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v);
+ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
+                     float scale, const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                     const void* v, const int64_t* v_stride, const float* g, const float* beta, const float* h0,
+                     const void* dout, const float* dh_final, void* dq, void* dk, void* dv,
+                     float* dg, float* dbeta, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
 ss_status ss_gdr_step(int64_t batch, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io, float scale,
                       const float* state_in, float* state_out, const void* q, const int64_t* q_stride,
                       const void* k, const int64_t* k_stride, const void* v, const int64_t* v_stride,

@@ -21,7 +21,7 @@ PROBE_LIB = PKG / "libssprobe.so"
 SOURCES = ["api.cpp", "scan_fwd.hip", "scan_bf16_euler.hip", "scan_bf16_zoh.hip", "scan_f32_euler.hip",
            "scan_f32_zoh.hip", "scan_bwd.hip", "scan_bwd_zoh.hip", "state_update.hip", "scan_fwd_noalloc.hip",
            "api_glr.cpp", "glr_fwd.hip", "glr_bwd.hip", "api_qk.cpp", "qk_norm_rot.hip",
-           "qk_rows.hip", "qk_cols.hip", "api_gdr.cpp", "gdr_recur.hip", "gdr_prep.hip", "gdr_chunk.hip", "api_norms.cpp", "norms.hip"]
+           "qk_rows.hip", "qk_cols.hip", "api_gdr.cpp", "gdr_recur.hip", "gdr_prep.hip", "gdr_chunk.hip", "gdr_chunk_bwd.hip", "gdr_grad.hip", "api_norms.cpp", "norms.hip"]
 ARCH = "gfx950"
 
 # Packed-FP32 VALU ops are disabled for all device code; see the design notes.

@@ -122,6 +122,10 @@ def _load():
     lib.ss_gdr_fwd_workspace_bytes.argtypes = [_i64, _i64] + [_int] * 4
     lib.ss_gdr_fwd.restype = _int
     lib.ss_gdr_fwd.argtypes = [_i64, _i64] + [_int] * 5 + [_f32] + _rows * 3 + [_vp] * 6 + [_sz, _vp]
+    lib.ss_gdr_bwd_workspace_bytes.restype = _sz
+    lib.ss_gdr_bwd_workspace_bytes.argtypes = [_i64, _i64] + [_int] * 4
+    lib.ss_gdr_bwd.restype = _int
+    lib.ss_gdr_bwd.argtypes = [_i64, _i64] + [_int] * 5 + [_f32] + _rows * 3 + [_vp] * 12 + [_sz, _vp]
     lib.ss_gdr_step.restype = _int
     lib.ss_gdr_step.argtypes = [_i64] + [_int] * 5 + [_f32, _vp, _vp] + _rows * 3 + [_vp] * 4
     lib.ss_gated_norm.restype = _int
@@ -374,6 +378,18 @@ def ss_gdr_fwd(batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, q_st
     _check(lib.ss_gdr_fwd(batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, _strides(q_stride), k,
                           _strides(k_stride), v, _strides(v_stride), g, beta, h0, o, h_final, workspace,
                           workspace_bytes, stream))
+
+
+@functools.lru_cache(maxsize=256)
+def ss_gdr_bwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) -> int:
+    return int(lib.ss_gdr_bwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v))
+
+
+def ss_gdr_bwd(batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, q_stride, k, k_stride, v, v_stride, g, beta,
+               h0, dout, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace, workspace_bytes, stream=None):
+    _check(lib.ss_gdr_bwd(batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, _strides(q_stride), k,
+                          _strides(k_stride), v, _strides(v_stride), g, beta, h0, dout, dh_final, dq, dk, dv, dg, dbeta,
+                          dh0, workspace, workspace_bytes, stream))
 
 
 def ss_gdr_step(batch, heads_k, heads_v, dim_k, dim_v, io, scale, state_in, state_out, q, q_stride, k, k_stride, v,

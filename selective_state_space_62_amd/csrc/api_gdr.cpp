@@ -23,7 +23,7 @@ ss_status check_sizes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, i
   if (dim_v < 1 || dim_v > kMaxDimV) return record_error(SS_ERR_UNSUPPORTED, "dim_v %d is not 1 to %d", dim_v, kMaxDimV);
   if (batch > kMaxDim || seqlen > kMaxDim ||
       (__int128)batch * (seqlen > 0 ? seqlen : 1) * heads_v * (dim_k + (int64_t)dim_v) * 8 > ((__int128)1 << 62) ||
-      (__int128)batch * heads_v * dim_k * dim_v * 4 * (1 + seqlen / 64) > ((__int128)1 << 62))
+      (__int128)batch * heads_v * (1 + seqlen / 64) * (dim_k + 128) * (dim_v + 128) * 16 > ((__int128)1 << 62))
     return record_error(SS_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte offsets");
   return SS_OK;
 }
@@ -106,8 +106,8 @@ ss_status check_blocks(int64_t blocks) {
 constexpr int64_t kRecurTokens = 16;
 constexpr int64_t kMostStride = int64_t(1) << 22;
 
-bool one_by_one(const Inputs& in) {
-  return in.seqlen <= kRecurTokens || in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride;
+bool far_apart(const Inputs& in) {
+  return in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride;
 }
 
 bool aligned_rows(const void* p, const int64_t* st, ss_dtype io) {
@@ -133,6 +133,30 @@ FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v) {
   l.p = round256(gdr_tri_bytes(n));
   l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, false));
   l.total = l.vecs + round256(gdr_vecs_bytes(n));
+  return l;
+}
+
+// Scratch of the backward: the preparation's, then for every chunk of a head the state before it and the gradient of the one
+// behind it, U and the gradient of R, and the largest values of their tiles.
+struct BwdLayout {
+  size_t tri_t, p, vecs, states, dstates, u, dr, maxima, total;
+  int64_t ldv, max_apart;
+};
+
+BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_v, int dim_k, int dim_v) {
+  const int64_t n = batch * heads_v * chunks_of(seqlen), rows = (dim_k + 31) / 32 * 32;
+  BwdLayout l;
+  l.ldv = (int64_t)(dim_v + 31) / 32 * 32;
+  l.max_apart = n * (l.ldv / 32);
+  l.tri_t = round256(gdr_tri_bytes(n));
+  l.p = l.tri_t + round256(gdr_tri_bytes(n));
+  l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, true));
+  l.states = l.vecs + round256(gdr_vecs_bytes(n));
+  l.dstates = l.states + round256((size_t)(n * rows * l.ldv) * 4);
+  l.u = l.dstates + round256((size_t)(n * rows * l.ldv) * 4);
+  l.dr = l.u + round256((size_t)(n * kGdrChunk * l.ldv) * 4);
+  l.maxima = l.dr + round256((size_t)(n * kGdrChunk * l.ldv) * 4);
+  l.total = l.maxima + round256((size_t)(kMaxKinds * l.max_apart) * 4);
   return l;
 }
 
@@ -167,7 +191,7 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     if (h_final) e = h0 ? launch_copy_state(state_numel(in), h0, h_final, s) : launch_fill_zero(h_final, state_numel(in), s);
     return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
   }
-  const bool recur = one_by_one(in);
+  const bool recur = seqlen <= kRecurTokens || far_apart(in);
   if ((st = check_blocks(recur ? gdr_recur_blocks(batch, heads_v, dim_v) : batch * heads_v * chunks_of(seqlen))) != SS_OK)
     return st;
   GdrArgs a = make_args(in);
@@ -187,6 +211,78 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     if (e == hipSuccess) e = launch_gdr_chunk(a, false, s);
   }
   return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule launch");
+}
+
+size_t ss_gdr_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
+  if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen == 0) return 0;
+  return bwd_layout(batch, seqlen, heads_v, dim_k, dim_v).total;
+}
+
+ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
+                     float scale, const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride,
+                     const void* v, const int64_t* v_stride, const float* g, const float* beta, const float* h0,
+                     const void* dout, const float* dh_final, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                     float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  const Inputs in{batch, seqlen, heads_k, heads_v, dim_k, dim_v, io, scale, q, q_stride, k, k_stride, v, v_stride, g, beta, h0};
+  Range own[6];
+  ss_status st = check_inputs(in, own);
+  if (st != SS_OK) return st;
+  const int64_t eb = elem_bytes(io), tokens = batch * seqlen;
+  const struct { const char* name; const void* p; } rows[] = {{"dout", dout}, {"dq", dq}, {"dk", dk}, {"dv", dv}};
+  for (const auto& r : rows) {
+    if (seqlen > 0 && !r.p) return record_error(SS_ERR_INVALID_ARG, "%s is NULL", r.name);
+    if (!aligned(r.p, 16)) return record_error(SS_ERR_INVALID_ARG, "%s is not 16-byte aligned", r.name);
+  }
+  const struct { const char* name; const float* p; } vecs[] = {{"dh_final", dh_final}, {"dg", dg}, {"dbeta", dbeta}, {"dh0", dh0}};
+  for (const auto& n : vecs)
+    if (!aligned(n.p, 4)) return record_error(SS_ERR_INVALID_ARG, "%s is not 4-byte aligned", n.name);
+  if (far_apart(in) || (int64_t)heads_v * dim_v >= kMostStride)
+    return record_error(SS_ERR_UNSUPPORTED, "tokens 2^22 values and more apart are not supported here");
+  const size_t need = ss_gdr_bwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v);
+  if ((st = check_scratch(workspace, workspace_bytes, need)) != SS_OK) return st;
+  const Range ins[] = {own[0], own[1], own[2], own[3], own[4], own[5], rng("dout", dout, tokens * heads_v * dim_v * eb),
+                       rng("dh_final", dh_final, state_numel(in) * 4)};
+  const Range outs[] = {rng("dq", dq, tokens * heads_k * dim_k * eb), rng("dk", dk, tokens * heads_k * dim_k * eb),
+                        rng("dv", dv, tokens * heads_v * dim_v * eb), rng("dg", dg, gates(in) * 4),
+                        rng("dbeta", dbeta, gates(in) * 4), rng("dh0", dh0, state_numel(in) * 4),
+                        rng("workspace", workspace, (int64_t)need)};
+  if ((st = check_disjoint(ins, 8, outs, 7)) != SS_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (seqlen == 0) {
+    if (dh0) e = dh_final ? launch_copy_state(state_numel(in), dh_final, dh0, s) : launch_fill_zero(dh0, state_numel(in), s);
+    return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
+  }
+  if ((st = check_blocks(batch * heads_v * chunks_of(seqlen))) != SS_OK) return st;
+  const BwdLayout l = bwd_layout(batch, seqlen, heads_v, dim_k, dim_v);
+  char* ws = static_cast<char*>(workspace);
+  GdrArgs a = make_args(in);
+  a.chunks = chunks_of(seqlen);
+  a.whole = whole_runs(in);
+  a.tri = ws;
+  a.tri_t = ws + l.tri_t;
+  a.p = ws + l.p;
+  a.vecs = reinterpret_cast<float*>(ws + l.vecs);
+  a.ldv = l.ldv;
+  a.states = reinterpret_cast<float*>(ws + l.states);
+  a.dstates = reinterpret_cast<float*>(ws + l.dstates);
+  a.u = reinterpret_cast<float*>(ws + l.u);
+  a.dr = reinterpret_cast<float*>(ws + l.dr);
+  a.maxima = reinterpret_cast<float*>(ws + l.maxima);
+  a.max_apart = l.max_apart;
+  a.dout = dout;
+  a.dh_final = dh_final;
+  a.dq = dq;
+  a.dk_out = dk;
+  a.dv_out = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.dh0 = dh0;
+  e = launch_gdr_prep(a, true, s);
+  if (e == hipSuccess) e = launch_gdr_chunk(a, true, s);
+  if (e == hipSuccess) e = launch_gdr_chunk_bwd(a, s);
+  if (e == hipSuccess) e = launch_gdr_grad(a, s);
+  return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule backward launch");
 }
 
 ss_status ss_gdr_step(int64_t batch, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io, float scale,

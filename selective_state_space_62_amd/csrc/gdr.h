@@ -38,11 +38,21 @@ struct GdrArgs {
   int64_t ldv;
   float* states;         // the state before it
   float* u;              // U
+  float* dstates;        // the gradient of the state behind it
+  float* dr;             // the gradient of R
   float* maxima;
   int64_t max_apart;
+  const void* dout;      // gradient of o
+  const float* dh_final; // nullable
+  void* dq;              // (batch, seqlen, hk, dk)
+  void* dk_out;
+  void* dv_out;          // (batch, seqlen, hv, dv)
+  float* dg;             // nullable
+  float* dbeta;          // nullable
+  float* dh0;            // nullable
 };
 
-enum GdrMax { kMaxS, kMaxU };
+enum GdrMax { kMaxS, kMaxU, kMaxDs, kMaxDr, kMaxDo, kMaxKinds };
 
 // Chunk by chunk on the matrix cores: what needs no state for all chunks at once, then the states in turn.
 size_t gdr_tri_bytes(int64_t chunk_heads);                    // of tri, tri_t
@@ -50,6 +60,9 @@ size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward);
 size_t gdr_vecs_bytes(int64_t chunk_heads);
 hipError_t launch_gdr_prep(const GdrArgs& a, bool backward, hipStream_t s);
 hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s);
+// The backward after the states: their gradients in turn, from the last chunk on, then all other gradients of all chunks.
+hipError_t launch_gdr_chunk_bwd(const GdrArgs& a, hipStream_t s);
+hipError_t launch_gdr_grad(const GdrArgs& a, hipStream_t s);
 
 // Token by token, the state in registers: one token of a serving loop, and short sequences.
 hipError_t launch_gdr_recur(const GdrArgs& a, hipStream_t s);

@@ -350,9 +350,11 @@ enum Vec {
   kVecQ,       // scale 2^gam_i / z_i
   kVecJoin,    // kVecQ / kVecOut
   kVecC,       // 1 / c_j
-  kVecs = 12   // as far apart: a whole number of waves' 16-byte loads
+  kVecHi,      // gam_j in two floats
+  kVecLo,
+  kVecs
 };
-static_assert(kVecC < kVecs && kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
+static_assert(kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
 
 // The operand blocks of a triangular matrix of a chunk: tiles (0, 0), (1, 0), (1, 1), of each two steps of 16; two planes.
 constexpr int kTriBlocks = 3 * 2;

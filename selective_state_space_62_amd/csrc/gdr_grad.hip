@@ -1,0 +1,334 @@
+// The gated delta rule backward, last step: the gradients that need no turn, a workgroup to each chunk of a key head
+// (gdr_device.h has the layouts).
+//
+// With S before the chunk, dS behind it, U, dR and dO, D_ij = 2^(gam_i - gam_j), and M_ij = D_ij dR_i.U_j (j < i),
+// N_ij = scale D_ij dO_i.U_j (j <= i):
+//   dq_i = scale G_i S dO_i + sum_j N_ij k_j
+//   X_i  = G_i S dR_i + sum_j M_ij k_j                      (what k_i reads, over -beta_i)
+//   Y_j  = D_Cj dS U_j + sum_i N_ij q_i - sum_i beta_i M_ij k_i
+//   dk = Y - beta X,  dbeta = dR.v - k.X,
+//   dgam_i = q_i.dq_i - beta_i k_i.X_i - k_i.Y_i, at the chunk's last token also sum_j k_j.(D_Cj dS U_j) + G_C <dS, S>,
+// and dg the sums of dgam from a token to the chunk's end.  Everything is fp32 in two planes, as dbeta and dg are differences.
+// Rows of dO, U and dR pass LDS 64 columns at a time; a wave reads its own rows of S and dS from memory, each value once.
+// The products run transposed, a lane a token, so that gradients are stored in runs.  The value heads of a key head are
+// taken one after the other and summed in registers.
+#include "gdr_device.h"
+
+namespace ssscan {
+namespace {
+
+using namespace gdr;
+
+constexpr int kThreads = 512;
+constexpr int kRowBytes = 2 * 4 * kBlock;                  // 64 rows by 64 columns, of a plane
+
+template <typename IO, int KP, bool WHOLE>
+__global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
+  using T = typename IO::T;
+  constexpr int NP = planes_of<IO>(), kTiles = KP / 32, kTurned = kTiles * 4 * kBlock;
+  constexpr int kRegion = (NP + 4) * kRowBytes;            // dO, U, dR; then two triangles at a time
+  static_assert(kRegion >= 4 * kTriBytes, "");
+  __shared__ alignas(16) char s_kt[NP * kTurned], s_qt[NP * kTurned], s_r[kRegion];
+  __shared__ alignas(16) float s_vec[kVecs][kC], s_beta[kC];
+  __shared__ float s_mx[8], s_sd[8], s_rv[kC], s_dot[4][kTiles][kC];
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, low = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t bk = blockIdx.x / a.chunks, chunk = blockIdx.x - bk * a.chunks;
+  const int64_t b = bk / a.hk;
+  const int hkey = (int)(bk - b * a.hk), group = a.hv / a.hk;
+  const int64_t first = chunk * kC, ostride = (int64_t)a.hv * a.dv;
+  const int valid = (int)min(a.seqlen - first, (int64_t)kC);
+  const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + first * a.qs[1] + hkey * a.qs[2];
+  const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + first * a.ks[1] + hkey * a.ks[2];
+  const __amdgpu_buffer_rsrc_t qr = chunk_rows<IO>(q, a.qs[1], valid, a.dk), kr = chunk_rows<IO>(k, a.ks[1], valid, a.dk);
+  const uint32_t krow = (uint32_t)a.ks[1] * sizeof(T), qrow = (uint32_t)a.qs[1] * sizeof(T);
+
+  // k and q, transposed, each with one scale: threads 0-255 k, the others q
+  int ek, eq;
+  {
+    const int t = tid & 255, g = t & 15, c = t >> 4;
+    float x[4][8], m = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const Raw8<IO> r = tid < 256 ? buf_load8<IO, WHOLE>(kr, (4 * g + n) * krow, 0, 8 * c, a.dk)
+                                   : buf_load8<IO, WHOLE>(qr, (4 * g + n) * qrow, 0, 8 * c, a.dk);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[n][j] = raw_value<IO>(r, j);
+        m = fmaxf(m, fabsf(x[n][j]));
+      }
+    }
+    m = wave_max(m);
+    if (lane == 0) s_mx[wave] = m;
+    __syncthreads();
+    const Scale sk = scale_of(fmaxf(fmaxf(s_mx[0], s_mx[1]), fmaxf(s_mx[2], s_mx[3])), 100);
+    const Scale sq = scale_of(fmaxf(fmaxf(s_mx[4], s_mx[5]), fmaxf(s_mx[6], s_mx[7])), 100);
+    ek = sk.e;
+    eq = sq.e;
+    const float f = tid < 256 ? sk.f : sq.f, s[4] = {f, f, f, f};
+    char* to = tid < 256 ? s_kt : s_qt;
+    if (c < KP / 8) store_operand_turned<IO>(to, to + (NP - 1) * kTurned, g, c, x, s);
+  }
+
+  // this wave's rows of keys 32 m .. and tokens 32 ti ..; of the triangles its type and tiles
+  const int m = wave >> 1, ti = wave & 1, type = wave >> 1, tok = 32 * ti + low;
+  const bool active = m < kTiles;
+  acc16 dQ = zero16(), dK = zero16();
+
+  for (int n = 0; n < group; ++n) {
+    const int h = hkey * group + n;
+    const int64_t at = (b * a.hv + h) * a.chunks + chunk, gate = (b * a.seqlen + first) * a.hv + h;
+    __syncthreads();
+    for (int e = tid; e < kVecs * kC; e += kThreads) (&s_vec[0][0])[e] = a.vecs[at * (kVecs * kC) + e];
+    if (tid < kC) s_beta[tid] = tid < valid ? a.beta[gate + (int64_t)tid * a.hv] : 0.0f;
+    auto largest = [&](int kind) {
+      float v = 0.0f;
+      for (int64_t e = lane; e < a.ldv / 32; e += 64) v = fmaxf(v, a.maxima[kind * a.max_apart + at * (a.ldv / 32) + e]);
+      return scale_of(wave_max(v), 100);
+    };
+    const Scale cS = largest(kMaxS), cU = largest(kMaxU), cE = largest(kMaxDs), cD = largest(kMaxDr), cO = largest(kMaxDo);
+    const T* dout = static_cast<const T*>(a.dout) + (b * a.seqlen + first) * ostride + (int64_t)h * a.dv;
+    const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + first * a.vs[1] + h * a.vs[2];
+    const __amdgpu_buffer_rsrc_t orows = chunk_rows<IO>(dout, ostride, valid, a.dv), vrows = chunk_rows<IO>(v, a.vs[1], valid, a.dv);
+    char* const s_o = s_r;
+    char* const s_u = s_r + NP * kRowBytes;
+    char* const s_d = s_u + 2 * kRowBytes;
+
+    acc16 Q = zero16(), X = zero16(), Y = zero16(), C[2] = {zero16(), zero16()};
+    float sd = 0.0f, rv = 0.0f;
+    for (int64_t v0 = 0; v0 < a.ldv; v0 += 64) {
+      const int row = tid >> 3, run = tid & 7;
+      const int64_t col = v0 + 8 * run;
+      {
+        const Raw8<IO> ro = buf_load8<IO, WHOLE>(orows, row * (uint32_t)ostride * sizeof(T), 0, (int)col, a.dv);
+        const Raw8<IO> rw = buf_load8<IO, WHOLE>(vrows, row * (uint32_t)a.vs[1] * sizeof(T), 0, (int)col, a.dv);
+        float o[8], u[8] = {}, d[8] = {};
+        if (col < a.ldv) {
+          const float* up = a.u + (at * kC + row) * a.ldv + col;
+          const float* dp = a.dr + (at * kC + row) * a.ldv + col;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = up[j];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = dp[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = raw_value<IO>(ro, j);
+          rv = fmaf(d[j], raw_value<IO>(rw, j), rv);
+        }
+        __syncthreads();                                   // the columns before have been read
+        store_operand_rows<IO>(s_o, s_o + (NP - 1) * kRowBytes, row, run, 4, o, cO.f);
+        store_operand_rows<F32>(s_u, s_u + kRowBytes, row, run, 4, u, cU.f);
+        store_operand_rows<F32>(s_d, s_d + kRowBytes, row, run, 4, d, cD.f);
+      }
+      __syncthreads();
+      // triangles: types 0, 1 of N with a lane a row i, a column j; 2, 3 of M
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tile = (wave & 1) ? 2 : e, i = tile > 0, j = tile > 1;
+        if (e && (wave & 1)) break;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const Planes u = operand<2>(s_u + (j * 4 + s) * kBlock, lane, kRowBytes);
+          if (type < 2) {
+            const Planes o = operand<NP>(s_o + (i * 4 + s) * kBlock, lane, kRowBytes);
+            C[e] = type & 1 ? mm<NP, 2>(o, u, C[e]) : mm<2, NP>(u, o, C[e]);
+          } else {
+            const Planes d = operand<2>(s_d + (i * 4 + s) * kBlock, lane, kRowBytes);
+            C[e] = type & 1 ? mm<2, 2>(d, u, C[e]) : mm<2, 2>(u, d, C[e]);
+          }
+        }
+      }
+      if (active) {
+        const float* sp = a.states + (at * KP + 32 * m + low) * a.ldv + v0 + 4 * half;
+        const float* dp = a.dstates + (at * KP + 32 * m + low) * a.ldv + v0 + 4 * half;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if (v0 + 16 * s >= a.ldv) break;
+          const float4 s0 = *reinterpret_cast<const float4*>(sp + 16 * s), s1 = *reinterpret_cast<const float4*>(sp + 16 * s + 8);
+          const float4 d0 = *reinterpret_cast<const float4*>(dp + 16 * s), d1 = *reinterpret_cast<const float4*>(dp + 16 * s + 8);
+          const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+          const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+          Planes S, E;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sd = fmaf(sv[j], dv[j], sd);
+            S.hi[j] = (_Float16)(sv[j] * cS.f);
+            S.lo[j] = (_Float16)fmaf(sv[j], cS.f, -(float)S.hi[j]);
+            E.hi[j] = (_Float16)(dv[j] * cE.f);
+            E.lo[j] = (_Float16)fmaf(dv[j], cE.f, -(float)E.hi[j]);
+          }
+          Q = mm<2, NP>(S, operand<NP>(s_o + (ti * 4 + s) * kBlock, lane, kRowBytes), Q);
+          X = mm<2, 2>(S, operand<2>(s_d + (ti * 4 + s) * kBlock, lane, kRowBytes), X);
+          Y = mm<2, 2>(E, operand<2>(s_u + (ti * 4 + s) * kBlock, lane, kRowBytes), Y);
+        }
+      }
+    }
+
+    // the triangles' values; their sums over rows of dR.v; <dS, S>
+    float mC = 0.0f;
+    {
+      const float f = type < 2 ? a.scale * pow2(-cU.e) * pow2(-cO.e) : pow2(-cU.e) * pow2(-cD.e);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tile = (wave & 1) ? 2 : e, i0 = 32 * (tile > 0), j0 = 32 * (tile > 1);
+        const int col = (type & 1 ? j0 : i0) + low;
+        const float hi = s_vec[kVecHi][col], lo = s_vec[kVecLo][col];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = (type & 1 ? i0 : j0) + tile_row(r, lane);
+          const float d = (hi - s_vec[kVecHi][row]) + (lo - s_vec[kVecLo][row]);
+          const int i = type & 1 ? row : col, j = type & 1 ? col : row;
+          const float w = C[e][r] * f * __builtin_amdgcn_exp2f(type & 1 ? -d : d);
+          C[e][r] = j < i || (j == i && type < 2) ? (type == 3 ? w * s_beta[row] : w) : 0.0f;
+        }
+        if (!(e && (wave & 1))) mC = max_of(C[e], mC);
+      }
+    }
+    mC = wave_max(mC);
+    rv = group_sum(rv, 8);
+    sd = group_sum(sd, 64);
+    if (lane == 0) {
+      s_mx[wave] = mC;
+      s_sd[wave] = active && ti == 0 ? sd : 0.0f;
+    }
+    if ((lane & 7) == 0) s_rv[tid >> 3] = rv;
+    __syncthreads();
+    const Scale t0 = scale_of(fmaxf(s_mx[0], s_mx[1]), 100), t1 = scale_of(fmaxf(s_mx[2], s_mx[3]), 100);
+    const Scale t2 = scale_of(fmaxf(s_mx[4], s_mx[5]), 100), t3 = scale_of(fmaxf(s_mx[6], s_mx[7]), 100);
+    auto write_triangle = [&]() {
+      char* out = s_r + (type & 1) * (2 * kTriBytes) + lane * 16;
+      const float f = type == 0 ? t0.f : type == 1 ? t1.f : type == 2 ? t2.f : t3.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (e && (wave & 1)) break;
+        const int tile = (wave & 1) ? 2 : e;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const Planes p = split(C[e], s, f);
+          *reinterpret_cast<h8*>(out + (tile * 2 + s) * 1024) = p.hi;
+          *reinterpret_cast<h8*>(out + kTriBytes + (tile * 2 + s) * 1024) = p.lo;
+        }
+      }
+    };
+    // sum over tokens of a transposed side (rows 32 m) times a triangle, for this wave's tokens; `lower`: over tokens not after
+    // this one, else over those not before it
+    auto through = [&](const char* side, int which, bool lower) {
+      acc16 acc = zero16();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {                        // tile of the summed tokens
+        if (lower ? t > ti : t < ti) continue;
+        const int tile = t + ti;                           // (0, 0), (1, 0) either way round, (1, 1)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          acc = mm<NP, 2>(operand<NP>(side + (m * 4 + 2 * t + s) * kBlock, lane, kTurned),
+                          operand<2>(s_r + which * (2 * kTriBytes) + (tile * 2 + s) * 1024, lane, kTriBytes), acc);
+      }
+      return acc;
+    };
+    if (type < 2) write_triangle();
+    __syncthreads();
+    float kend = 0.0f, into = s_vec[kVecInto][tok];
+    acc16 kv;
+    if (active) {
+      const acc16 nk = through(s_kt, 0, true), nq = through(s_qt, 1, false);
+      const float f = a.scale * into * pow2(-cS.e) * pow2(-cO.e), fn = pow2(-ek - t0.e), fy = pow2(-eq - t1.e);
+      const float fe = s_vec[kVecEnd][tok] * s_vec[kVecS][tok] * pow2(-cE.e) * pow2(-cU.e);
+      const float fx = into * pow2(-cS.e) * pow2(-cD.e);
+      float qdq = 0.0f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int at_k = 32 * m + 8 * g + 4 * half;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 4 * g + j;
+          const uint32_t ko = at_k + j < a.dk ? tok * krow + (at_k + j) * (int)sizeof(T) : kNowhere;
+          const uint32_t qo = at_k + j < a.dk ? tok * qrow + (at_k + j) * (int)sizeof(T) : kNowhere;
+          float qv;
+          if constexpr (NP == 2) {
+            kv[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(kr, ko, 0, 0));
+            qv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(qr, qo, 0, 0));
+          } else {
+            kv[r] = bf16_bits_to_float((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(kr, ko, 0, 0));
+            qv = bf16_bits_to_float((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(qr, qo, 0, 0));
+          }
+          const float dq = fmaf(Q[r], f, nk[r] * fn);
+          qdq = fmaf(qv, dq, qdq);
+          dQ[r] += dq;
+          const float e = Y[r] * fe;
+          kend = fmaf(kv[r], e, kend);
+          Y[r] = fmaf(nq[r], fy, e);
+          X[r] *= fx;
+        }
+      }
+      qdq += __shfl_xor(qdq, 32);
+      kend += __shfl_xor(kend, 32);
+      if (half == 0) {
+        s_dot[0][m][tok] = qdq;
+        s_dot[3][m][tok] = kend;
+      }
+    }
+    __syncthreads();
+    if (type >= 2) write_triangle();
+    __syncthreads();
+    if (active) {
+      const acc16 mk = through(s_kt, 0, true), mb = through(s_kt, 1, false);
+      const float fm = pow2(-ek - t2.e), fb = pow2(-ek - t3.e), beta = s_beta[tok];
+      float kx = 0.0f, ky = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float x = fmaf(mk[r], fm, X[r]), y = fmaf(-mb[r], fb, Y[r]);
+        kx = fmaf(kv[r], x, kx);
+        ky = fmaf(kv[r], y, ky);
+        dK[r] += fmaf(-beta, x, y);
+      }
+      kx += __shfl_xor(kx, 32);
+      ky += __shfl_xor(ky, 32);
+      if (half == 0) {
+        s_dot[1][m][tok] = kx;
+        s_dot[2][m][tok] = ky;
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {
+      float d[4] = {};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) d[i] += s_dot[i][t][lane];
+      float all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) all += s_sd[i];
+      const float end = group_sum(d[3], 64) + s_vec[kVecInto][kC - 1] * all;
+      float dgam = d[0] - s_beta[lane] * d[1] - d[2] + (lane == kC - 1 ? end : 0.0f);
+#pragma unroll
+      for (int i = 1; i < kC; i <<= 1) {
+        const float o = __shfl_down(dgam, i);
+        if (lane + i < kC) dgam += o;
+      }
+      if (lane < valid) {
+        if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = s_rv[lane] - d[1];
+        if (a.dg) a.dg[gate + (int64_t)lane * a.hv] = dgam;
+      }
+    }
+  }
+  if (active && tok < valid) {
+    const int64_t row = ((b * a.seqlen + first + tok) * a.hk + hkey) * a.dk;
+    store_runs<IO>(static_cast<T*>(a.dq) + row, 32 * m + 4 * half, a.dk, dQ, 1.0f);
+    store_runs<IO>(static_cast<T*>(a.dk_out) + row, 32 * m + 4 * half, a.dk, dK, 1.0f);
+  }
+}
+
+template <typename IO>
+hipError_t launch(const GdrArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.batch * a.hk * a.chunks));
+  return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
+    gdr_grad_kernel<IO, decltype(kp)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>(a);
+  });
+}
+
+}  // namespace
+
+hipError_t launch_gdr_grad(const GdrArgs& a, hipStream_t s) { return a.io == kIoBf16 ? launch<BF16>(a, s) : launch<F32>(a, s); }
+
+}  // namespace ssscan

@@ -256,6 +256,9 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
     v[kVecQ * kC] = scaled * into;
     v[kVecJoin * kC] = into * pow2(least - p);
     v[kVecC * kC] = inv_c;
+    const Two g2 = two(gam);
+    v[kVecHi * kC] = g2.hi;
+    v[kVecLo * kC] = g2.lo;
   }
   __syncthreads();
   // tiles as operands: slot (tile, step, lane)

@@ -75,6 +75,35 @@ def gdr_fwd(q, k, v, g, beta, h0=None, *, scale=None, o=None, h_final=None, retu
     return o, h_final
 
 
+def gdr_bwd(q, k, v, g, beta, do, h0=None, dh_final=None, *, scale=None, need_dg=True, need_dbeta=True, need_dh0=None,
+            workspace=None):
+    """Gradients of ``gdr_fwd`` for upstream gradients do (batch, L, heads_v, V), contiguous, and dh_final (batch, heads_v,
+    K, V) float32 (None = 0), given the forward's inputs.
+
+    Returns a dict: dq, dk (batch, L, heads_k, K) and dv (batch, L, heads_v, V) in q's dtype, contiguous; dg (None
+    without g), dbeta (batch, L, heads_v) and dh0 (batch, heads_v, K, V) float32, None where not needed (dh0: by default
+    where h0 is None).
+    """
+    dev, dtype, sv, head, ins = _checked(q, k, v, g, beta, scale, 4)
+    batch, L, hv, dv = sv
+    hk, _, dk = head[:3]
+    if do is None:
+        raise ValueError("do is None")
+    need((("do", do),), dtype, sv, dev)
+    need((("h0", h0), ("dh_final", dh_final)), _F32, (batch, hv, dk, dv), dev)
+
+    def vec(wanted, *shape):
+        return torch.empty(shape, dtype=_F32, device=dev) if wanted else None
+
+    out = dict(dq=torch.empty((batch, L, hk, dk), dtype=dtype, device=dev), dk=torch.empty((batch, L, hk, dk), dtype=dtype, device=dev),
+               dv=torch.empty(sv, dtype=dtype, device=dev), dg=vec(need_dg and g is not None, batch, L, hv),
+               dbeta=vec(need_dbeta, batch, L, hv), dh0=vec(h0 is not None if need_dh0 is None else need_dh0, batch, hv, dk, dv))
+    keep, ws, nbytes = _workspace(workspace, _b.ss_gdr_bwd_workspace_bytes(batch, L, hk, hv, dk, dv), dev)
+    launch(dev, _b.lib.ss_gdr_bwd, batch, L, *head, *ins, ptr(h0), do.data_ptr(), ptr(dh_final), ptr(out["dq"]), ptr(out["dk"]),
+           ptr(out["dv"]), ptr(out["dg"]), ptr(out["dbeta"]), ptr(out["dh0"]), ws, nbytes)
+    return out
+
+
 def gdr_step(state, q, k, v, g, beta, *, scale=None, o=None, state_out=None):
     """One token of ``gdr_fwd``: ``state`` (batch, heads_v, K, V) float32 is updated in place, or the
     new state is written to state_out.  q, k: (batch, heads_k, K), v: (batch, heads_v, V), g, beta:
