@@ -3,8 +3,8 @@
 // Products run on the matrix cores in fp16 planes: a value x scaled by a power of 2 s is hi = fp16(x s) and
 // lo = fp16(x s - hi), 22 bits together, and a product of two such operands is hi hi + hi lo + lo hi in fp32, within
 // about 2^-22 of the sizes of its terms: fp32 results at 3 of the 16 times that an fp32 matrix instruction costs.  A
-// bf16 input is one plane, exact to 2^-17 of its row's largest value and within 2^-25 of it below.  Scales keep a tile's largest
-// value near 2^13 (rows of keys and queries: in [1, 2)), so what an fp16 exponent cannot hold is below 2^-38 of it.
+// bf16 input is one plane.  Scales keep a tile's (of keys and queries a row's, of T a column's) largest value near 2^13, so that
+// what an fp16 cannot hold, 2^-25, is below 2^-37 of it: a chunk's later tokens may be as much smaller as decays make them.
 //
 // Tiles are 32x32x16.  A result's lane holds column l & 31 and rows (r & 3) + 8 (r >> 2) + 4 (l >> 5): for 16 rows
 // these are the 8 values that the same lane gives an operand whose summed index is that row, if the other operand
@@ -126,10 +126,13 @@ __device__ __forceinline__ Scale scale_of(float m, int most) {
   return s;
 }
 
-// The scale that takes a row whose largest |value| is m to [1, 2); 1 for a row of zeros or with an infinity (which then stays one).
+// The scale that takes a row whose largest |value| is m to [2^12, 2^13); 2^kZeroRow, larger than any row's that counts, for a row of
+// zeros, and 1 with an infinity (which then stays one).
+constexpr int kZeroRow = 100;
+
 __device__ __forceinline__ float row_scale(float m) {
   const int e = exponent(m);
-  return m == 0.0f || e == 128 ? 1.0f : pow2(-e);
+  return m == 0.0f ? pow2(kZeroRow) : e == 128 ? 1.0f : pow2(12 - e < kZeroRow ? 12 - e : kZeroRow);
 }
 
 __device__ __forceinline__ float quad_max(float m) {
@@ -337,24 +340,35 @@ hipError_t by_keys(int dk, bool whole, F f) {
 
 // The vectors that belong to a chunk of a head, kC floats each, as the preparation leaves them.  c_j scales column j of the
 // inverse T, s_j row j of k, z_i row i of q (powers of 2); gam_j is the sum of log decays up to j (over log 2), gam_C the
-// whole chunk's; s the smallest s_j, and p_i >= 0 a whole number with gam_i - gam_j <= p_i + log2(s_j / s) for j <= i, 0 where no
-// gate grows.  The operand P holds q_i.k_j s z_i 2^(gam_i - gam_j - p_i).
+// whole chunk's; s the smallest s_j.  p_i is a whole number: what the gates let the state grow up to token i since it was smallest, less
+// half of what it has decayed till then (16 at most).  T, P, U and their like are kept balanced by it, rows times 2^-p_i,
+// columns times 2^p_j, U and R as 2^-p_i U_i (their gradients times 2^p_i), so that growth costs no digits, and neither does a decay
+// of 2^-32 within the chunk, whether a token's value or the old state is the larger.  The operand P holds
+// q_i.k_j s z_i 2^(gam_i - gam_j - p_i + p_j - 18).
 enum Vec {
-  kVecF1,      // beta_j / c_j
-  kVecF2,      // beta_j 2^gam_j / (c_j s_j)
-  kVecEnd,     // 2^(gam_C - gam_j) / s_j
+  kVecF1,      // beta_j 2^-p_j / c_j
+  kVecF2,      // beta_j 2^(gam_j - p_j) / (c_j s_j)
+  kVecEnd,     // 2^(gam_C - gam_j + p_j) / s_j
   kVecInto,    // 2^gam_j
   kVecS,       // s_j
   kVecZ,       // z_i
-  kVecOut,     // scale 2^p_i / (z_i s)
+  kVecOut,     // scale 2^(p_i + 18) / (z_i s)
   kVecQ,       // scale 2^gam_i / z_i
   kVecJoin,    // kVecQ / kVecOut
+  kVecGrow = kVecJoin,   // backward: p_j
   kVecC,       // 1 / c_j
-  kVecHi,      // gam_j in two floats
-  kVecLo,
+  kVecWhole,   // gam_j - p_j as a whole number and the rest
+  kVecRest,
   kVecs
 };
 static_assert(kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
+
+constexpr int kPShift = 18;    // rows of q and k are below 2^13 and up to 2^7 long, so that P stays below 2^15
+
+// 2^(whole + rest) of a difference of two such numbers: what an fp32 exponent of that size would lose stays in the rest.
+__device__ __forceinline__ float exp2_of(float whole, float rest) {
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(rest), (int)whole);
+}
 
 // The operand blocks of a triangular matrix of a chunk: tiles (0, 0), (1, 0), (1, 1), of each two steps of 16; two planes.
 constexpr int kTriBlocks = 3 * 2;

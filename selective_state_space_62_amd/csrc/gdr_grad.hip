@@ -1,6 +1,7 @@
 // The gated delta rule backward, last step: the gradients that need no turn, a workgroup to each chunk of a key head
 // (gdr_device.h has the layouts).
 //
+// (U, dR and the triangles come and stay balanced by the growth p; gdr_device.h says how.)
 // With S before the chunk, dS behind it, U, dR and dO, D_ij = 2^(gam_i - gam_j), and M_ij = D_ij dR_i.U_j (j < i),
 // N_ij = scale D_ij dO_i.U_j (j <= i):
 //   dq_i = scale G_i S dO_i + sum_j N_ij k_j
@@ -173,14 +174,14 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
       for (int e = 0; e < 2; ++e) {
         const int tile = (wave & 1) ? 2 : e, i0 = 32 * (tile > 0), j0 = 32 * (tile > 1);
         const int col = (type & 1 ? j0 : i0) + low;
-        const float hi = s_vec[kVecHi][col], lo = s_vec[kVecLo][col];
+        const float whole = s_vec[kVecWhole][col], rest = s_vec[kVecRest][col], sign = type & 1 ? -1.0f : 1.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int row = (type & 1 ? i0 : j0) + tile_row(r, lane);
-          const float d = (hi - s_vec[kVecHi][row]) + (lo - s_vec[kVecLo][row]);
+          const float d = exp2_of(sign * (whole - s_vec[kVecWhole][row]), sign * (rest - s_vec[kVecRest][row]));
           const int i = type & 1 ? row : col, j = type & 1 ? col : row;
-          const float w = C[e][r] * f * __builtin_amdgcn_exp2f(type & 1 ? -d : d);
-          C[e][r] = j < i || (j == i && type < 2) ? (type == 3 ? w * s_beta[row] : w) : 0.0f;
+          const float w = C[e][r] * f * d;
+          C[e][r] = j < i || (j == i && type < 2) ? (type == 3 ? w * s_beta[row] : type == 1 ? w * pow2((int)s_vec[kVecGrow][row]) : w) : 0.0f;
         }
         if (!(e && (wave & 1))) mC = max_of(C[e], mC);
       }
@@ -232,9 +233,9 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
     acc16 kv;
     if (active) {
       const acc16 nk = through(s_kt, 0, true), nq = through(s_qt, 1, false);
-      const float f = a.scale * into * pow2(-cS.e) * pow2(-cO.e), fn = pow2(-ek - t0.e), fy = pow2(-eq - t1.e);
+      const float f = a.scale * into * pow2(-cS.e) * pow2(-cO.e), fn = pow2((int)s_vec[kVecGrow][tok] - ek - t0.e), fy = pow2(-eq - t1.e);
       const float fe = s_vec[kVecEnd][tok] * s_vec[kVecS][tok] * pow2(-cE.e) * pow2(-cU.e);
-      const float fx = into * pow2(-cS.e) * pow2(-cD.e);
+      const float fx = exp2_of(s_vec[kVecWhole][tok], s_vec[kVecRest][tok]) * pow2(-cS.e) * pow2(-cD.e);
       float qdq = 0.0f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -307,7 +308,7 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
         if (lane + i < kC) dgam += o;
       }
       if (lane < valid) {
-        if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = s_rv[lane] - d[1];
+        if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = s_rv[lane] * pow2(-(int)s_vec[kVecGrow][lane]) - d[1];
         if (a.dg) a.dg[gate + (int64_t)lane * a.hv] = dgam;
       }
     }

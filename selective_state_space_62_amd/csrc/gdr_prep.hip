@@ -5,8 +5,9 @@
 // beta_i 2^(gam_i - gam_j) k_i.k_j.  This kernel makes T = (I + A)^-1, P, the lower triangle of 2^(gam_i - gam_j) q_i.k_j, and the
 // decays' vectors, a workgroup to each chunk of a head.  k.k^T and q.k^T are matrix products; the inverse is by 16x16
 // triangles on the diagonal, a lane to a column, and then by twice joining neighbours, T21 = -T22 A21 T11, in fp32.
-// Sums of log decays are formed in fp64 and kept as two floats: a forgotten state (a decay of -inf, held to -2000 here)
-// must not cost the decays behind it their digits.
+// (A, T and P are formed balanced by the growth p; gdr_device.h says how.)
+// Sums of log decays are formed in fp64 and kept as a whole number and the rest: a forgotten state (a decay of -inf, held to -2000
+// here) must not cost the decays behind it their digits.
 #include "gdr_device.h"
 
 namespace ssscan {
@@ -17,14 +18,19 @@ using namespace gdr;
 constexpr int kThreads = 256;
 constexpr int kPitch = 68;               // floats of a row in LDS
 
-// A sum of log decays in two floats.
+// A sum of log decays as a whole number and the rest, at most 1/2.
 struct Two {
-  float hi, lo;
+  float whole, rest;
 };
 
 __device__ __forceinline__ Two two(double v) {
-  const float hi = (float)v;
-  return {hi, (float)(v - (double)hi)};
+  const double w = __builtin_rint(v);
+  return {(float)w, (float)(v - w)};
+}
+
+__device__ __forceinline__ float exp2_wide(double v) {
+  const Two t = two(v);
+  return exp2_of(t.whole, t.rest);
 }
 
 template <typename IO, int KP, bool WHOLE, bool BWD>
@@ -34,7 +40,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   constexpr int kSide = 2 * kSteps * kBlock, kRows = 2 * NP * kSide, kTile = kC * kPitch * 4;
   __shared__ alignas(16) char s_rows[kRows > kTile ? kRows : kTile];      // rows of k, of q; then T
   __shared__ alignas(16) float s_a[kC][kPitch];
-  __shared__ alignas(16) float s_hi[3][kC], s_lo[3][kC], s_beta[kC];      // of A's row, of P's row, of a column
+  __shared__ alignas(16) float s_whole[3][kC], s_rest[3][kC], s_beta[kC];      // of A's row, of P's row, of a column
   __shared__ float s_scale[2][kC], s_max[4][kC], s_col[kC];
   float(&s_t)[kC][kPitch] = *reinterpret_cast<float(*)[kC][kPitch]>(s_rows);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -91,7 +97,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
       acc[n] = mm<NP, NP>(operand<NP>((turned ? pj : pi) + s * kBlock, lane, kSide),
                           operand<NP>((turned ? pi : pj) + s * kBlock, lane, kSide), acc[n]);
   }
-  double gam = 0.0, end = 0.0;
+  double gam = 0.0, end = 0.0, bal = 0.0;
   float beta = 0.0f, into = 0.0f, sk = 1.0f, sq = 1.0f, grow = 0.0f;
   int least = 0;
   if (wave == 3) {
@@ -110,7 +116,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
     sq = s_scale[1][lane];
     const int es = exponent(sk);
     least = es;
-    double low = gam + (double)es;                         // the smallest gam_j + log2 s_j up to here
+    double low = gam;                                      // the smallest gam_j up to here
 #pragma unroll
     for (int d = 1; d < kC; d <<= 1) {
       const int o = __shfl_xor(least, d);
@@ -118,14 +124,16 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
       const double l = __shfl_up(low, d);
       if (lane >= d) low = l < low ? l : low;
     }
-    const double p = fmax(ceil(gam - (low - (double)least)), 0.0);
+    least = least == kZeroRow ? 0 : least;
+    const double p = ceil(gam - low) - floor(fmin(fmax(-0.5 * low, 0.0), 16.0));
     grow = (float)p;
-    const Two ri = two(gam - (double)es), pi = two(gam - p + (double)least), cj = two(gam + (double)es);
-    s_hi[0][lane] = ri.hi; s_lo[0][lane] = ri.lo;
-    s_hi[1][lane] = pi.hi; s_lo[1][lane] = pi.lo;
-    s_hi[2][lane] = cj.hi; s_lo[2][lane] = cj.lo;
+    bal = gam - p;
+    const Two ri = two(bal - (double)es), pi = two(bal + (double)(least - kPShift)), cj = two(bal + (double)es);
+    s_whole[0][lane] = ri.whole; s_rest[0][lane] = ri.rest;
+    s_whole[1][lane] = pi.whole; s_rest[1][lane] = pi.rest;
+    s_whole[2][lane] = cj.whole; s_rest[2][lane] = cj.rest;
     s_beta[lane] = beta;
-    into = __builtin_amdgcn_exp2f((float)gam);
+    into = exp2_wide(gam);
   }
   __syncthreads();
   const int64_t at = blockIdx.x;
@@ -137,12 +145,12 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
     if (task > 2) {
       const int v = !BWD ? 1 : 2, w = 3 - v;               // the vector of a lane's column, of its 16 rows
       const int c = 32 * (BWD ? tj : ti) + (lane & 31), r0 = 32 * (BWD ? ti : tj);
-      const float sign = BWD ? -1.0f : 1.0f, hi = s_hi[v][c], lo = s_lo[v][c];
+      const float sign = BWD ? -1.0f : 1.0f, whole = s_whole[v][c], rest = s_rest[v][c];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = r0 + tile_row(r, lane);
-        const float e = sign * ((hi - s_hi[w][row]) + (lo - s_lo[w][row]));
-        acc[n][r] = (BWD ? c <= row : row <= c) ? acc[n][r] * __builtin_amdgcn_exp2f(e) : 0.0f;
+        const float d = exp2_of(sign * (whole - s_whole[w][row]), sign * (rest - s_rest[w][row]));
+        acc[n][r] = (BWD ? c <= row : row <= c) ? acc[n][r] * d : 0.0f;
       }
       constexpr int NO = BWD ? 2 : NP;
       char* out = static_cast<char*>(a.p) + at * (NO * kTriBytes) + tile * 2048 + lane * 16;
@@ -154,12 +162,12 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
       }
     } else {
       const int j = 32 * tj + (lane & 31);
-      const float hi = s_hi[2][j], lo = s_lo[2][j];
+      const float whole = s_whole[2][j], rest = s_rest[2][j];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int i = 32 * ti + tile_row(r, lane);
-        const float e = (s_hi[0][i] - hi) + (s_lo[0][i] - lo);
-        s_a[i][j] = j < i ? s_beta[i] * (acc[n][r] * __builtin_amdgcn_exp2f(e)) : 0.0f;
+        const float d = exp2_of(s_whole[0][i] - whole, s_rest[0][i] - rest);
+        s_a[i][j] = j < i ? s_beta[i] * (acc[n][r] * d) : 0.0f;
       }
     }
   }
@@ -232,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
     *reinterpret_cast<float4*>(&s_t[32 + i][n]) = make_float4(m[0], m[1], m[2], m[3]);
   }
   __syncthreads();
-  // columns to [1, 2) or below 1 (the diagonal is 1)
+  // columns to [2^13, 2^14)
   {
     const int col = tid & 63, part = tid >> 6;
     float m = 0.0f;
@@ -242,23 +250,24 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   __syncthreads();
   if (wave == 3) {
     const float m = fmaxf(fmaxf(s_max[0][lane], s_max[1][lane]), fmaxf(s_max[2][lane], s_max[3][lane]));
-    const int ec = exponent(m), es = exponent(sk), ez = exponent(sq), p = (int)grow;
+    const int ec = exponent(m) - 13, es = exponent(sk), ez = exponent(sq), p = (int)grow;
     s_col[lane] = pow2(-ec);
     const float inv_c = pow2(ec), inv_s = pow2(-es), inv_z = pow2(-ez), scaled = a.scale * inv_z;
     float* v = a.vecs + at * (kVecs * kC) + lane;
-    v[kVecF1 * kC] = beta * inv_c;
-    v[kVecF2 * kC] = beta * into * inv_c * inv_s;
-    v[kVecEnd * kC] = __builtin_amdgcn_exp2f((float)(end - gam)) * inv_s;
+    v[kVecF1 * kC] = beta * pow2(-p) * inv_c;
+    v[kVecF2 * kC] = beta * exp2_wide(bal) * inv_c * inv_s;
+    v[kVecEnd * kC] = exp2_wide(end - bal) * inv_s;
     v[kVecInto * kC] = into;
     v[kVecS * kC] = sk;
     v[kVecZ * kC] = sq;
-    v[kVecOut * kC] = scaled * pow2(p - least);
+    v[kVecOut * kC] = scaled * pow2(p + kPShift - least);
     v[kVecQ * kC] = scaled * into;
-    v[kVecJoin * kC] = into * pow2(least - p);
+    if constexpr (BWD) v[kVecGrow * kC] = grow;
+    else v[kVecJoin * kC] = exp2_wide(bal) * pow2(least - kPShift);
     v[kVecC * kC] = inv_c;
-    const Two g2 = two(gam);
-    v[kVecHi * kC] = g2.hi;
-    v[kVecLo * kC] = g2.lo;
+    const Two b2 = two(bal);
+    v[kVecWhole * kC] = b2.whole;
+    v[kVecRest * kC] = b2.rest;
   }
   __syncthreads();
   // tiles as operands: slot (tile, step, lane)

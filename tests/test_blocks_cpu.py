@@ -20,12 +20,16 @@ def at(k, off=0):
 def gdr(entry="fwd", **kw):
     a = dict(batch=2, seqlen=100, hk=2, hv=4, dk=64, dv=80, io=b.SS_BF16, scale=0.125, q=at(0), qs=(12800, 128, 64), k=at(1),
              ks=(12800, 128, 64), v=at(2), vs=(32000, 320, 80), g=at(3), beta=at(4), h0=at(5), o=at(6), h_final=at(7), ws=at(8),
-             ws_bytes=1 << 29, state_in=at(5), state_out=at(5))
+             ws_bytes=1 << 29, state_in=at(5), state_out=at(5), do=at(10), dh_final=at(11), dq=at(12), dk_=at(13), dv_=at(14), dg=at(15),
+             dbeta=at(16), dh0=at(17))
     a.update(kw)
     ins = (a["q"], b._strides(a["qs"]), a["k"], b._strides(a["ks"]), a["v"], b._strides(a["vs"]), a["g"], a["beta"])
     sizes = (a["hk"], a["hv"], a["dk"], a["dv"], a["io"], a["scale"])
     if entry == "fwd":
         st = b.lib.ss_gdr_fwd(a["batch"], a["seqlen"], *sizes, *ins, a["h0"], a["o"], a["h_final"], a["ws"], a["ws_bytes"], None)
+    elif entry == "bwd":
+        st = b.lib.ss_gdr_bwd(a["batch"], a["seqlen"], *sizes, *ins, a["h0"], a["do"], a["dh_final"], a["dq"], a["dk_"], a["dv_"], a["dg"],
+                              a["dbeta"], a["dh0"], a["ws"], a["ws_bytes"], None)
     else:
         st = b.lib.ss_gdr_step(a["batch"], *sizes, a["state_in"], a["state_out"], *ins, a["o"], None)
     return st, b.last_error()
@@ -38,13 +42,16 @@ GDR = [
     (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(beta=None), INVALID), (dict(q=at(0, 1)), INVALID), (dict(io=b.SS_F32, v=at(2, 2)), INVALID), (dict(g=at(3, 2)), INVALID),
     (dict(beta=at(4, 1)), INVALID), (dict(qs=None), INVALID), (dict(ks=(-1, 128, 64)), INVALID), (dict(vs=(1 << 62, 320, 80)), INVALID),
-    (dict(o=None), INVALID), (dict(o=at(6, 8)), INVALID), (dict(o=at(0)), INVALID), (dict(o=at(4)), INVALID),
     (dict(batch=1 << 22, dk=1, dv=1, seqlen=1, qs=(2, 2, 1), ks=(2, 2, 1), vs=(4, 4, 1)), UNSUPPORTED),
 ]
 
 
-@pytest.mark.parametrize("case,status", GDR + [
+OUT = [(dict(o=None), INVALID), (dict(o=at(6, 8)), INVALID), (dict(o=at(0)), INVALID), (dict(o=at(4)), INVALID)]
+
+
+@pytest.mark.parametrize("case,status", GDR + OUT + [
     (dict(seqlen=-1), INVALID), (dict(seqlen=1 << 41), INVALID), (dict(h0=at(5, 2)), INVALID), (dict(h_final=at(7, 2)), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=at(8, 128)), WORKSPACE), (dict(ws_bytes=1 << 10), WORKSPACE), (dict(h_final=at(8)), INVALID),
     (dict(h_final=at(5)), INVALID), (dict(h_final=at(6)), INVALID),
 ])
 def test_gdr_fwd_refuses(case, status):
@@ -52,7 +59,20 @@ def test_gdr_fwd_refuses(case, status):
     assert st == status and msg, (st, msg)
 
 
-@pytest.mark.parametrize("case,status", GDR + [
+@pytest.mark.parametrize("case,status", [c for c in GDR if c[0].get("batch") != 1 << 22] + [
+    (dict(seqlen=-1), INVALID), (dict(do=None), INVALID), (dict(do=at(10, 8)), INVALID), (dict(dq=None), INVALID), (dict(dk_=None), INVALID),
+    (dict(dv_=at(14, 4)), INVALID), (dict(dh_final=at(11, 2)), INVALID), (dict(dg=at(15, 1)), INVALID), (dict(dbeta=at(16, 2)), INVALID),
+    (dict(dh0=at(17, 2)), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=at(8, 64)), WORKSPACE), (dict(ws_bytes=1 << 16), WORKSPACE),
+    (dict(dq=at(0)), INVALID), (dict(dv_=at(10)), INVALID), (dict(dk_=at(12)), INVALID), (dict(dh0=at(11)), INVALID), (dict(dh0=at(5)), INVALID),
+    (dict(dbeta=at(15)), INVALID), (dict(dg=at(8)), INVALID), (dict(vs=(1 << 30, 1 << 22, 80)), UNSUPPORTED), (dict(hv=1 << 10, dv=1 << 12), UNSUPPORTED),
+    (dict(batch=1 << 22, dk=1, dv=1, seqlen=1, qs=(2, 2, 1), ks=(2, 2, 1), vs=(4, 4, 1), ws=1 << 40, ws_bytes=1 << 42, h0=None, dh0=None, dh_final=None), UNSUPPORTED),
+])
+def test_gdr_bwd_refuses(case, status):
+    st, msg = gdr("bwd", **case)
+    assert st == status and msg, (st, msg)
+
+
+@pytest.mark.parametrize("case,status", GDR + OUT + [
     (dict(state_in=None), INVALID), (dict(state_out=None), INVALID), (dict(state_out=at(5, 256)), INVALID),
     (dict(state_out=at(9, 2)), INVALID), (dict(state_in=at(5, 2), state_out=at(9)), INVALID), (dict(o=at(5)), INVALID),
     (dict(state_out=at(6)), INVALID), (dict(state_out=at(2)), INVALID),
@@ -153,6 +173,7 @@ def test_empty_calls_launch_nothing():
     assert gated("bwd", seqlen=0, dw=None, ws=None, ws_bytes=0)[0] == OK
     assert residual("bwd", rows=0, dw=None, dw_post=None, dscale=None)[0] == OK
     assert gdr(seqlen=0, h_final=None, ws=None, ws_bytes=0)[0] == OK
+    assert gdr("bwd", seqlen=0, dh0=None, ws=None, ws_bytes=0)[0] == OK
 
 
 def test_sizes():
@@ -162,4 +183,8 @@ def test_sizes():
     assert 0 < b.ss_gated_norm_bwd_workspace_bytes(1, 1 << 11, 1 << 20, 8, b.SS_NORM_HEAD_WEIGHTS) <= 1 << 26
     assert b.ss_residual_norm_bwd_workspace_bytes(0, 16) == 0 and b.ss_residual_norm_bwd_workspace_bytes(5, 9000) == 0
     assert 0 < b.ss_residual_norm_bwd_workspace_bytes((1 << 32) - 1, 8192) < 1 << 30
+    assert b.ss_gdr_bwd_workspace_bytes(1, 0, 1, 1, 16, 16) == 0 and b.ss_gdr_bwd_workspace_bytes(1, 5, 2, 3, 16, 16) == 0
+    one, two = b.ss_gdr_bwd_workspace_bytes(1, 64, 1, 1, 128, 128), b.ss_gdr_bwd_workspace_bytes(1, 128, 1, 1, 128, 128)
+    assert two >= one + 2 * (128 + 64) * 128 * 4           # two states, U and the gradient of R
+    assert b.ss_gdr_fwd_workspace_bytes(1, 16, 1, 1, 16, 16) == 0 and b.ss_gdr_fwd_workspace_bytes(1, 17, 1, 1, 16, 16) > 0
     assert b.ss_gdr_fwd_workspace_bytes(0, 5, 1, 1, 16, 16) == 0 and b.ss_gdr_fwd_workspace_bytes(1, 5, 1, 1, 200, 16) == 0

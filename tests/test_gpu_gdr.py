@@ -1,0 +1,389 @@
+"""The gated delta rule on the GPU against the recurrence in 64 bits: outputs, states and gradients."""
+import pytest
+import torch
+
+from blocks import F32_REL, close, gdr64, leaves, rel, tolerance, up
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ss():
+    import selective_state_space_62_amd as ss
+    return ss
+
+
+def problem(batch, L, hk, hv, dk, dv, io, seed=0, g=True, h0=True):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+
+    def unit(common):
+        x = rn(batch, L, hk, dk) + common * rn(hk, dk)
+        return (x / x.norm(dim=-1, keepdim=True).clamp_min(1e-6)).to(io).cuda()
+    return dict(q=unit(0.0), k=unit(0.5), v=rn(batch, L, hv, dv).to(io).cuda(),
+                g=(-0.3 * torch.nn.functional.softplus(rn(batch, L, hv))).cuda() if g else None,
+                beta=torch.sigmoid(rn(batch, L, hv)).cuda(), h0=0.3 * rn(batch, hv, dk, dv).cuda() if h0 else None)
+
+
+def want(p, scale=None):
+    return gdr64(*[up(p[n]) for n in ("q", "k", "v", "g", "beta", "h0")], p["q"].shape[-1] ** -0.5 if scale is None else scale)
+
+
+def check_fwd(ss, p, tol=None, **kw):
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"], **kw)
+    wo, wh = want(p, kw.get("scale"))
+    close("o", o, wo, tol or tolerance(o))
+    close("h_final", h, wh, tol or F32_REL)
+    return o, h
+
+
+def check_bwd(ss, p, seed=1, dg_tol=None, dh=True):
+    gen = torch.Generator().manual_seed(seed)
+    do = torch.randn(p["v"].shape, generator=gen).to(p["v"].dtype).cuda()
+    b, _, hv, dv = p["v"].shape
+    dhf = torch.randn(b, hv, p["q"].shape[-1], dv, generator=gen).cuda() if dh else None
+    got = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], do, p["h0"], dhf)
+    ls = leaves(*[p[n] for n in ("q", "k", "v", "g", "beta", "h0")])
+    o, h = gdr64(*ls, p["q"].shape[-1] ** -0.5)
+    loss = (o * up(do)).sum() + ((h * up(dhf)).sum() if dh else 0.0)
+    loss.backward()
+    for n, l in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), ls):
+        if l is None:
+            assert got[n] is None
+            continue
+        if n == "dg":
+            # a decay's gradient is <dS, S>, what is left of sums over a chunk as large as |dS| |S| of its tokens: 2^-19 of those
+            size = float((up(dhf).norm() if dh else 0.0) * h.detach().norm() + (up(do).norm() * o.detach().norm())) / max(1.0, l.numel()) ** 0.5
+            off = float((got[n].double().cpu() - l.grad).norm())
+            assert off <= F32_REL * float(l.grad.norm()) + 2.0 ** -19 * size * l.numel() ** 0.5, (n, off, float(l.grad.norm()), size)
+        else:
+            close(n, got[n], l.grad, tolerance(got[n]))
+    return got
+
+
+SIZES = [
+    (1, 1, 1, 1, 1, 1, F), (2, 1, 2, 4, 16, 16, BF), (1, 2, 1, 1, 3, 5, F), (3, 16, 1, 2, 8, 33, BF), (1, 17, 1, 1, 16, 16, F),
+    (2, 63, 2, 2, 32, 32, BF), (1, 64, 1, 3, 64, 64, F), (2, 65, 1, 1, 33, 31, F), (1, 127, 2, 4, 72, 80, BF), (1, 128, 1, 1, 128, 128, F),
+    (2, 129, 3, 3, 96, 100, BF), (1, 200, 1, 4, 128, 257, BF), (1, 333, 2, 2, 50, 200, F), (1, 97, 1, 1, 127, 129, F), (1, 130, 1, 1, 1, 64, BF),
+    (1, 80, 2, 2, 100, 4, F), (1, 70, 1, 1, 128, 300, F),
+]
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_forward(ss, size):
+    check_fwd(ss, problem(*size))
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_backward(ss, size):
+    check_bwd(ss, problem(*size))
+
+
+@pytest.mark.parametrize("L", [1, 5, 64, 150])
+def test_without_gates_states_and_gradients_of_them(ss, L):
+    p = problem(2, L, 1, 2, 24, 40, F, g=False, h0=False)
+    check_fwd(ss, p)
+    got = check_bwd(ss, p, dh=False)
+    assert got["dg"] is None and got["dh0"] is None
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], None, p["beta"], return_final_state=False)
+    assert h is None
+    assert ss.gdr_bwd(p["q"], p["k"], p["v"], None, p["beta"], p["v"], need_dh0=True)["dh0"].shape == (2, 2, 24, 40)
+
+
+@pytest.mark.parametrize("io", [F, BF])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (72, 40), (30, 50)])
+def test_strided_rows(ss, io, offset, dk, dv):
+    """q, k and v as columns of one projection's rows, at even and odd places; and tokens as the slowest dimension."""
+    p = problem(2, 100, 2, 4, dk, dv, io)
+    n = 2 * dk + 2 * dk + 4 * dv
+    rows = torch.full((2, 100, n + 8), 7.0, dtype=io, device="cuda")
+    at = offset
+    cols = {}
+    for name, heads, d in (("q", 2, dk), ("k", 2, dk), ("v", 4, dv)):
+        cols[name] = rows[..., at:at + heads * d].unflatten(-1, (heads, d))
+        cols[name].copy_(p[name])
+        at += heads * d
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+    o2, h2 = ss.gdr_fwd(cols["q"], cols["k"], cols["v"], p["g"], p["beta"], p["h0"])
+    close("o", o2, up(o), 2 * tolerance(o))
+    close("h", h2, up(h), 2 * F32_REL)
+    g1 = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], o, p["h0"], h)
+    turned = {n: p[n].permute(1, 2, 0, 3).contiguous().permute(2, 0, 1, 3) for n in ("q", "k", "v")}
+    g2 = ss.gdr_bwd(turned["q"], turned["k"], cols["v"], p["g"], p["beta"], o, p["h0"], h)
+    for n in g1:
+        close(n, g2[n], up(g1[n]), 2 * tolerance(g1[n]) if n != "dg" else 1e-4)
+
+
+@pytest.mark.parametrize("L", [8, 100])
+def test_broadcast_rows(ss, L):
+    """A key for all heads, a value for all tokens: strides of 0."""
+    p = problem(2, L, 1, 4, 32, 48, F)
+    p["k"] = p["k"][:, :, :1].expand(2, L, 1, 32)
+    p["v"] = p["v"][:, :1].expand(2, L, 4, 48)
+    check_fwd(ss, p)
+    check_bwd(ss, p)
+
+
+def test_tokens_far_apart(ss):
+    """A token stride that the chunked kernels do not take goes token by token; the backward refuses it."""
+    buf = torch.zeros(40, 1 << 22, device="cuda")
+    p = problem(1, 40, 1, 1, 16, 16, F)
+    v = buf.as_strided((1, 40, 1, 16), (0, 1 << 22, 16, 1))
+    v.copy_(p["v"])
+    o, _ = ss.gdr_fwd(p["q"], p["k"], v, p["g"], p["beta"], p["h0"])
+    close("o", o, want(p)[0], F32_REL)
+    with pytest.raises(ss.SsError, match="2\\^22"):
+        ss.gdr_bwd(p["q"], p["k"], v, p["g"], p["beta"], o)
+
+
+def test_offsets_past_32_bits(ss):
+    """Batch rows 2^31 values apart."""
+    p = problem(2, 70, 1, 1, 32, 32, BF)
+    apart = (1 << 31) + 64
+    buf = torch.zeros(apart + 70 * 32, dtype=BF, device="cuda")
+    v = buf.as_strided((2, 70, 1, 32), (apart, 32, 32, 1))
+    v.copy_(p["v"])
+    q = buf.as_strided((2, 70, 1, 32), (apart - 70 * 64, 32, 32, 1), 70 * 64)
+    q.copy_(p["q"])
+    p["q"], p["v"] = q, v
+    check_fwd(ss, p)
+    check_bwd(ss, p)
+
+
+@pytest.mark.parametrize("L", [10, 90])
+def test_forgotten_states(ss, L):
+    """A log decay of -inf: nothing of what was before reaches the token or those behind it; nor its neighbours' digits."""
+    p = problem(2, L, 1, 2, 32, 32, F)
+    for t in (0, 3, L // 2, L - 1):
+        p["g"][:, t] = -float("inf")
+    o, h = check_fwd(ss, p)
+    p2 = dict(p, h0=p["h0"] * 100.0)
+    o2, h2 = ss.gdr_fwd(p2["q"], p2["k"], p2["v"], p2["g"], p2["beta"], p2["h0"])
+    assert rel(o2, up(o)) < 1e-12 and rel(h2, up(h)) < 1e-12
+    do = torch.ones_like(o)
+    got = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], do, p["h0"])
+    ls = leaves(*[p[n] for n in ("q", "k", "v", "g", "beta", "h0")])
+    gdr64(*ls, 32 ** -0.5)[0].sum().backward()
+    for n, l in zip(("dq", "dk", "dv", "dbeta"), (ls[0], ls[1], ls[2], ls[4])):
+        close(n, got[n], l.grad, F32_REL)
+    assert float(got["dh0"].abs().max()) == 0.0 and bool(torch.isfinite(got["dg"]).all())
+
+
+@pytest.mark.parametrize("rate", [-1e-4, -30.0, -3000.0])
+def test_decays_of_every_size(ss, rate):
+    p = problem(1, 140, 1, 2, 64, 64, F)
+    p["g"] = rate * torch.rand(1, 140, 2, generator=torch.Generator().manual_seed(3)).cuda()
+    check_fwd(ss, p)
+
+
+def test_gates_that_grow(ss):
+    """Log decays above 0: a state that grows by e^30 over a chunk, and shrinks again."""
+    p = problem(1, 200, 1, 2, 32, 32, F)
+    p["beta"] *= 0.2
+    p["g"] = torch.where(torch.arange(200, device="cuda")[None, :, None] // 50 % 2 == 0, 0.5, -0.5).expand(1, 200, 2).contiguous()
+    check_fwd(ss, p)
+    check_bwd(ss, p)
+
+
+@pytest.mark.parametrize("L", [12, 150])
+def test_padding(ss, L):
+    """beta = 0, g = 0: the state passes; a row of nothing else returns its state, and outputs that are of it alone."""
+    p = problem(3, L, 2, 2, 40, 24, F)
+    keep = [0, L // 3, L]
+    for b, n in enumerate(keep):
+        p["beta"][b, n:] = 0.0
+        p["g"][b, n:] = 0.0
+    o, h = check_fwd(ss, p)
+    assert rel(h[0], up(p["h0"][0])) < 2.0 ** -20
+    n = keep[1]
+    o1, h1 = ss.gdr_fwd(*[p[k][1:2, :n] for k in ("q", "k", "v")], *[p[k][1:2, :n].contiguous() for k in ("g", "beta")], p["h0"][1:2])
+    close("h", h[1:2], up(h1), 2 * F32_REL)
+    got = check_bwd(ss, p)
+    assert float(got["dv"][0].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("sv,sh,sk", [(1e18, 1.0, 1.0), (1.0, 1e-18, 1.0), (1e-20, 1e-20, 1.0), (1e15, 1e15, 1e-6), (1.0, 1.0, 0.0), (0.0, 1.0, 1.0),
+                                      (0.0, 0.0, 1.0), (1e12, 1e-12, 1e-3)])
+@pytest.mark.parametrize("io", [F, BF])
+def test_sizes_of_values(ss, sv, sh, sk, io):
+    """Results keep their digits whatever the inputs' sizes are; zeros stay zeros."""
+    p = problem(1, 130, 1, 2, 48, 40, io)
+    p["v"], p["h0"], p["k"] = (p["v"].float() * sv).to(io), p["h0"] * sh, (p["k"].float() * sk).to(io)
+    check_fwd(ss, p)
+    got = check_bwd(ss, p)
+    if sv == sh == 0.0:
+        assert all(float(got[n].abs().max()) == 0.0 for n in ("dbeta", "dg"))
+
+
+def test_rows_of_other_sizes(ss):
+    """Tokens whose keys, queries and values are 2^10 apart in size."""
+    p = problem(1, 128, 1, 1, 64, 64, F)
+    s = 2.0 ** torch.randint(-10, 1, (1, 128, 1, 1), generator=torch.Generator().manual_seed(5)).float().cuda()
+    p["q"], p["k"] = p["q"] * s.flip(1), p["k"] * s
+    check_fwd(ss, p)
+    check_bwd(ss, p)
+
+
+def test_keys_all_alike(ss):
+    """The same key at every token, beta 1: a chunk's triangle is full, and the state holds the last value."""
+    p = problem(1, 160, 1, 1, 32, 32, F, g=False, h0=False)
+    p["k"][:] = p["k"][:, :1]
+    p["beta"][:] = 1.0
+    o, h = check_fwd(ss, p)
+    check_bwd(ss, p)
+
+
+def test_nan_stays_in_its_head(ss):
+    p = problem(2, 100, 2, 4, 32, 32, F)
+    clean = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+    gc = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["v"], p["h0"])
+    for bad in (float("nan"), float("inf")):
+        v = p["v"].clone()
+        v[1, 70, 2, 5] = bad
+        o, h = ss.gdr_fwd(p["q"], p["k"], v, p["g"], p["beta"], p["h0"])
+        assert not bool(torch.isfinite(o[1, 70:, 2]).all()) and not bool(torch.isfinite(h[1, 2]).all())
+        assert torch.equal(o[1, :64], clean[0][1, :64])        # the chunk before
+        g = ss.gdr_bwd(p["q"], p["k"], v, p["g"], p["beta"], p["v"], p["h0"])
+        for b, hd in ((0, 0), (0, 2), (1, 0), (1, 1), (1, 3)):
+            assert torch.equal(o[b, :, hd], clean[0][b, :, hd]) and torch.equal(h[b, hd], clean[1][b, hd])
+            assert torch.equal(g["dv"][b, :, hd], gc["dv"][b, :, hd]) and torch.equal(g["dbeta"][b, :, hd], gc["dbeta"][b, :, hd])
+        assert torch.equal(g["dk"][0], gc["dk"][0]) and torch.equal(g["dk"][1, :, 0], gc["dk"][1, :, 0])
+
+
+@pytest.mark.parametrize("size", [(2, 1, 4, 16, 16, F), (3, 2, 2, 128, 128, BF), (2, 1, 3, 72, 80, BF), (1, 1, 1, 33, 1, F), (5, 2, 4, 64, 200, F),
+                                  (2, 1, 1, 1, 7, BF), (1, 1, 2, 128, 1000, F)], ids=str)
+def test_step(ss, size):
+    batch, hk, hv, dk, dv, io = size
+    p = problem(batch, 6, hk, hv, dk, dv, io)
+    state, outs = p["h0"].clone(), []
+    for t in range(6):
+        args = [p[n][:, t] for n in ("q", "k", "v")] + [p[n][:, t].contiguous() for n in ("g", "beta")]
+        if t % 2:
+            outs.append(ss.gdr_step(state, *args))
+        else:
+            new = torch.empty_like(state)
+            outs.append(ss.gdr_step(state, *args, state_out=new))
+            state = new
+    wo, wh = want(p)
+    close("o", torch.stack(outs, 1), wo, tolerance(p["v"]))
+    close("state", state, wh, F32_REL)
+    off = torch.empty(state.numel() + 1, device="cuda")[1:].view(state.shape)    # 4-byte aligned states
+    o = ss.gdr_step(p["h0"], *args, state_out=off)
+    ref = p["h0"].clone()
+    assert rel(o, up(ss.gdr_step(ref, *args))) <= tolerance(o) and rel(off, up(ref)) <= F32_REL
+
+
+def test_scale(ss):
+    p = problem(1, 100, 1, 1, 16, 16, F)
+    check_fwd(ss, p, scale=-2.5)
+    o, _ = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"], scale=0.0)
+    assert float(o.abs().max()) == 0.0
+
+
+def test_empty(ss):
+    p = problem(2, 0, 1, 2, 8, 8, F)
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+    assert o.shape == (2, 0, 2, 8) and torch.equal(h, p["h0"])
+    g = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["v"], p["h0"], p["h0"])
+    assert torch.equal(g["dh0"], p["h0"]) and g["dv"].shape == (2, 0, 2, 8)
+
+
+def test_runs_repeat_bit_for_bit(ss):
+    p = problem(2, 300, 2, 4, 128, 96, BF)
+    a = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+    ga = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], a[0], p["h0"], a[1])
+    for _ in range(3):
+        b = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+        gb = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], b[0], p["h0"], b[1])
+        assert all(torch.equal(x, y) for x, y in zip(a, b)) and all(torch.equal(ga[n], gb[n]) for n in ga)
+
+
+def test_gradient_against_differences(ss):
+    """Along a direction of all inputs at once: the 64-bit recurrence's differences against the kernels' gradients."""
+    p = problem(1, 90, 1, 2, 24, 24, F)
+    gen = torch.Generator().manual_seed(9)
+    do, dh = torch.randn(p["v"].shape, generator=gen).cuda(), torch.randn(p["h0"].shape, generator=gen).cuda()
+    g = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], do, p["h0"], dh)
+    names = ("q", "k", "v", "g", "beta", "h0")
+    d = {n: torch.randn(p[n].shape, generator=gen).double() for n in names}
+
+    def loss(e):
+        o, h = gdr64(*[up(p[n]) + e * d[n] for n in names], 24 ** -0.5)
+        return float((o * up(do)).sum() + (h * up(dh)).sum())
+    e = 1e-5                                               # the third derivative's part is e^2, the 64-bit noise 1e-16/e
+    diff = (loss(e) - loss(-e)) / (2 * e)
+    along = sum(float((up(g["d" + n]) * d[n]).sum()) for n in names)
+    size = sum(float(up(g["d" + n]).norm() * d[n].norm()) / d[n].numel() ** 0.5 for n in names)
+    assert abs(along - diff) <= 1e-4 * (abs(diff) + size), (along, diff)
+
+
+def test_streams_and_graphs(ss):
+    """On a stream of its own; captured (a forward and its backward), replayed with eager work in between."""
+    p = problem(2, 130, 1, 2, 64, 64, BF)
+    names = ("q", "k", "v", "g", "beta")
+    ref = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
+    gref = ss.gdr_bwd(*[p[n] for n in names], ref[0], p["h0"], ref[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o, h = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
+        st = p["h0"].clone()
+        ss.gdr_step(st, *[p[n][:, 0] for n in names[:3]], *[p[n][:, 0].contiguous() for n in names[3:]])
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(o, ref[0]) and torch.equal(h, ref[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go, gh = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
+        gg = ss.gdr_bwd(*[p[n] for n in names], go, p["h0"], gh)
+    for k in range(4):
+        p["v"].copy_((p["v"].float() * 0.5 + k).to(BF))
+        graph.replay()
+        e = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
+        eg = ss.gdr_bwd(*[p[n] for n in names], e[0], p["h0"], e[1])
+        torch.cuda.synchronize()
+        assert torch.equal(go, e[0]) and torch.equal(gh, e[1]) and all(torch.equal(gg[n], eg[n]) for n in gg)
+
+
+def test_workspace_may_hold_anything(ss):
+    """A caller's workspace, larger than needed and full of NaN; and one that is too small."""
+    p = problem(1, 100, 1, 2, 32, 48, F)
+    names = ("q", "k", "v", "g", "beta")
+    ref = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
+    gref = ss.gdr_bwd(*[p[n] for n in names], ref[0], p["h0"], ref[1])
+    ws = torch.full((1 << 24,), float("nan"), device="cuda")
+    o, h = ss.gdr_fwd(*[p[n] for n in names], p["h0"], workspace=ws)
+    ws.fill_(float("nan"))
+    g = ss.gdr_bwd(*[p[n] for n in names], ref[0], p["h0"], ref[1], workspace=ws)
+    assert torch.equal(o, ref[0]) and torch.equal(h, ref[1]) and all(torch.equal(g[n], gref[n]) for n in g)
+    with pytest.raises(ValueError, match="workspace"):
+        ss.gdr_bwd(*[p[n] for n in names], ref[0], workspace=torch.empty(16, device="cuda"))
+
+
+def test_outputs_stay_inside(ss):
+    """Nothing but the outputs is written: guards before and behind them keep their values."""
+    p = problem(1, 70, 1, 2, 24, 36, F)
+    n = 70 * 2 * 36
+    buf = torch.full((n + 64,), 5.0, device="cuda")
+    o = buf[32:32 + n].view(1, 70, 2, 36)
+    hb = torch.full((2 * 24 * 36 + 64,), 5.0, device="cuda")
+    h = hb[32:32 + 2 * 24 * 36].view(1, 2, 24, 36)
+    ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"], o=o, h_final=h)
+    close("o", o, want(p)[0], F32_REL)
+    assert bool((buf[:32] == 5).all()) and bool((buf[32 + n:] == 5).all()) and bool((hb[:32] == 5).all()) and bool((hb[-32:] == 5).all())
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(q=torch.zeros(2, 10, 2, 16)), ValueError), (dict(q=torch.zeros(2, 10, 2, 16, dtype=torch.float64)), TypeError),
+    (dict(k="short"), ValueError), (dict(v="heads"), ValueError), (dict(g="f64"), TypeError), (dict(beta=None), ValueError),
+    (dict(v="turned"), ValueError), (dict(h0="half"), TypeError), (dict(beta="strided"), ValueError),
+])
+def test_refusals(ss, change, error):
+    p = problem(2, 10, 2, 4, 16, 16, F)
+    made = {"short": p["k"][:, :9], "heads": p["v"][:, :, :3], "f64": p["g"].double(), "turned": p["v"].transpose(2, 3).contiguous().transpose(2, 3),
+            "half": p["h0"].half(), "strided": torch.zeros(2, 10, 8, device="cuda")[..., ::2]}
+    for n, x in change.items():
+        p[n] = made[x] if isinstance(x, str) else x
+    with pytest.raises(error):
+        ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
