@@ -183,6 +183,31 @@ __device__ __forceinline__ Raw8<IO> buf_load8(__amdgpu_buffer_rsrc_t r, uint32_t
   return o;
 }
 
+// Values at .. at + 3 of a row, as buf_load8.
+template <typename IO, bool WHOLE>
+__device__ __forceinline__ void buf_load4(__amdgpu_buffer_rsrc_t r, uint32_t voff, int at, int n, float (&x)[4]) {
+  constexpr int kSize = sizeof(typename IO::T);
+  if constexpr (WHOLE) {
+    const uint32_t off = at < n ? voff + at * kSize : kNowhere;
+    if constexpr (kSize == 4) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(v[j]);
+    } else {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = j & 1 ? __uint_as_float(v[j >> 1] & 0xffff0000u) : __uint_as_float(v[j >> 1] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t off = at + j < n ? voff + (at + j) * kSize : kNowhere;
+      if constexpr (kSize == 4) x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+      else x[j] = bf16_bits_to_float((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+    }
+  }
+}
+
 // The value again, in a scalar register that nothing formed from it leaves the loop around: products with it are formed where they
 // are used instead of being kept.
 __device__ __forceinline__ uint32_t here(uint32_t v) {

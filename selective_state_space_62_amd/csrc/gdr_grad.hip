@@ -23,7 +23,8 @@ using namespace gdr;
 constexpr int kThreads = 512;
 constexpr int kRowBytes = 2 * 4 * kBlock;                  // 64 rows by 64 columns, of a plane
 
-template <typename IO, int KP, bool WHOLE>
+// SHARED: value heads share key heads.
+template <typename IO, int KP, bool WHOLE, bool SHARED>
 __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
   using T = typename IO::T;
   constexpr int NP = planes_of<IO>(), kTiles = KP / 32, kTurned = kTiles * 4 * kBlock;
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t bk = blockIdx.x / a.chunks, chunk = blockIdx.x - bk * a.chunks;
   const int64_t b = bk / a.hk;
-  const int hkey = (int)(bk - b * a.hk), group = a.hv / a.hk;
+  const int hkey = (int)(bk - b * a.hk), group = SHARED ? a.hv / a.hk : 1;
   const int64_t first = chunk * kC, ostride = (int64_t)a.hv * a.dv;
   const int valid = (int)min(a.seqlen - first, (int64_t)kC);
   const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + first * a.qs[1] + hkey * a.qs[2];
@@ -44,23 +45,74 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
   const __amdgpu_buffer_rsrc_t qr = chunk_rows<IO>(q, a.qs[1], valid, a.dk), kr = chunk_rows<IO>(k, a.ks[1], valid, a.dk);
   const uint32_t krow = (uint32_t)a.ks[1] * sizeof(T), qrow = (uint32_t)a.qs[1] * sizeof(T);
 
+  // this wave's rows of keys 32 m .. and tokens 32 ti ..; of the triangles its type and tiles
+  const int m = wave >> 1, ti = wave & 1, type = wave >> 1, tok = 32 * ti + low;
+  const bool active = m < kTiles;
+
+  // What is loaded ahead: this thread's 8 columns of a row of dO, v, U and dR, its wave's rows of S and dS; of 64 columns.
+  const uint32_t ld = (uint32_t)a.ldv;
+  Raw8<IO> ro, rw;
+  Raw8<F32> ru, rd;
+  float4 rS[4][2], rE[4][2];
+  int64_t at, gate;
+  __amdgpu_buffer_rsrc_t orows, vrows, urows, drows, srows, erows;
+  auto open_head = [&](int n) {
+    const int h = hkey * group + n;
+    at = (b * a.hv + h) * a.chunks + chunk;
+    gate = (b * a.seqlen + first) * a.hv + h;
+    orows = chunk_rows<IO>(static_cast<const T*>(a.dout) + (b * a.seqlen + first) * ostride + (int64_t)h * a.dv, ostride, valid, a.dv);
+    vrows = chunk_rows<IO>(static_cast<const T*>(a.v) + b * a.vs[0] + first * a.vs[1] + h * a.vs[2], a.vs[1], valid, a.dv);
+    urows = make_rsrc(a.u + at * kC * a.ldv, kC * a.ldv * 4);
+    drows = make_rsrc(a.dr + at * kC * a.ldv, kC * a.ldv * 4);
+    srows = make_rsrc(a.states + at * KP * a.ldv, KP * a.ldv * 4);
+    erows = make_rsrc(a.dstates + at * KP * a.ldv, KP * a.ldv * 4);
+  };
+  auto load_rows = [&](int v0) {
+    const int row = anew(tid) >> 3, col = v0 + 8 * (anew(tid) & 7);
+    ro = buf_load8<IO, WHOLE>(orows, row * (uint32_t)ostride * sizeof(T), 0, col, a.dv);
+    rw = buf_load8<IO, WHOLE>(vrows, row * (uint32_t)a.vs[1] * sizeof(T), 0, col, a.dv);
+    ru = buf_load8<F32, true>(urows, row * ld * 4, 0, col, (int)ld);
+    rd = buf_load8<F32, true>(drows, row * ld * 4, 0, col, (int)ld);
+  };
+  auto load_states = [&](int v0) {
+    const uint32_t off = ((32 * m + (anew(lane) & 31)) * ld + v0 + 4 * (anew(lane) >> 5)) * 4;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t o = active && v0 + 16 * s < (int)ld ? off + 64 * s + 32 * e : kNowhere;
+        const auto x = __builtin_amdgcn_raw_buffer_load_b128(srows, o, 0, 0);
+        const auto y = __builtin_amdgcn_raw_buffer_load_b128(erows, o, 0, 0);
+        rS[s][e] = make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3]));
+        rE[s][e] = make_float4(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]), __uint_as_float(y[3]));
+      }
+  };
+
   // k and q, transposed, each with one scale: threads 0-255 k, the others q
   int ek, eq;
   {
     const int t = tid & 255, g = t & 15, c = t >> 4;
-    float x[4][8], m = 0.0f;
+    Raw8<IO> r[4];
+    if (wave < 4) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const Raw8<IO> r = tid < 256 ? buf_load8<IO, WHOLE>(kr, (4 * g + n) * krow, 0, 8 * c, a.dk)
-                                   : buf_load8<IO, WHOLE>(qr, (4 * g + n) * qrow, 0, 8 * c, a.dk);
+      for (int n = 0; n < 4; ++n) r[n] = buf_load8<IO, WHOLE>(kr, (4 * g + n) * krow, 0, 8 * c, a.dk);
+    } else {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) r[n] = buf_load8<IO, WHOLE>(qr, (4 * g + n) * qrow, 0, 8 * c, a.dk);
+    }
+    open_head(0);
+    load_rows(0);
+    load_states(0);
+    float x[4][8], mx = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[n][j] = raw_value<IO>(r, j);
-        m = fmaxf(m, fabsf(x[n][j]));
+        x[n][j] = raw_value<IO>(r[n], j);
+        mx = fmaxf(mx, fabsf(x[n][j]));
       }
-    }
-    m = wave_max(m);
-    if (lane == 0) s_mx[wave] = m;
+    mx = wave_max(mx);
+    if (lane == 0) s_mx[wave] = mx;
     __syncthreads();
     const Scale sk = scale_of(fmaxf(fmaxf(s_mx[0], s_mx[1]), fmaxf(s_mx[2], s_mx[3])), 100);
     const Scale sq = scale_of(fmaxf(fmaxf(s_mx[4], s_mx[5]), fmaxf(s_mx[6], s_mx[7])), 100);
@@ -71,58 +123,47 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
     if (c < KP / 8) store_operand_turned<IO>(to, to + (NP - 1) * kTurned, g, c, x, s);
   }
 
-  // this wave's rows of keys 32 m .. and tokens 32 ti ..; of the triangles its type and tiles
-  const int m = wave >> 1, ti = wave & 1, type = wave >> 1, tok = 32 * ti + low;
-  const bool active = m < kTiles;
   acc16 dQ = zero16(), dK = zero16();
-
   for (int n = 0; n < group; ++n) {
-    const int h = hkey * group + n;
-    const int64_t at = (b * a.hv + h) * a.chunks + chunk, gate = (b * a.seqlen + first) * a.hv + h;
-    __syncthreads();
+    if (n > 0) {
+      __syncthreads();
+      open_head(n);
+      load_rows(0);
+      load_states(0);
+    }
+    float most[kMaxKinds] = {};
+    for (int64_t e = lane; e < a.ldv / 32; e += 64)
+#pragma unroll
+      for (int i = 0; i < kMaxKinds; ++i) most[i] = fmaxf(most[i], a.maxima[i * a.max_apart + at * (a.ldv / 32) + e]);
     for (int e = tid; e < kVecs * kC; e += kThreads) (&s_vec[0][0])[e] = a.vecs[at * (kVecs * kC) + e];
     if (tid < kC) s_beta[tid] = tid < valid ? a.beta[gate + (int64_t)tid * a.hv] : 0.0f;
-    auto largest = [&](int kind) {
-      float v = 0.0f;
-      for (int64_t e = lane; e < a.ldv / 32; e += 64) v = fmaxf(v, a.maxima[kind * a.max_apart + at * (a.ldv / 32) + e]);
-      return scale_of(wave_max(v), 100);
-    };
-    const Scale cS = largest(kMaxS), cU = largest(kMaxU), cE = largest(kMaxDs), cD = largest(kMaxDr), cO = largest(kMaxDo);
-    const T* dout = static_cast<const T*>(a.dout) + (b * a.seqlen + first) * ostride + (int64_t)h * a.dv;
-    const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + first * a.vs[1] + h * a.vs[2];
-    const __amdgpu_buffer_rsrc_t orows = chunk_rows<IO>(dout, ostride, valid, a.dv), vrows = chunk_rows<IO>(v, a.vs[1], valid, a.dv);
+    const Scale cS = scale_of(wave_max(most[kMaxS]), 100), cU = scale_of(wave_max(most[kMaxU]), 100);
+    const Scale cE = scale_of(wave_max(most[kMaxDs]), 100), cD = scale_of(wave_max(most[kMaxDr]), 100);
+    const Scale cO = scale_of(wave_max(most[kMaxDo]), 100);
     char* const s_o = s_r;
     char* const s_u = s_r + NP * kRowBytes;
     char* const s_d = s_u + 2 * kRowBytes;
 
     acc16 Q = zero16(), X = zero16(), Y = zero16(), C[2] = {zero16(), zero16()};
     float sd = 0.0f, rv = 0.0f;
-    for (int64_t v0 = 0; v0 < a.ldv; v0 += 64) {
-      const int row = tid >> 3, run = tid & 7;
-      const int64_t col = v0 + 8 * run;
+    for (int v0 = 0; v0 < (int)ld; v0 += 64) {
       {
-        const Raw8<IO> ro = buf_load8<IO, WHOLE>(orows, row * (uint32_t)ostride * sizeof(T), 0, (int)col, a.dv);
-        const Raw8<IO> rw = buf_load8<IO, WHOLE>(vrows, row * (uint32_t)a.vs[1] * sizeof(T), 0, (int)col, a.dv);
-        float o[8], u[8] = {}, d[8] = {};
-        if (col < a.ldv) {
-          const float* up = a.u + (at * kC + row) * a.ldv + col;
-          const float* dp = a.dr + (at * kC + row) * a.ldv + col;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] = up[j];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = dp[j];
-        }
+        const int row = tid >> 3, run = tid & 7;
+        float o[8], u[8], d[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           o[j] = raw_value<IO>(ro, j);
+          u[j] = raw_value<F32>(ru, j);
+          d[j] = raw_value<F32>(rd, j);
           rv = fmaf(d[j], raw_value<IO>(rw, j), rv);
         }
-        __syncthreads();                                   // the columns before have been read
+        if (v0 > 0) __syncthreads();                       // the columns before have been read
         store_operand_rows<IO>(s_o, s_o + (NP - 1) * kRowBytes, row, run, 4, o, cO.f);
         store_operand_rows<F32>(s_u, s_u + kRowBytes, row, run, 4, u, cU.f);
         store_operand_rows<F32>(s_d, s_d + kRowBytes, row, run, 4, d, cD.f);
       }
       __syncthreads();
+      if (v0 + 64 < (int)ld) load_rows(v0 + 64);
       // triangles: types 0, 1 of N with a lane a row i, a column j; 2, 3 of M
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -141,15 +182,10 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
         }
       }
       if (active) {
-        const float* sp = a.states + (at * KP + 32 * m + low) * a.ldv + v0 + 4 * half;
-        const float* dp = a.dstates + (at * KP + 32 * m + low) * a.ldv + v0 + 4 * half;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          if (v0 + 16 * s >= a.ldv) break;
-          const float4 s0 = *reinterpret_cast<const float4*>(sp + 16 * s), s1 = *reinterpret_cast<const float4*>(sp + 16 * s + 8);
-          const float4 d0 = *reinterpret_cast<const float4*>(dp + 16 * s), d1 = *reinterpret_cast<const float4*>(dp + 16 * s + 8);
-          const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-          const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+          const float sv[8] = {rS[s][0].x, rS[s][0].y, rS[s][0].z, rS[s][0].w, rS[s][1].x, rS[s][1].y, rS[s][1].z, rS[s][1].w};
+          const float dv[8] = {rE[s][0].x, rE[s][0].y, rE[s][0].z, rE[s][0].w, rE[s][1].x, rE[s][1].y, rE[s][1].z, rE[s][1].w};
           Planes S, E;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -162,8 +198,10 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
           Q = mm<2, NP>(S, operand<NP>(s_o + (ti * 4 + s) * kBlock, lane, kRowBytes), Q);
           X = mm<2, 2>(S, operand<2>(s_d + (ti * 4 + s) * kBlock, lane, kRowBytes), X);
           Y = mm<2, 2>(E, operand<2>(s_u + (ti * 4 + s) * kBlock, lane, kRowBytes), Y);
+          step_end();
         }
       }
+      if (v0 + 64 < (int)ld) load_states(v0 + 64);
     }
 
     // the triangles' values; their sums over rows of dR.v; <dS, S>
@@ -237,30 +275,28 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
       const float fe = s_vec[kVecEnd][tok] * s_vec[kVecS][tok] * pow2(-cE.e) * pow2(-cU.e);
       const float fx = exp2_of(s_vec[kVecWhole][tok], s_vec[kVecRest][tok]) * pow2(-cS.e) * pow2(-cD.e);
       float qdq = 0.0f;
+      acc16 qv;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int at_k = 32 * m + 8 * g + 4 * half;
+        float x[4];
+        buf_load4<IO, WHOLE>(kr, tok * krow, at_k, a.dk, x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * g + j;
-          const uint32_t ko = at_k + j < a.dk ? tok * krow + (at_k + j) * (int)sizeof(T) : kNowhere;
-          const uint32_t qo = at_k + j < a.dk ? tok * qrow + (at_k + j) * (int)sizeof(T) : kNowhere;
-          float qv;
-          if constexpr (NP == 2) {
-            kv[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(kr, ko, 0, 0));
-            qv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(qr, qo, 0, 0));
-          } else {
-            kv[r] = bf16_bits_to_float((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(kr, ko, 0, 0));
-            qv = bf16_bits_to_float((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(qr, qo, 0, 0));
-          }
-          const float dq = fmaf(Q[r], f, nk[r] * fn);
-          qdq = fmaf(qv, dq, qdq);
-          dQ[r] += dq;
-          const float e = Y[r] * fe;
-          kend = fmaf(kv[r], e, kend);
-          Y[r] = fmaf(nq[r], fy, e);
-          X[r] *= fx;
-        }
+        for (int j = 0; j < 4; ++j) kv[4 * g + j] = x[j];
+        buf_load4<IO, WHOLE>(qr, tok * qrow, at_k, a.dk, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qv[4 * g + j] = x[j];
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float dq = fmaf(Q[r], f, nk[r] * fn);
+        qdq = fmaf(qv[r], dq, qdq);
+        if constexpr (SHARED) dQ[r] += dq;
+        else dQ[r] = dq;
+        const float e = Y[r] * fe;
+        kend = fmaf(kv[r], e, kend);
+        Y[r] = fmaf(nq[r], fy, e);
+        X[r] *= fx;
       }
       qdq += __shfl_xor(qdq, 32);
       kend += __shfl_xor(kend, 32);
@@ -281,7 +317,8 @@ __global__ __launch_bounds__(kThreads, 2) void gdr_grad_kernel(GdrArgs a) {
         const float x = fmaf(mk[r], fm, X[r]), y = fmaf(-mb[r], fb, Y[r]);
         kx = fmaf(kv[r], x, kx);
         ky = fmaf(kv[r], y, ky);
-        dK[r] += fmaf(-beta, x, y);
+        if constexpr (SHARED) dK[r] += fmaf(-beta, x, y);
+        else dK[r] = fmaf(-beta, x, y);
       }
       kx += __shfl_xor(kx, 32);
       ky += __shfl_xor(ky, 32);
@@ -324,7 +361,8 @@ template <typename IO>
 hipError_t launch(const GdrArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.hk * a.chunks));
   return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
-    gdr_grad_kernel<IO, decltype(kp)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>(a);
+    if (a.hv > a.hk) gdr_grad_kernel<IO, decltype(kp)::value, decltype(whole)::value, true><<<grid, kThreads, 0, s>>>(a);
+    else gdr_grad_kernel<IO, decltype(kp)::value, decltype(whole)::value, false><<<grid, kThreads, 0, s>>>(a);
   });
 }
 
