@@ -137,13 +137,13 @@ FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v) {
 }
 
 // Scratch of the backward: the preparation's, then for every chunk of a head the state before it and the gradient of the one
-// behind it, U and the gradient of R, and the largest values of their tiles.
+// behind it, U and the gradient of R, the largest values of their tiles, and dq and dk of value heads that share keys.
 struct BwdLayout {
-  size_t tri_t, p, vecs, states, dstates, u, dr, maxima, total;
+  size_t tri_t, p, vecs, states, dstates, u, dr, maxima, part_q, part_k, total;
   int64_t ldv, max_apart;
 };
 
-BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_v, int dim_k, int dim_v) {
+BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
   const int64_t n = batch * heads_v * chunks_of(seqlen), rows = (dim_k + 31) / 32 * 32;
   BwdLayout l;
   l.ldv = (int64_t)(dim_v + 31) / 32 * 32;
@@ -156,7 +156,9 @@ BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_v, int dim_k, int 
   l.u = l.dstates + round256((size_t)(n * rows * l.ldv) * 4);
   l.dr = l.u + round256((size_t)(n * kGdrChunk * l.ldv) * 4);
   l.maxima = l.dr + round256((size_t)(n * kGdrChunk * l.ldv) * 4);
-  l.total = l.maxima + round256((size_t)(kMaxKinds * l.max_apart) * 4);
+  l.part_q = l.maxima + round256((size_t)(kMaxKinds * l.max_apart) * 4);
+  l.part_k = l.part_q + (heads_v > heads_k ? round256((size_t)(n * kGdrChunk * rows) * 4) : 0);
+  l.total = l.part_k + (l.part_k - l.part_q);
   return l;
 }
 
@@ -215,7 +217,7 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
 
 size_t ss_gdr_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
   if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen == 0) return 0;
-  return bwd_layout(batch, seqlen, heads_v, dim_k, dim_v).total;
+  return bwd_layout(batch, seqlen, heads_k, heads_v, dim_k, dim_v).total;
 }
 
 ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
@@ -254,7 +256,7 @@ ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
   }
   if ((st = check_blocks(batch * heads_v * chunks_of(seqlen))) != SS_OK) return st;
-  const BwdLayout l = bwd_layout(batch, seqlen, heads_v, dim_k, dim_v);
+  const BwdLayout l = bwd_layout(batch, seqlen, heads_k, heads_v, dim_k, dim_v);
   char* ws = static_cast<char*>(workspace);
   GdrArgs a = make_args(in);
   a.chunks = chunks_of(seqlen);
@@ -270,6 +272,8 @@ ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   a.dr = reinterpret_cast<float*>(ws + l.dr);
   a.maxima = reinterpret_cast<float*>(ws + l.maxima);
   a.max_apart = l.max_apart;
+  a.part_q = reinterpret_cast<float*>(ws + l.part_q);
+  a.part_k = reinterpret_cast<float*>(ws + l.part_k);
   a.dout = dout;
   a.dh_final = dh_final;
   a.dq = dq;

@@ -42,6 +42,8 @@ struct GdrArgs {
   float* dr;             // the gradient of R
   float* maxima;
   int64_t max_apart;
+  float* part_q;         // where value heads share keys: dq and dk of each alone, rows of dk rounded up to tiles of 32
+  float* part_k;
   const void* dout;      // gradient of o
   const float* dh_final; // nullable
   void* dq;              // (batch, seqlen, hk, dk)
