@@ -33,7 +33,7 @@ struct GdrArgs {
   void* tri_t;           // backward: of T transposed
   void* p;               // operand blocks of P; backward: of P transposed
   float* vecs;           // kVecs vectors
-  // backward, for every chunk of a head: rows of ldv columns (dv rounded up to tiles of 32), and of each tile the largest
+  // backward, for every chunk of a head: rows of ldv columns (dv rounded up to tiles of 32) as operands, and of each tile the largest
   // |value| (of every kind in a run of its own, max_apart floats behind the one before)
   int64_t ldv;
   float* states;         // the state before it

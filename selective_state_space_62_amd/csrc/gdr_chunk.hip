@@ -6,8 +6,8 @@
 // S stay in registers from one product to the next.  The chunks of a head follow one another, so what counts is how long one
 // takes: the next chunk's tiles are on their way while this one is computed, those that need no conversion straight
 // to LDS, and nothing waits for a value that a workgroup could not form beforehand.
-// For the backward the same kernel makes S before every chunk and U (transposed by a product with the identity, so that
-// rows are stored 16 bytes a lane) instead of O.
+// For the backward the same kernel makes S before every chunk and U (transposed by a product with the identity, as
+// operands of the gradients) instead of O.
 #include "gdr_device.h"
 
 namespace ssscan {
@@ -156,13 +156,13 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     }
     if constexpr (STATES) {
       // the state before the chunk, its rows behind dk and columns behind dv zeros
-      float* out = a.states + ((bh * a.chunks + chunk) * KP + low) * a.ldv + col0 + 4 * half;
+      float* out = a.states + (bh * a.chunks + chunk) * KP * a.ldv;
       const float f = pow2(ce - es);
       if (col0 < a.ldv) {
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
           const acc16 t = transposed(sp[2 * m], sp[2 * m + 1], lane);
-          store_runs<F32>(out + 32 * m * a.ldv, 0, 32, t, f);
+          store_blocks(out, m, col0, a.ldv, lane, t, f);
           step_end();
         }
         if (lane == 0) a.maxima[kMaxS * a.max_apart + (bh * a.chunks + chunk) * (a.ldv / 32) + col0 / 32] = mS * pow2(ce);
@@ -193,12 +193,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     const float mU = wave_max(max_of(U[1], max_of(U[0], 0.0f)));
     if constexpr (STATES) {
       const Scale cu = scale_of(mU, 20);
-      float* out = a.u + ((bh * a.chunks + chunk) * kC + low) * a.ldv + col0 + 4 * half;
+      float* out = a.u + (bh * a.chunks + chunk) * kC * a.ldv;
       if (col0 < a.ldv) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const acc16 t = transposed(split(U[i], 0, cu.f), split(U[i], 1, cu.f), lane);
-          store_runs<F32>(out + 32 * i * a.ldv, 0, 32, t, pow2(-(er + cu.e)));
+          store_blocks(out, i, col0, a.ldv, lane, t, pow2(-(er + cu.e)));
         }
         if (lane == 0) a.maxima[kMaxU * a.max_apart + (bh * a.chunks + chunk) * (a.ldv / 32) + col0 / 32] = mU * pow2(-er);
       }

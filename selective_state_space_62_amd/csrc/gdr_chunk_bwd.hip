@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     const float back = pow2(ce - cs.e);
     X[0] = X[1] = zero16();
     {
-      float* out = a.dstates + (at * KP + low) * a.ldv + col0 + 4 * half;
+      float* out = a.dstates + at * KP * a.ldv;
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) {
         Planes sp[2];
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
             X[i] = mm<NP, 2>(operand<NP>(s_k + (i * kSteps + 2 * m + s) * kBlock, lane, kSide), sp[s], X[i]);
         }
         const acc16 t = transposed(sp[0], sp[1], lane);
-        if (stores) store_runs<F32>(out + 32 * m * a.ldv, 0, 32, t, back);
+        if (stores) store_blocks(out, m, col0, a.ldv, lane, t, back);
         step_end();
       }
       if (stores && lane == 0) maxima[kMaxDs * a.max_apart] = mS * pow2(ce);
@@ -201,13 +201,13 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
       const float m = wave_max(max_of(y[1], max_of(y[0], 0.0f)));
       const Scale c = scale_of(m, 100);
       if (stores) {
-        float* out = a.dr + (at * kC + low) * a.ldv + col0 + 4 * half;
+        float* out = a.dr + at * kC * a.ldv;
         const float f = pow2(-c.e);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int tok = 32 * i + low;
           const acc16 t = transposed(split(y[i], 0, c.f), split(y[i], 1, c.f), lane);
-          store_runs<F32>(out + 32 * i * a.ldv, 0, 32, t, f);
+          store_blocks(out, i, col0, a.ldv, lane, t, f);
           if (tok < valid)
             store_runs<IO>(static_cast<T*>(a.dv_out) + ((b * a.seqlen + first + tok) * a.hv + h) * a.dv, col0 + 4 * half, a.dv, t,
                            s_vec[kVecF1][tok] / s_vec[kVecC][tok] * f);

@@ -183,29 +183,44 @@ __device__ __forceinline__ Raw8<IO> buf_load8(__amdgpu_buffer_rsrc_t r, uint32_t
   return o;
 }
 
+// Four consecutive values as they stand in memory.
+template <typename IO>
+struct Raw4 {
+  uint32_t w[sizeof(typename IO::T)];
+
+  __device__ __forceinline__ float value(int j) const {
+    if constexpr (IO::kPerSpan == 4) return __uint_as_float(w[j]);
+    else return (j & 1) ? __uint_as_float(w[j >> 1] & 0xffff0000u) : __uint_as_float(w[j >> 1] << 16);
+  }
+};
+
 // Values at .. at + 3 of a row, as buf_load8.
 template <typename IO, bool WHOLE>
-__device__ __forceinline__ void buf_load4(__amdgpu_buffer_rsrc_t r, uint32_t voff, int at, int n, float (&x)[4]) {
+__device__ __forceinline__ Raw4<IO> buf_load4(__amdgpu_buffer_rsrc_t r, uint32_t voff, int at, int n) {
   constexpr int kSize = sizeof(typename IO::T);
+  Raw4<IO> o;
   if constexpr (WHOLE) {
     const uint32_t off = at < n ? voff + at * kSize : kNowhere;
     if constexpr (kSize == 4) {
       const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(v[j]);
+      o.w[0] = v[0]; o.w[1] = v[1]; o.w[2] = v[2]; o.w[3] = v[3];
     } else {
       const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = j & 1 ? __uint_as_float(v[j >> 1] & 0xffff0000u) : __uint_as_float(v[j >> 1] << 16);
+      o.w[0] = v[0]; o.w[1] = v[1];
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t off = at + j < n ? voff + (at + j) * kSize : kNowhere;
-      if constexpr (kSize == 4) x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-      else x[j] = bf16_bits_to_float((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+      if constexpr (kSize == 4) {
+        o.w[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+      } else {
+        const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+        o.w[j >> 1] = j & 1 ? o.w[j >> 1] | v << 16 : v;
+      }
     }
   }
+  return o;
 }
 
 // The value again, in a scalar register that nothing formed from it leaves the loop around: products with it are formed where they
@@ -302,6 +317,18 @@ __device__ __forceinline__ acc16 transposed(const Planes& p0, const Planes& p1, 
     acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p1.lo, e1, acc, 0, 0, 0);
   }
   return acc;
+}
+
+// Rows of ldv columns in fp32 stand in memory as operands too: for 32 rows by 16 columns 2 x 64 x 16 bytes, of which a lane has its
+// first four values in the first half, its others in the second, so that every access is of whole lines.  The values of such a
+// lane after transposed are those of steps col0 / 16 and the next.
+__device__ __forceinline__ int64_t block_of(int tile, int step, int64_t ldv) { return ((int64_t)tile * (ldv / 16) + step) * 512; }
+
+__device__ __forceinline__ void store_blocks(float* rows, int tile, int col0, int64_t ldv, int lane, const acc16& v, float f) {
+  float* p = rows + block_of(tile, col0 / 16, ldv) + lane * 4;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<float4*>(p + 256 * g) = make_float4(v[4 * g] * f, v[4 * g + 1] * f, v[4 * g + 2] * f, v[4 * g + 3] * f);
 }
 
 // Runs of four of such a lane's columns at `at`, times f, to a row of n in the I/O type.

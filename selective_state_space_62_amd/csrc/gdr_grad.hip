@@ -29,11 +29,12 @@ template <typename IO, int KP, bool WHOLE>
 __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_kernel(GdrArgs a) {
   using T = typename IO::T;
   constexpr int NP = planes_of<IO>(), kTiles = KP / 32, kTurned = kTiles * 4 * kBlock;
+  constexpr bool kAhead = NP == 2;                         // one workgroup on a CU, with registers to spare
   constexpr int kRegion = (NP + 4) * kRowBytes;            // dO, U, dR; then two triangles at a time, and sums over values of keys
   static_assert(kRegion >= 4 * kTriBytes + 4 * kTiles * kC * 4, "");
   __shared__ alignas(16) char s_kt[NP * kTurned], s_qt[NP * kTurned], s_r[kRegion];
   __shared__ alignas(16) float s_vec[kVecs][kC], s_beta[kC];
-  __shared__ float s_mx[8], s_sd[8], s_rv[kC];
+  __shared__ float s_mx[8], s_sd[8], s_rv[4][kC];
   float(&s_dot)[4][kTiles][kC] = *reinterpret_cast<float(*)[4][kTiles][kC]>(s_r + 4 * kTriBytes);
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, low = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -97,27 +98,52 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     const __amdgpu_buffer_rsrc_t urows = make_rsrc(a.u + at * kC * a.ldv, kC * a.ldv * 4), drows = make_rsrc(a.dr + at * kC * a.ldv, kC * a.ldv * 4);
     const __amdgpu_buffer_rsrc_t srows = make_rsrc(a.states + at * KP * a.ldv, KP * a.ldv * 4);
     const __amdgpu_buffer_rsrc_t erows = make_rsrc(a.dstates + at * KP * a.ldv, KP * a.ldv * 4);
+    // rows of 64 columns: of dO a thread has 8 columns of one, of U and dR (with v) the operand that its lane is of its wave's block
+    const int utile = wave >> 2, ustep = wave & 3;
+    Raw8<IO> ro;
+    Raw4<IO> rw[2];
+    Raw8<F32> ru, rd;
+    auto load_rows = [&](int v0) {
+      const int ln = anew(lane), c = v0 + 16 * ustep, w = (utile * (ld / 16) + c / 16) * 512 + ln * 4;
+      ro = buf_load8<IO, WHOLE>(orows, (8 * wave + (ln >> 3)) * (uint32_t)ostride * sizeof(T), 0, v0 + 8 * (ln & 7), a.dv);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rw[e] = buf_load4<IO, WHOLE>(vrows, (32 * utile + (ln & 31)) * (uint32_t)a.vs[1] * sizeof(T), c + 8 * e + 4 * (ln >> 5), a.dv);
+        const auto x = __builtin_amdgcn_raw_buffer_load_b128(urows, c < ld ? w * 4 + 1024 * e : kNowhere, 0, 0);
+        const auto y = __builtin_amdgcn_raw_buffer_load_b128(drows, c < ld ? w * 4 + 1024 * e : kNowhere, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ru.w[4 * e + j] = x[j];
+          rd.w[4 * e + j] = y[j];
+        }
+      }
+    };
+    if constexpr (kAhead) load_rows(0);
     for (int v0 = 0; v0 < ld; v0 += 64) {
+      if constexpr (!kAhead) load_rows(v0);
       {
-        const int row = tid >> 3, run = tid & 7, col = v0 + 8 * run;
-        const Raw8<IO> ro = buf_load8<IO, WHOLE>(orows, row * (uint32_t)ostride * sizeof(T), 0, col, a.dv);
-        const Raw8<IO> rw = buf_load8<IO, WHOLE>(vrows, row * (uint32_t)a.vs[1] * sizeof(T), 0, col, a.dv);
-        const Raw8<F32> ru = buf_load8<F32, true>(urows, row * ld * 4, 0, col, ld);
-        const Raw8<F32> rd = buf_load8<F32, true>(drows, row * ld * 4, 0, col, ld);
-        float o[8], u[8], d[8];
+        float o[8];
+        Planes u, d;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           o[j] = raw_value<IO>(ro, j);
-          u[j] = raw_value<F32>(ru, j);
-          d[j] = raw_value<F32>(rd, j);
-          rv = fmaf(d[j], raw_value<IO>(rw, j), rv);
+          const float x = raw_value<F32>(ru, j), y = raw_value<F32>(rd, j);
+          u.hi[j] = (_Float16)(x * cU.f);
+          u.lo[j] = (_Float16)fmaf(x, cU.f, -(float)u.hi[j]);
+          d.hi[j] = (_Float16)(y * cD.f);
+          d.lo[j] = (_Float16)fmaf(y, cD.f, -(float)d.hi[j]);
+          rv = fmaf(y, rw[j >> 2].value(j & 3), rv);
         }
         __syncthreads();                                   // the columns before have been read
-        store_operand_rows<IO>(s_o, s_o + (NP - 1) * kRowBytes, row, run, 4, o, cO.f);
-        store_operand_rows<F32>(s_u, s_u + kRowBytes, row, run, 4, u, cU.f);
-        store_operand_rows<F32>(s_d, s_d + kRowBytes, row, run, 4, d, cD.f);
+        store_operand_rows<IO>(s_o, s_o + (NP - 1) * kRowBytes, tid >> 3, tid & 7, 4, o, cO.f);
+        *reinterpret_cast<h8*>(s_u + wave * kBlock + lane * 16) = u.hi;
+        *reinterpret_cast<h8*>(s_u + kRowBytes + wave * kBlock + lane * 16) = u.lo;
+        *reinterpret_cast<h8*>(s_d + wave * kBlock + lane * 16) = d.hi;
+        *reinterpret_cast<h8*>(s_d + kRowBytes + wave * kBlock + lane * 16) = d.lo;
       }
       __syncthreads();
+      if constexpr (kAhead)
+        if (v0 + 64 < ld) load_rows(v0 + 64);
       if (tile < 3) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -127,12 +153,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
         }
       }
       if (active) {
-        const uint32_t off = ((32 * m + low) * ld + v0 + 4 * half) * 4;
+        const uint32_t off = ((m * (ld / 16) + v0 / 16) * 512 + lane * 4) * 4;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const uint32_t o = v0 + 16 * s < ld ? off + 64 * s : kNowhere;
-          const auto s0 = __builtin_amdgcn_raw_buffer_load_b128(srows, o, 0, 0), s1 = __builtin_amdgcn_raw_buffer_load_b128(srows, o + 32, 0, 0);
-          const auto d0 = __builtin_amdgcn_raw_buffer_load_b128(erows, o, 0, 0), d1 = __builtin_amdgcn_raw_buffer_load_b128(erows, o + 32, 0, 0);
+          const uint32_t o = v0 + 16 * s < ld ? off + 2048 * s : kNowhere;
+          const auto s0 = __builtin_amdgcn_raw_buffer_load_b128(srows, o, 0, 0), s1 = __builtin_amdgcn_raw_buffer_load_b128(srows, o + 1024, 0, 0);
+          const auto d0 = __builtin_amdgcn_raw_buffer_load_b128(erows, o, 0, 0), d1 = __builtin_amdgcn_raw_buffer_load_b128(erows, o + 1024, 0, 0);
           Planes S, E;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -164,13 +190,13 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     }
   }
   const float mC = wave_max(max_of(C, 0.0f));
-  rv = group_sum(rv, 8);
+  rv += __shfl_xor(rv, 32);
   sd = group_sum(sd, 64);
   if (lane == 0) {
     s_mx[wave] = tile < 3 ? mC : 0.0f;
     s_sd[wave] = active && ti == 0 ? sd : 0.0f;
   }
-  if ((lane & 7) == 0) s_rv[tid >> 3] = rv;
+  if (half == 0) s_rv[wave & 3][32 * (wave >> 2) + low] = rv;
   __syncthreads();
   const Scale t0 = scale_of(fmaxf(s_mx[0], fmaxf(s_mx[1], s_mx[2])), 100), t1 = scale_of(fmaxf(s_mx[4], fmaxf(s_mx[5], s_mx[6])), 100);
   // the other orientation: a lane a column j, rows times what is not yet theirs: 2^p_i of N, beta_i of M, at most 2^rise
@@ -214,6 +240,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   };
   if (of_n && tile < 3) write_triangles();
   __syncthreads();
+  Raw4<IO> rq[4], rk[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    rq[g] = buf_load4<IO, WHOLE>(qr, tok * qrow, 32 * m + 8 * g + 4 * half, active ? a.dk : 0);
+    rk[g] = buf_load4<IO, WHOLE>(kr, tok * krow, 32 * m + 8 * g + 4 * half, active ? a.dk : 0);
+  }
   if (active) {
     const float into = s_vec[kVecInto][tok];
     const float f = a.scale * into * pow2(-cS.e) * pow2(-cO.e), fn = pow2((int)s_vec[kVecGrow][tok] - ek - t0.e), fy = pow2(rise_n - eq - t0.e);
@@ -222,29 +254,17 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     float qdq = 0.0f, kend = 0.0f;
     const acc16 nk = through(s_kt, true);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float x[4];
-      buf_load4<IO, WHOLE>(qr, tok * qrow, 32 * m + 8 * g + 4 * half, a.dk, x);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * g + j;
-        Q[r] = fmaf(Q[r], f, nk[r] * fn);
-        qdq = fmaf(x[j], Q[r], qdq);
-      }
+    for (int r = 0; r < 16; ++r) {
+      Q[r] = fmaf(Q[r], f, nk[r] * fn);
+      qdq = fmaf(rq[r >> 2].value(r & 3), Q[r], qdq);
     }
     const acc16 nq = through(s_qt, false);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float x[4];
-      buf_load4<IO, WHOLE>(kr, tok * krow, 32 * m + 8 * g + 4 * half, a.dk, x);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * g + j;
-        const float e = Y[r] * fe;
-        kend = fmaf(x[j], e, kend);
-        Y[r] = fmaf(nq[r], fy, e);
-        X[r] *= fx;
-      }
+    for (int r = 0; r < 16; ++r) {
+      const float e = Y[r] * fe;
+      kend = fmaf(rk[r >> 2].value(r & 3), e, kend);
+      Y[r] = fmaf(nq[r], fy, e);
+      X[r] *= fx;
     }
     qdq += __shfl_xor(qdq, 32);
     kend += __shfl_xor(kend, 32);
@@ -268,17 +288,11 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     const acc16 mk = through(s_kt, true), mb = through(s_kt, false);
     float kx = 0.0f, ky = 0.0f;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float kv[4];
-      buf_load4<IO, WHOLE>(kr, tok * krow, 32 * m + 8 * g + 4 * half, a.dk, kv);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * g + j;
-        const float x = fmaf(mk[r], fm, X[r]), y = fmaf(-mb[r], fb, Y[r]);
-        kx = fmaf(kv[j], x, kx);
-        ky = fmaf(kv[j], y, ky);
-        Y[r] = fmaf(-beta, x, y);
-      }
+    for (int r = 0; r < 16; ++r) {
+      const float kv = rk[r >> 2].value(r & 3), x = fmaf(mk[r], fm, X[r]), y = fmaf(-mb[r], fb, Y[r]);
+      kx = fmaf(kv, x, kx);
+      ky = fmaf(kv, y, ky);
+      Y[r] = fmaf(-beta, x, y);
     }
     kx += __shfl_xor(kx, 32);
     ky += __shfl_xor(ky, 32);
@@ -312,7 +326,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
       if (lane + i < kC) dgam += o;
     }
     if (lane < valid) {
-      if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = s_rv[lane] * pow2(-(int)s_vec[kVecGrow][lane]) - d[1];
+      if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = (s_rv[0][lane] + s_rv[1][lane] + s_rv[2][lane] + s_rv[3][lane]) * pow2(-(int)s_vec[kVecGrow][lane]) - d[1];
       if (a.dg) a.dg[gate + (int64_t)lane * a.hv] = dgam;
     }
   }
