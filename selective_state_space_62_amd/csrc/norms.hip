@@ -115,7 +115,7 @@ template <int NV>
 __device__ __forceinline__ void block_columns(float (&acc)[NV][kVec], const NormPlan& pl, int n, float* __restrict__ out) {
   constexpr int kMost = 64 * NV * kVec;
   __shared__ float s_col[3][kMost];
-  const int tid = threadIdx.x, l = tid & (pl.lanes - 1), wave = tid >> 6;
+  const int tid = threadIdx.x, l = pl.lanes > 64 ? tid : tid & (pl.lanes - 1), wave = tid >> 6;
   if (pl.lanes < 64) {
     for (int m = pl.lanes; m < 64; m <<= 1)
 #pragma unroll
@@ -188,7 +188,7 @@ template <typename IO, int NV, bool GATE, int THREADS>
 __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a) {
   using T = typename IO::T;
   const NormPlan& pl = a.plan;
-  const int tid = threadIdx.x, l = tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
+  const int tid = threadIdx.x, l = pl.lanes > 64 ? tid : tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
   const int64_t rows = a.per_head ? a.tokens : a.tokens * a.heads;
   int slot = 0;
   float w[NV][kVec];
@@ -199,34 +199,39 @@ __global__ __launch_bounds__(THREADS) void gated_norm_kernel(GatedNormArgs a) {
     valid[i] = a.n - at;
     load_weights(a.per_head && a.w ? a.w + (int64_t)blockIdx.y * a.n : a.w, at, valid[i], 1.0f, w[i]);
   }
-  for (int64_t first = (int64_t)blockIdx.x * per; first < rows; first += (int64_t)gridDim.x * per) {
-    const int64_t row = first + tid / pl.lanes;
-    const bool live = row < rows;
-    const RowPlace at = place(a, live ? row : first);
+  const int64_t step = (int64_t)gridDim.x * per;
+  Raw<IO> nx[NV], nz[NV];
+  auto fetch = [&](int64_t row) {
+    const RowPlace at = place(a, row);
     const T* x = static_cast<const T*>(a.x.p) + offset(a.x, at);
-    Raw<IO> rx[NV], rz[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) rx[i] = load_raw<IO>(x + (i * pl.lanes + l) * kVec, live ? valid[i] : 0);
+    for (int i = 0; i < NV; ++i) nx[i] = load_raw<IO>(x + (i * pl.lanes + l) * kVec, valid[i]);
     if constexpr (GATE) {
       const T* z = static_cast<const T*>(a.z.p) + offset(a.z, at);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) rz[i] = load_raw<IO>(z + (i * pl.lanes + l) * kVec, live ? valid[i] : 0);
+      for (int i = 0; i < NV; ++i) nz[i] = load_raw<IO>(z + (i * pl.lanes + l) * kVec, valid[i]);
     }
+  };
+  // every lane stays to the end, as sums pass barriers; rows behind the last are the last again, and not stored
+  int64_t row = (int64_t)blockIdx.x * per + tid / pl.lanes;
+  fetch(min(row, rows - 1));
+  for (int64_t first = (int64_t)blockIdx.x * per; first < rows; first += step, row += step) {
     float v[NV][kVec], sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const float xv = value<IO>(rx[i], j);
-        const float gate = GATE ? silu(value<IO>(rz[i], j)) : 1.0f;
+        const float xv = value<IO>(nx[i], j);
+        const float gate = GATE ? silu(value<IO>(nz[i], j)) : 1.0f;
         const float m = GATE && a.gate_first ? xv * gate : xv;
         sum[0] = fmaf(m, m, sum[0]);
         v[i][j] = xv * gate;
       }
+    if (first + step < rows) fetch(min(row + step, rows - 1));
     row_sums(sum, pl.lanes, slot);
     const float rho = inv_rms(sum[0], a.inv_n, a.eps);
-    if (!live) continue;
-    T* y = static_cast<T*>(a.y) + ((at.b * a.seqlen + at.t) * a.heads + at.h) * a.n;
+    if (row >= rows) continue;
+    T* y = static_cast<T*>(a.y) + (a.per_head ? row * a.heads + blockIdx.y : row) * a.n;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -242,7 +247,7 @@ template <typename IO, int NV, bool GATE, int THREADS>
 __global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a) {
   using T = typename IO::T;
   const NormPlan& pl = a.plan;
-  const int tid = threadIdx.x, l = tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
+  const int tid = threadIdx.x, l = pl.lanes > 64 ? tid : tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
   const int64_t rows = a.per_head ? a.tokens : a.tokens * a.heads;
   int slot = 0;
   float w[NV][kVec], dw[NV][kVec] = {};
@@ -253,23 +258,34 @@ __global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a
     valid[i] = a.n - at;
     load_weights(a.per_head && a.w ? a.w + (int64_t)blockIdx.y * a.n : a.w, at, valid[i], 1.0f, w[i]);
   }
-  for (int64_t first = (int64_t)blockIdx.x * per; first < rows; first += (int64_t)gridDim.x * per) {
-    const int64_t row = first + tid / pl.lanes;
-    const bool live = row < rows;
-    const RowPlace at = place(a, live ? row : first);
+  const int64_t step = (int64_t)gridDim.x * per;
+  Raw<IO> nx[NV], nz[NV], nd[NV];
+  auto fetch = [&](int64_t row) {
+    const RowPlace at = place(a, row);
     const T* x = static_cast<const T*>(a.x.p) + offset(a.x, at);
-    const T* dy = static_cast<const T*>(a.dy) + ((at.b * a.seqlen + at.t) * a.heads + at.h) * a.n;
-    Raw<IO> rx[NV], rz[NV], rd[NV];
+    const T* dy = static_cast<const T*>(a.dy) + (a.per_head ? row * a.heads + blockIdx.y : row) * a.n;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      rx[i] = load_raw<IO>(x + (i * pl.lanes + l) * kVec, live ? valid[i] : 0);
-      rd[i] = load_raw<IO>(dy + (i * pl.lanes + l) * kVec, live ? valid[i] : 0);
+      nx[i] = load_raw<IO>(x + (i * pl.lanes + l) * kVec, valid[i]);
+      nd[i] = load_raw<IO>(dy + (i * pl.lanes + l) * kVec, valid[i]);
     }
     if constexpr (GATE) {
       const T* z = static_cast<const T*>(a.z.p) + offset(a.z, at);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) rz[i] = load_raw<IO>(z + (i * pl.lanes + l) * kVec, live ? valid[i] : 0);
+      for (int i = 0; i < NV; ++i) nz[i] = load_raw<IO>(z + (i * pl.lanes + l) * kVec, valid[i]);
     }
+  };
+  int64_t row = (int64_t)blockIdx.x * per + tid / pl.lanes;
+  fetch(min(row, rows - 1));
+  for (int64_t first = (int64_t)blockIdx.x * per; first < rows; first += step, row += step) {
+    Raw<IO> rx[NV], rz[NV], rd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      rx[i] = nx[i];
+      rd[i] = nd[i];
+      if constexpr (GATE) rz[i] = nz[i];
+    }
+    if (first + step < rows) fetch(min(row + step, rows - 1));
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -285,7 +301,8 @@ __global__ __launch_bounds__(THREADS) void gated_norm_bwd_kernel(GatedNormArgs a
     row_sums(sum, pl.lanes, slot);
     const float rho = inv_rms(sum[0], a.inv_n, a.eps);
     const float c = rho * rho * (sum[1] * a.inv_n);
-    if (!live) continue;
+    if (row >= rows) continue;
+    const RowPlace at = place(a, row);
     T* dx = static_cast<T*>(const_cast<void*>(a.dx.p)) + offset(a.dx, at);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -315,7 +332,7 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
   using T = typename IO::T;
   using R = typename RO::T;
   const NormPlan& pl = a.plan;
-  const int tid = threadIdx.x, l = tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
+  const int tid = threadIdx.x, l = pl.lanes > 64 ? tid : tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
   int slot = 0, slot_post = 0;
   float w[NV][kVec], by[NV][kVec];
   int valid[NV];
@@ -330,17 +347,30 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
 #pragma unroll
     for (int j = 0; j < kVec; ++j) by[i][j] *= a.alpha * wp[j];
   }
-  for (int64_t first = (int64_t)blockIdx.x * per; first < a.rows; first += (int64_t)gridDim.x * per) {
-    const int64_t row = first + tid / pl.lanes;
-    const bool live = row < a.rows;
-    const T* x = static_cast<const T*>(a.x) + (live ? row : first) * a.n;
+  const int64_t step = (int64_t)gridDim.x * per;
+  Raw<IO> nx[NV];
+  Raw<RO> nr[NV];
+  auto fetch = [&](int64_t row) {
+    const T* x = static_cast<const T*>(a.x) + row * a.n;
+    const R* res = static_cast<const R*>(a.res) + row * a.n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      nx[i] = load_raw<IO>(x + (i * pl.lanes + l) * kVec, valid[i]);
+      nr[i] = load_raw<RO>(res + (i * pl.lanes + l) * kVec, a.res ? valid[i] : 0);
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * per + tid / pl.lanes;
+  fetch(min(row, a.rows - 1));
+  for (int64_t first = (int64_t)blockIdx.x * per; first < a.rows; first += step, row += step) {
     Raw<IO> rx[NV];
     Raw<RO> rr[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) rx[i] = load_raw<IO>(x + (i * pl.lanes + l) * kVec, live ? valid[i] : 0);
-    const R* res = static_cast<const R*>(a.res) + (live ? row : first) * a.n;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) rr[i] = load_raw<RO>(res + (i * pl.lanes + l) * kVec, live && a.res ? valid[i] : 0);
+    for (int i = 0; i < NV; ++i) {
+      rx[i] = nx[i];
+      rr[i] = nr[i];
+    }
+    // in place: a row is read by the lanes that write it, and the next one is another
+    if (first + step < a.rows) fetch(min(row + step, a.rows - 1));
     float rho_x = 1.0f;
     if (a.post) {
       float s[1] = {0.0f};
@@ -351,7 +381,7 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
       row_sums(s, pl.lanes, slot_post);
       rho_x = inv_rms(s[0], a.inv_n, a.eps);
     }
-    float sum[2] = {0.0f, 0.0f};
+    float sum[2] = {0.0f, 0.0f};                           // (two: the sums of x have a place of their own in LDS)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[kVec];
@@ -363,7 +393,7 @@ __global__ __launch_bounds__(THREADS) void residual_norm_kernel(ResidualNormArgs
     }
     row_sums(sum, pl.lanes, slot);
     const float rho = inv_rms(sum[0], a.inv_n, a.eps);
-    if (!live) continue;
+    if (row >= a.rows) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * pl.lanes + l) * kVec;
@@ -383,7 +413,7 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
   using T = typename IO::T;
   using R = typename RO::T;
   const NormPlan& pl = a.plan;
-  const int tid = threadIdx.x, l = tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
+  const int tid = threadIdx.x, l = pl.lanes > 64 ? tid : tid & (pl.lanes - 1), per = pl.threads / pl.lanes;
   int slot = 0, slot_post = 0;
   float w[NV][kVec], wp[NV][kVec], by[NV][kVec], dw[NV][kVec] = {}, dp[NV][kVec] = {}, ds[NV][kVec] = {};
   int valid[NV];
@@ -397,20 +427,35 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
 #pragma unroll
     for (int j = 0; j < kVec; ++j) by[i][j] *= a.alpha;
   }
-  for (int64_t first = (int64_t)blockIdx.x * per; first < a.rows; first += (int64_t)gridDim.x * per) {
-    const int64_t row = first + tid / pl.lanes;
+  const int64_t step = (int64_t)gridDim.x * per;
+  Raw<IO> nx[NV], nd[NV];
+  Raw<RO> nr[NV], no[NV];
+  auto fetch = [&](int64_t row) {
+    const int64_t base = row * a.n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * pl.lanes + l) * kVec;
+      nd[i] = load_raw<IO>(static_cast<const T*>(a.dy) + base + e, valid[i]);
+      nr[i] = load_raw<RO>(static_cast<const R*>(a.res) + base + e, valid[i]);
+      no[i] = load_raw<RO>(static_cast<const R*>(a.dres_out) + base + e, a.dres_out ? valid[i] : 0);
+      nx[i] = load_raw<IO>(static_cast<const T*>(a.x) + base + e, a.x ? valid[i] : 0);
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * per + tid / pl.lanes;
+  fetch(min(row, a.rows - 1));
+  for (int64_t first = (int64_t)blockIdx.x * per; first < a.rows; first += step, row += step) {
     const bool live = row < a.rows;
-    const int64_t base = (live ? row : first) * a.n;
+    const int64_t base = row * a.n;
     Raw<IO> rx[NV], rd[NV];
     Raw<RO> rr[NV], ro[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * pl.lanes + l) * kVec, k = live ? valid[i] : 0;
-      rd[i] = load_raw<IO>(static_cast<const T*>(a.dy) + base + e, k);
-      rr[i] = load_raw<RO>(static_cast<const R*>(a.res) + base + e, k);
-      ro[i] = load_raw<RO>(static_cast<const R*>(a.dres_out) + base + e, a.dres_out ? k : 0);
-      rx[i] = load_raw<IO>(static_cast<const T*>(a.x) + base + e, a.x ? k : 0);
+      rx[i] = nx[i];
+      rd[i] = nd[i];
+      rr[i] = nr[i];
+      ro[i] = no[i];
     }
+    if (first + step < a.rows) fetch(min(row + step, a.rows - 1));
     float sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -470,65 +515,84 @@ __global__ __launch_bounds__(THREADS) void residual_norm_bwd_kernel(ResidualNorm
   }
 }
 
-// out[y][j]: the sum of rows of partial sums in a fixed order.  16 threads to a column.
-__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int rows, int n, float* __restrict__ out) {
-  __shared__ float s_run[16][64];
-  const int c = threadIdx.x & 63, run = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + c;
-  const float* p = part + (int64_t)blockIdx.y * rows * n;
+struct Columns {
+  const float* part[3];
+  float* out[3];
+};
+
+// out[y][j] of weights z: the sum of rows of partial sums in a fixed order.  64 threads to a column, four loads ahead.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(Columns c, int rows, int n) {
+  __shared__ float s_run[64][17];
+  const int lane = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + lane;
+  const float* p = c.part[blockIdx.z] + (int64_t)blockIdx.y * rows * n;
   float v = 0.0f;
   if (col < n)
-    for (int r = run; r < rows; r += 16) v += p[(int64_t)r * n + col];
-  s_run[run][c] = v;
+#pragma unroll 4
+    for (int r = run; r < rows; r += 64) v += p[(int64_t)r * n + col];
+  s_run[run][lane] = v;
   __syncthreads();
-  if (run == 0 && col < n) {
+  if (run < 4) {
 #pragma unroll
-    for (int k = 1; k < 16; ++k) v += s_run[k][c];
-    out[(int64_t)blockIdx.y * n + col] = v;
+    for (int k = 4; k < 64; k += 4) v += s_run[run + k][lane];
+    s_run[run][lane] = v;
   }
+  __syncthreads();
+  if (run == 0 && col < n)
+    c.out[blockIdx.z][(int64_t)blockIdx.y * n + col] = (s_run[0][lane] + s_run[1][lane]) + (s_run[2][lane] + s_run[3][lane]);
 }
 
-hipError_t launch_columns(const float* part, int rows, int n, int heads, float* out, hipStream_t s) {
-  norm_columns_kernel<<<dim3((n + 63) / 64, heads), 1024, 0, s>>>(part, rows, n, out);
+hipError_t launch_columns(const Columns& c, int count, int rows, int n, int heads, hipStream_t s) {
+  norm_columns_kernel<<<dim3((n + 15) / 16, heads, count), 1024, 0, s>>>(c, rows, n);
   return hipGetLastError();
 }
 
-NormPlan plan(int64_t rows, int n, int64_t blocks) {
+// About as many workgroups as the card holds at once: each takes several rows, with its weights in registers and
+// the next row's loads ahead.
+NormPlan plan(int64_t rows, int n, int heads_apart, bool backward) {
   NormPlan p{};
   const int vec = (n + kVec - 1) / kVec;
-  int lanes = 1;
-  while (lanes < vec) lanes <<= 1;
-  // two vectors to a lane where a wave or a workgroup of four then holds a row that otherwise would not fit it
-  p.vectors = lanes > 256 || lanes == 128 ? 2 : 1;
-  p.lanes = lanes / p.vectors;
+  // two vectors to a lane where a row would not fit a workgroup of 512, and forward where it then fits a wave (the backward has up to
+  // three sums for every value of a lane)
+  p.vectors = vec > 512 || (!backward && vec > 64 && vec <= 128) ? 2 : 1;
+  const int need_lanes = (vec + p.vectors - 1) / p.vectors;
+  p.lanes = 1;
+  while (p.lanes < need_lanes && p.lanes < 64) p.lanes <<= 1;
+  if (need_lanes > 64) p.lanes = (need_lanes + 63) / 64 * 64;
   p.threads = p.lanes > 64 ? p.lanes : 256;
   const int64_t per = p.threads / p.lanes, need = (rows + per - 1) / per;
-  p.blocks = (int32_t)(need < blocks ? need : blocks);
+  int64_t most = 256 * ((backward ? 768 : 1024) / p.threads) / heads_apart;
+  if (most < 1) most = 1;
+  p.blocks = (int32_t)(need < most ? need : most);
   if (p.blocks < 1) p.blocks = 1;
   return p;
 }
 
 // f with the kernel's vectors to a lane and bound on threads.
-template <typename F>
+template <bool BACKWARD, typename F>
 hipError_t by_plan(const NormPlan& p, F f) {
   using std::integral_constant;
-  if (p.vectors == 1) f(integral_constant<int, 1>(), integral_constant<int, 256>());
-  else if (p.threads <= 256) f(integral_constant<int, 2>(), integral_constant<int, 256>());
-  else f(integral_constant<int, 2>(), integral_constant<int, 512>());
+  if (p.vectors == 1 && p.threads <= 256) {
+    f(integral_constant<int, 1>(), integral_constant<int, 256>());
+  } else if (p.threads <= 256) {
+    if constexpr (!BACKWARD) f(integral_constant<int, 2>(), integral_constant<int, 256>());
+  } else if (p.vectors == 2) {
+    f(integral_constant<int, 2>(), integral_constant<int, 512>());
+  } else {
+    f(integral_constant<int, 1>(), integral_constant<int, 512>());
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-NormPlan gated_norm_plan(int64_t rows, int n, int heads_apart, bool backward) {
-  return plan(rows, n, !backward ? 1 << 20 : heads_apart >= 1024 ? 1 : 1024 / heads_apart);
-}
+NormPlan gated_norm_plan(int64_t rows, int n, int heads_apart, bool backward) { return plan(rows, n, heads_apart, backward); }
 
-NormPlan residual_norm_plan(int64_t rows, int n, bool backward) { return plan(rows, n, backward ? 1024 : 1 << 20); }
+NormPlan residual_norm_plan(int64_t rows, int n, bool backward) { return plan(rows, n, 1, backward); }
 
 hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t s) {
   const dim3 grid(a.plan.blocks, a.per_head ? a.heads : 1), block(a.plan.threads);
-  return by_plan(a.plan, [&](auto nv, auto nt) {
+  return by_plan<false>(a.plan, [&](auto nv, auto nt) {
     constexpr int NV = decltype(nv)::value, NT = decltype(nt)::value;
     if (a.io == kIoBf16) {
       if (a.z.p) gated_norm_kernel<BF16, NV, true, NT><<<grid, block, 0, s>>>(a);
@@ -543,7 +607,7 @@ hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t s) {
 hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, float* dw, hipStream_t s) {
   const int heads = a.per_head ? a.heads : 1;
   const dim3 grid(a.plan.blocks, heads), block(a.plan.threads);
-  const hipError_t e = by_plan(a.plan, [&](auto nv, auto nt) {
+  const hipError_t e = by_plan<true>(a.plan, [&](auto nv, auto nt) {
     constexpr int NV = decltype(nv)::value, NT = decltype(nt)::value;
     if (a.io == kIoBf16) {
       if (a.z.p) gated_norm_bwd_kernel<BF16, NV, true, NT><<<grid, block, 0, s>>>(a);
@@ -553,7 +617,7 @@ hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, float* dw, hipStream_t 
       else gated_norm_bwd_kernel<F32, NV, false, NT><<<grid, block, 0, s>>>(a);
     }
   });
-  return e == hipSuccess && dw ? launch_columns(a.part, a.plan.blocks, a.n, heads, dw, s) : e;
+  return e == hipSuccess && dw ? launch_columns({{a.part}, {dw}}, 1, a.plan.blocks, a.n, heads, s) : e;
 }
 
 template <typename F>
@@ -564,7 +628,7 @@ static hipError_t by_types(const ResidualNormArgs& a, F f) {
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) {
   return by_types(a, [&](auto io, auto ro) {
-    return by_plan(a.plan, [&](auto nv, auto nt) {
+    return by_plan<false>(a.plan, [&](auto nv, auto nt) {
       residual_norm_kernel<decltype(io), decltype(ro), decltype(nv)::value, decltype(nt)::value>
           <<<a.plan.blocks, a.plan.threads, 0, s>>>(a);
     });
@@ -573,14 +637,19 @@ hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) {
 
 hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, float* const (&dw)[3], hipStream_t s) {
   hipError_t e = by_types(a, [&](auto io, auto ro) {
-    return by_plan(a.plan, [&](auto nv, auto nt) {
+    return by_plan<true>(a.plan, [&](auto nv, auto nt) {
       residual_norm_bwd_kernel<decltype(io), decltype(ro), decltype(nv)::value, decltype(nt)::value>
           <<<a.plan.blocks, a.plan.threads, 0, s>>>(a);
     });
   });
-  for (int i = 0; i < 3 && e == hipSuccess; ++i)
-    if (dw[i]) e = launch_columns(a.part[i], a.plan.blocks, a.n, 1, dw[i], s);
-  return e;
+  Columns c{};
+  int count = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!dw[i]) continue;
+    c.part[count] = a.part[i];
+    c.out[count++] = dw[i];
+  }
+  return e == hipSuccess && count ? launch_columns(c, count, a.plan.blocks, a.n, 1, s) : e;
 }
 
 }  // namespace ssscan
