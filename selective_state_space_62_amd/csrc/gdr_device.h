@@ -83,6 +83,17 @@ __device__ __forceinline__ void step_end() { __builtin_amdgcn_sched_barrier(0); 
 // Row (of 32) of register r in a result tile.
 __device__ __forceinline__ int tile_row(int r, int lane) { return (r & 3) + 8 * (r >> 2) + 4 * (lane >> 5); }
 
+// A vector's values of a lane's 16 rows in a result tile.
+__device__ __forceinline__ acc16 rows_of(const float* v, int lane) {
+  acc16 o;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float4 x = *reinterpret_cast<const float4*>(v + 8 * g + 4 * (lane >> 5));
+    o[4 * g] = x.x; o[4 * g + 1] = x.y; o[4 * g + 2] = x.z; o[4 * g + 3] = x.w;
+  }
+  return o;
+}
+
 // Largest of nonnegative values over the wave, NaN left out, in a scalar register: quad permutes and mirrors of 8 and of
 // 16 lanes, then the four rows' (as integers, which order nonnegative floats as they are).
 __device__ __forceinline__ float wave_max(float v) {

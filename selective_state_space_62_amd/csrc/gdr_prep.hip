@@ -33,6 +33,39 @@ __device__ __forceinline__ float exp2_wide(double v) {
   return exp2_of(t.whole, t.rest);
 }
 
+// Running sums or minima over the wave's lanes: shifts within rows of 16, then the last lane of a row to the rows behind it.
+// These moves cost a few cycles each where a shuffle through LDS costs about a hundred.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double from, double none) {
+  const int lo = __builtin_amdgcn_update_dpp(__double2loint(none), __double2loint(from), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(__double2hiint(none), __double2hiint(from), CTRL, ROWS, 0xf, false);
+  return __hiloint2double(hi, lo);
+}
+
+template <typename Op>
+__device__ __forceinline__ double running(double v, double none, Op op) {
+  v = op(v, moved<0x111, 0xf>(v, none));
+  v = op(v, moved<0x112, 0xf>(v, none));
+  v = op(v, moved<0x114, 0xf>(v, none));
+  v = op(v, moved<0x118, 0xf>(v, none));
+  v = op(v, moved<0x142, 0xa>(v, none));
+  return op(v, moved<0x143, 0xc>(v, none));
+}
+
+__device__ __forceinline__ double last_of(double v) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), kC - 1), __builtin_amdgcn_readlane(__double2loint(v), kC - 1));
+}
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+// 16 inner elements of a 16x16 product in fp32: lane l holds row (column) l & 15, inner elements 4 (l >> 4) + 0..3.  The result's
+// lane has column l & 15 and rows 4 (l >> 4) + 0..3, so that it is the right operand of the next product as it is.
+__device__ __forceinline__ f4 mm16(f4 x, f4 y, f4 acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], acc, 0, 0, 0);
+  return acc;
+}
+
 template <typename IO, int KP, bool WHOLE, bool BWD>
 __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   using T = typename IO::T;
@@ -82,20 +115,25 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   }
   __syncthreads();
 
-  // products: tasks 0-2 the tiles of A, 3-5 those of P, two to each of the first two waves; then the vectors by the last wave
-  acc16 acc[2] = {zero16(), zero16()};
+  // products: waves 0-2 a tile of A each, waves 1-3 one of P
+  const bool of_a = wave < 3, of_p = wave > 0;
+  const int ta = wave, tp = wave - 1;
+  acc16 A = zero16(), P = zero16();
+  {
+    const char* ai = s_rows + (ta > 0) * kSteps * kBlock;
+    const char* aj = s_rows + (ta > 1) * kSteps * kBlock;
+    const char* pi = s_rows + NP * kSide + (tp > 0) * kSteps * kBlock;
+    const char* pj = s_rows + (tp > 1) * kSteps * kBlock;
+    if (of_a) {
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int task = wave + 4 * n;
-    if (task > 5) break;
-    const int tile = task % 3, ti = tile > 0, tj = tile > 1;
-    const bool of_p = task > 2, turned = of_p && !BWD;     // P as the forward reads it is made transposed
-    const char* pi = s_rows + (of_p ? NP * kSide : 0) + ti * kSteps * kBlock;
-    const char* pj = s_rows + tj * kSteps * kBlock;
+      for (int s = 0; s < kSteps; ++s)
+        A = mm<NP, NP>(operand<NP>(ai + s * kBlock, lane, kSide), operand<NP>(aj + s * kBlock, lane, kSide), A);
+    }
+    if (of_p) {                                            // as the forward reads it, P is made transposed
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      acc[n] = mm<NP, NP>(operand<NP>((turned ? pj : pi) + s * kBlock, lane, kSide),
-                          operand<NP>((turned ? pi : pj) + s * kBlock, lane, kSide), acc[n]);
+      for (int s = 0; s < kSteps; ++s)
+        P = mm<NP, NP>(operand<NP>((BWD ? pi : pj) + s * kBlock, lane, kSide), operand<NP>((BWD ? pj : pi) + s * kBlock, lane, kSide), P);
+    }
   }
   double gam = 0.0, end = 0.0, bal = 0.0;
   float beta = 0.0f, into = 0.0f, sk = 1.0f, sq = 1.0f, grow = 0.0f;
@@ -106,24 +144,14 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
     float g = lane < valid && a.g ? a.g[at] : 0.0f;
     g = g < -2000.0f ? -2000.0f : g;                       // a NaN stays one
     gam = (double)g * 1.4426950408889634074;
-#pragma unroll
-    for (int d = 1; d < kC; d <<= 1) {
-      const double o = __shfl_up(gam, d);
-      if (lane >= d) gam += o;
-    }
-    end = __shfl(gam, kC - 1);
+    gam = running(gam, 0.0, [](double x, double o) { return x + o; });
+    end = last_of(gam);
     sk = s_scale[0][lane];
     sq = s_scale[1][lane];
     const int es = exponent(sk);
-    least = es;
-    double low = gam;                                      // the smallest gam_j up to here
-#pragma unroll
-    for (int d = 1; d < kC; d <<= 1) {
-      const int o = __shfl_xor(least, d);
-      least = o < least ? o : least;
-      const double l = __shfl_up(low, d);
-      if (lane >= d) low = l < low ? l : low;
-    }
+    const auto less = [](double x, double o) { return o < x ? o : x; };
+    const double low = running(gam, HUGE_VAL, less);       // the smallest gam_j up to here
+    least = (int)last_of(running((double)es, HUGE_VAL, less));
     least = least == kZeroRow ? 0 : least;
     const double p = ceil(gam - low) - floor(fmin(fmax(-0.5 * low, 0.0), 16.0));
     grow = (float)p;
@@ -137,107 +165,97 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   }
   __syncthreads();
   const int64_t at = blockIdx.x;
+  if (of_a) {
+    const int i0 = 32 * (ta > 0), j = 32 * (ta > 1) + (lane & 31);
+    const float whole = s_whole[2][j], rest = s_rest[2][j];
+    const acc16 w = rows_of(s_whole[0] + i0, lane), v = rows_of(s_rest[0] + i0, lane), f = rows_of(s_beta + i0, lane);
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int task = wave + 4 * n;
-    if (task > 5) break;
-    const int tile = task % 3, ti = tile > 0, tj = tile > 1;
-    if (task > 2) {
-      const int v = !BWD ? 1 : 2, w = 3 - v;               // the vector of a lane's column, of its 16 rows
-      const int c = 32 * (BWD ? tj : ti) + (lane & 31), r0 = 32 * (BWD ? ti : tj);
-      const float sign = BWD ? -1.0f : 1.0f, whole = s_whole[v][c], rest = s_rest[v][c];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = r0 + tile_row(r, lane);
-        const float d = exp2_of(sign * (whole - s_whole[w][row]), sign * (rest - s_rest[w][row]));
-        acc[n][r] = (BWD ? c <= row : row <= c) ? acc[n][r] * d : 0.0f;
-      }
-      constexpr int NO = BWD ? 2 : NP;
-      char* out = static_cast<char*>(a.p) + at * (NO * kTriBytes) + tile * 2048 + lane * 16;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Planes p = split<NO>(acc[n], s, 1.0f);
-        *reinterpret_cast<h8*>(out + s * 1024) = p.hi;
-        if constexpr (NO == 2) *reinterpret_cast<h8*>(out + kTriBytes + s * 1024) = p.lo;
-      }
-    } else {
-      const int j = 32 * tj + (lane & 31);
-      const float whole = s_whole[2][j], rest = s_rest[2][j];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int i = 32 * ti + tile_row(r, lane);
-        const float d = exp2_of(s_whole[0][i] - whole, s_rest[0][i] - rest);
-        s_a[i][j] = j < i ? s_beta[i] * (acc[n][r] * d) : 0.0f;
-      }
+    for (int r = 0; r < 16; ++r) {
+      const int i = i0 + tile_row(r, lane);
+      const float x = f[r] * (A[r] * exp2_of(w[r] - whole, v[r] - rest));
+      s_a[i][j] = j < i ? x : 0.0f;
     }
   }
   // above the diagonal T stays zero (the rows of k and q have been read)
   for (int e = tid; e < 32 * 32; e += kThreads) s_t[e >> 5][32 + (e & 31)] = 0.0f;
   __syncthreads();
 
+  // P, while the first wave solves the triangles
+  if (of_p) {
+    constexpr int NO = BWD ? 2 : NP;
+    const int i0 = 32 * (tp > 0), j0 = 32 * (tp > 1), c = (BWD ? j0 : i0) + (lane & 31), r0 = BWD ? i0 : j0;
+    const float whole = s_whole[BWD ? 2 : 1][c], rest = s_rest[BWD ? 2 : 1][c], sign = BWD ? 1.0f : -1.0f;
+    const acc16 w = rows_of(s_whole[BWD ? 1 : 2] + r0, lane), v = rows_of(s_rest[BWD ? 1 : 2] + r0, lane);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int row = r0 + tile_row(r, lane);
+      const float x = P[r] * exp2_of(sign * (w[r] - whole), sign * (v[r] - rest));
+      P[r] = (BWD ? c <= row : row <= c) ? x : 0.0f;
+    }
+    char* out = static_cast<char*>(a.p) + at * (NO * kTriBytes) + tp * 2048 + lane * 16;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const Planes p = split<NO>(P, s, 1.0f);
+      *reinterpret_cast<h8*>(out + s * 1024) = p.hi;
+      if constexpr (NO == 2) *reinterpret_cast<h8*>(out + kTriBytes + s * 1024) = p.lo;
+    }
+  }
   // 16x16 triangles: lane 16 q + c solves column c of triangle q
   if (wave == 0) {
     const int q = lane >> 4, c = lane & 15;
     float x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == c ? 1.0f : 0.0f;
+    for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) v = fmaf(-s_a[16 * q + i][16 * q + j], x[j], v);
-      x[i] = v;
-      s_t[16 * q + i][16 * q + c] = v;
+    for (int i = 1; i < 16; ++i) {
+      float v[2] = {x[i], 0.0f};                           // two sums: a row waits half as long for the one before
+#pragma unroll
+      for (int j = 0; j < i; j += 4) {
+        const f4 l = *reinterpret_cast<const f4*>(&s_a[16 * q + i][16 * q + j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (j + k < i) v[k & 1] = fmaf(-l[k], x[j + k], v[k & 1]);
+      }
+      x[i] = v[0] + v[1];
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s_t[16 * q + i][16 * q + c] = x[i];
     // the upper of the off-diagonal 16x16 blocks inside the 32x32 triangles
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (!(q & 1)) s_t[16 * q + i][16 * q + 16 + c] = 0.0f;
   }
   __syncthreads();
-  // 16 -> 32: both pairs at once, 128 threads to a pair, two elements of a row each
-  {
-    const int p = tid >> 7, e = tid & 127, i = e >> 3, n = (e & 7) * 2, o = 32 * p;
-    float m0 = 0.0f, m1 = 0.0f;
+  const int n16 = lane & 15, g4 = 4 * (lane >> 4);
+  // 16 -> 32: a wave to a pair
+  if (wave < 2) {
+    const int o = 32 * wave;
+    f4 t;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float l = s_a[o + 16 + i][o + k];
-      m0 = fmaf(l, s_t[o + k][o + n], m0);
-      m1 = fmaf(l, s_t[o + k][o + n + 1], m1);
-    }
-    s_a[o + i][o + 16 + n] = m0;                           // above A's diagonal there is room
-    s_a[o + i][o + 16 + n + 1] = m1;
-    __syncthreads();
-    m0 = m1 = 0.0f;
+    for (int i = 0; i < 4; ++i) t[i] = s_t[o + g4 + i][o + n16];
+    const f4 none = {};
+    const f4 m = mm16(*reinterpret_cast<const f4*>(&s_a[o + 16 + n16][o + g4]), t, none);
+    const f4 r = mm16(*reinterpret_cast<const f4*>(&s_t[o + 16 + n16][o + 16 + g4]), m, none);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float l = s_t[o + 16 + i][o + 16 + k];
-      m0 = fmaf(-l, s_a[o + k][o + 16 + n], m0);
-      m1 = fmaf(-l, s_a[o + k][o + 16 + n + 1], m1);
-    }
-    s_t[o + 16 + i][o + n] = m0;
-    s_t[o + 16 + i][o + n + 1] = m1;
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) s_t[o + 16 + g4 + i][o + n16] = -r[i];
   }
-  // 32 -> 64: four elements of a row to a thread
+  __syncthreads();
+  // 32 -> 64: a wave to a 16x16 block; A21 T11 is formed for its 16 columns by each wave of two
   {
-    const int i = tid >> 3, n = (tid & 7) * 4;
-    float m[4] = {};
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      const float l = s_a[32 + i][k];
-      const float4 t = *reinterpret_cast<const float4*>(&s_t[k][n]);
-      m[0] = fmaf(l, t.x, m[0]); m[1] = fmaf(l, t.y, m[1]); m[2] = fmaf(l, t.z, m[2]); m[3] = fmaf(l, t.w, m[3]);
-    }
-    *reinterpret_cast<float4*>(&s_a[i][32 + n]) = make_float4(m[0], m[1], m[2], m[3]);
-    __syncthreads();
+    const int i0 = 16 * (wave >> 1), n0 = 16 * (wave & 1);
+    f4 m[2] = {}, r = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      const float l = -s_t[32 + i][32 + k];
-      const float4 t = *reinterpret_cast<const float4*>(&s_a[k][32 + n]);
-      m[0] = fmaf(l, t.x, m[0]); m[1] = fmaf(l, t.y, m[1]); m[2] = fmaf(l, t.z, m[2]); m[3] = fmaf(l, t.w, m[3]);
+    for (int k = 0; k < 32; k += 16) {
+      f4 t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = s_t[k + g4 + i][n0 + n16];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[i] = mm16(*reinterpret_cast<const f4*>(&s_a[32 + 16 * i + n16][k + g4]), t, m[i]);
     }
-    *reinterpret_cast<float4*>(&s_t[32 + i][n]) = make_float4(m[0], m[1], m[2], m[3]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) r = mm16(*reinterpret_cast<const f4*>(&s_t[32 + i0 + n16][32 + 16 * k + g4]), m[k], r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_t[32 + i0 + g4 + i][n0 + n16] = -r[i];
   }
   __syncthreads();
   // columns to [2^13, 2^14)
