@@ -1,4 +1,5 @@
 // C ABI of the gated delta rule: argument checks and launches.  See include/ssscan.h.
+#include <algorithm>
 #include <cmath>
 
 #include "api_rows.h"
@@ -122,17 +123,41 @@ bool whole_runs(const Inputs& in) {
 
 int64_t chunks_of(int64_t seqlen) { return (seqlen + kGdrChunk - 1) / kGdrChunk; }
 
-// Scratch of the chunked forward: the inverses, P, then the vectors.  P is taken as large as either I/O type needs it.
-struct FwdLayout {
-  size_t p, vecs, total;
+struct Segments {
+  int64_t count, per;
 };
 
-FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v) {
-  const int64_t n = batch * heads_v * chunks_of(seqlen);
+// Segments of at least two chunks, as many as fill the GPU.  Made in segments a row costs about 1.7 times as much, the factors
+// and the states first, so two of them gain nothing.  In one and in segments, us: 16 heads of 131072 tokens 15742, 2341; 12 x 8 heads
+// (fp32, keys of 64) of 2048 335, 271; 40 heads of 4096 496, 247; 8 heads of 500 67, 53; 2 heads of 1000 91, 43; 4 x 40 heads of
+// 2048 318, 320; 8 x 40 heads of 2048, which fill it, 509 and, in three, 614.
+Segments segments_of(int64_t batch, int64_t chunks, int heads_v, int dim_k, int dim_v, int io) {
+  const int64_t groups = batch * heads_v * ((dim_v + 127) / 128);
+  const int64_t n = std::min(gdr_chunk_room(io, dim_k) / groups, chunks / 2);
+  if (n < 3) return {1, chunks};
+  const int64_t per = (chunks + n - 1) / n;
+  return {(chunks + per - 1) / per, per};
+}
+
+// Scratch of the chunked forward: the inverses, P, then the vectors.  P is taken as large as either I/O type needs it.
+struct FwdLayout {
+  size_t p, vecs, ends, moves, moves_e, total;
+  int64_t ldv;
+};
+
+FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v, int dim_k, int dim_v) {
+  const int64_t chunks = chunks_of(seqlen), n = batch * heads_v * chunks, rows = (dim_k + 31) / 32 * 32;
+  const int64_t segments = std::max(segments_of(batch, chunks, heads_v, dim_k, dim_v, kIoBf16).count,
+                                    segments_of(batch, chunks, heads_v, dim_k, dim_v, kIoF32).count);
+  const int64_t ends = segments > 1 ? batch * heads_v * segments * rows : 0;
   FwdLayout l;
+  l.ldv = (int64_t)(dim_v + 31) / 32 * 32;
   l.p = round256(gdr_tri_bytes(n));
   l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, false));
-  l.total = l.vecs + round256(gdr_vecs_bytes(n));
+  l.ends = l.vecs + round256(gdr_vecs_bytes(n));
+  l.moves = l.ends + round256((size_t)(ends * l.ldv) * 4);
+  l.moves_e = l.moves + round256((size_t)(ends * rows) * 4);
+  l.total = l.moves_e + round256((size_t)(segments > 1 ? batch * heads_v * segments * 4 : 0) * 4);
   return l;
 }
 
@@ -168,7 +193,7 @@ extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
   if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen <= kRecurTokens) return 0;
-  return fwd_layout(batch, seqlen, heads_v).total;
+  return fwd_layout(batch, seqlen, heads_v, dim_k, dim_v).total;
 }
 
 ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
@@ -202,14 +227,22 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   if (recur) {
     e = launch_gdr_recur(a, s);
   } else {
-    const FwdLayout l = fwd_layout(batch, seqlen, heads_v);
+    const FwdLayout l = fwd_layout(batch, seqlen, heads_v, dim_k, dim_v);
     char* ws = static_cast<char*>(workspace);
     a.chunks = chunks_of(seqlen);
     a.whole = whole_runs(in);
     a.tri = ws;
     a.p = ws + l.p;
     a.vecs = reinterpret_cast<float*>(ws + l.vecs);
+    const Segments seg = segments_of(batch, a.chunks, heads_v, dim_k, dim_v, a.io);
+    a.segments = seg.count;
+    a.per = seg.per;
+    a.ldv = l.ldv;
+    a.ends = reinterpret_cast<float*>(ws + l.ends);
+    a.moves = reinterpret_cast<float*>(ws + l.moves);
+    a.moves_e = reinterpret_cast<int32_t*>(ws + l.moves_e);
     e = launch_gdr_prep(a, false, s);
+    if (e == hipSuccess) e = launch_gdr_segments(a, s);
     if (e == hipSuccess) e = launch_gdr_chunk(a, false, s);
   }
   return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule launch");
@@ -265,6 +298,8 @@ ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   a.tri_t = ws + l.tri_t;
   a.p = ws + l.p;
   a.vecs = reinterpret_cast<float*>(ws + l.vecs);
+  a.segments = 1;
+  a.per = a.chunks;
   a.ldv = l.ldv;
   a.states = reinterpret_cast<float*>(ws + l.states);
   a.dstates = reinterpret_cast<float*>(ws + l.dstates);

@@ -28,14 +28,20 @@ struct GdrArgs {
   float* h_final;        // nullable
   // chunked: what the preparation leaves for every (batch row, head, chunk)
   int64_t chunks;        // of a row
+  // segments that a row's chunks go in, `per` chunks each but the last: with more than one, the state's change over each of them
+  // but the last comes first, as a product with the state before it and a sum
+  int64_t segments, per;
+  float* ends;           // the state behind a segment, dk rounded up to tiles of 32 by ldv
+  float* moves;          // the factor, dk by dk rounded up to tiles of 32 (the first segment has the state before it and needs none),
+  int32_t* moves_e;      // over a power of 2 for each 32 of its columns, four of them to a segment: what decays leave may be below 2^-126
   int32_t whole;         // dk and dv are multiples of 8 and the rows of q, k and v are aligned to 4 bytes
   void* tri;             // operand blocks of the inverse T
   void* tri_t;           // backward: of T transposed
   void* p;               // operand blocks of P; backward: of P transposed
   float* vecs;           // kVecs vectors
-  // backward, for every chunk of a head: rows of ldv columns (dv rounded up to tiles of 32) as operands, and of each tile the largest
-  // |value| (of every kind in a run of its own, max_apart floats behind the one before)
-  int64_t ldv;
+  int64_t ldv;           // dv rounded up to tiles of 32
+  // backward, for every chunk of a head: rows of ldv columns as operands, and of each tile the largest |value| (of every kind in a run
+  // of its own, max_apart floats behind the one before)
   float* states;         // the state before it
   float* u;              // U
   float* dstates;        // the gradient of the state behind it
@@ -62,6 +68,10 @@ size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward);
 size_t gdr_vecs_bytes(int64_t chunk_heads);
 hipError_t launch_gdr_prep(const GdrArgs& a, bool backward, hipStream_t s);
 hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s);
+// The states behind all segments but the last, where there is more than one.
+hipError_t launch_gdr_segments(const GdrArgs& a, hipStream_t s);
+// Workgroups of a forward chunk kernel that the GPU holds at once.
+int gdr_chunk_room(int io, int dk);
 // The backward after the states: their gradients in turn, from the last chunk on, then all other gradients of all chunks.
 hipError_t launch_gdr_chunk_bwd(const GdrArgs& a, hipStream_t s);
 hipError_t launch_gdr_grad(const GdrArgs& a, hipStream_t s);

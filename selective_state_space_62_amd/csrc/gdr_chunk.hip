@@ -6,6 +6,8 @@
 // S stay in registers from one product to the next.  The chunks of a head follow one another, so what counts is how long one
 // takes: the next chunk's tiles are on their way while this one is computed, those that need no conversion straight
 // to LDS, and nothing waits for a value that a workgroup could not form beforehand.
+// Where there are too few heads for the GPU, the chunks of one go in segments at the same time: the state behind a segment is a
+// product with the state before it and a sum, both made first (Of::kEnds) and put together in turn by a small kernel.
 // For the backward the same kernel makes S before every chunk and U (transposed by a product with the identity, as
 // operands of the gradients) instead of O.
 #include "gdr_device.h"
@@ -18,20 +20,33 @@ using namespace gdr;
 constexpr int kThreads = 256;
 constexpr int kCols = 128;               // of a workgroup
 
-template <typename IO, int KP, bool WHOLE, bool STATES>
-__global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) void gdr_chunk_kernel(GdrArgs a) {
+enum class Of {
+  kOut,        // O and the last state
+  kStates,     // the backward's states and U
+  kEnds,       // the states behind segments
+};
+
+constexpr int per_cu(bool bf16, int keys) { return bf16 || keys <= 64 ? 2 : 1; }
+
+template <typename IO, int KP, bool WHOLE, Of OF>
+__global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_chunk_kernel(GdrArgs a) {
   using T = typename IO::T;
+  constexpr bool OUT = OF == Of::kOut, STATES = OF == Of::kStates, ENDS = OF == Of::kEnds;
   // What leads to O alone is rounded to bf16 where the I/O is: there one fp16 plane (2^-12) of S, U and P does.
   constexpr int NP = planes_of<IO>(), NO = NP, kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
-  constexpr int kSide = 2 * kSteps * kBlock, kTurned = kTiles * 4 * kBlock, kP = STATES ? 0 : NO * kTriBytes;
-  __shared__ alignas(16) char s_k[NP * kSide], s_kt[NP * kTurned], s_q[STATES ? 16 : NP * kSide];
+  constexpr int kSide = 2 * kSteps * kBlock, kTurned = kTiles * 4 * kBlock, kP = OUT ? NO * kTriBytes : 0;
+  __shared__ alignas(16) char s_k[NP * kSide], s_kt[NP * kTurned], s_q[OUT ? NP * kSide : 16];
   __shared__ alignas(16) char s_t[2 * kTriBytes], s_p[kP + 16];
   __shared__ alignas(16) float s_vecs[2][kVecs][kC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t bh = blockIdx.x;
-  const int64_t b = bh / a.hv;
+  const int64_t bh = blockIdx.x / a.segments, seg = blockIdx.x - bh * a.segments;
+  const int64_t b = bh / a.hv, begin = seg * a.per, stop = min(begin + a.per, a.chunks);
   const int h = (int)(bh - b * a.hv), hkey = h / (a.hv / a.hk);
-  const int col0 = blockIdx.y * kCols + 32 * wave;
+  // behind the columns of the values, the columns of the segment's factor: what the identity becomes without values
+  const int blocks = (a.dv + kCols - 1) / kCols;
+  const bool moves = ENDS && (int)blockIdx.y >= blocks;
+  const int col0 = ((int)blockIdx.y - (moves ? blocks : 0)) * kCols + 32 * wave, ncols = moves ? 0 : a.dv;
+  if (ENDS && (seg == a.segments - 1 || (moves && seg == 0))) return;
 
   const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + hkey * a.qs[2];
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hkey * a.ks[2];
@@ -41,13 +56,16 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   int ce = 0;
   {
     const int lane = threadIdx.x & 63, col = col0 + (lane & 31);
-    const float* h0 = a.h0 + bh * a.dk * a.dv;
+    const bool first = seg == 0 || ENDS;
+    const int64_t ld = first ? a.dv : a.ldv;
+    const float* from = first ? (seg == 0 ? a.h0 : nullptr) : a.ends;
+    if (from) from += first ? bh * a.dk * a.dv : (bh * a.segments + seg - 1) * KP * a.ldv;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 32 * m + tile_row(r, lane);
-        st[m][r] = a.h0 && row < a.dk && col < a.dv ? h0[(uint32_t)(row * a.dv + col)] : 0.0f;
+        st[m][r] = moves ? (row == col ? 1.0f : 0.0f) : from && row < a.dk && col < a.dv ? from[(uint32_t)(row * ld + col)] : 0.0f;
       }
   }
 
@@ -65,7 +83,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
     for (int t = 0; t < 4; ++t) rk[t] = buf_load8<IO, WHOLE>(kr, 4 * kg * krow, t * here(krow), 8 * kc, a.dk);
     rs = *reinterpret_cast<const float4*>(vec + kVecS * kC + 4 * kg);
-    if constexpr (!STATES) {
+    if constexpr (OUT) {
       const __amdgpu_buffer_rsrc_t qr = chunk_rows<IO>(q + first * a.qs[1], a.qs[1], valid, a.dk);
 #pragma unroll
       for (int r = 0; r < kRuns; ++r) rq[r] = buf_load8<IO, WHOLE>(qr, qtok * qrow, 0, 8 * (qsub + 4 * r), a.dk);
@@ -79,7 +97,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     const char* tri = static_cast<const char*>(a.tri) + at * (2 * kTriBytes);
 #pragma unroll
     for (int i = 0; i < 3; ++i) load_to_lds(tri + 4096 * i + off, s_t + 4096 * i + wave * 1024);
-    if constexpr (!STATES) {
+    if constexpr (OUT) {
       const char* p = static_cast<const char*>(a.p) + at * kP;
 #pragma unroll
       for (int i = 0; i < (kP + 4095) / 4096; ++i)
@@ -99,12 +117,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int s = 0; s < 2; ++s)
-        rvv[i][s] = buf_load8<IO, WHOLE>(vr, (32 * i + (lane & 31)) * vrow, 0, col0 + 16 * (lane >> 5) + 8 * s, a.dv);
+        rvv[i][s] = buf_load8<IO, WHOLE>(vr, (32 * i + (lane & 31)) * vrow, 0, col0 + 16 * (lane >> 5) + 8 * s, ncols);
   };
 
-  fetch(0);
-  fetch_lds(0);
-  for (int64_t chunk = 0; chunk < a.chunks; ++chunk) {
+  fetch(begin);
+  fetch_lds(begin);
+  for (int64_t chunk = begin; chunk < stop; ++chunk) {
     const int64_t first = chunk * kC;
     const int valid = (int)min(a.seqlen - first, (int64_t)kC);
     const int tid = anew(threadIdx.x), lane = tid & 63, half = lane >> 5, low = lane & 31;
@@ -125,7 +143,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
         store_operand_turned<IO>(s_kt, s_kt + (NP - 1) * kTurned, kg, kc, x, s);
       }
     }
-    if constexpr (!STATES) {
+    if constexpr (OUT) {
       const int qtok = tid >> 2, qsub = tid & 3;
 #pragma unroll
       for (int r = 0; r < kRuns; ++r) {
@@ -175,7 +193,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 32 * i + tile_row(r, lane);
-        R[i][r] = s_vec[kVecF1][row] * V[r] - s_vec[kVecF2][row] * (back * R[i][r]);
+        R[i][r] = s_vec[kVecF1][row] * V[r] - back * (s_vec[kVecF2][row] * R[i][r]);
       }
     }
     const Scale cr = scale_of(wave_max(max_of(R[1], max_of(R[0], 0.0f))), 100);
@@ -189,7 +207,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
         U[i] = mm<2, 2>(operand<2>(s_t + ((i + (s >> 1)) * 2 + (s & 1)) * 1024, lane, kTriBytes), rp, U[i]);
       step_end();
     }
-    if (chunk + 1 < a.chunks) fetch(chunk + 1);
+    if (chunk + 1 < stop) fetch(chunk + 1);
     const float mU = wave_max(max_of(U[1], max_of(U[0], 0.0f)));
     if constexpr (STATES) {
       const Scale cu = scale_of(mU, 20);
@@ -202,7 +220,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
         }
         if (lane == 0) a.maxima[kMaxU * a.max_apart + (bh * a.chunks + chunk) * (a.ldv / 32) + col0 / 32] = mU * pow2(-er);
       }
-    } else {
+    } else if constexpr (OUT) {
       O[0] = O[1] = zero16();
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
@@ -236,7 +254,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
       }
     }
     __syncthreads();                                       // T and P have been read
-    if (chunk + 1 < a.chunks) fetch_lds(chunk + 1);
+    if (chunk + 1 < stop) fetch_lds(chunk + 1);
     float mE = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -263,8 +281,25 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     ce = -(er + ue.e);
   }
   const int lane = anew(threadIdx.x & 63), col = col0 + (lane & 31);
-  if (a.h_final && col < a.dv) {
-    const float f = pow2(ce);
+  float f = pow2(ce);
+  if constexpr (ENDS) {
+    if (moves) {                                           // largest value to [1, 2)
+      float m = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) m = max_of(st[t], m);
+      const int e = exponent(wave_max(m));
+      f = pow2(-e);
+      if (lane == 0) a.moves_e[(bh * a.segments + seg) * 4 + wave] = ce + e;
+    }
+    const int64_t ld = moves ? KP : a.ldv;
+    float* to = (moves ? a.moves : a.ends) + (bh * a.segments + seg) * KP * ld;
+    if (col < ld) {
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) to[(uint32_t)((32 * m + tile_row(r, lane)) * ld + col)] = st[m][r] * f;
+    }
+  } else if (a.h_final && seg == a.segments - 1 && col < a.dv) {
     float* hf = a.h_final + bh * a.dk * a.dv;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
@@ -276,19 +311,85 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   }
 }
 
-template <typename IO>
-hipError_t launch(const GdrArgs& a, bool states, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.hv), (unsigned)((a.dv + kCols - 1) / kCols));
+// The segments' ends in turn, end <- move * (the end before it) + end, from the second on: a workgroup has 16 columns of a head, a
+// wave 16 rows of every product, in fp32.  The next segment's values are on their way meanwhile.
+template <int KP>
+__global__ __launch_bounds__(KP * 4) void gdr_join_ends_kernel(GdrArgs a) {
+  constexpr int kPitch = 20;
+  __shared__ alignas(16) float s_end[2][KP][kPitch];       // columns as rows would be read: [inner][column]
+  const int lane = threadIdx.x & 63, n = lane & 15, g4 = 4 * (lane >> 4), i0 = 16 * (threadIdx.x >> 6);
+  const int64_t col = 16 * (int64_t)blockIdx.y + n;
+  float* ends = a.ends + (int64_t)blockIdx.x * a.segments * KP * a.ldv + (i0 + g4) * a.ldv + col;
+  const float* moves = a.moves + (int64_t)blockIdx.x * a.segments * KP * KP + (i0 + n) * KP + g4;
+  const int32_t* moves_e = a.moves_e + (int64_t)blockIdx.x * a.segments * 4;
+  f4 m[KP / 16], end, acc;
+  int e[KP / 32];
+  auto fetch = [&](int64_t seg) {
+#pragma unroll
+    for (int s = 0; s < KP / 16; ++s) m[s] = *reinterpret_cast<const f4*>(moves + seg * KP * KP + 16 * s);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) end[r] = ends[seg * KP * a.ldv + r * a.ldv];
+#pragma unroll
+    for (int t = 0; t < KP / 32; ++t) e[t] = moves_e[seg * 4 + t];
+  };
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc[r] = ends[r * a.ldv];
+  fetch(1);
+  for (int64_t seg = 1; seg < a.segments - 1; ++seg) {
+    float(&s)[KP][kPitch] = s_end[seg & 1];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[i0 + g4 + r][n] = acc[r];
+    __syncthreads();                                       // the other buffer is written a barrier after its last use
+    acc = end;
+    f4 now[KP / 16];
+    int now_e[KP / 32];
+#pragma unroll
+    for (int t = 0; t < KP / 16; ++t) now[t] = m[t];
+#pragma unroll
+    for (int t = 0; t < KP / 32; ++t) now_e[t] = e[t];
+    if (seg + 1 < a.segments - 1) fetch(seg + 1);
+#pragma unroll
+    for (int t = 0; t < KP / 16; ++t) {
+      f4 y;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = ldexpf(s[16 * t + g4 + r][n], now_e[t >> 1]);
+      acc = mm16(now[t], y, acc);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) ends[seg * KP * a.ldv + r * a.ldv] = acc[r];
+  }
+}
+
+template <typename IO, Of OF>
+hipError_t launch(const GdrArgs& a, hipStream_t s) {
+  const int blocks = (a.dv + kCols - 1) / kCols + (OF == Of::kEnds ? (a.dk + kCols - 1) / kCols : 0);
+  const dim3 grid((unsigned)(a.batch * a.hv * a.segments), (unsigned)blocks);
   return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
-    if (states) gdr_chunk_kernel<IO, decltype(kp)::value, decltype(whole)::value, true><<<grid, kThreads, 0, s>>>(a);
-    else gdr_chunk_kernel<IO, decltype(kp)::value, decltype(whole)::value, false><<<grid, kThreads, 0, s>>>(a);
+    gdr_chunk_kernel<IO, decltype(kp)::value, decltype(whole)::value, OF><<<grid, kThreads, 0, s>>>(a);
   });
+}
+
+template <Of OF>
+hipError_t launch(const GdrArgs& a, hipStream_t s) {
+  return a.io == kIoBf16 ? launch<BF16, OF>(a, s) : launch<F32, OF>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s) {
-  return a.io == kIoBf16 ? launch<BF16>(a, states, s) : launch<F32>(a, states, s);
+  return states ? launch<Of::kStates>(a, s) : launch<Of::kOut>(a, s);
 }
+
+hipError_t launch_gdr_segments(const GdrArgs& a, hipStream_t s) {
+  if (a.segments == 1) return hipSuccess;
+  const hipError_t e = launch<Of::kEnds>(a, s);
+  if (e != hipSuccess || a.segments == 2) return e;
+  const dim3 grid((unsigned)(a.batch * a.hv), (unsigned)(a.ldv / 16));
+  return by_keys(a.dk, true, [&](auto kp, auto) {
+    gdr_join_ends_kernel<decltype(kp)::value><<<grid, decltype(kp)::value * 4, 0, s>>>(a);
+  });
+}
+
+int gdr_chunk_room(int io, int dk) { return 256 * per_cu(io == kIoBf16, dk); }
 
 }  // namespace ssscan

@@ -27,6 +27,7 @@ constexpr int kC = kGdrChunk;            // tokens of a chunk: two tiles
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float acc16 __attribute__((ext_vector_type(16)));
 
 // An operand block in LDS is 64 x 16 bytes; blocks are 32 bytes further apart than that, so that a row's blocks start in
@@ -46,6 +47,14 @@ __device__ __forceinline__ acc16 mm(const Planes& a, const Planes& b, acc16 acc)
   if constexpr (NB == 2) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.hi, b.lo, acc, 0, 0, 0);
   if constexpr (NA == 2) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.lo, b.hi, acc, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a.hi, b.hi, acc, 0, 0, 0);
+}
+
+// 16 inner elements of a 16x16 product in fp32: lane l holds row (column) l & 15, inner elements 4 (l >> 4) + 0..3.  The result's
+// lane has column l & 15 and rows 4 (l >> 4) + 0..3, so that it is the right operand of the next product as it is.
+__device__ __forceinline__ f4 mm16(f4 x, f4 y, f4 acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], acc, 0, 0, 0);
+  return acc;
 }
 
 // Values 8 half .. 8 half + 7 of a result tile as an operand of N planes, scaled.

@@ -56,16 +56,6 @@ __device__ __forceinline__ double last_of(double v) {
   return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), kC - 1), __builtin_amdgcn_readlane(__double2loint(v), kC - 1));
 }
 
-typedef float f4 __attribute__((ext_vector_type(4)));
-
-// 16 inner elements of a 16x16 product in fp32: lane l holds row (column) l & 15, inner elements 4 (l >> 4) + 0..3.  The result's
-// lane has column l & 15 and rows 4 (l >> 4) + 0..3, so that it is the right operand of the next product as it is.
-__device__ __forceinline__ f4 mm16(f4 x, f4 y, f4 acc) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], acc, 0, 0, 0);
-  return acc;
-}
-
 template <typename IO, int KP, bool WHOLE, bool BWD>
 __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
   using T = typename IO::T;

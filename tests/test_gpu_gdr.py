@@ -75,6 +75,34 @@ def test_forward(ss, size):
     check_fwd(ss, problem(*size))
 
 
+@pytest.mark.parametrize("size", [(1, 384, 1, 1, 16, 16, F), (1, 385, 2, 2, 128, 128, BF), (2, 700, 1, 3, 72, 40, BF), (1, 1000, 1, 2, 33, 200, F),
+                                  (1, 650, 2, 2, 96, 130, F), (1, 1500, 1, 1, 128, 257, BF), (3, 515, 2, 4, 1, 5, F)], ids=str)
+@pytest.mark.parametrize("h0", [True, False])
+def test_rows_in_segments(ss, size, h0):
+    """Few heads, so that the GPU takes parts of a row at the same time."""
+    check_fwd(ss, problem(*size, h0=h0))
+
+
+def test_decays_over_segments(ss):
+    """No token writes and every one decays: what a segment leaves of a large state is far below 2^-126 of it, and the state is not."""
+    p = problem(1, 1024, 1, 2, 64, 64, F)
+    p["beta"].zero_()
+    p["g"].fill_(-1.0 / 6)                                 # e^-170, 2^-246, over the row
+    p["h0"] = p["h0"].sign() * 2.0 ** 125
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+    decay = torch.exp(p["g"].double().cpu().cumsum(1))
+    hw = up(p["h0"]) * decay[:, -1][..., None, None]
+    # a forward in one goes from h0 and the sum of decays in 64 bits; one in parts rounds each part's once
+    assert rel(h, hw) <= F32_REL
+    ow = torch.einsum("blk,bhkv->blhv", up(p["q"])[:, :, 0], up(p["h0"])) * decay[..., None] * 64 ** -0.5
+    assert rel(o[:, 512:], ow[:, 512:]) <= F32_REL
+    p["g"] = -p["g"]                                       # and growth from as small a state
+    p["h0"] = p["h0"].sign() * 2.0 ** -125
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["h0"])
+    decay = torch.exp(p["g"].double().cpu().cumsum(1))
+    assert rel(h, up(p["h0"]) * decay[:, -1][..., None, None]) <= F32_REL
+
+
 @pytest.mark.parametrize("size", SIZES, ids=str)
 def test_backward(ss, size):
     check_bwd(ss, problem(*size))
