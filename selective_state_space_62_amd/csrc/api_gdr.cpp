@@ -130,7 +130,8 @@ struct Segments {
 // Segments of at least two chunks, as many as fill the GPU.  Made in segments a row costs about 1.7 times as much, the factors
 // and the states first, so two of them gain nothing.  In one and in segments, us: 16 heads of 131072 tokens 15742, 2341; 12 x 8 heads
 // (fp32, keys of 64) of 2048 335, 271; 40 heads of 4096 496, 247; 8 heads of 500 67, 53; 2 heads of 1000 91, 43; 4 x 40 heads of
-// 2048 318, 320; 8 x 40 heads of 2048, which fill it, 509 and, in three, 614.
+// 2048 318, 320; 8 x 40 heads of 2048, which fill it, 509 and, in three, 614.  Backward: 16 heads of 32768 10455, 2130; 3 x 10 heads
+// (fp32, 72 by 80) of 1111 471, 263; 2 heads of 1000 236, 101; 4 x 40 heads of 2048 1283, 1255.
 Segments segments_of(int64_t batch, int64_t chunks, int heads_v, int dim_k, int dim_v, int io) {
   const int64_t groups = batch * heads_v * ((dim_v + 127) / 128);
   const int64_t n = std::min(gdr_chunk_room(io, dim_k) / groups, chunks / 2);
@@ -139,51 +140,72 @@ Segments segments_of(int64_t batch, int64_t chunks, int heads_v, int dim_k, int 
   return {(chunks + per - 1) / per, per};
 }
 
-// Scratch of the chunked forward: the inverses, P, then the vectors.  P is taken as large as either I/O type needs it.
+// Scratch of the segments, behind what a direction has besides.
+struct SegmentsLayout {
+  size_t ends, moves, moves_e, total;
+};
+
+SegmentsLayout segments_layout(size_t from, int64_t batch, int64_t seqlen, int heads_v, int dim_k, int dim_v) {
+  const int64_t chunks = chunks_of(seqlen), rows = (dim_k + 31) / 32 * 32, cols = ((int64_t)dim_v + 31) / 32 * 32;
+  const int64_t most = std::max(segments_of(batch, chunks, heads_v, dim_k, dim_v, kIoBf16).count,
+                                segments_of(batch, chunks, heads_v, dim_k, dim_v, kIoF32).count);
+  const int64_t n = most > 1 ? batch * heads_v * most : 0;
+  SegmentsLayout l;
+  l.ends = from;
+  l.moves = l.ends + round256((size_t)(n * rows * cols) * 4);
+  l.moves_e = l.moves + round256((size_t)(n * rows * rows) * 4);
+  l.total = l.moves_e + round256((size_t)(n * 4) * 4);
+  return l;
+}
+
+void set_segments(GdrArgs& a, const SegmentsLayout& l, char* ws) {
+  const Segments seg = segments_of(a.batch, a.chunks, a.hv, a.dk, a.dv, a.io);
+  a.segments = seg.count;
+  a.per = seg.per;
+  a.ldv = ((int64_t)a.dv + 31) / 32 * 32;
+  a.ends = reinterpret_cast<float*>(ws + l.ends);
+  a.moves = reinterpret_cast<float*>(ws + l.moves);
+  a.moves_e = reinterpret_cast<int32_t*>(ws + l.moves_e);
+}
+
+// Scratch of the chunked forward: the inverses, P, the vectors, then the segments'.  Each is taken as large as either I/O type needs it.
 struct FwdLayout {
-  size_t p, vecs, ends, moves, moves_e, total;
-  int64_t ldv;
+  size_t p, vecs;
+  SegmentsLayout segments;
 };
 
 FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v, int dim_k, int dim_v) {
-  const int64_t chunks = chunks_of(seqlen), n = batch * heads_v * chunks, rows = (dim_k + 31) / 32 * 32;
-  const int64_t segments = std::max(segments_of(batch, chunks, heads_v, dim_k, dim_v, kIoBf16).count,
-                                    segments_of(batch, chunks, heads_v, dim_k, dim_v, kIoF32).count);
-  const int64_t ends = segments > 1 ? batch * heads_v * segments * rows : 0;
+  const int64_t n = batch * heads_v * chunks_of(seqlen);
   FwdLayout l;
-  l.ldv = (int64_t)(dim_v + 31) / 32 * 32;
   l.p = round256(gdr_tri_bytes(n));
   l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, false));
-  l.ends = l.vecs + round256(gdr_vecs_bytes(n));
-  l.moves = l.ends + round256((size_t)(ends * l.ldv) * 4);
-  l.moves_e = l.moves + round256((size_t)(ends * rows) * 4);
-  l.total = l.moves_e + round256((size_t)(segments > 1 ? batch * heads_v * segments * 4 : 0) * 4);
+  l.segments = segments_layout(l.vecs + round256(gdr_vecs_bytes(n)), batch, seqlen, heads_v, dim_k, dim_v);
   return l;
 }
 
 // Scratch of the backward: the preparation's, then for every chunk of a head the state before it and the gradient of the one
 // behind it, U and the gradient of R, the largest values of their tiles, and dq and dk of value heads that share keys.
 struct BwdLayout {
-  size_t tri_t, p, vecs, states, dstates, u, dr, maxima, part_q, part_k, total;
-  int64_t ldv, max_apart;
+  size_t tri_t, p, vecs, states, dstates, u, dr, maxima, part_q, part_k;
+  SegmentsLayout segments;
+  int64_t max_apart;
 };
 
 BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
-  const int64_t n = batch * heads_v * chunks_of(seqlen), rows = (dim_k + 31) / 32 * 32;
+  const int64_t n = batch * heads_v * chunks_of(seqlen), rows = (dim_k + 31) / 32 * 32, ldv = ((int64_t)dim_v + 31) / 32 * 32;
   BwdLayout l;
-  l.ldv = (int64_t)(dim_v + 31) / 32 * 32;
-  l.max_apart = n * (l.ldv / 32);
+  l.max_apart = n * (ldv / 32);
   l.tri_t = round256(gdr_tri_bytes(n));
   l.p = l.tri_t + round256(gdr_tri_bytes(n));
   l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, true));
   l.states = l.vecs + round256(gdr_vecs_bytes(n));
-  l.dstates = l.states + round256((size_t)(n * rows * l.ldv) * 4);
-  l.u = l.dstates + round256((size_t)(n * rows * l.ldv) * 4);
-  l.dr = l.u + round256((size_t)(n * kGdrChunk * l.ldv) * 4);
-  l.maxima = l.dr + round256((size_t)(n * kGdrChunk * l.ldv) * 4);
+  l.dstates = l.states + round256((size_t)(n * rows * ldv) * 4);
+  l.u = l.dstates + round256((size_t)(n * rows * ldv) * 4);
+  l.dr = l.u + round256((size_t)(n * kGdrChunk * ldv) * 4);
+  l.maxima = l.dr + round256((size_t)(n * kGdrChunk * ldv) * 4);
   l.part_q = l.maxima + round256((size_t)(kMaxKinds * l.max_apart) * 4);
   l.part_k = l.part_q + (heads_v > heads_k ? round256((size_t)(n * kGdrChunk * rows) * 4) : 0);
-  l.total = l.part_k + (l.part_k - l.part_q);
+  l.segments = segments_layout(l.part_k + (l.part_k - l.part_q), batch, seqlen, heads_v, dim_k, dim_v);
   return l;
 }
 
@@ -193,7 +215,7 @@ extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
   if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen <= kRecurTokens) return 0;
-  return fwd_layout(batch, seqlen, heads_v, dim_k, dim_v).total;
+  return fwd_layout(batch, seqlen, heads_v, dim_k, dim_v).segments.total;
 }
 
 ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
@@ -234,15 +256,8 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     a.tri = ws;
     a.p = ws + l.p;
     a.vecs = reinterpret_cast<float*>(ws + l.vecs);
-    const Segments seg = segments_of(batch, a.chunks, heads_v, dim_k, dim_v, a.io);
-    a.segments = seg.count;
-    a.per = seg.per;
-    a.ldv = l.ldv;
-    a.ends = reinterpret_cast<float*>(ws + l.ends);
-    a.moves = reinterpret_cast<float*>(ws + l.moves);
-    a.moves_e = reinterpret_cast<int32_t*>(ws + l.moves_e);
+    set_segments(a, l.segments, ws);
     e = launch_gdr_prep(a, false, s);
-    if (e == hipSuccess) e = launch_gdr_segments(a, s);
     if (e == hipSuccess) e = launch_gdr_chunk(a, false, s);
   }
   return e == hipSuccess ? SS_OK : record_hip_error(e, "gated delta rule launch");
@@ -250,7 +265,7 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
 
 size_t ss_gdr_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
   if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen == 0) return 0;
-  return bwd_layout(batch, seqlen, heads_k, heads_v, dim_k, dim_v).total;
+  return bwd_layout(batch, seqlen, heads_k, heads_v, dim_k, dim_v).segments.total;
 }
 
 ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v, ss_dtype io,
@@ -298,9 +313,7 @@ ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   a.tri_t = ws + l.tri_t;
   a.p = ws + l.p;
   a.vecs = reinterpret_cast<float*>(ws + l.vecs);
-  a.segments = 1;
-  a.per = a.chunks;
-  a.ldv = l.ldv;
+  set_segments(a, l.segments, ws);
   a.states = reinterpret_cast<float*>(ws + l.states);
   a.dstates = reinterpret_cast<float*>(ws + l.dstates);
   a.u = reinterpret_cast<float*>(ws + l.u);

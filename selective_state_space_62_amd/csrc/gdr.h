@@ -31,7 +31,7 @@ struct GdrArgs {
   // segments that a row's chunks go in, `per` chunks each but the last: with more than one, the state's change over each of them
   // but the last comes first, as a product with the state before it and a sum
   int64_t segments, per;
-  float* ends;           // the state behind a segment, dk rounded up to tiles of 32 by ldv
+  float* ends;           // the state behind a segment, then the gradient of the one before it; dk rounded up to tiles of 32 by ldv
   float* moves;          // the factor, dk by dk rounded up to tiles of 32 (the first segment has the state before it and needs none),
   int32_t* moves_e;      // over a power of 2 for each 32 of its columns, four of them to a segment: what decays leave may be below 2^-126
   int32_t whole;         // dk and dv are multiples of 8 and the rows of q, k and v are aligned to 4 bytes
@@ -68,8 +68,9 @@ size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward);
 size_t gdr_vecs_bytes(int64_t chunk_heads);
 hipError_t launch_gdr_prep(const GdrArgs& a, bool backward, hipStream_t s);
 hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s);
-// The states behind all segments but the last, where there is more than one.
-hipError_t launch_gdr_segments(const GdrArgs& a, hipStream_t s);
+// Of more than one segment: from what each adds to a state, or to a state's gradient, and the factors to the states behind all but
+// the last, the gradients before all but the first.
+hipError_t launch_gdr_join(const GdrArgs& a, bool backward, hipStream_t s);
 // Workgroups of a forward chunk kernel that the GPU holds at once.
 int gdr_chunk_room(int io, int dk);
 // The backward after the states: their gradients in turn, from the last chunk on, then all other gradients of all chunks.

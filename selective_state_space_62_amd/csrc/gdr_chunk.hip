@@ -311,52 +311,65 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
   }
 }
 
-// The segments' ends in turn, end <- move * (the end before it) + end, from the second on: a workgroup has 16 columns of a head, a
-// wave 16 rows of every product, in fp32.  The next segment's values are on their way meanwhile.
-template <int KP>
+// The segments' ends in turn, end <- move * (the end before it) + end from the second on, or, of gradients, with the transposed
+// factors from the last but one to the second: a workgroup has 16 columns of a head, a wave 16 rows of every product, in fp32.  The
+// next segment's values are on their way meanwhile.
+template <int KP, bool BWD>
 __global__ __launch_bounds__(KP * 4) void gdr_join_ends_kernel(GdrArgs a) {
   constexpr int kPitch = 20;
-  __shared__ alignas(16) float s_end[2][KP][kPitch];       // columns as rows would be read: [inner][column]
+  __shared__ alignas(16) float s_end[2][KP][kPitch];
   const int lane = threadIdx.x & 63, n = lane & 15, g4 = 4 * (lane >> 4), i0 = 16 * (threadIdx.x >> 6);
   const int64_t col = 16 * (int64_t)blockIdx.y + n;
   float* ends = a.ends + (int64_t)blockIdx.x * a.segments * KP * a.ldv + (i0 + g4) * a.ldv + col;
-  const float* moves = a.moves + (int64_t)blockIdx.x * a.segments * KP * KP + (i0 + n) * KP + g4;
+  const float* moves = a.moves + (int64_t)blockIdx.x * a.segments * KP * KP + (BWD ? g4 * KP + i0 + n : (i0 + n) * KP + g4);
   const int32_t* moves_e = a.moves_e + (int64_t)blockIdx.x * a.segments * 4;
   f4 m[KP / 16], end, acc;
   int e[KP / 32];
   auto fetch = [&](int64_t seg) {
 #pragma unroll
-    for (int s = 0; s < KP / 16; ++s) m[s] = *reinterpret_cast<const f4*>(moves + seg * KP * KP + 16 * s);
+    for (int t = 0; t < KP / 16; ++t) {
+      if constexpr (BWD) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[t][r] = moves[seg * KP * KP + (16 * t + r) * KP];
+      } else {
+        m[t] = *reinterpret_cast<const f4*>(moves + seg * KP * KP + 16 * t);
+      }
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) end[r] = ends[seg * KP * a.ldv + r * a.ldv];
 #pragma unroll
-    for (int t = 0; t < KP / 32; ++t) e[t] = moves_e[seg * 4 + t];
+    for (int t = 0; t < KP / 32; ++t) e[t] = moves_e[seg * 4 + (BWD ? i0 / 32 : t)];
   };
+  const int64_t step = BWD ? -1 : 1, stop = BWD ? 0 : a.segments - 1;
+  int64_t seg = BWD ? a.segments - 1 : 0;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) acc[r] = ends[r * a.ldv];
-  fetch(1);
-  for (int64_t seg = 1; seg < a.segments - 1; ++seg) {
+  for (int r = 0; r < 4; ++r) acc[r] = ends[seg * KP * a.ldv + r * a.ldv];
+  seg += step;
+  if (seg != stop) fetch(seg);
+  for (; seg != stop; seg += step) {
     float(&s)[KP][kPitch] = s_end[seg & 1];
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[i0 + g4 + r][n] = acc[r];
     __syncthreads();                                       // the other buffer is written a barrier after its last use
-    acc = end;
-    f4 now[KP / 16];
+    f4 now[KP / 16], sum = end, out = {};
     int now_e[KP / 32];
 #pragma unroll
     for (int t = 0; t < KP / 16; ++t) now[t] = m[t];
 #pragma unroll
     for (int t = 0; t < KP / 32; ++t) now_e[t] = e[t];
-    if (seg + 1 < a.segments - 1) fetch(seg + 1);
+    if (seg + step != stop) fetch(seg + step);
 #pragma unroll
     for (int t = 0; t < KP / 16; ++t) {
       f4 y;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[r] = ldexpf(s[16 * t + g4 + r][n], now_e[t >> 1]);
-      acc = mm16(now[t], y, acc);
+      for (int r = 0; r < 4; ++r) y[r] = BWD ? s[16 * t + g4 + r][n] : ldexpf(s[16 * t + g4 + r][n], now_e[t >> 1]);
+      out = mm16(now[t], y, out);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) ends[seg * KP * a.ldv + r * a.ldv] = acc[r];
+    for (int r = 0; r < 4; ++r) {
+      acc[r] = (BWD ? ldexpf(out[r], now_e[0]) : out[r]) + sum[r];
+      ends[seg * KP * a.ldv + r * a.ldv] = acc[r];
+    }
   }
 }
 
@@ -376,18 +389,22 @@ hipError_t launch(const GdrArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s) {
-  return states ? launch<Of::kStates>(a, s) : launch<Of::kOut>(a, s);
-}
-
-hipError_t launch_gdr_segments(const GdrArgs& a, hipStream_t s) {
-  if (a.segments == 1) return hipSuccess;
-  const hipError_t e = launch<Of::kEnds>(a, s);
-  if (e != hipSuccess || a.segments == 2) return e;
+hipError_t launch_gdr_join(const GdrArgs& a, bool backward, hipStream_t s) {
   const dim3 grid((unsigned)(a.batch * a.hv), (unsigned)(a.ldv / 16));
   return by_keys(a.dk, true, [&](auto kp, auto) {
-    gdr_join_ends_kernel<decltype(kp)::value><<<grid, decltype(kp)::value * 4, 0, s>>>(a);
+    constexpr int KP = decltype(kp)::value;
+    if (backward) gdr_join_ends_kernel<KP, true><<<grid, KP * 4, 0, s>>>(a);
+    else gdr_join_ends_kernel<KP, false><<<grid, KP * 4, 0, s>>>(a);
   });
+}
+
+hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s) {
+  if (a.segments > 1) {
+    hipError_t e = launch<Of::kEnds>(a, s);
+    if (e == hipSuccess) e = launch_gdr_join(a, false, s);
+    if (e != hipSuccess) return e;
+  }
+  return states ? launch<Of::kStates>(a, s) : launch<Of::kOut>(a, s);
 }
 
 int gdr_chunk_room(int io, int dk) { return 256 * per_cu(io == kIoBf16, dk); }

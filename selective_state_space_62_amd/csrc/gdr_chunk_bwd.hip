@@ -4,7 +4,7 @@
 // With dS the gradient of the state behind a chunk, D = 2^(gam_C - gam), and T, P, G as in the forward:
 //   dU = P^T dO + D K dS,  dR = T^T dU,  dV = beta dR,  dS <- G_C dS + (scale G Q)^T dO - (beta G K)^T dR.
 // It is the forward's recurrence with other operands: 32 columns to a wave, everything in registers from one product to the
-// next.  dS and dR are stored, transposed by a product with the identity, for the gradients that need no turn.
+// next; where there are few heads, in segments as well, with the forward's factors transposed.  dS and dR are stored, transposed by a product with the identity, for the gradients that need no turn.
 #include "gdr_device.h"
 
 namespace ssscan {
@@ -15,7 +15,8 @@ using namespace gdr;
 constexpr int kThreads = 256;
 constexpr int kCols = 128;               // of a workgroup
 
-template <typename IO, int KP, bool WHOLE>
+// ENDS: nothing but the gradients of the states before segments.
+template <typename IO, int KP, bool WHOLE, bool ENDS>
 __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) void gdr_chunk_bwd_kernel(GdrArgs a) {
   using T = typename IO::T;
   constexpr int NP = planes_of<IO>(), kSteps = KP / 16, kTiles = KP / 32;
@@ -24,7 +25,9 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   __shared__ alignas(16) char s_t[2 * kTriBytes], s_p[2 * kTriBytes];
   __shared__ alignas(16) float s_vecs[2][kVecs][kC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t bh = blockIdx.x;
+  const int64_t bh = blockIdx.x / a.segments, seg = blockIdx.x - bh * a.segments;
+  const int64_t begin = seg * a.per, last = min(begin + a.per, a.chunks) - 1;
+  if (ENDS && seg == 0) return;
   const int64_t b = bh / a.hv;
   const int h = (int)(bh - b * a.hv), hkey = h / (a.hv / a.hk);
   const int col0 = blockIdx.y * kCols + 32 * wave;
@@ -38,13 +41,16 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   int ce = 0;
   {
     const int lane = threadIdx.x & 63, col = col0 + (lane & 31);
-    const float* h0 = a.dh_final + bh * a.dk * a.dv;
+    const bool first = seg == a.segments - 1 || ENDS;
+    const int64_t ld = first ? a.dv : a.ldv;
+    const float* from = first ? (seg == a.segments - 1 ? a.dh_final : nullptr) : a.ends;
+    if (from) from += first ? bh * a.dk * a.dv : (bh * a.segments + seg + 1) * KP * a.ldv;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 32 * m + tile_row(r, lane);
-        st[m][r] = a.dh_final && row < a.dk && col < a.dv ? h0[(uint32_t)(row * a.dv + col)] : 0.0f;
+        st[m][r] = from && row < a.dk && col < a.dv ? from[(uint32_t)(row * ld + col)] : 0.0f;
       }
   }
 
@@ -91,14 +97,14 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
         ro[i][s] = buf_load8<IO, WHOLE>(rows, (32 * i + (lane & 31)) * orow, 0, col0 + 16 * (lane >> 5) + 8 * s, a.dv);
   };
 
-  fetch(a.chunks - 1);
-  fetch_lds(a.chunks - 1);
-  for (int64_t chunk = a.chunks - 1; chunk >= 0; --chunk) {
+  fetch(last);
+  fetch_lds(last);
+  for (int64_t chunk = last; chunk >= begin; --chunk) {
     const int64_t first = chunk * kC, at = bh * a.chunks + chunk;
     const int valid = (int)min(a.seqlen - first, (int64_t)kC);
     const int tid = anew(threadIdx.x), lane = tid & 63, half = lane >> 5, low = lane & 31;
     const float(&s_vec)[kVecs][kC] = s_vecs[chunk & 1];
-    const bool stores = col0 < a.ldv;
+    const bool stores = !ENDS && col0 < a.ldv;
     float* const maxima = a.maxima + at * (a.ldv / 32) + col0 / 32;
     fetch_o(chunk);
     __syncthreads();
@@ -144,8 +150,10 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
           for (int i = 0; i < 2; ++i)
             X[i] = mm<NP, 2>(operand<NP>(s_k + (i * kSteps + 2 * m + s) * kBlock, lane, kSide), sp[s], X[i]);
         }
-        const acc16 t = transposed(sp[0], sp[1], lane);
-        if (stores) store_blocks(out, m, col0, a.ldv, lane, t, back);
+        if constexpr (!ENDS) {
+          const acc16 t = transposed(sp[0], sp[1], lane);
+          if (stores) store_blocks(out, m, col0, a.ldv, lane, t, back);
+        }
         step_end();
       }
       if (stores && lane == 0) maxima[kMaxDs * a.max_apart] = mS * pow2(ce);
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
         for (int r = 0; r < 16; ++r) W[j][r] = fmaf(W[j][r], f, s_vec[kVecEnd][32 * j + tile_row(r, lane)] * (back * X[j][r]));
     }
-    if (chunk > 0) fetch(chunk - 1);
+    if (chunk > begin) fetch(chunk - 1);
     // dR = T^T dU, in units of the inverse's columns
     const Scale cu = scale_of(wave_max(max_of(W[1], max_of(W[0], 0.0f))), 100);
     X[0] = X[1] = zero16();
@@ -216,7 +224,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
       }
     }
     __syncthreads();                                       // T and P have been read
-    if (chunk > 0) fetch_lds(chunk - 1);
+    if (chunk > begin) fetch_lds(chunk - 1);
     float mE = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -249,8 +257,16 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
     ce = -ue.e;
   }
   const int lane = anew(threadIdx.x & 63), col = col0 + (lane & 31);
-  if (a.dh0 && col < a.dv) {
-    const float f = pow2(ce);
+  const float f = pow2(ce);
+  if constexpr (ENDS) {
+    float* to = a.ends + (bh * a.segments + seg) * KP * a.ldv;
+    if (col < a.ldv) {
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) to[(uint32_t)((32 * m + tile_row(r, lane)) * a.ldv + col)] = st[m][r] * f;
+    }
+  } else if (a.dh0 && seg == 0 && col < a.dv) {
     float* d = a.dh0 + bh * a.dk * a.dv;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
@@ -262,16 +278,28 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   }
 }
 
-template <typename IO>
+template <typename IO, bool ENDS>
 hipError_t launch(const GdrArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.batch * a.hv), (unsigned)((a.dv + kCols - 1) / kCols));
+  const dim3 grid((unsigned)(a.batch * a.hv * a.segments), (unsigned)((a.dv + kCols - 1) / kCols));
   return by_keys(a.dk, a.whole, [&](auto kp, auto whole) {
-    gdr_chunk_bwd_kernel<IO, decltype(kp)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>(a);
+    gdr_chunk_bwd_kernel<IO, decltype(kp)::value, decltype(whole)::value, ENDS><<<grid, kThreads, 0, s>>>(a);
   });
+}
+
+template <bool ENDS>
+hipError_t launch(const GdrArgs& a, hipStream_t s) {
+  return a.io == kIoBf16 ? launch<BF16, ENDS>(a, s) : launch<F32, ENDS>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_gdr_chunk_bwd(const GdrArgs& a, hipStream_t s) { return a.io == kIoBf16 ? launch<BF16>(a, s) : launch<F32>(a, s); }
+hipError_t launch_gdr_chunk_bwd(const GdrArgs& a, hipStream_t s) {
+  if (a.segments > 1) {
+    hipError_t e = launch<true>(a, s);
+    if (e == hipSuccess) e = launch_gdr_join(a, true, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch<false>(a, s);
+}
 
 }  // namespace ssscan

@@ -75,12 +75,23 @@ def test_forward(ss, size):
     check_fwd(ss, problem(*size))
 
 
-@pytest.mark.parametrize("size", [(1, 384, 1, 1, 16, 16, F), (1, 385, 2, 2, 128, 128, BF), (2, 700, 1, 3, 72, 40, BF), (1, 1000, 1, 2, 33, 200, F),
-                                  (1, 650, 2, 2, 96, 130, F), (1, 1500, 1, 1, 128, 257, BF), (3, 515, 2, 4, 1, 5, F)], ids=str)
+IN_SEGMENTS = [
+    (1, 384, 1, 1, 16, 16, F), (1, 385, 2, 2, 128, 128, BF), (2, 700, 1, 3, 72, 40, BF), (1, 1000, 1, 2, 33, 200, F), (1, 650, 2, 2, 96, 130, F),
+    (1, 1500, 1, 1, 128, 257, BF), (3, 515, 2, 4, 1, 5, F),
+]
+
+
+@pytest.mark.parametrize("size", IN_SEGMENTS, ids=str)
 @pytest.mark.parametrize("h0", [True, False])
 def test_rows_in_segments(ss, size, h0):
     """Few heads, so that the GPU takes parts of a row at the same time."""
     check_fwd(ss, problem(*size, h0=h0))
+
+
+@pytest.mark.parametrize("size", IN_SEGMENTS, ids=str)
+@pytest.mark.parametrize("h0", [True, False])
+def test_gradients_of_rows_in_segments(ss, size, h0):
+    check_bwd(ss, problem(*size, h0=h0), dh=h0)
 
 
 def test_decays_over_segments(ss):
