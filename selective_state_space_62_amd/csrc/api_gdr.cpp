@@ -108,7 +108,8 @@ constexpr int64_t kRecurTokens = 16;
 constexpr int64_t kMostStride = int64_t(1) << 22;
 
 bool far_apart(const Inputs& in) {
-  return in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride;
+  return in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride ||
+         (int64_t)in.heads_v * in.dim_v >= kMostStride;
 }
 
 bool aligned_rows(const void* p, const int64_t* st, ss_dtype io) {
@@ -286,7 +287,7 @@ ss_status ss_gdr_bwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   const struct { const char* name; const float* p; } vecs[] = {{"dh_final", dh_final}, {"dg", dg}, {"dbeta", dbeta}, {"dh0", dh0}};
   for (const auto& n : vecs)
     if (!aligned(n.p, 4)) return record_error(SS_ERR_INVALID_ARG, "%s is not 4-byte aligned", n.name);
-  if (far_apart(in) || (int64_t)heads_v * dim_v >= kMostStride)
+  if (far_apart(in))
     return record_error(SS_ERR_UNSUPPORTED, "tokens 2^22 values and more apart are not supported here");
   const size_t need = ss_gdr_bwd_workspace_bytes(batch, seqlen, heads_k, heads_v, dim_k, dim_v);
   if ((st = check_scratch(workspace, workspace_bytes, need)) != SS_OK) return st;

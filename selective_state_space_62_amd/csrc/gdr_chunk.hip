@@ -52,6 +52,9 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
   const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + hkey * a.ks[2];
   const T* v = static_cast<const T*>(a.v) + b * a.vs[0] + h * a.vs[2];
 
+  const int64_t ostride = (int64_t)a.hv * a.dv;
+  T* o = static_cast<T*>(a.o) + b * a.seqlen * ostride + (int64_t)h * a.dv;
+
   acc16 st[kTiles];                      // the state is st 2^ce
   int ce = 0;
   {
@@ -71,6 +74,7 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
 
   // What this thread brings of a chunk: 4 tokens by 8 values of k, a quarter of a token's runs of q.
   const uint32_t krow = (uint32_t)a.ks[1] * sizeof(T), qrow = (uint32_t)a.qs[1] * sizeof(T), vrow = (uint32_t)a.vs[1] * sizeof(T);
+  const uint32_t orow = (uint32_t)ostride * sizeof(T);
   Raw8<IO> rk[4], rq[kRuns];
   float4 rs;
   float rz;
@@ -245,12 +249,11 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
         step_end();
       }
       // O, transposed: a lane has a token and runs of four columns
+      const __amdgpu_buffer_rsrc_t rows = chunk_rows<IO>(o + first * ostride, ostride, valid, a.dv);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tok = 32 * i + low;
-        if (tok < valid)
-          store_runs<IO>(static_cast<T*>(a.o) + ((b * a.seqlen + first + tok) * a.hv + h) * a.dv, col0 + 4 * half, a.dv, O[i],
-                         s_vec[kVecOut][tok] * pow2(-(er + cu.e)));
+        store_runs<IO, WHOLE>(rows, tok * orow, col0 + 4 * half, a.dv, O[i], s_vec[kVecOut][tok] * pow2(-(er + cu.e)));
       }
     }
     __syncthreads();                                       // T and P have been read

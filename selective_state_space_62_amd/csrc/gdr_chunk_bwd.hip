@@ -37,6 +37,8 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
   const int64_t ostride = (int64_t)a.hv * a.dv;
   const T* dout = static_cast<const T*>(a.dout) + b * a.seqlen * ostride + (int64_t)h * a.dv;
 
+  T* dv = static_cast<T*>(a.dv_out) + b * a.seqlen * ostride + (int64_t)h * a.dv;
+
   acc16 st[kTiles];                      // the gradient is st 2^ce
   int ce = 0;
   {
@@ -210,15 +212,14 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
       const Scale c = scale_of(m, 100);
       if (stores) {
         float* out = a.dr + at * kC * a.ldv;
+        const __amdgpu_buffer_rsrc_t rows = chunk_rows<IO>(dv + first * ostride, ostride, valid, a.dv);
         const float f = pow2(-c.e);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int tok = 32 * i + low;
           const acc16 t = transposed(split(y[i], 0, c.f), split(y[i], 1, c.f), lane);
           store_blocks(out, i, col0, a.ldv, lane, t, f);
-          if (tok < valid)
-            store_runs<IO>(static_cast<T*>(a.dv_out) + ((b * a.seqlen + first + tok) * a.hv + h) * a.dv, col0 + 4 * half, a.dv, t,
-                           s_vec[kVecF1][tok] / s_vec[kVecC][tok] * f);
+          store_runs<IO, WHOLE>(rows, tok * orow, col0 + 4 * half, a.dv, t, s_vec[kVecF1][tok] / s_vec[kVecC][tok] * f);
         }
         if (lane == 0) maxima[kMaxDr * a.max_apart] = m;
       }

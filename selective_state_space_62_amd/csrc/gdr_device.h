@@ -351,13 +351,44 @@ __device__ __forceinline__ void store_blocks(float* rows, int tile, int col0, in
     *reinterpret_cast<float4*>(p + 256 * g) = make_float4(v[4 * g] * f, v[4 * g + 1] * f, v[4 * g + 2] * f, v[4 * g + 3] * f);
 }
 
-// Runs of four of such a lane's columns at `at`, times f, to a row of n in the I/O type.
-template <typename IO>
-__device__ __forceinline__ void store_runs(typename IO::T* row, int at, int n, const acc16& v, float f) {
+// Runs of four of such a lane's columns at `at`, times f, to the row of n at byte offset voff in the I/O type; what lies behind the
+// buffer is not written.  WHOLE: n is a multiple of 8 and the tensor is 16-byte aligned.
+template <typename IO, bool WHOLE>
+__device__ __forceinline__ void store_runs(__amdgpu_buffer_rsrc_t rows, uint32_t voff, int at, int n, const acc16& v, float f) {
+  constexpr int kSize = sizeof(typename IO::T);
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const int c = at + 8 * g;
     const float x[4] = {v[4 * g] * f, v[4 * g + 1] * f, v[4 * g + 2] * f, v[4 * g + 3] * f};
+    if constexpr (WHOLE) {
+      const uint32_t off = c < n ? voff + c * kSize : kNowhere;
+      if constexpr (kSize == 4) {
+        const u4 w = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+        __builtin_amdgcn_raw_buffer_store_b128(w, rows, off, 0, 0);
+      } else {
+        const u2 w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(w, rows, off, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t off = c + j < n ? voff + (c + j) * kSize : kNowhere;
+        if constexpr (kSize == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[j]), rows, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16x2(x[j], x[j]), rows, off, 0, 0);
+      }
+    }
+  }
+}
+
+// The same, times 1, by address and without knowing n.
+template <typename IO>
+__device__ __forceinline__ void store_runs(typename IO::T* row, int at, int n, const acc16& v) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int c = at + 8 * g;
+    const float x[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
     if (n % 4 == 0) {                                      // the tensor is 16-byte aligned: runs of four are too
       if (c < n) {
         if constexpr (IO::kPerSpan == 4) *reinterpret_cast<float4*>(row + c) = make_float4(x[0], x[1], x[2], x[3]);

@@ -274,9 +274,9 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     }
     if (tok < valid) {
       if (a.hv > a.hk) {
-        store_runs<F32>(a.part_q + (at * kC + tok) * KP + 32 * m + 4 * half, 0, 32, Q, 1.0f);
+        store_runs<F32>(a.part_q + (at * kC + tok) * KP + 32 * m + 4 * half, 0, 32, Q);
       } else {
-        store_runs<IO>(static_cast<T*>(a.dq) + ((b * a.seqlen + first + tok) * a.hk + hkey) * a.dk, 32 * m + 4 * half, a.dk, Q, 1.0f);
+        store_runs<IO>(static_cast<T*>(a.dq) + ((b * a.seqlen + first + tok) * a.hk + hkey) * a.dk, 32 * m + 4 * half, a.dk, Q);
       }
     }
   }
@@ -302,9 +302,9 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     }
     if (tok < valid) {
       if (a.hv > a.hk) {
-        store_runs<F32>(a.part_k + (at * kC + tok) * KP + 32 * m + 4 * half, 0, 32, Y, 1.0f);
+        store_runs<F32>(a.part_k + (at * kC + tok) * KP + 32 * m + 4 * half, 0, 32, Y);
       } else {
-        store_runs<IO>(static_cast<T*>(a.dk_out) + ((b * a.seqlen + first + tok) * a.hk + hkey) * a.dk, 32 * m + 4 * half, a.dk, Y, 1.0f);
+        store_runs<IO>(static_cast<T*>(a.dk_out) + ((b * a.seqlen + first + tok) * a.hk + hkey) * a.dk, 32 * m + 4 * half, a.dk, Y);
       }
     }
   }
