@@ -465,8 +465,9 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
  * projection's rows, and are what ss_qk_norm_rot writes token-major (weights of
  * 1/sqrt(dim_k) make keys of unit length).  dim_k is 1 to 128, dim_v 1 to 65536;
  * batch, heads and columns together make fewer than 2^23 workgroups.
- * The state and all sums are fp32, outputs rounded once; sequences of more than 16
- * tokens are taken in chunks of 64, with products in pairs of fp16 (22 bits).  g of
+ * The state and all sums are fp32, outputs rounded once; sequences of more than 10 to
+ * 16 tokens are taken in chunks of 64, with products in pairs of fp16 (22 bits), and
+ * where the heads are few a sequence's parts at the same time.  g of
  * -inf forgets the state; a padding token has beta = 0, g = 0 and finite q, k and v.
  * Anything infinite or NaN in a token may reach all outputs of its head from the 64
  * tokens (of t / 64) that it is among onwards, in the backward also those before.
@@ -481,8 +482,9 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
  *    zero), writes dq, dk (batch, seqlen, heads_k, dim_k; summed over a key head's value
  *    heads) and dv (batch, seqlen, heads_v, dim_v), contiguous and 16-byte aligned, and,
  *    where not NULL, the fp32 gradients dg (also of a g that is NULL), dbeta and dh0.  The workspace
- *    (ss_gdr_bwd_workspace_bytes) holds two states for every 64 tokens.  Tokens of q, k
- *    or v, or of a row of v, 2^22 values and more apart return SS_ERR_UNSUPPORTED.
+ *    (ss_gdr_bwd_workspace_bytes) holds two states for every 64 tokens.  Tokens of q, k,
+ *    v or o 2^22 values and more apart return SS_ERR_UNSUPPORTED (forward they are
+ *    taken one by one).
  *  ss_gdr_step: one token, q, k, v, g, beta and o without their seqlen dimension
  *    (the strides' second entry is not used).  state_out may be state_in itself. */
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v);

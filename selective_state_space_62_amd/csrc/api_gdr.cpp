@@ -103,8 +103,10 @@ ss_status check_blocks(int64_t blocks) {
   return SS_OK;
 }
 
-// Up to this many tokens go one by one, and tokens so far apart that 64 of them pass 2^31 bytes.
-constexpr int64_t kRecurTokens = 16;
+// Up to this many tokens go one by one, and tokens so far apart that 64 of them pass 2^31 bytes.  One by one and in a chunk, us: keys
+// of 64, 4 heads, 12 tokens 15, 19, 16 tokens 19, 19, 24 tokens 27, 19; keys of 128, 16 heads, 8 tokens 18, 20, 16 tokens 30, 20;
+// 128 x 40 heads, 8 tokens 217, 259, 16 tokens 339, 268.
+constexpr int64_t recur_tokens(int dim_k) { return dim_k <= 64 ? 16 : 10; }
 constexpr int64_t kMostStride = int64_t(1) << 22;
 
 bool far_apart(const Inputs& in) {
@@ -215,7 +217,7 @@ BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
 extern "C" {
 
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v) {
-  if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen <= kRecurTokens) return 0;
+  if (check_sizes(batch, seqlen, heads_k, heads_v, dim_k, dim_v) != SS_OK || seqlen <= recur_tokens(dim_k)) return 0;
   return fwd_layout(batch, seqlen, heads_v, dim_k, dim_v).segments.total;
 }
 
@@ -241,7 +243,7 @@ ss_status ss_gdr_fwd(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
     if (h_final) e = h0 ? launch_copy_state(state_numel(in), h0, h_final, s) : launch_fill_zero(h_final, state_numel(in), s);
     return e == hipSuccess ? SS_OK : record_hip_error(e, "state copy launch");
   }
-  const bool recur = seqlen <= kRecurTokens || far_apart(in);
+  const bool recur = seqlen <= recur_tokens(dim_k) || far_apart(in);
   if ((st = check_blocks(recur ? gdr_recur_blocks(batch, heads_v, dim_v) : batch * heads_v * chunks_of(seqlen))) != SS_OK)
     return st;
   GdrArgs a = make_args(in);
