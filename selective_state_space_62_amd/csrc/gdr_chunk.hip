@@ -8,8 +8,11 @@
 // to LDS, and nothing waits for a value that a workgroup could not form beforehand.
 // Where there are too few heads for the GPU, the chunks of one go in segments at the same time: the state behind a segment is a
 // product with the state before it and a sum, both made first (Of::kEnds) and put together in turn by a small kernel.
+// 8 x 40 heads of 2048 tokens, 128 by 128, bf16: 379 us, 12 us to a chunk with two workgroups on a CU; 4 x 40 heads, one on a CU, 7.
+// Its matrix instructions alone would take 1.4 us of that (3456 cycles of a SIMD), the other vector instructions 2 (about 1200); the
+// rest is the latency of seven products in turn.  Loads of V a chunk ahead (more registers) made it 397.
 // For the backward the same kernel makes S before every chunk and U (transposed by a product with the identity, as
-// operands of the gradients) instead of O.
+// operands of the gradients) instead of O: 415 us, of them about 200 the 1 GB that it writes.
 #include "gdr_device.h"
 
 namespace ssscan {
@@ -316,7 +319,7 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
 
 // The segments' ends in turn, end <- move * (the end before it) + end from the second on, or, of gradients, with the transposed
 // factors from the last but one to the second: a workgroup has 16 columns of a head, a wave 16 rows of every product, in fp32.  The
-// next segment's values are on their way meanwhile.
+// next segment's values are on their way meanwhile: 3 us to a segment (16 heads, 128 by 128, 32 segments: 97 us).
 template <int KP, bool BWD>
 __global__ __launch_bounds__(KP * 4) void gdr_join_ends_kernel(GdrArgs a) {
   constexpr int kPitch = 20;

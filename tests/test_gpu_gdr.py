@@ -119,6 +119,22 @@ def test_backward(ss, size):
     check_bwd(ss, problem(*size))
 
 
+def test_every_token_by_itself(ss):
+    """The tolerance for each token's gradients of q, k and v (over its own norm and the mean one), not for all together: no value
+    among many may have lost its second plane."""
+    p = problem(1, 450, 40, 40, 72, 80, F, seed=4)
+    gen = torch.Generator().manual_seed(4)
+    do = torch.randn(p["v"].shape, generator=gen).cuda()
+    got = ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], do, p["h0"])
+    ls = leaves(*[p[n] for n in ("q", "k", "v", "g", "beta", "h0")])
+    o, _ = gdr64(*ls, 72 ** -0.5)
+    (o * up(do)).sum().backward()
+    for n, l in zip(("dq", "dk", "dv"), ls):
+        off, size = (got[n].double().cpu() - l.grad).norm(dim=-1), l.grad.norm(dim=-1)
+        worst = float((off / (size + size.mean())).max())
+        assert worst <= F32_REL, (n, worst)
+
+
 @pytest.mark.parametrize("L", [1, 5, 64, 150])
 def test_without_gates_states_and_gradients_of_them(ss, L):
     p = problem(2, L, 1, 2, 24, 40, F, g=False, h0=False)
@@ -175,6 +191,21 @@ def test_tokens_far_apart(ss):
     close("o", o, want(p)[0], F32_REL)
     with pytest.raises(ss.SsError, match="2\\^22"):
         ss.gdr_bwd(p["q"], p["k"], v, p["g"], p["beta"], o)
+
+
+def test_outputs_far_apart(ss):
+    """So many columns to a token that 64 tokens of o pass 2^28 values, though v repeats one token."""
+    p = problem(1, 20, 1, 64, 1, 1, BF)
+    p["v"] = torch.randn(1, 1, 64, 1 << 16, generator=torch.Generator().manual_seed(5)).to(BF).cuda().expand(1, 20, -1, -1)
+    p["h0"] = None
+    o, h = ss.gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"])
+    few = {n: p[n] for n in p}
+    few["v"] = p["v"][..., -64:]
+    wo, wh = want(few)
+    close("o", o[..., -64:], wo, tolerance(o))
+    close("h_final", h[..., -64:], wh, F32_REL)
+    with pytest.raises(ss.SsError, match="2\\^22"):
+        ss.gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], o)
 
 
 def test_offsets_past_32_bits(ss):
@@ -358,9 +389,10 @@ def test_gradient_against_differences(ss):
     assert abs(along - diff) <= 1e-4 * (abs(diff) + size), (along, diff)
 
 
-def test_streams_and_graphs(ss):
+@pytest.mark.parametrize("L", [130, 450])
+def test_streams_and_graphs(ss, L):
     """On a stream of its own; captured (a forward and its backward), replayed with eager work in between."""
-    p = problem(2, 130, 1, 2, 64, 64, BF)
+    p = problem(2, L, 1, 2, 64, 64, BF)
     names = ("q", "k", "v", "g", "beta")
     ref = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
     gref = ss.gdr_bwd(*[p[n] for n in names], ref[0], p["h0"], ref[1])
@@ -385,9 +417,10 @@ def test_streams_and_graphs(ss):
         assert torch.equal(go, e[0]) and torch.equal(gh, e[1]) and all(torch.equal(gg[n], eg[n]) for n in gg)
 
 
-def test_workspace_may_hold_anything(ss):
+@pytest.mark.parametrize("L", [100, 450])
+def test_workspace_may_hold_anything(ss, L):
     """A caller's workspace, larger than needed and full of NaN; and one that is too small."""
-    p = problem(1, 100, 1, 2, 32, 48, F)
+    p = problem(1, L, 1, 2, 32, 48, F)
     names = ("q", "k", "v", "g", "beta")
     ref = ss.gdr_fwd(*[p[n] for n in names], p["h0"])
     gref = ss.gdr_bwd(*[p[n] for n in names], ref[0], p["h0"], ref[1])
