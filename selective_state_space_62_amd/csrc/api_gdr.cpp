@@ -130,14 +130,16 @@ struct Segments {
   int64_t count, per;
 };
 
-// Segments of at least two chunks, as many as fill the GPU.  Made in segments a row costs about 1.7 times as much, the factors
+// Segments of at least two chunks, as many as fill the GPU, but no more than 2 sqrt(chunks): a segment's join takes as long as a
+// quarter of a chunk's two passes (one head of 2^20 tokens, 256 segments 1864, 512 2487; 2 heads of 32768, 64 segments 289, 256 727;
+// one head of 4096, 16 segments 105, 32 125; backward, one head of 131072, 128 segments 1366, 512 2854).  Made in segments a row costs about 1.7 times as much, the factors
 // and the states first, so two of them gain nothing.  In one and in segments, us: 16 heads of 131072 tokens 15742, 2341; 12 x 8 heads
 // (fp32, keys of 64) of 2048 335, 271; 40 heads of 4096 496, 247; 8 heads of 500 67, 53; 2 heads of 1000 91, 43; 4 x 40 heads of
 // 2048 318, 320; 8 x 40 heads of 2048, which fill it, 509 and, in three, 614.  Backward: 16 heads of 32768 10455, 2130; 3 x 10 heads
 // (fp32, 72 by 80) of 1111 471, 263; 2 heads of 1000 236, 101; 4 x 40 heads of 2048 1283, 1255.
 Segments segments_of(int64_t batch, int64_t chunks, int heads_v, int dim_k, int dim_v, int io) {
   const int64_t groups = batch * heads_v * ((dim_v + 127) / 128);
-  const int64_t n = std::min(gdr_chunk_room(io, dim_k) / groups, chunks / 2);
+  const int64_t n = std::min({gdr_chunk_room(io, dim_k) / groups, chunks / 2, (int64_t)(2.0 * std::sqrt((double)chunks))});
   if (n < 3) return {1, chunks};
   const int64_t per = (chunks + n - 1) / n;
   return {(chunks + per - 1) / per, per};
