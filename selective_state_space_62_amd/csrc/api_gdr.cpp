@@ -173,7 +173,7 @@ void set_segments(GdrArgs& a, const SegmentsLayout& l, char* ws) {
   a.moves_e = reinterpret_cast<int32_t*>(ws + l.moves_e);
 }
 
-// Scratch of the chunked forward: the inverses, P, the vectors, then the segments'.  Each is taken as large as either I/O type needs it.
+// Scratch of the chunked forward: the inverses, P, the vectors, then the segments'.
 struct FwdLayout {
   size_t p, vecs;
   SegmentsLayout segments;
@@ -183,7 +183,7 @@ FwdLayout fwd_layout(int64_t batch, int64_t seqlen, int heads_v, int dim_k, int 
   const int64_t n = batch * heads_v * chunks_of(seqlen);
   FwdLayout l;
   l.p = round256(gdr_tri_bytes(n));
-  l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, false));
+  l.vecs = l.p + round256(gdr_tri_bytes(n));
   l.segments = segments_layout(l.vecs + round256(gdr_vecs_bytes(n)), batch, seqlen, heads_v, dim_k, dim_v);
   return l;
 }
@@ -202,7 +202,7 @@ BwdLayout bwd_layout(int64_t batch, int64_t seqlen, int heads_k, int heads_v, in
   l.max_apart = n * (ldv / 32);
   l.tri_t = round256(gdr_tri_bytes(n));
   l.p = l.tri_t + round256(gdr_tri_bytes(n));
-  l.vecs = l.p + round256(gdr_p_bytes(n, kIoF32, true));
+  l.vecs = l.p + round256(gdr_tri_bytes(n));
   l.states = l.vecs + round256(gdr_vecs_bytes(n));
   l.dstates = l.states + round256((size_t)(n * rows * ldv) * 4);
   l.u = l.dstates + round256((size_t)(n * rows * ldv) * 4);

@@ -63,8 +63,7 @@ struct GdrArgs {
 enum GdrMax { kMaxS, kMaxU, kMaxDs, kMaxDr, kMaxDo, kMaxKinds };
 
 // Chunk by chunk on the matrix cores: what needs no state for all chunks at once, then the states in turn.
-size_t gdr_tri_bytes(int64_t chunk_heads);                    // of tri, tri_t
-size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward);
+size_t gdr_tri_bytes(int64_t chunk_heads);                    // of tri, tri_t, p
 size_t gdr_vecs_bytes(int64_t chunk_heads);
 hipError_t launch_gdr_prep(const GdrArgs& a, bool backward, hipStream_t s);
 hipError_t launch_gdr_chunk(const GdrArgs& a, bool states, hipStream_t s);

@@ -35,11 +35,13 @@ template <typename IO, int KP, bool WHOLE, Of OF>
 __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_chunk_kernel(GdrArgs a) {
   using T = typename IO::T;
   constexpr bool OUT = OF == Of::kOut, STATES = OF == Of::kStates, ENDS = OF == Of::kEnds;
-  // What leads to O alone is rounded to bf16 where the I/O is: there one fp16 plane (2^-12) of S, U and P does.
-  constexpr int NP = planes_of<IO>(), NO = NP, kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
-  constexpr int kSide = 2 * kSteps * kBlock, kTurned = kTiles * 4 * kBlock, kP = OUT ? NO * kTriBytes : 0;
+  constexpr int NP = planes_of<IO>(), kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
+  // In bf16 the state's part of O is formed beside K S: its planes kept till U stands would spill at 128 keys (8 x 40 heads of 2048: 557
+  // us, 582 behind U).  In fp32 (one workgroup on a CU) there is room for them, and K S is done sooner without it (1036, 1046 beside).
+  constexpr bool kEarly = OUT && NP == 1;
+  constexpr int kSide = 2 * kSteps * kBlock, kTurned = kTiles * 4 * kBlock, kP = OUT ? 2 * kTriBytes : 0;
   __shared__ alignas(16) char s_k[NP * kSide], s_kt[NP * kTurned], s_q[OUT ? NP * kSide : 16];
-  __shared__ alignas(16) char s_t[2 * kTriBytes], s_p[kP + 16];
+  __shared__ alignas(16) char s_t[2 * kTriBytes], s_p[OUT ? kP : 16];
   __shared__ alignas(16) float s_vecs[2][kVecs][kC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t bh = blockIdx.x / a.segments, seg = blockIdx.x - bh * a.segments;
@@ -107,8 +109,7 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
     if constexpr (OUT) {
       const char* p = static_cast<const char*>(a.p) + at * kP;
 #pragma unroll
-      for (int i = 0; i < (kP + 4095) / 4096; ++i)
-        if (4096 * (i + 1) <= kP || wave < (kP & 4095) / 1024) load_to_lds(p + 4096 * i + off, s_p + 4096 * i + wave * 1024);
+      for (int i = 0; i < kP / 4096; ++i) load_to_lds(p + 4096 * i + off, s_p + 4096 * i + wave * 1024);
     }
     if (wave < 3)
       load_to_lds(reinterpret_cast<const char*>(a.vecs) + at * (kVecs * kC * 4) + off,
@@ -172,11 +173,17 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
     const Scale cs = scale_of(mS, 100);
     const int es = cs.e;
     R[0] = R[1] = zero16();
+    O[0] = O[1] = zero16();
+    auto through_q = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) O[i] = mm<2, NP>(sp[s], operand<NP>(s_q + (i * kSteps + s) * kBlock, lane, kSide), O[i]);
+    };
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       sp[s] = split(st[s >> 1], s & 1, cs.f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) R[i] = mm<NP, 2>(operand<NP>(s_k + (i * kSteps + s) * kBlock, lane, kSide), sp[s], R[i]);
+      if constexpr (kEarly) through_q(s);
       if (s & 1) step_end();
     }
     if constexpr (STATES) {
@@ -228,12 +235,12 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
         if (lane == 0) a.maxima[kMaxU * a.max_apart + (bh * a.chunks + chunk) * (a.ldv / 32) + col0 / 32] = mU * pow2(-er);
       }
     } else if constexpr (OUT) {
-      O[0] = O[1] = zero16();
+      if constexpr (!kEarly) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) O[i] = mm<NO, NP>(sp[s], operand<NP>(s_q + (i * kSteps + s) * kBlock, lane, kSide), O[i]);
-        if (s & 1) step_end();
+        for (int s = 0; s < kSteps; ++s) {
+          through_q(s);
+          if (s & 1) step_end();
+        }
       }
       const Scale cu = scale_of(mU, min(20, 40 - (ce - es + er)));
       const float join = pow2(ce - es + er + cu.e);
@@ -245,10 +252,10 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
       }
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const Planes up = split<NO>(U[s >> 1], s & 1, cu.f);
+        const Planes up = split(U[s >> 1], s & 1, cu.f);
 #pragma unroll
         for (int i = s >> 1; i < 2; ++i)
-          O[i] = mm<NO, NO>(up, operand<NO>(s_p + ((i + (s >> 1)) * 2 + (s & 1)) * 1024, lane, kTriBytes), O[i]);
+          O[i] = mm<2, 2>(up, operand<2>(s_p + ((i + (s >> 1)) * 2 + (s & 1)) * 1024, lane, kTriBytes), O[i]);
         step_end();
       }
       // O, transposed: a lane has a token and runs of four columns

@@ -65,15 +65,14 @@ __device__ __forceinline__ float held(float v) {
   return v;
 }
 
-// Values 8 half .. 8 half + 7 of a result tile as an operand of N planes, times s, a power of 2 (so that it rounds nothing).
-template <int N = 2>
+// Values 8 half .. 8 half + 7 of a result tile as an operand of two planes, times s, a power of 2 (so that it rounds nothing).
 __device__ __forceinline__ Planes split(const acc16& v, int half, float s) {
   Planes p;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x = v[8 * half + j];
     p.hi[j] = (_Float16)(x * s);
-    if constexpr (N == 2) p.lo[j] = (_Float16)fmaf(x, s, -(float)p.hi[j]);
+    p.lo[j] = (_Float16)fmaf(x, s, -(float)p.hi[j]);
   }
   return p;
 }
@@ -335,15 +334,12 @@ __device__ __forceinline__ h8 identity(int s, int lane) {
 
 // A result tile that has been split (both steps), back as fp32 and transposed: a lane has a row of the tile and 16 of its columns,
 // runs of four at 8 g + 4 (lane >> 5).
-template <int N = 2>
 __device__ __forceinline__ acc16 transposed(const Planes& p0, const Planes& p1, int lane) {
   const h8 e0 = identity(0, lane), e1 = identity(1, lane);
   acc16 acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p0.hi, e0, zero16(), 0, 0, 0);
   acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p1.hi, e1, acc, 0, 0, 0);
-  if constexpr (N == 2) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p0.lo, e0, acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p1.lo, e1, acc, 0, 0, 0);
-  }
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p0.lo, e0, acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(p1.lo, e1, acc, 0, 0, 0);
   return acc;
 }
 

@@ -176,7 +176,6 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
 
   // P, while the first wave solves the triangles
   if (of_p) {
-    constexpr int NO = BWD ? 2 : NP;
     const int i0 = 32 * (tp > 0), j0 = 32 * (tp > 1), c = (BWD ? j0 : i0) + (lane & 31), r0 = BWD ? i0 : j0;
     const float whole = s_whole[BWD ? 2 : 1][c], rest = s_rest[BWD ? 2 : 1][c], sign = BWD ? 1.0f : -1.0f;
     const acc16 w = rows_of(s_whole[BWD ? 1 : 2] + r0, lane), v = rows_of(s_rest[BWD ? 1 : 2] + r0, lane);
@@ -186,12 +185,12 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(GdrArgs a) {
       const float x = held(P[r] * exp2_of(sign * (w[r] - whole), sign * (v[r] - rest)));
       P[r] = (BWD ? c <= row : row <= c) ? x : 0.0f;
     }
-    char* out = static_cast<char*>(a.p) + at * (NO * kTriBytes) + tp * 2048 + lane * 16;
+    char* out = static_cast<char*>(a.p) + at * (2 * kTriBytes) + tp * 2048 + lane * 16;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Planes p = split<NO>(P, s, 1.0f);
+      const Planes p = split(P, s, 1.0f);
       *reinterpret_cast<h8*>(out + s * 1024) = p.hi;
-      if constexpr (NO == 2) *reinterpret_cast<h8*>(out + kTriBytes + s * 1024) = p.lo;
+      *reinterpret_cast<h8*>(out + kTriBytes + s * 1024) = p.lo;
     }
   }
   // 16x16 triangles: lane 16 q + c solves column c of triangle q
@@ -313,10 +312,6 @@ hipError_t launch(const GdrArgs& a, bool backward, hipStream_t s) {
 }  // namespace
 
 size_t gdr_tri_bytes(int64_t chunk_heads) { return (size_t)chunk_heads * 2 * kTriBytes; }
-
-size_t gdr_p_bytes(int64_t chunk_heads, int io, bool backward) {
-  return (size_t)chunk_heads * kTriBytes * (backward || io == kIoF32 ? 2 : 1);
-}
 
 size_t gdr_vecs_bytes(int64_t chunk_heads) { return (size_t)chunk_heads * kVecs * kC * sizeof(float); }
 
