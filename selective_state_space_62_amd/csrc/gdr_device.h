@@ -451,7 +451,7 @@ hipError_t by_keys(int dk, bool whole, F f) {
 // half of what it has decayed till then (16 at most).  T, P, U and their like are kept balanced by it, rows times 2^-p_i,
 // columns times 2^p_j, U and R as 2^-p_i U_i (their gradients times 2^p_i), so that growth costs no digits, and neither does a decay
 // of 2^-32 within the chunk, whether a token's value or the old state is the larger.  The operand P holds
-// q_i.k_j s z_i 2^(gam_i - gam_j - p_i + p_j - 18).
+// q_i.k_j s z_i 2^(gam_i - gam_j - p_i + p_j - kPShift).
 enum Vec {
   kVecF1,      // beta_j 2^-p_j / c_j
   kVecF2,      // beta_j 2^(gam_j - p_j) / (c_j s_j)
@@ -459,7 +459,7 @@ enum Vec {
   kVecInto,    // 2^gam_j
   kVecS,       // s_j
   kVecZ,       // z_i
-  kVecOut,     // scale 2^(p_i + 18) / (z_i s)
+  kVecOut,     // scale 2^(p_i + kPShift) / (z_i s)
   kVecQ,       // scale 2^gam_i / z_i
   kVecJoin,    // kVecQ / kVecOut
   kVecGrow = kVecJoin,   // backward: p_j
@@ -470,7 +470,11 @@ enum Vec {
 };
 static_assert(kVecs * kC * 4 == 3 * 1024, "three waves load the vectors");
 
-constexpr int kPShift = 18;    // rows of q and k are below 2^13 and up to 2^7 long, so that P stays below 2^15
+// P in an fp16 plane: rows of q and k are of up to 2^7 values below 2^13, so that q_i.k_j is up to 2^33, and the balance adds a factor
+// below 2^2.  With low the smallest sum so far, which only falls, and half what is let decay of it (between 0 and 16), gam - p is
+// gam - ceil(gam - low), in (low - 1, low], plus floor(half).  From j to a later i low falls by some d >= 0 and half rises by
+// d / 2 at most, its whole part by less than d / 2 + 1: gam - p rises by less than 1 - d + d / 2 + 1 <= 2.  So P stays below 2^15.
+constexpr int kPShift = 20;
 
 // 2^(whole + rest) of a difference of two such numbers: what an fp32 exponent of that size would lose stays in the rest.
 __device__ __forceinline__ float exp2_of(float whole, float rest) {
