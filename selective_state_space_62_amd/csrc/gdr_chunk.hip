@@ -36,9 +36,10 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
   using T = typename IO::T;
   constexpr bool OUT = OF == Of::kOut, STATES = OF == Of::kStates, ENDS = OF == Of::kEnds;
   constexpr int NP = planes_of<IO>(), kSteps = KP / 16, kTiles = KP / 32, kRuns = KP / 32;
-  // In bf16 the state's part of O is formed beside K S: its planes kept till U stands would spill at 128 keys (8 x 40 heads of 2048: 557
-  // us, 582 behind U).  In fp32 (one workgroup on a CU) there is room for them, and K S is done sooner without it (1036, 1046 beside).
-  constexpr bool kEarly = OUT && NP == 1;
+  // In bf16 the state's part of O is formed beside K S where keys are many: its planes kept till U stands would spill at 128 (8 x 40 heads
+  // of 2048: 557 us, 582 behind U).  Behind U it leaves a third workgroup on a CU at 32 keys, and in fp32, with registers to spare, K S is
+  // done sooner (1036 us, 1046 beside).
+  constexpr bool kEarly = OUT && NP == 1 && KP > 64;
   constexpr int kSide = 2 * kSteps * kBlock, kTurned = kTiles * 4 * kBlock, kP = OUT ? 2 * kTriBytes : 0;
   __shared__ alignas(16) char s_k[NP * kSide], s_kt[NP * kTurned], s_q[OUT ? NP * kSide : 16];
   __shared__ alignas(16) char s_t[2 * kTriBytes], s_p[OUT ? kP : 16];
@@ -60,8 +61,8 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
   const int64_t ostride = (int64_t)a.hv * a.dv;
   T* o = static_cast<T*>(a.o) + b * a.seqlen * ostride + (int64_t)h * a.dv;
 
-  acc16 st[kTiles];                      // the state is st 2^ce
-  int ce = 0;
+  acc16 st[kTiles];                      // the state is st 2^ce, a factor st 2^(ce + moved)
+  int ce = 0, moved = 0;
   {
     const int lane = threadIdx.x & 63, col = col0 + (lane & 31);
     const bool first = seg == 0 || ENDS;
@@ -170,8 +171,13 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) mS = max_of(st[m], mS);
     mS = wave_max(mS);
-    const Scale cs = scale_of(mS, 100);
+    if (moves) {                                           // a factor goes on from 1: without values only its proportions count
+      moved += ce;
+      ce = 0;
+    }
+    const Scale cs = scale_of(mS, kMostE + min(ce, 0));    // (its inverse times 2^ce is a normal number)
     const int es = cs.e;
+    const float back = pow2(ce - es);
     R[0] = R[1] = zero16();
     O[0] = O[1] = zero16();
     auto through_q = [&](int s) {
@@ -189,18 +195,16 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
     if constexpr (STATES) {
       // the state before the chunk, its rows behind dk and columns behind dv zeros
       float* out = a.states + (bh * a.chunks + chunk) * KP * a.ldv;
-      const float f = pow2(ce - es);
       if (col0 < a.ldv) {
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
           const acc16 t = transposed(sp[2 * m], sp[2 * m + 1], lane);
-          store_blocks(out, m, col0, a.ldv, lane, t, f);
+          store_blocks(out, m, col0, a.ldv, lane, t, back);
           step_end();
         }
         if (lane == 0) a.maxima[kMaxS * a.max_apart + (bh * a.chunks + chunk) * (a.ldv / 32) + col0 / 32] = mS * pow2(ce);
       }
     }
-    const float back = pow2(ce - es);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const acc16 V = turn<IO>(rvv[i], lane);
@@ -210,7 +214,7 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
         R[i][r] = s_vec[kVecF1][row] * V[r] - back * (s_vec[kVecF2][row] * R[i][r]);
       }
     }
-    const Scale cr = scale_of(wave_max(max_of(R[1], max_of(R[0], 0.0f))), 100);
+    const Scale cr = scale_of(wave_max(max_of(R[1], max_of(R[0], 0.0f))), kMostE);
     const int er = cr.e;
     U[0] = U[1] = zero16();
 #pragma unroll
@@ -224,7 +228,7 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
     if (chunk + 1 < stop) fetch(chunk + 1);
     const float mU = wave_max(max_of(U[1], max_of(U[0], 0.0f)));
     if constexpr (STATES) {
-      const Scale cu = scale_of(mU, 20);
+      const Scale cu = scale_of(mU, min(20, kMostE - er));
       float* out = a.u + (bh * a.chunks + chunk) * kC * a.ldv;
       if (col0 < a.ldv) {
 #pragma unroll
@@ -242,7 +246,8 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
           if (s & 1) step_end();
         }
       }
-      const Scale cu = scale_of(mU, min(20, 40 - (ce - es + er)));
+      // (of a U of zeros the largest scale that is allowed: the state's part is then all there is)
+      const Scale cu = scale_of(fmaxf(mU, 0x1p-126f), min(min(20, kMostE - er), 40 - (ce - es + er)));
       const float join = pow2(ce - es + er + cu.e);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -263,7 +268,10 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tok = 32 * i + low;
-        store_runs<IO, WHOLE>(rows, tok * orow, col0 + 4 * half, a.dv, O[i], s_vec[kVecOut][tok] * pow2(-(er + cu.e)));
+        const float by = s_vec[kVecOut][tok];              // not at once with the power, which may be 2^-126
+#pragma unroll
+        for (int r = 0; r < 16; ++r) O[i][r] *= by;
+        store_runs<IO, WHOLE>(rows, tok * orow, col0 + 4 * half, a.dv, O[i], pow2(-(er + cu.e)));
       }
     }
     __syncthreads();                                       // T and P have been read
@@ -275,10 +283,11 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
       for (int r = 0; r < 16; ++r) U[i][r] *= s_vec[kVecEnd][32 * i + tile_row(r, lane)];
       mE = max_of(U[i], mE);
     }
-    const float gC = s_vec[kVecInto][kC - 1], kept = mS * gC;
-    // in units in which the kept state stays below 2^60
-    const int room = kept > 0.0f ? 60 - exponent(kept) - ce - er : 100;
-    const Scale ue = scale_of(wave_max(mE), min(room, 100 - er));
+    const float gC = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(s_vec[kVecInto][kC - 1])));
+    const int eG = exponent(gC);
+    // in units in which the kept state stays below 2^61 and its factor a float
+    const int room = min(59 - exponent(mS) - eG, kMostE - max(eG, 0)) - ce - er;
+    const Scale ue = scale_of(fmaxf(wave_max(mE), 0x1p-126f), min(room, kMostE - er));
     const float f = gC * pow2(ce + er + ue.e);
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
@@ -300,9 +309,11 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
       float m = 0.0f;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) m = max_of(st[t], m);
-      const int e = exponent(wave_max(m));
+      m = wave_max(m);
+      const int e = exponent(m);
       f = pow2(-e);
-      if (lane == 0) a.moves_e[(bh * a.segments + seg) * 4 + wave] = ce + e;
+      // (zeros meet a state times 0, not one times what they have been)
+      if (lane == 0) a.moves_e[(bh * a.segments + seg) * 4 + wave] = m == 0.0f ? -(1 << 20) : moved + ce + e;
     }
     const int64_t ld = moves ? KP : a.ldv;
     float* to = (moves ? a.moves : a.ends) + (bh * a.segments + seg) * KP * ld;

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) mS = max_of(st[m], mS);
     mS = wave_max(mS);
-    const Scale cs = scale_of(mS, 100);
+    const Scale cs = scale_of(mS, kMostE + min(ce, 0));    // (its inverse times 2^ce is a normal number)
     const float back = pow2(ce - cs.e);
     X[0] = X[1] = zero16();
     {
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) y[i][r] = D[i][r] * s_vec[kVecOut][32 * i + tile_row(r, lane)];
-      const Scale c = scale_of(wave_max(max_of(y[1], max_of(y[0], 0.0f))), 100);
+      const Scale c = scale_of(wave_max(max_of(y[1], max_of(y[0], 0.0f))), kMostE);
       W[0] = W[1] = zero16();
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -192,8 +192,8 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
         for (int r = 0; r < 16; ++r) W[j][r] = fmaf(W[j][r], f, s_vec[kVecEnd][32 * j + tile_row(r, lane)] * (back * X[j][r]));
     }
     if (chunk > begin) fetch(chunk - 1);
-    // dR = T^T dU, in units of the inverse's columns
-    const Scale cu = scale_of(wave_max(max_of(W[1], max_of(W[0], 0.0f))), 100);
+    // dR = T^T dU, over the inverse's columns' scales
+    const Scale cu = scale_of(wave_max(max_of(W[1], max_of(W[0], 0.0f))), kMostE);
     X[0] = X[1] = zero16();
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -209,9 +209,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) y[i][r] = (X[i][r] * unit) * s_vec[kVecC][32 * i + tile_row(r, lane)];
+        for (int r = 0; r < 16; ++r) {
+          X[i][r] *= unit;
+          y[i][r] = X[i][r] * s_vec[kVecC][32 * i + tile_row(r, lane)];
+        }
       const float m = wave_max(max_of(y[1], max_of(y[0], 0.0f)));
-      const Scale c = scale_of(m, 100);
+      const Scale c = scale_of(m, kMostE);
       if (stores) {
         float* out = a.dr + at * kC * a.ldv;
         const __amdgpu_buffer_rsrc_t rows = chunk_rows<IO>(dv + first * ostride, ostride, valid, a.dv);
@@ -234,14 +237,15 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 || KP <= 64 ? 2 : 1) vo
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 32 * i + tile_row(r, lane);
-        X[i][r] *= -(s_vec[kVecF2][row] * unit);
+        X[i][r] *= -s_vec[kVecF2][row];
         D[i][r] *= s_vec[kVecQ][row];
       }
       mE = max_of(D[i], max_of(X[i], mE));
     }
-    const float gC = s_vec[kVecInto][kC - 1], kept = mS * gC;
-    const int room = kept > 0.0f ? 60 - exponent(kept) - ce : 100;
-    const Scale ue = scale_of(wave_max(mE), min(room, 100));
+    const float gC = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(s_vec[kVecInto][kC - 1])));
+    const int eG = exponent(gC);
+    const int room = min(59 - exponent(mS) - eG, kMostE - max(eG, 0)) - ce;
+    const Scale ue = scale_of(wave_max(mE), min(room, kMostE));
     const float f = gC * pow2(ce + ue.e);
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)

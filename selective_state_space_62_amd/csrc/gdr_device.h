@@ -138,6 +138,12 @@ __device__ __forceinline__ float pow2(int e) {
 // Exponent of a largest |value|: floor(log2 m), -127 for zero and what is below normal numbers, 128 for an infinity.
 __device__ __forceinline__ int exponent(float m) { return (int)(__float_as_uint(m) >> 23) - 127; }
 
+// x 2^e, where e may be the sum of several scales' exponents: too small a power leaves zero, where pow2 would hold it at 2^-126.
+__device__ __forceinline__ float times_pow2(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
+
+// The largest exponent of a scale whose inverse is a normal number too.
+constexpr int kMostE = 126;
+
 // The scale 2^e that takes a largest |value| m to [2^13, 2^14), e at most `most`.  With an infinity among the values it is NaN:
 // what stands beside it could not be held, and is not lost silently.
 struct Scale {

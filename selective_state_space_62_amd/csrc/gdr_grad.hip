@@ -74,17 +74,17 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
     mx = wave_max(mx);
     if (lane == 0) s_mx[wave] = mx;
     __syncthreads();
-    const Scale sk = scale_of(fmaxf(fmaxf(s_mx[0], s_mx[1]), fmaxf(s_mx[2], s_mx[3])), 100);
-    const Scale sq = scale_of(fmaxf(fmaxf(s_mx[4], s_mx[5]), fmaxf(s_mx[6], s_mx[7])), 100);
+    const Scale sk = scale_of(fmaxf(fmaxf(s_mx[0], s_mx[1]), fmaxf(s_mx[2], s_mx[3])), kMostE);
+    const Scale sq = scale_of(fmaxf(fmaxf(s_mx[4], s_mx[5]), fmaxf(s_mx[6], s_mx[7])), kMostE);
     ek = sk.e;
     eq = sq.e;
     const float f = tid < 256 ? sk.f : sq.f, s[4] = {f, f, f, f};
     char* to = tid < 256 ? s_kt : s_qt;
     if (c < KP / 8) store_operand_turned<IO>(to, to + (NP - 1) * kTurned, g, c, x, s);
   }
-  const Scale cS = scale_of(wave_max(most[kMaxS]), 100), cU = scale_of(wave_max(most[kMaxU]), 100);
-  const Scale cE = scale_of(wave_max(most[kMaxDs]), 100), cD = scale_of(wave_max(most[kMaxDr]), 100);
-  const Scale cO = scale_of(wave_max(most[kMaxDo]), 100);
+  const Scale cS = scale_of(wave_max(most[kMaxS]), kMostE), cU = scale_of(wave_max(most[kMaxU]), kMostE);
+  const Scale cE = scale_of(wave_max(most[kMaxDs]), kMostE), cD = scale_of(wave_max(most[kMaxDr]), kMostE);
+  const Scale cO = scale_of(wave_max(most[kMaxDo]), kMostE);
 
   // this wave's rows of keys 32 m .. and tokens 32 ti ..; of the triangles N (waves 0-2) and M (4-6) its tile, a lane a row i
   const int m = wave >> 1, ti = wave & 1, tok = 32 * ti + low, tile = wave & 3, i0 = 32 * (tile > 0), j0 = 32 * (tile > 1);
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
 
   // the triangles' values; sums over rows of dR.v; <dS, S>
   {
-    const float f = of_n ? a.scale * pow2(-cU.e) * pow2(-cO.e) : pow2(-cU.e) * pow2(-cD.e);
+    const float f = times_pow2(of_n ? a.scale : 1.0f, -cU.e - (of_n ? cO.e : cD.e));
     const int i = i0 + low;
     const float whole = s_vec[kVecWhole][i], rest = s_vec[kVecRest][i];
 #pragma unroll
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   }
   if (half == 0) s_rv[wave & 3][32 * (wave >> 2) + low] = rv;
   __syncthreads();
-  const Scale t0 = scale_of(fmaxf(s_mx[0], fmaxf(s_mx[1], s_mx[2])), 100), t1 = scale_of(fmaxf(s_mx[4], fmaxf(s_mx[5], s_mx[6])), 100);
+  const Scale t0 = scale_of(fmaxf(s_mx[0], fmaxf(s_mx[1], s_mx[2])), kMostE), t1 = scale_of(fmaxf(s_mx[4], fmaxf(s_mx[5], s_mx[6])), kMostE);
   // the other orientation: a lane a column j, rows times what is not yet theirs: 2^p_i of N, beta_i of M, at most 2^rise
   const int rise_n = (int)wave_max(fmaxf(s_vec[kVecGrow][lane], 0.0f));
   const int rise_m = max(exponent(wave_max(fabsf(s_beta[lane]))) + 1, 0);
@@ -250,9 +250,9 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   }
   if (active) {
     const float into = s_vec[kVecInto][tok];
-    const float f = a.scale * into * pow2(-cS.e) * pow2(-cO.e), fn = pow2((int)s_vec[kVecGrow][tok] - ek - t0.e), fy = pow2(rise_n - eq - t0.e);
-    const float fe = s_vec[kVecEnd][tok] * s_vec[kVecS][tok] * pow2(-cE.e) * pow2(-cU.e);
-    const float fx = exp2_of(s_vec[kVecWhole][tok], s_vec[kVecRest][tok]) * pow2(-cS.e) * pow2(-cD.e);
+    const float f = times_pow2(a.scale * into, -cS.e - cO.e), fn = times_pow2(1.0f, (int)s_vec[kVecGrow][tok] - ek - t0.e), fy = times_pow2(1.0f, rise_n - eq - t0.e);
+    const float fe = times_pow2(s_vec[kVecEnd][tok] * s_vec[kVecS][tok], -cE.e - cU.e);
+    const float fx = times_pow2(exp2_of(s_vec[kVecWhole][tok], s_vec[kVecRest][tok]), -cS.e - cD.e);
     float qdq = 0.0f, kend = 0.0f;
     const acc16 nk = through(s_kt, true);
 #pragma unroll
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   if (!of_n && tile < 3) write_triangles();
   __syncthreads();
   if (active) {
-    const float fm = pow2(-ek - t1.e), fb = pow2(rise_m - ek - t1.e), beta = s_beta[tok];
+    const float fm = times_pow2(1.0f, -ek - t1.e), fb = times_pow2(1.0f, rise_m - ek - t1.e), beta = s_beta[tok];
     const acc16 mk = through(s_kt, true), mb = through(s_kt, false);
     float kx = 0.0f, ky = 0.0f;
 #pragma unroll

@@ -98,3 +98,120 @@ def test_gates_that_grow_in_bf16(ss, L):  # noqa: F811
     p["g"] = torch.where(torch.arange(L, device="cuda")[None, :, None] // 50 % 2 == 0, 0.5, -0.5).expand(1, L, 2).contiguous()
     check_fwd(ss, p)
     check_bwd(ss, p)
+
+
+def sizes64(p, do, dh):
+    """Norms, for every token and head, of what a backward is formed of in 64 bits: a dict of (batch, L, heads) tensors S (the state),
+    dS (its gradient), F (the decayed state before the token), u, dv; the outputs, the last state, and the inputs with their gradients."""
+    ls = leaves(*[p[n] for n in NAMES])
+    q, k, v, g, beta, s = ls
+    spread = torch.arange(v.shape[2]) // (v.shape[2] // q.shape[2])
+    outs, states, faded, us = [], [], [], []
+    for t in range(q.shape[1]):
+        kt = k[:, t][:, spread]
+        f = s * torch.exp(g[:, t])[..., None, None]
+        u = beta[:, t][..., None] * (v[:, t] - (f * kt[..., None]).sum(-2))
+        s = f + kt[..., None] * u[..., None, :]
+        s.retain_grad()
+        outs.append((s * q[:, t][:, spread][..., None]).sum(-2) * q.shape[-1] ** -0.5)
+        states.append(s)
+        faded.append(f.detach().flatten(-2).norm(dim=-1))
+        us.append(u.detach().norm(dim=-1))
+    o = torch.stack(outs, 1)
+    ((o * do).sum() + (s * dh).sum()).backward()
+    n = dict(S=torch.stack([x.detach().flatten(-2).norm(dim=-1) for x in states], 1), dS=torch.stack([x.grad.flatten(-2).norm(dim=-1) for x in states], 1),
+             F=torch.stack(faded, 1), u=torch.stack(us, 1), dv=v.grad.norm(dim=-1))
+    return n, o.detach(), s.detach(), ls
+
+
+def left(sizes, decays, back, width):
+    """What may be off in a state of `width` values, by norm, before every token and behind the last (L + 1 norms `sizes`; `back`: of a
+    gradient, against the tokens).  From every chunk on: F32_REL of the state that it starts from, which decays and grows by the gates and
+    is not taken back by keys as the state is (the factor of a segment is a matrix, whose errors are of its own size); what its rows
+    are held to, 2^-38 of the largest, over the square root of 64 tokens 2^-35, less the balance of a token's row, half of what the gates
+    have decayed till then, 2^16 at most (see gdr_device.h; against the tokens less what it is behind the largest row, the last); and a value's smallest step at the largest scale, 2^-25 of 2^-126, times rows up to 2^13, again
+    over the root of 64 tokens: 2^-135."""
+    L = decays.shape[1]
+    out, e = torch.zeros_like(sizes), torch.zeros_like(sizes[:, 0])
+    chunks = list(range(0, L, 64))
+    for c in reversed(chunks) if back else chunks:
+        ts = list(range(c, min(c + 64, L)))
+        start = sizes[:, ts[-1] + 1 if back else ts[0]]
+        low = (decays[:, ts].cumsum(1) / math.log(2.0)).clamp_max(0.0).cummin(1)[0]
+        half = torch.floor((-0.5 * low).clamp(0, 16))
+        floors = 2.0 ** -35 * 2.0 ** ((half - half[:, -1:]) if back else -half) * start[:, None] + 2.0 ** -135 * width ** 0.5
+        e = e + F32_REL * start
+        for t in reversed(ts) if back else ts:
+            e = e * torch.exp(decays[:, t])
+            out[:, t if back else t + 1] = e + floors[:, t - c]
+        e = e + floors[:, 0 if back else -1]
+    return out
+
+
+def check_linear(ss, p, dh):  # noqa: F811
+    """A row without values, all of which is a product with the state before, and the gradient behind: every result against 64 bits,
+    within F32_REL of the sizes of the terms and what the chunks may leave."""
+    o, h = ss.gdr_fwd(*[p[n] for n in NAMES])
+    got = ss.gdr_bwd(*[p[n] for n in NAMES[:5]], torch.zeros_like(p["v"]), p["h0"], dh)
+    n, wo, wh, ls = sizes64(p, torch.zeros(p["v"].shape, dtype=torch.float64), up(dh))
+    q, k, v, g, beta, h0 = ls
+    gates, b, scale = up(p["g"]), beta.detach(), q.shape[-1] ** -0.5
+    before = torch.cat((up(p["h0"]).flatten(-2).norm(dim=-1)[:, None], n["S"]), 1)
+    after = torch.cat((h0.grad.flatten(-2).norm(dim=-1)[:, None], n["dS"]), 1)
+    width = h0.shape[-1] * h0.shape[-2]
+    E, D = left(before, gates, False, width)[:, 1:], left(after, gates, True, width)
+    D0, D = D[:, 0], D[:, 1:]                              # (of the last state's gradient, which is given, nothing is off)
+    nq, nk = q.detach().norm(dim=-1), k.detach().norm(dim=-1)
+
+    def within(name, x, w, allowed, least=2.0 ** -126):
+        off = (x.double().cpu() - w.detach()).abs()
+        off = off.flatten(allowed.dim()).norm(dim=-1) if off.dim() > allowed.dim() else off
+        allowed = allowed + least                          # (results below the normal numbers)
+        assert bool((off <= allowed).all()), (name, float((off / allowed).max()))
+    r = F32_REL
+    within("o", o, wo, scale * nq * (r * n["S"] + E))
+    within("h_final", h, wh, r * n["S"][:, -1] + E[:, -1])
+    within("dv", got["dv"], v.grad, r * n["dv"] + b * nk * (r * n["dS"] + D))
+    # (in the last step a factor is a float, so a multiple of 2^-149, and a product's sum up to 2^35: 2^-114)
+    within("dbeta", got["dbeta"], beta.grad, nk * nk * (r * n["dS"] * n["F"] + D * n["F"] + n["dS"] * E), 2.0 ** -114)
+    within("dk", got["dk"], k.grad, r * (n["dS"] * n["u"] + n["F"] * n["dv"]) + D * n["u"] + E * n["dv"] + b * nk * (n["dS"] * E + n["F"] * D), 2.0 ** -114)
+    within("dh0", got["dh0"], h0.grad, r * after[:, 0] + D0)
+
+
+def linear(batch, L, heads, n, rate, at, size, beta):
+    p = problem(batch, L, heads, heads, n, n, F, seed=6)
+    p["v"].zero_()
+    p["beta"] *= beta
+    p["g"].zero_()
+    p["g"][:, at] = rate
+    p["h0"] *= size
+    return p, torch.randn(p["h0"].shape, generator=torch.Generator().manual_seed(7)).cuda()
+
+
+@pytest.mark.parametrize("rate,size,after", [(-0.76, 2.0 ** 110, 2.0 ** -60), (-1.0, 2.0 ** 120, 2.0 ** -60), (0.76, 2.0 ** -115, 2.0 ** -60), (1.0, 2.0 ** -100, 2.0 ** -110),
+                                             (-0.76, 2.0 ** 20, 2.0 ** 60), (0.76, 2.0 ** -30, 2.0 ** -70)])
+@pytest.mark.parametrize("beta", [0.0, 0.3])
+def test_factors_of_segments(ss, rate, size, after, beta):  # noqa: F811
+    """Segments of 128 tokens, the second of which decays or grows by e^(128 rate), a factor below 2^-126 or above 2^127."""
+    p, dh = linear(1, 1024, 2, 64, rate, slice(128, 256), size, beta)
+    check_linear(ss, p, dh * after)
+
+
+@pytest.mark.parametrize("rate,size,after", [(-0.26, 2.0 ** 110, 2.0 ** -60), (0.26, 2.0 ** -100, 2.0 ** -100), (-0.26, 2.0 ** -10, 2.0 ** 100)])
+def test_factors_of_long_segments(ss, rate, size, after):  # noqa: F811
+    """The same in segments of 512 tokens whose chunks decay or grow by 2^24 each, so that every token's part of the factor counts."""
+    p, dh = linear(2, 2048, 64, 16, rate, slice(512, 1024), size, 0.3)
+    check_linear(ss, p, dh * after)
+
+
+@pytest.mark.parametrize("L", [150, 1024])
+@pytest.mark.parametrize("h0", [True, False])
+def test_growth_of_nothing(ss, L, h0):  # noqa: F811
+    """Gates that grow a state of zeros, or of next to nothing, by 2^46 in a chunk: it stays what it is."""
+    p, dh = linear(1, L, 2, 64, 0.5, slice(64, 128), 2.0 ** -120 if h0 else 0.0, 0.5)
+    check_linear(ss, p, dh * 0.0)
+    p["h0"] = p["h0"] if h0 else None
+    got = ss.gdr_bwd(*[p[n] for n in NAMES[:5]], torch.zeros_like(p["v"]), p["h0"], dh * 0.0)
+    assert all(float(x.abs().max()) == 0.0 for x in got.values() if x is not None)
+    if not h0:
+        assert all(float(x.abs().max()) == 0.0 for x in ss.gdr_fwd(*[p[n] for n in NAMES]))
