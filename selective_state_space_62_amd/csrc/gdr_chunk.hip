@@ -246,8 +246,11 @@ __global__ __launch_bounds__(kThreads, per_cu(IO::kPerSpan == 8, KP)) void gdr_c
           if (s & 1) step_end();
         }
       }
-      // (of a U of zeros the largest scale that is allowed: the state's part is then all there is)
-      const Scale cu = scale_of(fmaxf(mU, 0x1p-126f), min(min(20, kMostE - er), 40 - (ce - es + er)));
+      // The state's part, below 2^34, is multiplied into U's units, by 2^40 at most, and stays a float: kVecJoin, which is large where keys
+      // are next to nothing, rises by less than 2^2 from the first token on, as P does.  (Of a U of zeros the largest scale that is
+      // allowed: the state's part is then all there is.)
+      const int eJ = exponent(__int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(s_vec[kVecJoin][0]))));
+      const Scale cu = scale_of(fmaxf(mU, 0x1p-126f), min(min(20, kMostE - er), min(40, 87 - eJ) - (ce - es + er)));
       const float join = pow2(ce - es + er + cu.e);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {

@@ -104,8 +104,8 @@ def sizes64(p, do, dh):
     """Norms, for every token and head, of what a backward is formed of in 64 bits: a dict of (batch, L, heads) tensors S (the state),
     dS (its gradient), F (the decayed state before the token), u, dv; the outputs, the last state, and the inputs with their gradients."""
     ls = leaves(*[p[n] for n in NAMES])
-    q, k, v, g, beta, s = ls
-    spread = torch.arange(v.shape[2]) // (v.shape[2] // q.shape[2])
+    q, k, v, g, beta, s = on = [x.detach().cuda().requires_grad_() for x in ls]
+    spread = torch.arange(v.shape[2], device="cuda") // (v.shape[2] // q.shape[2])
     outs, states, faded, us = [], [], [], []
     for t in range(q.shape[1]):
         kt = k[:, t][:, spread]
@@ -118,10 +118,12 @@ def sizes64(p, do, dh):
         faded.append(f.detach().flatten(-2).norm(dim=-1))
         us.append(u.detach().norm(dim=-1))
     o = torch.stack(outs, 1)
-    ((o * do).sum() + (s * dh).sum()).backward()
+    ((o * do.cuda()).sum() + (s * dh.cuda()).sum()).backward()
     n = dict(S=torch.stack([x.detach().flatten(-2).norm(dim=-1) for x in states], 1), dS=torch.stack([x.grad.flatten(-2).norm(dim=-1) for x in states], 1),
              F=torch.stack(faded, 1), u=torch.stack(us, 1), dv=v.grad.norm(dim=-1))
-    return n, o.detach(), s.detach(), ls
+    for x, y in zip(ls, on):
+        x.grad = torch.zeros_like(x) if y.grad is None else y.grad.cpu()
+    return {a: b.cpu() for a, b in n.items()}, o.detach().cpu(), s.detach().cpu(), ls
 
 
 def left(sizes, decays, back, width):
@@ -215,3 +217,13 @@ def test_growth_of_nothing(ss, L, h0):  # noqa: F811
     assert all(float(x.abs().max()) == 0.0 for x in got.values() if x is not None)
     if not h0:
         assert all(float(x.abs().max()) == 0.0 for x in ss.gdr_fwd(*[p[n] for n in NAMES]))
+
+
+@pytest.mark.parametrize("sk", [2.0 ** -30, 2.0 ** -62, 2.0 ** -84])
+@pytest.mark.parametrize("values", [0.0, 1.0])
+@pytest.mark.parametrize("io", [F, BF])
+def test_keys_of_next_to_nothing(ss, sk, values, io):  # noqa: F811
+    """Keys so small that outputs are the state's alone: finite, and the state's."""
+    p = problem(1, 100, 1, 2, 64, 64, io, seed=3)
+    p["k"], p["v"] = (p["k"].float() * sk).to(io), p["v"] * values
+    check_fwd(ss, p)
