@@ -484,7 +484,7 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
  *    where not NULL, the fp32 gradients dg (also of a g that is NULL), dbeta and dh0.  The workspace
  *    (ss_gdr_bwd_workspace_bytes) holds two states for every 64 tokens.  Tokens of q, k,
  *    v or o 2^22 values and more apart return SS_ERR_UNSUPPORTED (forward they are
- *    taken one by one).
+ *    taken one by one; the stride of a single token of q, k or v does not count).
  *  ss_gdr_step: one token, q, k, v, g, beta and o without their seqlen dimension
  *    (the strides' second entry is not used).  state_out may be state_in itself. */
 size_t ss_gdr_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int heads_k, int heads_v, int dim_k, int dim_v);

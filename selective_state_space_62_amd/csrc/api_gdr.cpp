@@ -91,6 +91,7 @@ GdrArgs make_args(const Inputs& in) {
     a.ks[i] = in.k_stride[i];
     a.vs[i] = in.v_stride[i];
   }
+  if (in.seqlen == 1) a.qs[1] = a.ks[1] = a.vs[1] = 0;     // a token without a next one
   a.g = in.g;
   a.beta = in.beta;
   a.h0 = in.h0;
@@ -110,8 +111,8 @@ constexpr int64_t recur_tokens(int dim_k) { return dim_k <= 64 ? 16 : 10; }
 constexpr int64_t kMostStride = int64_t(1) << 22;
 
 bool far_apart(const Inputs& in) {
-  return in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride ||
-         (int64_t)in.heads_v * in.dim_v >= kMostStride;
+  if ((int64_t)in.heads_v * in.dim_v >= kMostStride) return true;
+  return in.seqlen > 1 && (in.q_stride[1] >= kMostStride || in.k_stride[1] >= kMostStride || in.v_stride[1] >= kMostStride);
 }
 
 bool aligned_rows(const void* p, const int64_t* st, ss_dtype io) {

@@ -227,3 +227,16 @@ def test_keys_of_next_to_nothing(ss, sk, values, io):  # noqa: F811
     p = problem(1, 100, 1, 2, 64, 64, io, seed=3)
     p["k"], p["v"] = (p["k"].float() * sk).to(io), p["v"] * values
     check_fwd(ss, p)
+
+
+@pytest.mark.parametrize("io", [F, BF])
+def test_a_single_token_of_a_far_stride(ss, io):  # noqa: F811
+    """One token has no neighbour: its stride, of a slice of time-major rows, does not count, in either direction."""
+    p = problem(2, 1, 1, 2, 16, 24, io)
+    buf = torch.zeros(2, 1 << 22, dtype=io, device="cuda")
+    far = dict(p)
+    for n, at in (("q", 0), ("k", 64), ("v", 128)):
+        far[n] = buf.as_strided(p[n].shape, (1 << 10, 1 << 22, p[n].shape[-1], 1), at)
+        far[n].copy_(p[n])
+    check_fwd(ss, far)
+    check_bwd(ss, far)
