@@ -240,3 +240,64 @@ def test_a_single_token_of_a_far_stride(ss, io):  # noqa: F811
         far[n].copy_(p[n])
     check_fwd(ss, far)
     check_bwd(ss, far)
+
+
+def parts64(p, do, dh):
+    """The 64-bit gradients, with a key's where it reads the state and where it is written apart, and what they are formed of."""
+    q, k, v, g, beta, h0 = leaves(*[p[n] for n in NAMES])
+    kr, kw = k.detach().clone().requires_grad_(), k.detach().clone().requires_grad_()
+    hk, hv, scale = q.shape[2], v.shape[2], q.shape[-1] ** -0.5
+    # a row for every value head, so that no gradient is a sum of several
+    q, kr, kw = [x.detach().repeat_interleave(hv // hk, 2).requires_grad_() for x in (q, kr, kw)]
+    h, out, states = h0, [], []
+    for t in range(q.shape[1]):
+        h = h * torch.exp(g[:, t])[..., None, None]
+        u = beta[:, t][..., None] * (v[:, t] - (h * kr[:, t][..., None]).sum(-2))
+        h = h + kw[:, t][..., None] * u[..., None, :]
+        h.retain_grad()
+        states.append(h)
+        out.append((h * q[:, t][..., None]).sum(-2) * scale)
+    ((torch.stack(out, 1) * do).sum() + (h * dh).sum()).backward()
+    return q, kr, kw, v, g, beta, states
+
+
+@pytest.mark.parametrize("case", ["plain", "bf16", "strong", "forgotten", "growing", "segments", "shared"])
+def test_gates_gradients_token_by_token(ss, case):  # noqa: F811
+    """dg and dbeta of every head and chunk by themselves.
+
+    A vector of dq, or of dk where k reads (r) or is written (w), is within F32_REL of its own and its chunk's mean size; a sum over
+    its K elements with a row takes that as independent roundings, |row| |vector| F32_REL / sqrt(K).  dg_t is the sum of
+    q.dq - k.r - k.w over the chunk's tokens from t on, and of G <dS, S> over the K V elements of the chunk's end, dbeta_t is
+    dR.v and k.r over beta; independent errors add their squares.  (F32_REL is
+    the most that eight products in a row leave; a second plane that is lost in any of the three is two to ten times what is allowed.)"""
+    L = {"segments": 700}.get(case, 200)
+    hk, hv, dk, dv = (2, 4, 64, 48) if case == "shared" else (3, 3, 64, 48)
+    p = problem(1, L, hk, hv, dk, dv, BF if case == "bf16" else F, seed=11)
+    gen = torch.Generator().manual_seed(12)
+    if case == "strong":
+        p["g"] = (-8.0 * torch.rand(1, L, hv, generator=gen)).cuda()
+    elif case == "forgotten":
+        p["g"][:, ::37] = -float("inf")
+    elif case == "growing":
+        p["beta"] *= 0.2
+        p["g"] = (0.3 * torch.randn(1, L, hv, generator=gen)).cuda()
+    do, dh = torch.randn(p["v"].shape, generator=gen).to(p["v"].dtype).cuda(), torch.randn(p["h0"].shape, generator=gen).cuda()
+    got = ss.gdr_bwd(*[p[n] for n in NAMES[:5]], do, p["h0"], dh)
+    q, kr, kw, v, g, beta, states = parts64(p, up(do), up(dh))
+    size = lambda x: x.norm(dim=-1)  # noqa: E731
+    for c in range(0, L, 64):
+        s = slice(c, min(c + 64, L))
+        mean = lambda x: x + x.mean(1, keepdim=True)  # noqa: E731
+        read = size(kr.grad[:, s])
+        terms = (size(q[:, s]) * mean(size(q.grad[:, s]))) ** 2 + (size(kr[:, s]) * mean(read)) ** 2 + (size(kw[:, s]) * mean(size(kw.grad[:, s]))) ** 2
+        from_here = terms.flip(1).cumsum(1).flip(1) / dk
+        end = states[min(c + 63, L - 1)]
+        ends = (size(end.detach().flatten(2)) * size(end.grad.flatten(2))) ** 2 / (dk * dv)
+        allowed = F32_REL * (from_here + ends[:, None]).sum(1).sqrt()
+        off = (got["dg"][:, s].double().cpu() - g.grad[:, s]).norm(dim=1)
+        assert bool((off <= allowed).all()), ("dg", c, off, allowed)
+        bt = beta.detach()[:, s]
+        pieces = (size(v.detach()[:, s]) * mean(size(v.grad[:, s]) / bt)) ** 2 / dv + (size(kr[:, s]) * mean(read / bt)) ** 2 / dk
+        allowed = F32_REL * pieces.sum(1).sqrt()
+        off = (got["dbeta"][:, s].double().cpu() - beta.grad[:, s]).norm(dim=1)
+        assert bool((off <= allowed).all()), ("dbeta", c, off, allowed)
