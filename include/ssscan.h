@@ -515,7 +515,8 @@ ss_status ss_gdr_step(int64_t batch, int heads_k, int heads_v, int dim_k, int di
  *    contiguous (batch, seqlen, heads, n).  w fp32, NULL = ones: (n), or (heads, n)
  *    under SS_NORM_HEAD_WEIGHTS.  Fewer than 2^32 rows.
  *  ss_gated_norm_bwd: dy as y; writes dx, dz (given exactly when z is) under strides of
- *    their own (no two values may share an address) and, where not NULL, dw shaped as
+ *    their own (no two values may share an address; with the same batch and token
+ *    strides both may be columns of one buffer's rows) and, where not NULL, dw shaped as
  *    w, also of a w that is NULL.  Only dw needs the workspace.
  *
  *  ss_residual_norm: rows of a residual stream between two blocks,

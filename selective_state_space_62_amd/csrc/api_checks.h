@@ -60,5 +60,22 @@ bool distinct(int64_t n, int64_t (&size)[D], int64_t (&stride)[D]) {
   return true;
 }
 
+// Whether two strided gradients, each without shared addresses and the second's first value `apart` after
+// the first's, share none: with the same batch and token strides, either all heads of the one lie behind
+// those of the other in each token's columns, or their heads alternate under one head stride.
+inline bool columns_of_one(int64_t batch, int64_t seqlen, int n, int heads_a, const int64_t* sa, int heads_b,
+                           const int64_t* sb, int64_t apart) {
+  if ((batch > 1 && sa[0] != sb[0]) || (seqlen > 1 && sa[1] != sb[1])) return false;
+  const int64_t ea = (heads_a - 1) * sa[2] + n, eb = (heads_b - 1) * sb[2] + n;
+  if (apart >= 0 ? apart >= ea : -apart >= eb) {
+    const int64_t lo = apart < 0 ? apart : 0, hi = apart + eb > ea ? apart + eb : ea;
+    int64_t size[] = {batch, seqlen}, stride[] = {sa[0], sa[1]};
+    if (distinct(hi - lo, size, stride)) return true;
+  }
+  if (heads_a > 1 && heads_b > 1 && sa[2] != sb[2]) return false;
+  int64_t size[] = {batch, seqlen, heads_a > heads_b ? heads_a : heads_b, 2};
+  int64_t stride[] = {sa[0], sa[1], heads_a > 1 ? sa[2] : sb[2], apart < 0 ? -apart : apart};
+  return distinct(n, size, stride);
+}
 
 }  // namespace ssscan

@@ -165,9 +165,17 @@ ss_status ss_gated_norm_bwd(int64_t batch, int64_t seqlen, int heads, int n, ss_
   const int64_t nw = (int64_t)n * (flags & SS_NORM_HEAD_WEIGHTS ? heads : 1);
   const Range ins[] = {rng("x", x, sx * eb), rng("z", z, sz * eb), rng("w", w, nw * 4),
                        rng("dy", dy, tokens * heads * n * eb)};
-  const Range outs[] = {rng("dx", dx, sdx * eb), rng("dz", dz, sdz * eb), rng("dw", dw, nw * 4),
-                        rng("workspace", workspace, (int64_t)need)};
-  if ((st = check_disjoint(ins, 4, outs, 4)) != SS_OK) return st;
+  const Range outs[] = {rng("dx", dx, sdx * eb), rng("dw", dw, nw * 4), rng("workspace", workspace, (int64_t)need),
+                        rng("dz", dz, sdz * eb)};
+  if ((st = check_disjoint(ins, 4, outs, 3)) != SS_OK) return st;
+  if ((st = check_disjoint(ins, 4, outs + 3, 1)) != SS_OK) return st;
+  // dx and dz may be columns of one buffer's rows
+  const int64_t apart = (int64_t)(outs[3].lo - outs[0].lo);
+  for (int i = 0; i < 3; ++i) {
+    if (!overlap(outs[i], outs[3])) continue;
+    if (i == 0 && apart % eb == 0 && columns_of_one(batch, seqlen, n, heads, dx_stride, heads, dz_stride, apart / eb)) continue;
+    return record_error(SS_ERR_INVALID_ARG, "%s overlaps dz", outs[i].name);
+  }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (tokens == 0) {
     const hipError_t e = launch_fill_zero(dw, nw, s);

@@ -48,24 +48,6 @@ ss_status check_side(const char* name, const void* p, const int64_t* st, int64_t
   return SS_OK;
 }
 
-// Whether two strided gradients, each without shared addresses and dk's first value `apart` after
-// dq's, share none: with the same batch and token strides, either all heads of the one lie behind
-// those of the other in each token's columns, or their heads alternate under one head stride.
-bool columns_of_one(int64_t batch, int64_t seqlen, int n, int heads_q, const int64_t* sq, int heads_k,
-                    const int64_t* sk, int64_t apart) {
-  if ((batch > 1 && sq[0] != sk[0]) || (seqlen > 1 && sq[1] != sk[1])) return false;
-  const int64_t eq = (heads_q - 1) * sq[2] + n, ek = (heads_k - 1) * sk[2] + n;
-  if (apart >= 0 ? apart >= eq : -apart >= ek) {
-    const int64_t lo = apart < 0 ? apart : 0, hi = apart + ek > eq ? apart + ek : eq;
-    int64_t size[] = {batch, seqlen}, stride[] = {sq[0], sq[1]};
-    if (distinct(hi - lo, size, stride)) return true;
-  }
-  if (heads_q > 1 && heads_k > 1 && sq[2] != sk[2]) return false;
-  int64_t size[] = {batch, seqlen, heads_q > heads_k ? heads_q : heads_k, 2};
-  int64_t stride[] = {sq[0], sq[1], heads_q > 1 ? sq[2] : sk[2], apart < 0 ? -apart : apart};
-  return distinct(n, size, stride);
-}
-
 ss_status check_common(int64_t batch, int64_t seqlen, int heads_q, int heads_k, int head_dim, int rot_dim, ss_dtype io,
                        uint32_t flags, float eps, const void* q, const int64_t* q_stride, const void* k,
                        const int64_t* k_stride, const float* wq, const float* wk, const double* inv_freq,

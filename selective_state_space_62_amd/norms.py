@@ -49,7 +49,7 @@ def gated_norm_bwd(x, z, dy, w=None, *, eps=1e-6, gate_first=False, dx=None, dz=
     """Gradients of ``gated_norm`` for the upstream gradient dy (contiguous, shaped like x), given the forward's inputs.
 
     dx, dz: optional tensors shaped like x that receive the gradients under strides of their
-    own.  Returns a dict: dx, dz (None without z) and dw float32 shaped like w ((N,) without one;
+    own, also as columns of the same rows.  Returns a dict: dx, dz (None without z) and dw float32 shaped like w ((N,) without one;
     None where need_dw is False).
     """
     dev, dtype, head, ins = _gated(x, z, w, eps, gate_first)
