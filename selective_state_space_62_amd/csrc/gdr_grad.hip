@@ -9,7 +9,8 @@
 //   Y_j  = D_Cj dS U_j + sum_i N_ij q_i - sum_i beta_i M_ij k_i
 //   dk = Y - beta X,  dbeta = dR.v - k.X,
 //   dgam_i = q_i.dq_i - beta_i k_i.X_i - k_i.Y_i, at the chunk's last token also sum_j k_j.(D_Cj dS U_j) + G_C <dS, S>,
-// and dg the sums of dgam from a token to the chunk's end.  Everything is fp32 in two planes, as dbeta and dg are differences.
+// and dg the sums of dgam from a token to the chunk's end.  Everything is fp32 in two planes, as dbeta and dg are differences, and the dot
+// products and sums that dg is what remains of (64 tokens' parts, each several times as large) are fp64: they were most of its error.
 // Rows of dO, U and dR pass LDS 64 columns at a time; a wave reads its own rows of S and dS from memory.  The products run
 // transposed, a lane a token, so that gradients are stored in runs.  A triangle is summed over its rows and over its
 // columns; its other orientation is a product with the identity.  The chunks depend on nothing of each other: memory's
@@ -33,11 +34,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   constexpr int NP = planes_of<IO>(), kTiles = KP / 32, kTurned = kTiles * 4 * kBlock;
   constexpr bool kAhead = NP == 2;                         // one workgroup on a CU, with registers to spare
   constexpr int kRegion = (NP + 4) * kRowBytes;            // dO, U, dR; then two triangles at a time, and sums over values of keys
-  static_assert(kRegion >= 4 * kTriBytes + 4 * kTiles * kC * 4, "");
+  static_assert(kRegion >= 4 * kTriBytes + 4 * kTiles * kC * 8, "");
   __shared__ alignas(16) char s_kt[NP * kTurned], s_qt[NP * kTurned], s_r[kRegion];
   __shared__ alignas(16) float s_vec[kVecs][kC], s_beta[kC];
-  __shared__ float s_mx[8], s_sd[8], s_rv[4][kC];
-  float(&s_dot)[4][kTiles][kC] = *reinterpret_cast<float(*)[4][kTiles][kC]>(s_r + 4 * kTriBytes);
+  __shared__ float s_mx[8], s_rv[4][kC];
+  __shared__ double s_sd[8];
+  double(&s_dot)[4][kTiles][kC] = *reinterpret_cast<double(*)[4][kTiles][kC]>(s_r + 4 * kTriBytes);
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, low = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t at = blockIdx.x, bh = at / a.chunks, chunk = at - bh * a.chunks;
@@ -93,7 +95,8 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   char* const s_u = s_r + NP * kRowBytes;
   char* const s_d = s_u + 2 * kRowBytes;
   acc16 Q = zero16(), X = zero16(), Y = zero16(), C = zero16();
-  float sd = 0.0f, rv = 0.0f;
+  double sd = 0.0;
+  float rv = 0.0f;
   {
     const __amdgpu_buffer_rsrc_t orows = chunk_rows<IO>(static_cast<const T*>(a.dout) + (b * a.seqlen + first) * ostride + (int64_t)h * a.dv, ostride, valid, a.dv);
     const __amdgpu_buffer_rsrc_t vrows = chunk_rows<IO>(static_cast<const T*>(a.v) + b * a.vs[0] + first * a.vs[1] + h * a.vs[2], a.vs[1], valid, a.dv);
@@ -156,6 +159,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
       }
       if (active) {
         const uint32_t off = ((m * (ld / 16) + v0 / 16) * 512 + lane * 4) * 4;
+        float part = 0.0f;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t o = v0 + 16 * s < ld ? off + 2048 * s : kNowhere;
@@ -165,7 +169,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float sv = __uint_as_float(j < 4 ? s0[j & 3] : s1[j & 3]), ev = __uint_as_float(j < 4 ? d0[j & 3] : d1[j & 3]);
-            sd = fmaf(sv, ev, sd);
+            part = fmaf(sv, ev, part);
             S.hi[j] = (_Float16)(sv * cS.f);
             S.lo[j] = (_Float16)fmaf(sv, cS.f, -(float)S.hi[j]);
             E.hi[j] = (_Float16)(ev * cE.f);
@@ -175,6 +179,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
           X = mm<2, 2>(S, operand<2>(s_d + (ti * 4 + s) * kBlock, lane, kRowBytes), X);
           Y = mm<2, 2>(E, operand<2>(s_u + (ti * 4 + s) * kBlock, lane, kRowBytes), Y);
         }
+        sd += part;
       }
     }
   }
@@ -183,7 +188,9 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   {
     const float f = times_pow2(of_n ? a.scale : 1.0f, -cU.e - (of_n ? cO.e : cD.e));
     const int i = i0 + low;
-    const float whole = s_vec[kVecWhole][i], rest = s_vec[kVecRest][i];
+    // U comes times 2^-p_j, so N would be times 2^-p_i; of that only growth is left in it.  So that both orientations hold the same
+    // values where gates decay: what one of them adds to dg the other takes back (else dg of strong decays is off by 10^-5).
+    const float whole = s_vec[kVecWhole][i] + (of_n ? fminf(s_vec[kVecGrow][i], 0.0f) : 0.0f), rest = s_vec[kVecRest][i];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int j = j0 + tile_row(r, lane);
@@ -193,15 +200,16 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   }
   const float mC = wave_max(max_of(C, 0.0f));
   rv += __shfl_xor(rv, 32);
-  sd = group_sum(sd, 64);
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) sd += __shfl_xor(sd, i);
   if (lane == 0) {
     s_mx[wave] = tile < 3 ? mC : 0.0f;
-    s_sd[wave] = active && ti == 0 ? sd : 0.0f;
+    s_sd[wave] = active && ti == 0 ? sd : 0.0;
   }
   if (half == 0) s_rv[wave & 3][32 * (wave >> 2) + low] = rv;
   __syncthreads();
   const Scale t0 = scale_of(fmaxf(s_mx[0], fmaxf(s_mx[1], s_mx[2])), kMostE), t1 = scale_of(fmaxf(s_mx[4], fmaxf(s_mx[5], s_mx[6])), kMostE);
-  // the other orientation: a lane a column j, rows times what is not yet theirs: 2^p_i of N, beta_i of M, at most 2^rise
+  // the other orientation: a lane a column j, rows times what is not yet theirs: 2^p_i of N where p_i > 0, beta_i of M, at most 2^rise
   const int rise_n = (int)wave_max(fmaxf(s_vec[kVecGrow][lane], 0.0f));
   const int rise_m = max(exponent(wave_max(fabsf(s_beta[lane]))) + 1, 0);
   auto write_triangles = [&]() {
@@ -217,7 +225,7 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int i = i0 + tile_row(r, lane);
-      t[r] = held(t[r] * (of_n ? pow2((int)s_vec[kVecGrow][i] - rise_n) : s_beta[i] * pow2(-rise_m)));
+      t[r] = held(t[r] * (of_n ? pow2(max((int)s_vec[kVecGrow][i], 0) - rise_n) : s_beta[i] * pow2(-rise_m)));
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -250,21 +258,21 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   }
   if (active) {
     const float into = s_vec[kVecInto][tok];
-    const float f = times_pow2(a.scale * into, -cS.e - cO.e), fn = times_pow2(1.0f, (int)s_vec[kVecGrow][tok] - ek - t0.e), fy = times_pow2(1.0f, rise_n - eq - t0.e);
+    const float f = times_pow2(a.scale * into, -cS.e - cO.e), fn = times_pow2(1.0f, max((int)s_vec[kVecGrow][tok], 0) - ek - t0.e), fy = times_pow2(1.0f, rise_n - eq - t0.e);
     const float fe = times_pow2(s_vec[kVecEnd][tok] * s_vec[kVecS][tok], -cE.e - cU.e);
     const float fx = times_pow2(exp2_of(s_vec[kVecWhole][tok], s_vec[kVecRest][tok]), -cS.e - cD.e);
-    float qdq = 0.0f, kend = 0.0f;
+    double qdq = 0.0, kend = 0.0;
     const acc16 nk = through(s_kt, true);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       Q[r] = fmaf(Q[r], f, nk[r] * fn);
-      qdq = fmaf(rq[r >> 2].value(r & 3), Q[r], qdq);
+      qdq = fma((double)rq[r >> 2].value(r & 3), (double)Q[r], qdq);
     }
     const acc16 nq = through(s_qt, false);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const float e = Y[r] * fe;
-      kend = fmaf(rk[r >> 2].value(r & 3), e, kend);
+      kend = fma((double)rk[r >> 2].value(r & 3), (double)e, kend);
       Y[r] = fmaf(nq[r], fy, e);
       X[r] *= fx;
     }
@@ -288,12 +296,12 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   if (active) {
     const float fm = times_pow2(1.0f, -ek - t1.e), fb = times_pow2(1.0f, rise_m - ek - t1.e), beta = s_beta[tok];
     const acc16 mk = through(s_kt, true), mb = through(s_kt, false);
-    float kx = 0.0f, ky = 0.0f;
+    double kx = 0.0, ky = 0.0;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const float kv = rk[r >> 2].value(r & 3), x = fmaf(mk[r], fm, X[r]), y = fmaf(-mb[r], fb, Y[r]);
-      kx = fmaf(kv, x, kx);
-      ky = fmaf(kv, y, ky);
+      kx = fma((double)kv, (double)x, kx);
+      ky = fma((double)kv, (double)y, ky);
       Y[r] = fmaf(-beta, x, y);
     }
     kx += __shfl_xor(kx, 32);
@@ -312,24 +320,26 @@ __global__ __launch_bounds__(kThreads, IO::kPerSpan == 8 ? 4 : 2) void gdr_grad_
   }
   __syncthreads();
   if (wave == 0) {
-    float d[4] = {};
+    double d[4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) d[i] += s_dot[i][t][lane];
-    float all = 0.0f;
+    double end = d[3], all = 0.0;
+#pragma unroll
+    for (int i = 1; i < kC; i <<= 1) end += __shfl_xor(end, i);
 #pragma unroll
     for (int i = 0; i < 8; ++i) all += s_sd[i];
-    const float end = group_sum(d[3], 64) + s_vec[kVecInto][kC - 1] * all;
-    float dgam = d[0] - s_beta[lane] * d[1] - d[2] + (lane == kC - 1 ? end : 0.0f);
+    end += s_vec[kVecInto][kC - 1] * all;
+    double dgam = d[0] - s_beta[lane] * d[1] - d[2] + (lane == kC - 1 ? end : 0.0);
 #pragma unroll
     for (int i = 1; i < kC; i <<= 1) {
-      const float o = __shfl_down(dgam, i);
+      const double o = __shfl_down(dgam, i);
       if (lane + i < kC) dgam += o;
     }
     if (lane < valid) {
-      if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = (s_rv[0][lane] + s_rv[1][lane] + s_rv[2][lane] + s_rv[3][lane]) * pow2(-(int)s_vec[kVecGrow][lane]) - d[1];
-      if (a.dg) a.dg[gate + (int64_t)lane * a.hv] = dgam;
+      if (a.dbeta) a.dbeta[gate + (int64_t)lane * a.hv] = (s_rv[0][lane] + s_rv[1][lane] + s_rv[2][lane] + s_rv[3][lane]) * pow2(-(int)s_vec[kVecGrow][lane]) - (float)d[1];
+      if (a.dg) a.dg[gate + (int64_t)lane * a.hv] = (float)dgam;
     }
   }
 }

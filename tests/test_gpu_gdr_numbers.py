@@ -301,3 +301,29 @@ def test_gates_gradients_token_by_token(ss, case):  # noqa: F811
         allowed = F32_REL * pieces.sum(1).sqrt()
         off = (got["dbeta"][:, s].double().cpu() - beta.grad[:, s]).norm(dim=1)
         assert bool((off <= allowed).all()), ("dbeta", c, off, allowed)
+
+
+@pytest.mark.parametrize("io", [F, BF])
+@pytest.mark.parametrize("rate", [0.3, 1.0, 3.0])
+@pytest.mark.parametrize("heads,K,V,L", [(1, 8, 16, 500), (1, 16, 128, 500), (1, 32, 16, 300), (2, 64, 128, 200), (2, 128, 64, 130)])
+def test_gates_gradients_of_strong_decays(ss, io, rate, heads, K, V, L):  # noqa: F811
+    """Where gates decay by several powers of 2 from token to token, dg is what is left of parts that tokens next to each other add and
+    take back.  Both are formed of the same values of N and of M, so only the sums' own roundings stay: an element of dq, r or w is
+    rounded by half a step, 2^-24 at most and 2^-24 / sqrt(3) in the mean, in each of some twelve additions of its own size, 2^-23
+    together; these are independent over a row's elements and the chunk's tokens, and sized as in the test above."""
+    p = problem(1, L, heads, heads, K, V, io, seed=13)
+    gen = torch.Generator().manual_seed(14)
+    p["g"] = (-rate * torch.nn.functional.softplus(torch.randn(1, L, heads, generator=gen))).cuda()
+    do, dh = torch.randn(p["v"].shape, generator=gen).to(io).cuda(), torch.randn(p["h0"].shape, generator=gen).cuda()
+    got = ss.gdr_bwd(*[p[n] for n in NAMES[:5]], do, p["h0"], dh)
+    q, kr, kw, v, g, beta, states = parts64(p, up(do), up(dh))
+    size = lambda x: x.norm(dim=-1)  # noqa: E731
+    total = 0.0
+    off = (got["dg"].double().cpu() - g.grad).norm()
+    for c in range(0, L, 64):
+        s = slice(c, min(c + 64, L))
+        terms = (size(q[:, s]) * size(q.grad[:, s])) ** 2 + (size(kr[:, s]) * size(kr.grad[:, s])) ** 2 + (size(kw[:, s]) * size(kw.grad[:, s])) ** 2
+        total += float(terms.detach().flip(1).cumsum(1).sum()) / K
+        end = states[min(c + 63, L - 1)]
+        total += float(((size(end.detach().flatten(2)) * size(end.grad.flatten(2))) ** 2).sum()) * (min(c + 64, L) - c) / (K * V)
+    assert float(off) <= 2.0 ** -23 * total ** 0.5, (float(off), 2.0 ** -23 * total ** 0.5)
