@@ -467,7 +467,12 @@ ss_status ss_qk_norm_rot_bwd(int64_t batch, int64_t seqlen, int heads_q, int hea
  * batch, heads and columns together make fewer than 2^23 workgroups.
  * The state and all sums are fp32, outputs rounded once; sequences of more than 10 to
  * 16 tokens are taken in chunks of 64, with products in pairs of fp16 (22 bits), and
- * where the heads are few a sequence's parts at the same time.  g of
+ * where the heads are few a sequence's parts at the same time.  A pair holds nothing
+ * below 2^-38 of the largest value that is scaled with it, one of 32 columns of v (or
+ * h0) by 64 tokens or all keys: a column, or a token before a larger one, that is
+ * 2^-24 of it keeps 14 bits, and so does what the gates of 64 tokens leave of a state
+ * that they decay by 2^-40.  By 2^-126 they count as having forgotten it, and they
+ * may not grow one by 2^100 or more.  Values of 1e-20 to 1e18 keep their digits.  g of
  * -inf forgets the state; a padding token has beta = 0, g = 0 and finite q, k and v.
  * Anything infinite or NaN in a token may reach all outputs of its head from the 64
  * tokens (of t / 64) that it is among onwards, in the backward also those before.

@@ -104,9 +104,13 @@ ss_status check_blocks(int64_t blocks) {
   return SS_OK;
 }
 
-// Up to this many tokens go one by one, and tokens so far apart that 64 of them pass 2^31 bytes.  One by one and in a chunk, us: keys
-// of 64, 4 heads, 12 tokens 15, 19, 16 tokens 19, 19, 24 tokens 27, 19; keys of 128, 16 heads, 8 tokens 18, 20, 16 tokens 30, 20;
-// 128 x 40 heads, 8 tokens 217, 259, 16 tokens 339, 268.
+// Up to this many tokens go one by one, and tokens so far apart that 64 of them pass 2^31 bytes.  Where the two meet goes by the heads and
+// the type too (fewer heads and bf16 sooner); this is between: one by one and in a chunk, kernels' us (values of 128, of 64 with keys of 16):
+//   bf16, keys of 128:  4 heads, 8 tokens 19, 21, 10 tokens 22, 21, 16 tokens 32, 21; 128 x 40 heads, 8 tokens 222, 274, 12 tokens 282, 280
+//   bf16, keys of 64:   4 heads, 10 tokens 17, 17, 16 tokens 24, 17; 8 x 40 heads, 16 tokens 29, 26; 128 x 40 heads, 16 tokens 203, 202
+//   bf16, keys of 16:   4 heads, 10 tokens 16, 15, 16 tokens 23, 15; 128 x 40 heads, 16 tokens 130, 119; 512 x 40 heads, 16 tokens 458, 489
+//   fp32, keys of 128:  4 heads, 10 tokens 19, 26, 16 tokens 27, 26; 128 x 40 heads, 10 tokens 203, 520, 32 tokens 476, 542
+//   fp32, keys of 64:   4 heads, 16 tokens 21, 19; 128 x 40 heads, 16 tokens 162, 241, 24 tokens 222, 249
 constexpr int64_t recur_tokens(int dim_k) { return dim_k <= 64 ? 16 : 10; }
 constexpr int64_t kMostStride = int64_t(1) << 22;
 
@@ -132,12 +136,13 @@ struct Segments {
 };
 
 // Segments of at least two chunks, as many as fill the GPU, but no more than 2 sqrt(chunks): a segment's join takes as long as a
-// quarter of a chunk's two passes (one head of 2^20 tokens, 256 segments 1864, 512 2487; 2 heads of 32768, 64 segments 289, 256 727;
-// one head of 4096, 16 segments 105, 32 125; backward, one head of 131072, 128 segments 1366, 512 2854).  Made in segments a row costs about 1.7 times as much, the factors
-// and the states first, so two of them gain nothing.  In one and in segments, us: 16 heads of 131072 tokens 15742, 2341; 12 x 8 heads
-// (fp32, keys of 64) of 2048 335, 271; 40 heads of 4096 496, 247; 8 heads of 500 67, 53; 2 heads of 1000 91, 43; 4 x 40 heads of
-// 2048 318, 320; 8 x 40 heads of 2048, which fill it, 509 and, in three, 614.  Backward: 16 heads of 32768 10455, 2130; 3 x 10 heads
-// (fp32, 72 by 80) of 1111 471, 263; 2 heads of 1000 236, 101; 4 x 40 heads of 2048 1283, 1255.
+// quarter of a chunk's two passes (one head of 2^20 tokens, 256 segments 1980, 512 2549; 2 heads of 32768, 64 segments 300, 256 736;
+// one head of 4096, 16 segments 112, 32 130; backward, one head of 131072, 128 segments 1399, 512 2879).  Made in segments a row costs
+// about 1.7 times as much, the factors and the states first, so two of them gain little.  In one and in segments, us: 16 heads of
+// 131072 tokens 16973, 2577; 12 x 8 heads (fp32, keys of 64) of 2048 337, 280; 40 heads of 4096 553, 279; 8 heads of 500 76, 59; 2
+// heads of 1000 133, 68; 4 x 40 heads of 2048 361, in two 347, in three 338; 8 x 40 heads of 2048, which fill it, 535 and, in three,
+// 656.  Backward: 16 heads of 32768 10405, 2192; 3 x 10 heads (fp32, 72 by 80) of 1111 467, 268; 2 heads of 1000 320, 156; 4 x 40 heads
+// of 2048 1308, in two 1300, in three 1280.
 Segments segments_of(int64_t batch, int64_t chunks, int heads_v, int dim_k, int dim_v, int io) {
   const int64_t groups = batch * heads_v * ((dim_v + 127) / 128);
   const int64_t n = std::min({gdr_chunk_room(io, dim_k) / groups, chunks / 2, (int64_t)(2.0 * std::sqrt((double)chunks))});

@@ -8,11 +8,12 @@
 // to LDS, and nothing waits for a value that a workgroup could not form beforehand.
 // Where there are too few heads for the GPU, the chunks of one go in segments at the same time: the state behind a segment is a
 // product with the state before it and a sum, both made first (Of::kEnds) and put together in turn by a small kernel.
-// 8 x 40 heads of 2048 tokens, 128 by 128, bf16: 379 us, 12 us to a chunk with two workgroups on a CU; 4 x 40 heads, one on a CU, 7.
-// Its matrix instructions alone would take 1.4 us of that (3456 cycles of a SIMD), the other vector instructions 2 (about 1200); the
-// rest is the latency of seven products in turn.  Loads of V a chunk ahead (more registers) made it 397.
+// 8 x 40 heads of 2048 tokens, 128 by 128, bf16: 418 us, 13 us to a chunk with two workgroups on a CU; 4 x 40 heads, one on a CU, 8.5.
+// Its matrix instructions alone would take 1.8 us of that (4352 cycles of a SIMD), the other vector instructions 2 (about 1200); the
+// rest is the latency of seven products in turn.  (S, U and P in one plane for bf16 outputs took 380, but then those are off by 2^-12
+// before they are rounded.)  Loads of V a chunk ahead (more registers) made that 397.
 // For the backward the same kernel makes S before every chunk and U (transposed by a product with the identity, as
-// operands of the gradients) instead of O: 415 us, of them about 200 the 1 GB that it writes.
+// operands of the gradients) instead of O: 420 us, of them about 200 the 1 GB that it writes.
 #include "gdr_device.h"
 
 namespace ssscan {

@@ -4,7 +4,8 @@
 // lo = fp16(x s - hi), 22 bits together, and a product of two such operands is hi hi + hi lo + lo hi in fp32, within
 // about 2^-22 of the sizes of its terms: fp32 results at 3 of the 16 times that an fp32 matrix instruction costs.  A
 // bf16 input is one plane.  Scales keep a tile's (of keys and queries a row's, of T a column's) largest value near 2^13, so that
-// what an fp16 cannot hold, 2^-25, is below 2^-37 of it: a chunk's later tokens may be as much smaller as decays make them.
+// what an fp16 cannot hold, 2^-25, is below 2^-37 of it: a chunk's later tokens may be as much smaller as decays make them.  A tile is
+// a wave's 32 columns of all keys or of 64 tokens: what is 2^-24 of the largest in it keeps 14 bits.
 //
 // Tiles are 32x32x16.  A result's lane holds column l & 31 and rows (r & 3) + 8 (r >> 2) + 4 (l >> 5): for 16 rows
 // these are the 8 values that the same lane gives an operand whose summed index is that row, if the other operand

@@ -16,8 +16,8 @@
 // columns; its other orientation is a product with the identity.  The chunks depend on nothing of each other: memory's
 // latency is hidden by a second workgroup on the CU, which bounds a lane to 128 registers (bf16).
 // Value heads that share a key head leave fp32 parts, added in their order afterwards.
-// 8 x 40 heads of 2048 tokens, 128 by 128, bf16: 975 us for 2.6 GB (500 us as a copy): loads that wait for one another, at four waves
-// to a SIMD.  One workgroup on a CU with all registers took 1352, rows loaded a pass ahead at 128 registers twice as long (spills).
+// 8 x 40 heads of 2048 tokens, 128 by 128, bf16: 1010 us for 2.6 GB (500 us as a copy): loads that wait for one another, at four waves
+// to a SIMD (dg's sums in fp32 took 975).  One workgroup on a CU with all registers took 1352, rows loaded a pass ahead at 128 registers twice as long (spills).
 #include "gdr_device.h"
 
 namespace ssscan {

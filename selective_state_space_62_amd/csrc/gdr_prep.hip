@@ -6,8 +6,8 @@
 // decays' vectors, a workgroup to each chunk of a head.  k.k^T and q.k^T are matrix products; the inverse is by 16x16
 // triangles on the diagonal, a lane to a column, and then by twice joining neighbours, T21 = -T22 A21 T11, in fp32: a product's
 // result is the next one's operand as it stands.  P's exponentials and stores run beside the triangles' chain.
-// The workgroups' chains bound it, not memory (0.28 GB of T, P and vectors, 53 us as a copy): 8 x 40 heads of 2048 tokens by 128 keys
-// in bf16 take 160 us (two workgroups on a CU), 222 before the joins were matrix products, the gates' sums went over lanes by DPP and
+// The workgroups' chains bound it, not memory (0.32 GB of T, P and vectors, 60 us as a copy): 8 x 40 heads of 2048 tokens by 128 keys
+// in bf16 take 163 us (two workgroups on a CU), 222 before the joins were matrix products, the gates' sums went over lanes by DPP and
 // P left the chain; with T transposed for the backward 221.
 // (A, T and P are formed balanced by the growth p; gdr_device.h says how.)
 // Sums of log decays are formed in fp64 and kept as a whole number and the rest: a forgotten state (a decay of -inf, held to -2000

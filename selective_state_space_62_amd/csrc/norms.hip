@@ -1,9 +1,9 @@
 // The norms before and after a block (include/ssscan.h): gated norm, residual norm, and their gradients.
 //
 // Bytes bound all four: a row is read once, kept in registers as it was read, its sums go over the row's lanes, and
-// everything else is formed from the registers.  G lanes (a power of 2 up to 512) take a row, each one or two vectors of
-// 8 consecutive values, so that a row of up to 1024 values needs one wave at most and no barrier.  Wider rows are a
-// workgroup's: their sums pass LDS, one barrier for each set of sums.
+// everything else is formed from the registers.  A row of up to 512 values (forward 1024, of two vectors to a lane) is a power of 2 of
+// lanes of one wave, which hold a vector of 8 consecutive values each, and its sums need no barrier.  Wider rows are a workgroup's, of
+// as many waves (up to eight) as its vectors fill, two to a lane from 4097 values on: their sums pass LDS, one barrier for each set of sums.
 // The weights' gradients stay in a lane's registers over the rows of its workgroup; the workgroups' sums are then
 // added in a fixed order.
 // bf16 unless said: rows of 5120, 16384 of them, gated 95 us, 5.3 TB/s (178 before a row's loads went out one row ahead and a weight's
