@@ -327,3 +327,19 @@ def test_gates_gradients_of_strong_decays(ss, io, rate, heads, K, V, L):  # noqa
         end = states[min(c + 63, L - 1)]
         total += float(((size(end.detach().flatten(2)) * size(end.grad.flatten(2))) ** 2).sum()) * (min(c + 64, L) - c) / (K * V)
     assert float(off) <= 2.0 ** -23 * total ** 0.5, (float(off), 2.0 ** -23 * total ** 0.5)
+
+
+@pytest.mark.parametrize("L,heads", [(1024, 2), (2048, 40)])
+@pytest.mark.parametrize("at", [(300,), (128, 255, 256), (5, 130, 131, 700)])
+def test_states_forgotten_in_segments(ss, L, heads, at):  # noqa: F811
+    """Segments whose factor is zero, also after it has grown by 2^180: neither the state before nor what it would have become gets by."""
+    p = problem(1, L, heads, heads, 32, 32, F, seed=17)
+    p["g"][:, list(at)] = -float("inf")
+    check_fwd(ss, p)
+    check_bwd(ss, p)
+    q, dh = linear(1, L, heads, 32, 1.0, slice(128, 254), 2.0 ** -100, 0.3)
+    q["g"][:, 254] = -float("inf")
+    o, h = ss.gdr_fwd(*[q[n] for n in NAMES])
+    assert float(h.abs().max()) == 0.0 == float(o[:, 254:].abs().max()) and bool(torch.isfinite(o).all())
+    back = ss.gdr_bwd(*[q[n] for n in NAMES[:5]], torch.zeros_like(q["v"]), q["h0"], dh)
+    assert float(back["dh0"].abs().max()) == 0.0 and all(bool(torch.isfinite(x).all()) for x in back.values())
